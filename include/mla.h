@@ -488,6 +488,116 @@ mla_status mla_plan_run(const mla_decode_plan* plan, void* stream);
 /* Frees a plan (NULL is ignored).  Launches already made are unaffected. */
 void mla_plan_destroy(mla_decode_plan* plan);
 
+/*
+ * mla_batch_build - the tables of one step, built on the GPU from its
+ * requests' lengths: block table, slot map, positions and cumulative lengths,
+ * with the new pages taken off a stack of free pages.
+ *
+ * The pages keep these as device buffers that the host refreshes before each
+ * step ([diff] triton_mla.py, TritonMLAState: slot_mapping, seq_lens,
+ * block_tables); here they come from two lengths per request.  A request
+ * owns a row of `req_block_table` for as long as it runs: its pages in token
+ * order.  For batch entry b with row r = req_ids[b] (b without req_ids),
+ * c = context_lens[b] tokens cached and n = query_lens[b] new ones:
+ *   seq_lens[b] = c + n;  cu_seqlens_q / cu_seqlens_k: sums of n / of c + n
+ *               over the entries before b (num_reqs + 1 values);
+ *   pages       the row holds ceil(c / bs) pages and gets ceil((c + n) / bs);
+ *               new page k of the batch (entries in order, pages in order) is
+ *               free_blocks[*free_count - 1 - k], written into the row;
+ *   block_table[b][0 .. ceil(seq_lens[b] / bs)) = the row (entries past the
+ *               last page are left as they were);
+ *   token j of entry b, output row t = cu_seqlens_q[b] + j < num_tokens:
+ *               positions[t] = c + j, slot_mapping[t] = page * bs +
+ *               (c + j) % bs;
+ *   rows t >= cu_seqlens_q[num_reqs] up to num_tokens (padding of a captured
+ *               graph): positions 0, slot -1 (mla_cache_write skips those);
+ *   *free_count_out = *free_count less the pages taken (at least 0).
+ *
+ *   req_ids         int32 [num_reqs], or NULL.  Different entries have
+ *                   different rows (else the row's new pages are unspecified).
+ *   num_reqs        0 .. 16384.
+ *   req_block_table int32 [num_table_rows][max_blocks_per_req] at row stride
+ *                   req_block_table_stride (elements); max_blocks_per_req *
+ *                   block_size <= 2^30.
+ *   block_size      1 .. 1024.  num_blocks: pages of the cache.
+ *   free_blocks     int32 [free_capacity], the stack, bottom first.
+ *   free_count      int32 [1], its height (clamped to [0, free_capacity]).
+ *   free_count_out  int32 [1]; may be free_count itself (costs one more small
+ *                   launch when the batch is larger than one CTA).
+ *   block_table     int32 [num_reqs][>= max_blocks_per_req] at row stride
+ *                   block_table_stride.
+ *   positions, slot_mapping   int64 [num_tokens].
+ *   err_count       device int, may be NULL: one for each token without a
+ *                   slot, each page that could not be taken (stack empty, or
+ *                   an id outside [0, num_blocks)), each entry whose lengths
+ *                   were clamped (negative, or beyond the row), and one when
+ *                   the tokens exceed num_tokens (the rest get no row).
+ * A page that could not be taken is -1 in both tables, and its tokens' slots
+ * are -1; so are those of an entry whose row is outside the table (it takes
+ * no page).  Apart from free_count_out no output may overlap an input.
+ */
+mla_status mla_batch_build(const int32_t* req_ids, const int32_t* query_lens,
+                           const int32_t* context_lens, int num_reqs,
+                           int32_t* req_block_table, int64_t req_block_table_stride,
+                           int num_table_rows, int max_blocks_per_req, int block_size,
+                           int num_blocks, const int32_t* free_blocks, int free_capacity,
+                           const int32_t* free_count, int32_t* free_count_out,
+                           int num_tokens, int32_t* block_table, int64_t block_table_stride,
+                           int32_t* seq_lens, int32_t* cu_seqlens_q, int32_t* cu_seqlens_k,
+                           int64_t* positions, int64_t* slot_mapping, int* err_count,
+                           void* stream);
+
+/*
+ * mla_blocks_release - finished requests' pages back onto the stack that
+ * mla_batch_build takes them from: the ceil(held_lens[b] / bs) pages of each
+ * entry's row, entries in order and pages in order, from free_blocks[
+ * *free_count] on; *free_count_out = the new height.  Entries of the table
+ * outside [0, num_blocks) are left out and counted, and so are pages beyond
+ * free_capacity.  The rows themselves are not changed.  Arguments as
+ * mla_batch_build; num_reqs * max_blocks_per_req <= INT32_MAX; free_count_out
+ * may be free_count.  Releasing one row twice in one call puts its pages on
+ * the stack twice.
+ */
+mla_status mla_blocks_release(const int32_t* req_ids, const int32_t* held_lens, int num_reqs,
+                              const int32_t* req_block_table, int64_t req_block_table_stride,
+                              int num_table_rows, int max_blocks_per_req, int block_size,
+                              int num_blocks, int32_t* free_blocks, int free_capacity,
+                              const int32_t* free_count, int32_t* free_count_out,
+                              int* err_count, void* stream);
+
+/*
+ * mla_gather_cache - cached rows of a ragged batch as contiguous bf16
+ * tensors, an fp8 cache dequantised: what the expanded form (mla_expand_kv,
+ * mla_prefill) reads of a cached prefix.
+ *
+ * For output row t of sequence b (cu_seqlens[b] <= t < cu_seqlens[b + 1]) and
+ * pos = seq_starts[b] + t - cu_seqlens[b]: [kv_c[t] | k_pe[t]] = cache row
+ * pos % bs of page block_table[b][pos / bs]; fp8 elements become
+ * bf16(value * *kv_scale), the product in fp32.
+ *
+ *   kv_cache .. block_table_stride   as in mla_decode; block_size 1 .. 1024.
+ *   cu_seqlens      int32 [num_seqs + 1], non-decreasing.
+ *   seq_starts      int32 [num_seqs], first cached token taken of each
+ *                   sequence, or NULL (token 0).
+ *   num_tokens      rows of kv_c and k_pe.  Rows at or past
+ *                   cu_seqlens[num_seqs] are left as they were.
+ *   kv_c            bf16 [num_tokens][kv_lora_rank], k_pe bf16
+ *                   [num_tokens][rope_dim] at the given row strides (multiples
+ *                   of 8); both 16-byte aligned.
+ *   kv_scale        device float, read only for the fp8 formats.
+ *   err_count       device int, may be NULL: counts the rows whose position
+ *                   lies outside the block table or whose block id lies
+ *                   outside [0, num_blocks); they become zeros.
+ */
+mla_status mla_gather_cache(const void* kv_cache, mla_kv_dtype kv_dtype, int num_blocks,
+                            int block_size, int64_t block_stride, int kv_lora_rank,
+                            int rope_dim, const int32_t* block_table,
+                            int64_t block_table_stride, int max_blocks_per_seq,
+                            const int32_t* cu_seqlens, const int32_t* seq_starts,
+                            int num_seqs, int num_tokens, const float* kv_scale, void* kv_c,
+                            int64_t kv_c_row_stride, void* k_pe, int64_t k_pe_row_stride,
+                            int* err_count, void* stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* mla_status_string(mla_status status);
 

@@ -11,6 +11,10 @@ Thin Python binding over the C ABI of ``libmla.so`` (``include/mla.h``):
   over fixed tensors whose ``run()`` only launches kernels (CUDA-graph safe).
 * ``mla_lse_merge`` and ``lse_merge(...)`` — the cross-shard LSE merge of
   per-shard (o, lse) pairs (decode context parallelism).
+* ``batch_build(...)`` and ``blocks_release(...)`` — a step's block table, slot
+  map, positions and cumulative lengths from its requests' lengths, pages
+  taken off and put back onto a stack of free ones.
+* ``gather_cache(...)`` — cached rows of a ragged batch as contiguous bf16.
 * ``cache_write(...)`` and ``decode(...)`` — torch-tensor conveniences that
   only marshal pointers, strides and the current CUDA stream; every step of
   the computation runs in the library's CUDA kernels.
@@ -18,6 +22,8 @@ Thin Python binding over the C ABI of ``libmla.so`` (``include/mla.h``):
 PyTorch supplies device memory and streams; nothing here computes the method.
 """
 from __future__ import annotations
+
+from typing import NamedTuple
 
 from . import _lib
 from ._lib import (MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_FP8_E5M2, MLA_PATH_AUTO,
@@ -27,6 +33,8 @@ __all__ = [
     "mla_cache_write", "mla_decode", "mla_decode_ex", "mla_num_kv_splits",
     "mla_decode_workspace_bytes", "mla_lse_merge", "mla_norm_rope_cache_write",
     "cache_write", "norm_rope_cache_write", "decode", "lse_merge", "DecodePlan",
+    "mla_batch_build", "mla_blocks_release", "mla_gather_cache",
+    "batch_build", "blocks_release", "gather_cache", "BatchTables",
     "MlaError", "load",
     "MLA_KV_BF16", "MLA_KV_FP8_E4M3", "MLA_KV_FP8_E5M2", "MLA_PATH_AUTO", "MLA_PATH_MMA_SYNC",
     "MLA_PATH_TCGEN05",
@@ -52,6 +60,18 @@ def mla_norm_rope_cache_write(*args) -> int:
 
 def mla_lse_merge(*args) -> int:
     return load().mla_lse_merge(*args)
+
+
+def mla_batch_build(*args) -> int:
+    return load().mla_batch_build(*args)
+
+
+def mla_blocks_release(*args) -> int:
+    return load().mla_blocks_release(*args)
+
+
+def mla_gather_cache(*args) -> int:
+    return load().mla_gather_cache(*args)
 
 
 def mla_num_kv_splits(max_seq_len: int, sm_count: int) -> int:
@@ -320,3 +340,201 @@ def lse_merge(o_parts, lse_parts, *, out=None, lse=None, stream=None):
         rows, H, R, out.data_ptr(), lse.data_ptr(), _stream_ptr(stream))
     _lib.check(st, "mla_lse_merge")
     return out, lse
+
+
+# ------------------------------------------------------- prompts and batches
+def _check(cond: bool, what: str) -> None:
+    if not cond:
+        raise ValueError(what)
+
+
+def _cuda(stream, **tensors):
+    """Checks that every tensor given is on the current CUDA device (where the
+    kernels run); returns that device."""
+    torch = _torch()
+    for name, t in tensors.items():
+        _check(t is None or t.is_cuda, f"{name} must be a CUDA tensor")
+    dev = torch.device("cuda", torch.cuda.current_device())
+    for name, t in tensors.items():
+        _check(t is None or t.device == dev, f"{name} is not on the current device {dev}")
+    _check(stream is None or stream.device == dev, f"the stream is not on the current device {dev}")
+    return dev
+
+
+def _empty(stream, *shape, dtype, device):
+    """A new tensor for a kernel that runs on `stream`."""
+    torch = _torch()
+    t = torch.empty(*shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _typed(t, dtype, shape, name):
+    """Checks dtype and shape (None: any size) and unit last stride."""
+    if t is None:
+        return
+    _check(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _check(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)),
+           f"{name} has shape {tuple(t.shape)}, not {shape}")
+    _check(t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1,
+           f"{name} must have unit last stride")
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+class BatchTables(NamedTuple):
+    """A step's tables, from :func:`batch_build`."""
+    block_table: object    # int32 [reqs, max_blocks]
+    seq_lens: object       # int32 [reqs]
+    cu_seqlens_q: object   # int32 [reqs + 1]
+    cu_seqlens_k: object   # int32 [reqs + 1]
+    positions: object      # int64 [tokens]
+    slot_mapping: object   # int64 [tokens]
+    free_count: object     # int32 [1]
+
+
+def batch_build(query_lens, context_lens, req_block_table, free_blocks, free_count,
+                block_size: int, num_blocks: int, num_tokens: int | None = None, *, req_ids=None,
+                block_table=None, seq_lens=None, cu_seqlens_q=None, cu_seqlens_k=None,
+                positions=None, slot_mapping=None, free_count_out=None, err_count=None,
+                stream=None) -> BatchTables:
+    """Build a step's tables from int32 [B] ``query_lens`` (new tokens) and
+    ``context_lens`` (cached tokens) of its requests.
+
+    ``req_block_table`` int32 [rows, max_blocks] holds each running request's
+    pages (row ``req_ids[b]``, or b) and gets the new ones, taken off the top
+    of the stack ``free_blocks`` int32 [n] of height ``free_count`` int32 [1].
+    ``num_tokens``: rows of positions and slot_mapping (padding rows get slot
+    -1); needed unless one of the two is given.  Outputs are allocated when
+    not given; a block table allocated here starts as zeros.
+    ``free_count_out`` may be ``free_count`` (updated in place).
+    """
+    torch = _torch()
+    i32, i64 = torch.int32, torch.int64
+    dev = _cuda(stream, query_lens=query_lens, context_lens=context_lens,
+                req_block_table=req_block_table, free_blocks=free_blocks, free_count=free_count,
+                req_ids=req_ids, block_table=block_table, seq_lens=seq_lens,
+                cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, positions=positions,
+                slot_mapping=slot_mapping, free_count_out=free_count_out, err_count=err_count)
+    _check(query_lens.dim() == 1, "query_lens must have one dimension")
+    B = query_lens.shape[0]
+    if num_tokens is None:
+        given = positions if positions is not None else slot_mapping
+        _check(given is not None, "num_tokens is needed when no token output is given")
+        num_tokens = given.shape[0]
+    _typed(req_block_table, i32, (None, None), "req_block_table")
+    rows, maxb = req_block_table.shape
+    if block_table is None:
+        with torch.cuda.stream(stream):
+            block_table = torch.zeros(B, maxb, dtype=i32, device=dev)
+    mk = lambda t, n, d: t if t is not None else _empty(stream, n, dtype=d, device=dev)  # noqa: E731
+    seq_lens = mk(seq_lens, B, i32)
+    cu_seqlens_q, cu_seqlens_k = mk(cu_seqlens_q, B + 1, i32), mk(cu_seqlens_k, B + 1, i32)
+    positions, slot_mapping = mk(positions, num_tokens, i64), mk(slot_mapping, num_tokens, i64)
+    free_count_out = mk(free_count_out, 1, i32)
+    for t, d, shape, name in (
+            (query_lens, i32, (B,), "query_lens"), (context_lens, i32, (B,), "context_lens"),
+            (req_ids, i32, (B,), "req_ids"), (free_blocks, i32, (None,), "free_blocks"),
+            (free_count, i32, (1,), "free_count"), (free_count_out, i32, (1,), "free_count_out"),
+            (block_table, i32, (B, maxb), "block_table"), (seq_lens, i32, (B,), "seq_lens"),
+            (cu_seqlens_q, i32, (B + 1,), "cu_seqlens_q"),
+            (cu_seqlens_k, i32, (B + 1,), "cu_seqlens_k"),
+            (positions, i64, (num_tokens,), "positions"),
+            (slot_mapping, i64, (num_tokens,), "slot_mapping"),
+            (err_count, i32, (1,), "err_count")):
+        _typed(t, d, shape, name)
+    st = load().mla_batch_build(
+        _ptr(req_ids), query_lens.data_ptr(), context_lens.data_ptr(), B,
+        req_block_table.data_ptr(), req_block_table.stride(0), rows, maxb, int(block_size),
+        int(num_blocks), free_blocks.data_ptr(), free_blocks.numel(), free_count.data_ptr(),
+        free_count_out.data_ptr(), int(num_tokens), block_table.data_ptr(),
+        block_table.stride(0), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
+        cu_seqlens_k.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), _ptr(err_count),
+        _stream_ptr(stream))
+    _lib.check(st, "mla_batch_build")
+    return BatchTables(block_table, seq_lens, cu_seqlens_q, cu_seqlens_k, positions,
+                       slot_mapping, free_count_out)
+
+
+def blocks_release(held_lens, req_block_table, free_blocks, free_count, block_size: int,
+                   num_blocks: int, *, req_ids=None, free_count_out=None, err_count=None,
+                   stream=None):
+    """Put the pages of finished requests (int32 [B] ``held_lens`` tokens each,
+    rows ``req_ids`` of ``req_block_table``) back onto the stack
+    ``free_blocks``; returns the new height (``free_count_out``, by default
+    ``free_count`` updated in place)."""
+    torch = _torch()
+    i32 = torch.int32
+    if free_count_out is None:
+        free_count_out = free_count
+    _cuda(stream, held_lens=held_lens, req_block_table=req_block_table, free_blocks=free_blocks,
+          free_count=free_count, req_ids=req_ids, free_count_out=free_count_out,
+          err_count=err_count)
+    _typed(held_lens, i32, (None,), "held_lens")
+    B = held_lens.shape[0]
+    for t, shape, name in ((req_block_table, (None, None), "req_block_table"),
+                           (req_ids, (B,), "req_ids"), (free_blocks, (None,), "free_blocks"),
+                           (free_count, (1,), "free_count"),
+                           (free_count_out, (1,), "free_count_out"),
+                           (err_count, (1,), "err_count")):
+        _typed(t, i32, shape, name)
+    rows, maxb = req_block_table.shape
+    st = load().mla_blocks_release(
+        _ptr(req_ids), held_lens.data_ptr(), B, req_block_table.data_ptr(),
+        req_block_table.stride(0), rows, maxb, int(block_size), int(num_blocks),
+        free_blocks.data_ptr(), free_blocks.numel(), free_count.data_ptr(),
+        free_count_out.data_ptr(), _ptr(err_count), _stream_ptr(stream))
+    _lib.check(st, "mla_blocks_release")
+    return free_count_out
+
+
+def gather_cache(kv_cache, block_table, cu_seqlens, num_tokens: int | None = None, *,
+                 kv_lora_rank: int | None = None, seq_starts=None,
+                 kv_cache_dtype: str | None = None, kv_scale=None, kv_c=None, k_pe=None,
+                 err_count=None, stream=None):
+    """Cached rows of a ragged batch as (kv_c bf16 [T, R], k_pe bf16 [T, P]).
+
+    Output row t of sequence b (``cu_seqlens`` int32 [B + 1]) is its cached
+    token ``seq_starts[b] + t - cu_seqlens[b]`` (``seq_starts`` int32 [B], by
+    default 0).  ``num_tokens`` rows are allocated unless kv_c and k_pe are
+    given; rows past ``cu_seqlens[B]`` are left as they were.  fp8 caches are
+    multiplied by the device scalar ``kv_scale``.
+    """
+    torch = _torch()
+    bf, i32 = torch.bfloat16, torch.int32
+    dev = _cuda(stream, kv_cache=kv_cache, block_table=block_table, cu_seqlens=cu_seqlens,
+                seq_starts=seq_starts, kv_scale=kv_scale, kv_c=kv_c, k_pe=k_pe,
+                err_count=err_count)
+    kvd = _kv_dtype(kv_cache, kv_cache_dtype)
+    _check(kv_cache.element_size() == (2 if kvd == MLA_KV_BF16 else 1),
+           "kv_cache_dtype does not fit the cache")
+    nb, bs, d, bstride = _cache_geom(kv_cache)
+    R = kv_lora_rank if kv_lora_rank is not None else d - 64
+    P = d - R
+    _typed(block_table, i32, (None, None), "block_table")
+    B = block_table.shape[0]
+    if num_tokens is None:
+        _check(kv_c is not None, "num_tokens is needed when kv_c is not given")
+        num_tokens = kv_c.shape[0]
+    if kv_c is None:
+        kv_c = _empty(stream, num_tokens, R, dtype=bf, device=dev)
+    if k_pe is None:
+        k_pe = _empty(stream, num_tokens, P, dtype=bf, device=dev)
+    for t, dt, shape, name in ((cu_seqlens, i32, (B + 1,), "cu_seqlens"),
+                               (seq_starts, i32, (B,), "seq_starts"),
+                               (kv_c, bf, (num_tokens, R), "kv_c"),
+                               (k_pe, bf, (num_tokens, P), "k_pe"),
+                               (err_count, i32, (1,), "err_count")):
+        _typed(t, dt, shape, name)
+    _check(kv_scale is None or (kv_scale.dtype == torch.float32 and kv_scale.numel() == 1),
+           "kv_scale must be one float32")
+    st = load().mla_gather_cache(
+        kv_cache.data_ptr(), kvd, nb, bs, bstride, R, P, block_table.data_ptr(),
+        block_table.stride(0), block_table.shape[1], cu_seqlens.data_ptr(), _ptr(seq_starts), B,
+        int(num_tokens), _ptr(kv_scale), kv_c.data_ptr(), kv_c.stride(0), k_pe.data_ptr(),
+        k_pe.stride(0), _ptr(err_count), _stream_ptr(stream))
+    _lib.check(st, "mla_gather_cache")
+    return kv_c, k_pe

@@ -89,6 +89,12 @@ SIGNATURES = {
     "mla_plan_create": (_I32, [ctypes.POINTER(DecodeDesc), ctypes.POINTER(ctypes.c_void_p)]),
     "mla_plan_run": (_I32, [_P, _P]),
     "mla_plan_destroy": (None, [_P]),
+    "mla_batch_build": (_I32, [_P, _P, _P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _I32,
+                               _P, _P, _I32, _P, _I64, _P, _P, _P, _P, _P, _P, _P]),
+    "mla_blocks_release": (_I32, [_P, _P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _I32,
+                                  _P, _P, _P, _P]),
+    "mla_gather_cache": (_I32, [_P, _I32, _I32, _I32, _I64, _I32, _I32, _P, _I64, _I32, _P,
+                                _P, _I32, _I32, _P, _P, _I64, _P, _I64, _P, _P]),
     "mla_status_string": (ctypes.c_char_p, [_I32]),
     "mla_last_cuda_error": (ctypes.c_char_p, []),
 }

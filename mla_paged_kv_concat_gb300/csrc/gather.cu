@@ -1,0 +1,132 @@
+// Rows of the paged cache taken out into contiguous bf16 tensors: the
+// latent and the rope part of each cached token of a ragged batch, an fp8
+// cache dequantised on the way.  What the expanded form's products read.
+//
+// out[t] = row (pos % bs) of page block_table[b][pos / bs], with b the
+// sequence of output row t and pos = start[b] + t - cu[b]; an fp8 element is
+// bf16(value * scale), the product in fp32 and rounded to bf16, what the
+// outputs are held in.
+//
+// Bound by memory traffic.  A CTA takes 32 output rows: the threads of one
+// warp look up their rows (binary search of cu, then the page id), then all
+// 256 threads move 16-byte pieces, neighbouring threads neighbouring pieces,
+// with up to four loads of a thread in flight.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace mla {
+
+namespace {
+
+constexpr int kRows = 32;
+constexpr int kThreads = 256;
+
+// Eight fp8 values times the scale as eight bf16 values.
+__device__ __forceinline__ uint4 dequant8(uint32_t a, uint32_t b, bool e5m2, float scale) {
+  uint32_t out[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = k < 2 ? a : b;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>((k & 1) ? w >> 16 : w & 0xFFFFu),
+        e5m2 ? __NV_E5M2 : __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    out[k] = pack_bf16x2(f.x * scale, f.y * scale);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+template <int R, bool FP8>
+__global__ void __launch_bounds__(kThreads) gather_cache_kernel(const GatherParams p) {
+  constexpr int ELT = FP8 ? 1 : 2;
+  constexpr int PIECES = (R + 64) * ELT / 16;  // 16-byte pieces of a cached row
+  constexpr int TOTAL = kRows * PIECES;
+  constexpr int PER = (TOTAL + kThreads - 1) / kThreads;
+  constexpr int kBatch = 4;
+  __shared__ int64_t src_of[kRows];  // element offset of the row; -1 zeros, -2 leave
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  if (threadIdx.x < kRows) {
+    const int64_t t = t0 + threadIdx.x;
+    int64_t src = -2;
+    int err = 0;
+    if (t < p.num_tokens && t >= __ldg(p.cu) && t < __ldg(p.cu + p.num_seqs)) {
+      int a = 0, z = p.num_seqs - 1;  // the last sequence whose first row is <= t
+      while (a < z) {
+        const int m = (a + z + 1) >> 1;
+        if (__ldg(p.cu + m) <= t) a = m; else z = m - 1;
+      }
+      const int64_t pos = t - __ldg(p.cu + a) + (p.starts ? __ldg(p.starts + a) : 0);
+      src = -1;
+      if (pos >= 0 && pos < p.capacity) {
+        const int page = static_cast<int>(pos / p.block_size);
+        const int id = __ldg(p.block_table + static_cast<int64_t>(a) * p.bt_stride + page);
+        if (id >= 0 && id < p.num_blocks)
+          src = id * p.block_stride + (pos - static_cast<int64_t>(page) * p.block_size) * (R + 64);
+      }
+      err = src < 0;
+    }
+    src_of[threadIdx.x] = src;
+    const uint32_t bad = __ballot_sync(0xffffffffu, err != 0);
+    if (threadIdx.x == 0 && bad && p.err_count) atomicAdd(p.err_count, __popc(bad));
+  }
+  const float scale = FP8 ? __ldg(p.scale) : 1.f;
+  __syncthreads();
+  const uint8_t* cache = static_cast<const uint8_t*>(p.cache);
+#pragma unroll
+  for (int j0 = 0; j0 < PER; j0 += kBatch) {
+    uint4 x[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = threadIdx.x + (j0 + j) * kThreads;
+      x[j] = make_uint4(0, 0, 0, 0);
+      if (j0 + j < PER && i < TOTAL) {
+        const int64_t src = src_of[i / PIECES];
+        if (src >= 0)
+          x[j] = __ldg(reinterpret_cast<const uint4*>(cache + src * ELT) + i % PIECES);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = threadIdx.x + (j0 + j) * kThreads;
+      if (j0 + j >= PER || i >= TOTAL) continue;
+      const int r = i / PIECES, c = (i % PIECES) * (16 / ELT);  // first element of the piece
+      const int64_t src = src_of[r];
+      if (src == -2) continue;
+      const int64_t t = t0 + r;
+      uint16_t* dst = c < R ? p.kv_c + t * p.kv_c_stride + c : p.k_pe + t * p.k_pe_stride + (c - R);
+      if constexpr (FP8) {
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        if (src >= 0) {
+          lo = dequant8(x[j].x, x[j].y, p.e5m2, scale);
+          hi = dequant8(x[j].z, x[j].w, p.e5m2, scale);
+        }
+        reinterpret_cast<uint4*>(dst)[0] = lo;
+        reinterpret_cast<uint4*>(dst)[1] = hi;
+      } else {
+        *reinterpret_cast<uint4*>(dst) = x[j];
+      }
+    }
+  }
+}
+
+template <int R, bool FP8>
+cudaError_t launch(const GatherParams& p, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>((p.num_tokens + kRows - 1) / kRows);
+  return launch_overlapped(gather_cache_kernel<R, FP8>, dim3(grid), dim3(kThreads), 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_gather_cache(const GatherParams& p, int R, bool fp8, cudaStream_t stream) {
+  if (R == 512) return fp8 ? launch<512, true>(p, stream) : launch<512, false>(p, stream);
+  return fp8 ? launch<256, true>(p, stream) : launch<256, false>(p, stream);
+}
+
+}  // namespace mla

@@ -161,4 +161,58 @@ cudaError_t launch_lse_merge(const void* o_parts, int64_t o_part_stride, const f
                              int64_t lse_part_stride, int num_parts, int64_t records, int R,
                              void* o, float* lse, cudaStream_t stream);
 
+// ---------------------------------------------------------------- prompts
+// Largest number of requests mla_batch_build and mla_blocks_release take
+// (their prefix sums live in shared memory).
+constexpr int kMaxBatchReqs = 16384;
+
+// Arguments of the batch tables after host validation (device pointers).
+struct BatchParams {
+  const int32_t* req_ids;       // [num_reqs] or nullptr (request b: row b)
+  const int32_t* query_lens;    // [num_reqs]
+  const int32_t* context_lens;  // [num_reqs]
+  int num_reqs;
+  int32_t* req_table;           // [num_table_rows, >= max_blocks]
+  int64_t rt_stride;
+  int num_table_rows;
+  int capacity;                 // max_blocks * block_size, at most INT32_MAX
+  int block_size, num_blocks;
+  const int32_t* free_blocks;   // the stack of free pages
+  int32_t* free_out;            // the same, for the release
+  int free_capacity;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  bool defer_count;             // set by the launch
+  int num_tokens;
+  int32_t* block_table;
+  int64_t bt_stride;
+  int32_t *seq_lens, *cu_q, *cu_k;
+  int64_t *positions, *slot_mapping;
+  int* err_count;
+};
+cudaError_t launch_batch_build(const BatchParams& p, int sm_count, cudaStream_t stream);
+// context_lens: the tokens each request holds; query_lens nullptr.
+cudaError_t launch_blocks_release(const BatchParams& p, cudaStream_t stream);
+
+// Arguments of the gather of cached rows after host validation.
+struct GatherParams {
+  const void* cache;
+  int64_t block_stride;  // elements
+  int num_blocks, block_size;
+  int64_t capacity;      // max_blocks * block_size
+  const int32_t* block_table;
+  int64_t bt_stride;
+  const int32_t* cu;      // [num_seqs + 1]
+  const int32_t* starts;  // [num_seqs] or nullptr
+  int num_seqs, num_tokens;
+  const float* scale;
+  bool e5m2;
+  uint16_t* kv_c;
+  int64_t kv_c_stride;
+  uint16_t* k_pe;
+  int64_t k_pe_stride;
+  int* err_count;
+};
+cudaError_t launch_gather_cache(const GatherParams& p, int R, bool fp8, cudaStream_t stream);
+
 }  // namespace mla

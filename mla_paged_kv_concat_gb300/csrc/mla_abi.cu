@@ -12,11 +12,14 @@
 #include <new>
 
 #include "../../include/mla.h"
+#include "abi.cuh"
 #include "kernels.cuh"
 
 namespace {
-
 thread_local char g_last_cuda_error[256] = "";
+}  // namespace
+
+namespace mla {
 
 mla_status cuda_fail(cudaError_t e) {
   snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "%s: %s",
@@ -24,12 +27,9 @@ mla_status cuda_fail(cudaError_t e) {
   return MLA_ERR_CUDA;
 }
 
-bool valid_kv_dtype(mla_kv_dtype t) {
-  return t == MLA_KV_BF16 || t == MLA_KV_FP8_E4M3 || t == MLA_KV_FP8_E5M2;
-}
-
-bool aligned16(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+mla_status cuda_fail_text(const char* text) {
+  snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "%s", text);
+  return MLA_ERR_CUDA;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -44,6 +44,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
   });
   return fn;
+}
+
+}  // namespace mla
+
+namespace {
+
+using mla::aligned16;
+using mla::cuda_fail;
+using mla::encode_fn;
+
+bool valid_kv_dtype(mla_kv_dtype t) {
+  return t == MLA_KV_BF16 || t == MLA_KV_FP8_E4M3 || t == MLA_KV_FP8_E5M2;
 }
 
 // Tensor map over the cache viewed as {R+P (dims), block_size (rows),
