@@ -598,6 +598,53 @@ mla_status mla_gather_cache(const void* kv_cache, mla_kv_dtype kv_dtype, int num
                             int64_t kv_c_row_stride, void* k_pe, int64_t k_pe_row_stride,
                             int* err_count, void* stream);
 
+/*
+ * The products with the kv_b weight, which join the absorbed form (mla_decode
+ * over the latent cache) and the expanded form (mla_prefill over full keys
+ * and values) to the model's heads.  The pages' backend takes them as given
+ * ([diff] vllm/attention/backends/mla/utils.py, W_UQ_UK and W_UV_O); here
+ * they read the weight of the model's own kv_b projection in place:
+ *   w_kv_b   bf16 [num_heads * (nope_dim + v_dim)][kv_lora_rank], row stride
+ *            w_row_stride (at most 2^20): for head h the rows W_UK[h] (nope_dim of them),
+ *            then W_UV[h] (v_dim of them).
+ *
+ * mla_expand_kv   k_nope[t, h, p] = sum_r kv_c[t, r] W_UK[h][p, r],
+ *                 v[t, h, j]      = sum_r kv_c[t, r] W_UV[h][j, r]
+ *                 (kv_c: normalised latents, of new tokens or gathered).
+ * mla_absorb_q    ql_nope[t, h, r] = sum_p q_nope[t, h, p] W_UK[h][p, r]
+ *                 (then (ql_nope, q_pe) is mla_decode's query).
+ * mla_project_v   y[t, h, j] = sum_r o[t, h, r] W_UV[h][j, r]
+ *                 (o: mla_decode's output).
+ *
+ * bf16 tensors with unit last stride and the given row (token) and head
+ * strides; fp32 accumulation, one rounding to bf16.  Every pointer is 16-byte
+ * aligned, every stride a positive multiple of 8 (a head stride is not read
+ * when num_heads is 1).  Outputs [num_tokens][num_heads][columns]: the
+ * elements of one must not overlap each other or an input; k_nope and v may
+ * be column ranges of one buffer.
+ *   kv_lora_rank    512 or 256; nope_dim = v_dim = 128 (else
+ *                   MLA_ERR_UNSUPPORTED).  num_heads 1 .. 1024.
+ *   err_count       device int, may be NULL: +(1 << 20) if a pipeline wait
+ *                   timed out (the kernel then returns early).
+ * Run-to-run deterministic.  num_tokens == 0 is a no-op.
+ */
+mla_status mla_expand_kv(const void* kv_c, int64_t kv_c_row_stride, int num_tokens,
+                         const void* w_kv_b, int64_t w_row_stride, int num_heads,
+                         int kv_lora_rank, int nope_dim, int v_dim, void* k_nope,
+                         int64_t k_row_stride, int64_t k_head_stride, void* v,
+                         int64_t v_row_stride, int64_t v_head_stride, int* err_count,
+                         void* stream);
+mla_status mla_absorb_q(const void* q_nope, int64_t q_row_stride, int64_t q_head_stride,
+                        int num_tokens, const void* w_kv_b, int64_t w_row_stride,
+                        int num_heads, int kv_lora_rank, int nope_dim, int v_dim,
+                        void* ql_nope, int64_t ql_row_stride, int64_t ql_head_stride,
+                        int* err_count, void* stream);
+mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_stride,
+                         int num_tokens, const void* w_kv_b, int64_t w_row_stride,
+                         int num_heads, int kv_lora_rank, int nope_dim, int v_dim, void* y,
+                         int64_t y_row_stride, int64_t y_head_stride, int* err_count,
+                         void* stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* mla_status_string(mla_status status);
 

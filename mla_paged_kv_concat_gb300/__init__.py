@@ -15,6 +15,8 @@ Thin Python binding over the C ABI of ``libmla.so`` (``include/mla.h``):
   map, positions and cumulative lengths from its requests' lengths, pages
   taken off and put back onto a stack of free ones.
 * ``gather_cache(...)`` — cached rows of a ragged batch as contiguous bf16.
+* ``expand_kv(...)``, ``absorb_q(...)`` and ``project_v(...)`` — the products
+  with the kv_b weight of the expanded and the absorbed form.
 * ``cache_write(...)`` and ``decode(...)`` — torch-tensor conveniences that
   only marshal pointers, strides and the current CUDA stream; every step of
   the computation runs in the library's CUDA kernels.
@@ -34,6 +36,7 @@ __all__ = [
     "mla_decode_workspace_bytes", "mla_lse_merge", "mla_norm_rope_cache_write",
     "cache_write", "norm_rope_cache_write", "decode", "lse_merge", "DecodePlan",
     "mla_batch_build", "mla_blocks_release", "mla_gather_cache",
+    "mla_expand_kv", "mla_absorb_q", "mla_project_v", "expand_kv", "absorb_q", "project_v",
     "batch_build", "blocks_release", "gather_cache", "BatchTables",
     "MlaError", "load",
     "MLA_KV_BF16", "MLA_KV_FP8_E4M3", "MLA_KV_FP8_E5M2", "MLA_PATH_AUTO", "MLA_PATH_MMA_SYNC",
@@ -72,6 +75,18 @@ def mla_blocks_release(*args) -> int:
 
 def mla_gather_cache(*args) -> int:
     return load().mla_gather_cache(*args)
+
+
+def mla_expand_kv(*args) -> int:
+    return load().mla_expand_kv(*args)
+
+
+def mla_absorb_q(*args) -> int:
+    return load().mla_absorb_q(*args)
+
+
+def mla_project_v(*args) -> int:
+    return load().mla_project_v(*args)
 
 
 def mla_num_kv_splits(max_seq_len: int, sm_count: int) -> int:
@@ -538,3 +553,83 @@ def gather_cache(kv_cache, block_table, cu_seqlens, num_tokens: int | None = Non
         k_pe.stride(0), _ptr(err_count), _stream_ptr(stream))
     _lib.check(st, "mla_gather_cache")
     return kv_c, k_pe
+
+
+NOPE_DIM = 128  # head dims of the expanded form: keys without the rope part
+V_DIM = 128     # and values
+
+
+def _strides(t):
+    """(row, head) strides of a [T, H, D] tensor; those of dimensions of size
+    1, which torch leaves arbitrary, as in a dense tensor."""
+    T, H, D = t.shape
+    hs = t.stride(1) if H > 1 else D
+    rs = t.stride(0) if T > 1 else (H * hs if H > 1 else D)
+    return rs, hs
+
+
+def _kv_b(w_kv_b, num_heads: int):
+    """Checks the kv_b weight [H * 256, R]; returns R."""
+    torch = _torch()
+    _typed(w_kv_b, torch.bfloat16, (num_heads * (NOPE_DIM + V_DIM), None), "w_kv_b")
+    return w_kv_b.shape[1]
+
+
+def expand_kv(kv_c, w_kv_b, num_heads: int, *, k_nope=None, v=None, err_count=None,
+              stream=None):
+    """Keys and values of latents ``kv_c`` [T, R]: (k_nope, v), bf16
+    [T, H, 128] each; ``w_kv_b`` [H * 256, R] is the kv_b projection's weight
+    (per head 128 rows of W_UK, then 128 of W_UV).  Allocated as the two
+    halves of one [T, H, 256] buffer unless both are given."""
+    torch = _torch()
+    bf = torch.bfloat16
+    dev = _cuda(stream, kv_c=kv_c, w_kv_b=w_kv_b, k_nope=k_nope, v=v, err_count=err_count)
+    R = _kv_b(w_kv_b, num_heads)
+    _typed(kv_c, bf, (None, R), "kv_c")
+    T = kv_c.shape[0]
+    _check((k_nope is None) == (v is None), "give both k_nope and v, or neither")
+    if k_nope is None:
+        kv = _empty(stream, T, num_heads, NOPE_DIM + V_DIM, dtype=bf, device=dev)
+        k_nope, v = kv[..., :NOPE_DIM], kv[..., NOPE_DIM:]
+    _typed(k_nope, bf, (T, num_heads, NOPE_DIM), "k_nope")
+    _typed(v, bf, (T, num_heads, V_DIM), "v")
+    _typed(err_count, torch.int32, (1,), "err_count")
+    st = load().mla_expand_kv(
+        kv_c.data_ptr(), kv_c.stride(0) if T > 1 else R, T, w_kv_b.data_ptr(), w_kv_b.stride(0),
+        num_heads, R, NOPE_DIM, V_DIM, k_nope.data_ptr(), *_strides(k_nope), v.data_ptr(),
+        *_strides(v), _ptr(err_count), _stream_ptr(stream))
+    _lib.check(st, "mla_expand_kv")
+    return k_nope, v
+
+
+def _head_product(fn, x, w_kv_b, n_in, n_out, out, err_count, stream):
+    torch = _torch()
+    bf = torch.bfloat16
+    dev = _cuda(stream, x=x, w_kv_b=w_kv_b, out=out, err_count=err_count)
+    _check(x.dim() == 3, "the input must be [tokens, heads, dims]")
+    T, H, _ = x.shape
+    R = _kv_b(w_kv_b, H)
+    n_in, n_out = n_in or R, n_out or R
+    _typed(x, bf, (T, H, n_in), "the input")
+    if out is None:
+        out = _empty(stream, T, H, n_out, dtype=bf, device=dev)
+    _typed(out, bf, (T, H, n_out), "out")
+    _typed(err_count, torch.int32, (1,), "err_count")
+    st = getattr(load(), fn)(
+        x.data_ptr(), *_strides(x), T, w_kv_b.data_ptr(), w_kv_b.stride(0), H, R, NOPE_DIM,
+        V_DIM, out.data_ptr(), *_strides(out), _ptr(err_count), _stream_ptr(stream))
+    _lib.check(st, fn)
+    return out
+
+
+def absorb_q(q_nope, w_kv_b, *, out=None, err_count=None, stream=None):
+    """The latent query ql_nope [T, H, R] of ``q_nope`` [T, H, 128] (any row
+    and head strides: a column slice of q will do): ``decode``'s query is then
+    the pair (ql_nope, q_pe).  ``w_kv_b`` as in :func:`expand_kv`."""
+    return _head_product("mla_absorb_q", q_nope, w_kv_b, NOPE_DIM, None, out, err_count, stream)
+
+
+def project_v(o, w_kv_b, *, out=None, err_count=None, stream=None):
+    """Values [T, H, 128] of ``decode``'s latent output ``o`` [T, H, R];
+    ``w_kv_b`` as in :func:`expand_kv`."""
+    return _head_product("mla_project_v", o, w_kv_b, None, V_DIM, out, err_count, stream)

@@ -95,6 +95,12 @@ SIGNATURES = {
                                   _P, _P, _P, _P]),
     "mla_gather_cache": (_I32, [_P, _I32, _I32, _I32, _I64, _I32, _I32, _P, _I64, _I32, _P,
                                 _P, _I32, _I32, _P, _P, _I64, _P, _I64, _P, _P]),
+    "mla_expand_kv": (_I32, [_P, _I64, _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _I64, _I64,
+                             _P, _I64, _I64, _P, _P]),
+    "mla_absorb_q": (_I32, [_P, _I64, _I64, _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _I64,
+                            _I64, _P, _P]),
+    "mla_project_v": (_I32, [_P, _I64, _I64, _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _I64,
+                             _I64, _P, _P]),
     "mla_status_string": (ctypes.c_char_p, [_I32]),
     "mla_last_cuda_error": (ctypes.c_char_p, []),
 }

@@ -215,4 +215,25 @@ struct GatherParams {
 };
 cudaError_t launch_gather_cache(const GatherParams& p, int R, bool fp8, cudaStream_t stream);
 
+// The products with the kv_b weight (latent_proj.cu).
+enum { kProjExpand = 0, kProjAbsorb = 1, kProjProject = 2 };
+struct ProjParams {
+  int tokens, heads;
+  int k;       // length of the sum: R (expand, project) or 128 (absorb)
+  int cols;    // output columns of a head: 256, R or 128
+  int bn;      // columns of a tile, from proj_tile_cols
+  int w_row0;  // first of the head's 256 weight rows that the product reads
+  int* err_count;
+};
+// a: {K, heads or 1, tokens}, box {64, 1, 128}.  b: the weight as
+// {R, 256, heads}, box {64, bn, 1}, or {64, 64, 1} for absorb.  c0, c1:
+// {cols, heads, tokens}, box {64, 1, 32}; c1 is expand's v.  All 128-byte
+// swizzled bf16.
+struct ProjMaps {
+  CUtensorMap a, b, c0, c1;
+};
+int proj_tile_cols(int tokens, int heads, int cols, int sm_count);
+cudaError_t launch_latent_proj(const ProjParams& p, const ProjMaps& m, int mode, int sm_count,
+                               cudaStream_t stream);
+
 }  // namespace mla

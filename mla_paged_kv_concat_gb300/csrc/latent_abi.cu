@@ -64,6 +64,107 @@ mla_status fill_batch(const int32_t* req_ids, const int32_t* context_lens, int n
   return MLA_OK;
 }
 
+constexpr int kNopeDim = 128, kVDim = 128;
+
+// Tensor map over bf16 [d2][d1][d0] at element strides s1, s2, 128-byte
+// swizzled, box {64, b1, b2}.
+mla_status make_map(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2,
+                    int64_t s1, int64_t s2, int b1, int b2) {
+  auto fn = mla::encode_fn();
+  if (!fn) return mla::cuda_fail_text("cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1),
+                              static_cast<cuuint64_t>(d2)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return mla::cuda_fail_text("cuTensorMapEncodeTiled failed");
+  return MLA_OK;
+}
+
+// A tensor [tokens][heads][cols] of bf16 that a tensor map can describe.
+struct Heads {
+  const void* p;
+  int64_t rs, hs;
+  int cols;
+};
+
+bool stride_ok(int64_t s) { return s > 0 && s % 8 == 0 && s < (int64_t{1} << 38); }
+
+bool heads_ok(const Heads& t, int tokens, int heads) {
+  return t.p && aligned16(t.p) && stride_ok(t.rs) && (heads == 1 || stride_ok(t.hs)) &&
+         (heads == 1 || t.hs >= t.cols) && t.rs >= t.cols &&
+         // no buffer is that long, and the products below stay in 64 bits
+         t.rs <= (int64_t{1} << 40) / tokens && (heads == 1 || t.hs <= (int64_t{1} << 40) / heads);
+}
+
+// Whether no two elements of an output share an address: one of the two
+// outer dimensions steps over the whole of the other.
+bool heads_disjoint(const Heads& t, int tokens, int heads) {
+  return heads == 1 || tokens == 1 || t.rs >= (heads - 1) * t.hs + t.cols ||
+         t.hs >= (tokens - 1) * t.rs + t.cols;
+}
+
+// Bytes from the first to the last element.
+int64_t heads_bytes(const Heads& t, int tokens, int heads) {
+  return 2 * ((tokens - 1) * t.rs + (heads > 1 ? (heads - 1) * t.hs : 0) + t.cols);
+}
+
+mla_status heads_map(CUtensorMap* m, const Heads& t, int tokens, int heads, int box_rows) {
+  // the stride of a dimension of size 1 is never used but has to be valid
+  return make_map(m, t.p, t.cols, heads, tokens, heads == 1 ? t.cols : t.hs, t.rs, 1, box_rows);
+}
+
+mla_status latent_proj(int mode, Heads in, int in_heads, int tokens, const void* w,
+                       int64_t w_stride, int heads, int R, int nope, int vdim, Heads out0,
+                       Heads out1, int* err_count, void* stream) {
+  if (tokens < 0 || heads < 1 || heads > 1024 || nope < 1 || vdim < 1) return MLA_ERR_INVALID_ARG;
+  if ((R != 512 && R != 256) || nope != kNopeDim || vdim != kVDim) return MLA_ERR_UNSUPPORTED;
+  if (tokens == 0) return MLA_OK;
+  const bool two = mode == mla::kProjExpand;
+  if (!heads_ok(in, tokens, in_heads) || !heads_ok(out0, tokens, heads) ||
+      (two && !heads_ok(out1, tokens, heads)) || !w || !aligned16(w) || w_stride % 8 != 0 ||
+      w_stride < R || w_stride > (int64_t{1} << 20) || !aligned4(err_count))
+    return MLA_ERR_INVALID_ARG;
+  if (!heads_disjoint(out0, tokens, heads) || (two && !heads_disjoint(out1, tokens, heads)))
+    return MLA_ERR_INVALID_ARG;
+  const int64_t wb = 2 * ((static_cast<int64_t>(heads) * (nope + vdim) - 1) * w_stride + R);
+  const int64_t ib = heads_bytes(in, tokens, in_heads);
+  for (int i = 0; i < (two ? 2 : 1); ++i) {
+    const Heads& o = i ? out1 : out0;
+    const int64_t ob = heads_bytes(o, tokens, heads);
+    if (overlap(o.p, ob, w, wb)) return MLA_ERR_INVALID_ARG;
+    // an output between an input's rows (columns of one buffer) is fine;
+    // only a dense overlap is refused
+    if (o.p == in.p || (ib == 2 * static_cast<int64_t>(tokens) * in_heads * in.cols &&
+                        overlap(o.p, ob, in.p, ib)))
+      return MLA_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  cudaError_t e = mla::device_sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  mla::ProjParams p = {};
+  p.tokens = tokens;
+  p.heads = heads;
+  p.k = in.cols;
+  p.cols = two ? nope + vdim : out0.cols;
+  p.w_row0 = mode == mla::kProjProject ? nope : 0;
+  p.bn = mla::proj_tile_cols(tokens, heads, p.cols, sms);
+  p.err_count = err_count;
+  mla::ProjMaps m;
+  mla_status st = heads_map(&m.a, in, tokens, in_heads, 128);
+  if (st == MLA_OK)
+    st = make_map(&m.b, w, R, nope + vdim, heads, w_stride, w_stride * (nope + vdim),
+                  mode == mla::kProjAbsorb ? 64 : p.bn, 1);
+  if (st == MLA_OK) st = heads_map(&m.c0, out0, tokens, heads, 32);
+  if (st == MLA_OK) st = heads_map(&m.c1, two ? out1 : out0, tokens, heads, 32);
+  if (st != MLA_OK) return st;
+  e = mla::launch_latent_proj(p, m, mode, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -214,6 +315,39 @@ mla_status mla_gather_cache(const void* kv_cache, mla_kv_dtype kv_dtype, int num
   p.err_count = err_count;
   cudaError_t e = mla::launch_gather_cache(p, kv_lora_rank, fp8, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+mla_status mla_expand_kv(const void* kv_c, int64_t kv_c_row_stride, int num_tokens,
+                         const void* w_kv_b, int64_t w_row_stride, int num_heads,
+                         int kv_lora_rank, int nope_dim, int v_dim, void* k_nope,
+                         int64_t k_row_stride, int64_t k_head_stride, void* v,
+                         int64_t v_row_stride, int64_t v_head_stride, int* err_count,
+                         void* stream) {
+  return latent_proj(mla::kProjExpand, {kv_c, kv_c_row_stride, 0, kv_lora_rank}, 1, num_tokens,
+                     w_kv_b, w_row_stride, num_heads, kv_lora_rank, nope_dim, v_dim,
+                     {k_nope, k_row_stride, k_head_stride, nope_dim},
+                     {v, v_row_stride, v_head_stride, v_dim}, err_count, stream);
+}
+
+mla_status mla_absorb_q(const void* q_nope, int64_t q_row_stride, int64_t q_head_stride,
+                        int num_tokens, const void* w_kv_b, int64_t w_row_stride,
+                        int num_heads, int kv_lora_rank, int nope_dim, int v_dim,
+                        void* ql_nope, int64_t ql_row_stride, int64_t ql_head_stride,
+                        int* err_count, void* stream) {
+  return latent_proj(mla::kProjAbsorb, {q_nope, q_row_stride, q_head_stride, nope_dim}, num_heads,
+                     num_tokens, w_kv_b, w_row_stride, num_heads, kv_lora_rank, nope_dim, v_dim,
+                     {ql_nope, ql_row_stride, ql_head_stride, kv_lora_rank}, {}, err_count,
+                     stream);
+}
+
+mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_stride,
+                         int num_tokens, const void* w_kv_b, int64_t w_row_stride,
+                         int num_heads, int kv_lora_rank, int nope_dim, int v_dim, void* y,
+                         int64_t y_row_stride, int64_t y_head_stride, int* err_count,
+                         void* stream) {
+  return latent_proj(mla::kProjProject, {o, o_row_stride, o_head_stride, kv_lora_rank}, num_heads,
+                     num_tokens, w_kv_b, w_row_stride, num_heads, kv_lora_rank, nope_dim, v_dim,
+                     {y, y_row_stride, y_head_stride, v_dim}, {}, err_count, stream);
 }
 
 }  // extern "C"

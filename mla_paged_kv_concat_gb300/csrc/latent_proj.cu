@@ -1,0 +1,298 @@
+// The products with the kv_b weight W [H * 256][R] (per head h the rows
+// [h*256, h*256+128) are W_UK[h], the next 128 are W_UV[h]):
+//
+//   expand   k_nope[t, h, p] = sum_r c[t, r] W_UK[h][p, r]
+//            v[t, h, j]      = sum_r c[t, r] W_UV[h][j, r]
+//   absorb   ql[t, h, r]     = sum_p q_nope[t, h, p] W_UK[h][p, r]
+//   project  y[t, h, j]      = sum_r o[t, h, r] W_UV[h][j, r]
+//
+// bf16 in and out, fp32 accumulation in TMEM, one rounding.  All three read
+// the weight where the model keeps it: expand and project with r contiguous
+// (a K-major B operand), absorb with the output dim contiguous (MN-major).
+//
+// One kernel: 128 tokens x BN columns of one head per tile, K in chunks of
+// 64 through a TMA ring (128-byte swizzle), tcgen05 M=128 N=BN K=16, two
+// accumulators in TMEM so that one tile's epilogue runs under the next one's
+// products, one persistent CTA per SM.  Epilogue warps own 32 rows each:
+// TMEM -> registers -> bf16 in a swizzled 4 KiB staging box -> TMA store,
+// which also clips the rows past the last token.  Roles: warps 0-3 epilogue,
+// warp 4 TMA producer, warp 5 MMA issuer and TMEM owner.
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace mla {
+
+namespace {
+
+constexpr int TM = 128;   // tokens per tile
+constexpr int KC = 64;    // K per ring stage
+constexpr int A_BYTES = TM * KC * 2;
+constexpr int STORE_ROWS = 32;
+constexpr int STORE_BYTES = STORE_ROWS * 128;
+
+template <int BN>
+struct ProjCfg {
+  static constexpr int B_BYTES = BN * KC * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  static constexpr int OFF_STORE = STAGES * STAGE;  // two boxes per epilogue warp
+  static constexpr int OFF_BAR = OFF_STORE + 4 * 2 * STORE_BYTES;
+  static constexpr int NBARS = 2 * STAGES + 4;
+  static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
+  static constexpr int SMEM = OFF_TMEM + 16 + 1024;
+  static constexpr uint32_t COLS = 2 * BN;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  const bool ok = mbar_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0,
+                                             int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+      "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+template <int MODE, int BN>
+__global__ void __launch_bounds__(192, 1)
+    latent_proj_kernel(const ProjParams p, const __grid_constant__ CUtensorMap ma,
+                       const __grid_constant__ CUtensorMap mb,
+                       const __grid_constant__ CUtensorMap mc0,
+                       const __grid_constant__ CUtensorMap mc1) {
+  using C = ProjCfg<BN>;
+  constexpr bool kBMn = MODE == kProjAbsorb;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [STAGES]
+  uint64_t* empty = full + C::STAGES;                               // [STAGES]
+  uint64_t* acc_full = empty + C::STAGES;                           // [2]
+  uint64_t* acc_empty = acc_full + 2;                               // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 128) {
+    tma_prefetch_desc(&ma);
+    tma_prefetch_desc(&mb);
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tc::tmem_alloc(tmem_slot, C::COLS);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int nk = p.k / KC;
+  const int ntiles_n = p.cols / BN;
+  // columns of a head fastest, then heads, then token blocks: the tiles of a
+  // wave write neighbouring columns of the same rows
+  auto tile_at = [&](int64_t t, int& m, int& h, int& n) {
+    n = static_cast<int>(t % ntiles_n);
+    const int64_t u = t / ntiles_n;
+    h = static_cast<int>(u % p.heads);
+    m = static_cast<int>(u / p.heads);
+  };
+  const int64_t total =
+      static_cast<int64_t>((p.tokens + TM - 1) / TM) * p.heads * ntiles_n;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        int m, h, n;
+        tile_at(t, m, h, n);
+        for (int kc = 0; kc < nk; ++kc, ++it) {
+          const int st = it % C::STAGES;
+          if (!mbar_wait(&empty[st], ((it / C::STAGES) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + st * C::STAGE;
+          mbar_arrive_expect_tx(&full[st], C::STAGE);
+          tma_load_3d(dst, &ma, &full[st], kc * KC, MODE == kProjExpand ? 0 : h, m * TM);
+          if (kBMn) {
+#pragma unroll
+            for (int j = 0; j < BN / 64; ++j)
+              tma_load_3d(dst + A_BYTES + j * (KC * 128), &mb, &full[st], n * BN + j * 64,
+                          p.w_row0 + kc * KC, h);
+          } else {
+            tma_load_3d(dst + A_BYTES, &mb, &full[st], kc * KC, p.w_row0 + n * BN, h);
+          }
+        }
+      }
+      if (!ok && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+    }
+  } else if (warp == 5) {
+    constexpr uint32_t idesc = tc::idesc_bf16(TM, BN, 0, kBMn ? 1 : 0);
+    int it = 0, ta = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x, ++ta) {
+      const int a = ta & 1;
+      if (!warp_wait(&acc_empty[a], ((ta >> 1) & 1) ^ 1)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      for (int kc = 0; kc < nk; ++kc, ++it) {
+        const int st = it % C::STAGES;
+        if (!warp_wait(&full[st], (it / C::STAGES) & 1)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+          const uint32_t base = smem_u32(smem + st * C::STAGE);
+          const uint64_t da = tc::smem_desc(base, 16, 1024, tc::kLayoutSw128);
+          // MN-major: the next 64 columns are one box on, 16 rows of K 2 KiB
+          const uint64_t db =
+              tc::smem_desc(base + A_BYTES, kBMn ? KC * 128 : 16, 1024, tc::kLayoutSw128);
+#pragma unroll
+          for (int k = 0; k < KC / 16; ++k)
+            tc::mma_ss(tmem + a * BN, da + static_cast<uint64_t>(k * 2),
+                       db + static_cast<uint64_t>(kBMn ? k * 128 : k * 2), idesc,
+                       (kc > 0 || k > 0) ? 1u : 0u);
+          tc::commit(&empty[st]);
+          if (kc == nk - 1) tc::commit(&acc_full[a]);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0 && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+    // nothing of this CTA's still runs on the tensor core when TMEM is freed
+    for (int j = 0; ok && j < 2 && j < ta; ++j) {
+      const int u = ta - 1 - j;
+      warp_wait(&acc_full[u & 1], (u >> 1) & 1);
+    }
+  } else {
+    uint8_t* box = smem + C::OFF_STORE + warp * 2 * STORE_BYTES;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    int ta = 0, nb = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < total; t += gridDim.x, ++ta) {
+      int m, h, n;
+      tile_at(t, m, h, n);
+      const int a = ta & 1;
+      if (!warp_wait(&acc_full[a], (ta >> 1) & 1)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      const int row0 = m * TM + warp * STORE_ROWS;
+#pragma unroll
+      for (int j = 0; j < BN / 64; ++j, ++nb) {
+        uint32_t r[64];
+        tc::ld_32x32b_x32(tmem + lanes + a * BN + j * 64,
+                          *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+        tc::ld_32x32b_x32(tmem + lanes + a * BN + j * 64 + 32,
+                          *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+        tc::wait_ld();
+        tc::reg_fence(r);
+        if (j == BN / 64 - 1) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[a]);
+        }
+        uint8_t* dst = box + (nb & 1) * STORE_BYTES;
+        // the store that last used this box has read it
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(r[q * 8 + 2 * e]),
+                               __uint_as_float(r[q * 8 + 2 * e + 1]));
+          *reinterpret_cast<uint4*>(dst + sw128(lane, q)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (row0 < p.tokens) {
+            const int c = n * BN + j * 64;
+            if (MODE == kProjExpand && c >= 128)
+              tma_store_3d(&mc1, dst, c - 128, h, row0);
+            else
+              tma_store_3d(&mc0, dst, c, h, row0);
+          }
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (!ok && lane == 0 && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 5) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, C::COLS);
+  }
+}
+
+template <int MODE, int BN>
+cudaError_t launch(const ProjParams& p, const ProjMaps& m, int sm_count, cudaStream_t stream) {
+  using C = ProjCfg<BN>;
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = set_smem_attr_once(latent_proj_kernel<MODE, BN>, C::SMEM, attr_done);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((p.tokens + TM - 1) / TM) * p.heads * (p.cols / BN);
+  const int grid = tiles < sm_count ? static_cast<int>(tiles) : sm_count;
+  return launch_overlapped(latent_proj_kernel<MODE, BN>, dim3(grid), dim3(192), C::SMEM, stream, p,
+                           m.a, m.b, m.c0, m.c1);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const ProjParams& p, const ProjMaps& m, int sm_count, cudaStream_t s) {
+  switch (p.bn) {
+    case 256: return launch<MODE, 256>(p, m, sm_count, s);
+    case 128: return launch<MODE, 128>(p, m, sm_count, s);
+    default: return launch<MODE, 64>(p, m, sm_count, s);
+  }
+}
+
+}  // namespace
+
+int proj_tile_cols(int tokens, int heads, int cols, int sm_count) {
+  const int64_t units = static_cast<int64_t>((tokens + TM - 1) / TM) * heads;
+  int bn = cols < 256 ? cols : 256;
+  while (bn > 64 && units * (cols / bn) < sm_count) bn /= 2;
+  return bn;
+}
+
+cudaError_t launch_latent_proj(const ProjParams& p, const ProjMaps& m, int mode, int sm_count,
+                               cudaStream_t stream) {
+  switch (mode) {
+    case kProjExpand: return launch_mode<kProjExpand>(p, m, sm_count, stream);
+    case kProjAbsorb: return launch_mode<kProjAbsorb>(p, m, sm_count, stream);
+    default: return p.bn == 128 ? launch<kProjProject, 128>(p, m, sm_count, stream)
+                                : launch<kProjProject, 64>(p, m, sm_count, stream);
+  }
+}
+
+}  // namespace mla
