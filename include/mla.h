@@ -645,6 +645,78 @@ mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_str
                          int64_t y_row_stride, int64_t y_head_stride, int* err_count,
                          void* stream);
 
+/*
+ * mla_prefill_num_kv_splits - how many parts mla_prefill should cut the key
+ * axis into: 1 when the 256-row query blocks of all heads fill the SMs, else
+ * enough parts to fill them, none shorter than 512 keys of the longest
+ * sequence; at most 64.  max_kv_len: longest sequence's keys (an upper bound
+ * will do).
+ */
+int mla_prefill_num_kv_splits(int num_tokens, int num_seqs, int num_heads, int64_t max_kv_len,
+                              int sm_count);
+
+/*
+ * mla_prefill_workspace_bytes - bytes of fp32 partials mla_prefill needs:
+ * num_tokens * num_heads * num_kv_splits * (v_dim + 1) * 4, or 0 when
+ * num_kv_splits == 1; SIZE_MAX when that does not fit a size_t.
+ */
+size_t mla_prefill_workspace_bytes(int num_tokens, int num_heads, int num_kv_splits,
+                                   int v_dim);
+
+/*
+ * mla_prefill - attention of the expanded form: several query rows per
+ * sequence (prompts, chunks of prompts behind a cached prefix), every head
+ * with its own keys and values, the rope part of the keys shared by all.
+ *
+ * The pages run this beside the decode (MLA common forward: k and v from the
+ * kv_b projection, an attention over ragged sequences with lse, merged with
+ * the cached context's); here one call covers prefix and new tokens.
+ * For sequence b with query rows [cu_seqlens_q[b], cu_seqlens_q[b + 1]) (Lq
+ * of them) and keys [cu_seqlens_k[b], cu_seqlens_k[b + 1]) (Lk), row i, head h:
+ *   s_j = sm_scale * (q[i, h, 0:nope] . k_nope[j, h] + q[i, h, nope:] . k_pe[j])
+ *         over j <= i + Lk - Lq (causal: the queries are the sequence's last
+ *         tokens) or over all j;
+ *   o[i, h] = sum_j softmax(s)_j v[j, h];   lse[i, h] = ln sum_j exp(s_j).
+ * A row that attends to no key (Lk = 0, or Lk < Lq and causal) gets o = 0,
+ * lse = -inf.  Keys and values that a row does not attend to do not
+ * influence it, whatever they hold (NaN included).
+ *
+ *   q               bf16 [num_tokens][num_heads][nope + rope], or
+ *                   [..][nope] with q_pe [..][rope] given apart.
+ *   k_nope, v       bf16 [num_kv_tokens][num_heads][nope_dim / v_dim] (as
+ *                   mla_expand_kv writes them); k_pe bf16 [num_kv_tokens]
+ *                   [rope_dim].
+ *   strides         of rows (tokens) and heads, elements, multiples of 8 (a
+ *                   head stride is not read when num_heads is 1); unit last
+ *                   stride; every tensor 16-byte aligned.
+ *   num_heads       1 .. 1024; nope_dim = v_dim = 128, rope_dim = 64 (else
+ *                   MLA_ERR_UNSUPPORTED).
+ *   cu_seqlens_*    device int32 [num_seqs + 1], non-decreasing; values are
+ *                   clamped to [0, num_tokens] / [0, num_kv_tokens] (counted).
+ *                   num_seqs 0 .. 65535.
+ *   sm_scale        1e-30 .. 1e30.
+ *   num_kv_splits   1 .. 64 parts of the key axis, joined by a second kernel
+ *                   (see mla_prefill_num_kv_splits); 1 needs no workspace.
+ *   workspace       >= mla_prefill_workspace_bytes(...), 16-byte aligned.
+ *   o               bf16 [num_tokens][num_heads][v_dim] at its strides; must
+ *                   not overlap an input.  lse fp32 [num_tokens][num_heads],
+ *                   contiguous.  Rows of no sequence are left as they were.
+ *   err_count       device int, may be NULL: clamped cu_seqlens; +(1 << 20)
+ *                   if a pipeline wait timed out.
+ * Run-to-run deterministic; a row's result depends on num_kv_splits but not on
+ * the other sequences of the batch.
+ */
+mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                       const void* q_pe, int64_t q_pe_row_stride, int64_t q_pe_head_stride,
+                       int num_tokens, int num_heads, const void* k_nope, int64_t k_row_stride,
+                       int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                       int64_t v_head_stride, const void* k_pe, int64_t k_pe_row_stride,
+                       int num_kv_tokens, int nope_dim, int rope_dim, int v_dim,
+                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int num_seqs,
+                       int causal, float sm_scale, int num_kv_splits, void* workspace,
+                       size_t workspace_bytes, void* o, int64_t o_row_stride,
+                       int64_t o_head_stride, float* lse, int* err_count, void* stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* mla_status_string(mla_status status);
 

@@ -17,6 +17,7 @@ Thin Python binding over the C ABI of ``libmla.so`` (``include/mla.h``):
 * ``gather_cache(...)`` — cached rows of a ragged batch as contiguous bf16.
 * ``expand_kv(...)``, ``absorb_q(...)`` and ``project_v(...)`` — the products
   with the kv_b weight of the expanded and the absorbed form.
+* ``prefill(...)`` — attention of the expanded form over ragged prompts.
 * ``cache_write(...)`` and ``decode(...)`` — torch-tensor conveniences that
   only marshal pointers, strides and the current CUDA stream; every step of
   the computation runs in the library's CUDA kernels.
@@ -37,6 +38,7 @@ __all__ = [
     "cache_write", "norm_rope_cache_write", "decode", "lse_merge", "DecodePlan",
     "mla_batch_build", "mla_blocks_release", "mla_gather_cache",
     "mla_expand_kv", "mla_absorb_q", "mla_project_v", "expand_kv", "absorb_q", "project_v",
+    "mla_prefill", "mla_prefill_num_kv_splits", "mla_prefill_workspace_bytes", "prefill",
     "batch_build", "blocks_release", "gather_cache", "BatchTables",
     "MlaError", "load",
     "MLA_KV_BF16", "MLA_KV_FP8_E4M3", "MLA_KV_FP8_E5M2", "MLA_PATH_AUTO", "MLA_PATH_MMA_SYNC",
@@ -87,6 +89,20 @@ def mla_absorb_q(*args) -> int:
 
 def mla_project_v(*args) -> int:
     return load().mla_project_v(*args)
+
+
+def mla_prefill(*args) -> int:
+    return load().mla_prefill(*args)
+
+
+def mla_prefill_num_kv_splits(num_tokens: int, num_seqs: int, num_heads: int, max_kv_len: int,
+                              sm_count: int) -> int:
+    return load().mla_prefill_num_kv_splits(num_tokens, num_seqs, num_heads, max_kv_len, sm_count)
+
+
+def mla_prefill_workspace_bytes(num_tokens: int, num_heads: int, num_kv_splits: int,
+                                v_dim: int) -> int:
+    return load().mla_prefill_workspace_bytes(num_tokens, num_heads, num_kv_splits, v_dim)
 
 
 def mla_num_kv_splits(max_seq_len: int, sm_count: int) -> int:
@@ -633,3 +649,57 @@ def project_v(o, w_kv_b, *, out=None, err_count=None, stream=None):
     """Values [T, H, 128] of ``decode``'s latent output ``o`` [T, H, R];
     ``w_kv_b`` as in :func:`expand_kv`."""
     return _head_product("mla_project_v", o, w_kv_b, None, V_DIM, out, err_count, stream)
+
+
+def prefill(q, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, sm_scale: float, *,
+            causal: bool = True, num_kv_splits: int = 1, workspace=None, out=None, lse=None,
+            err_count=None, stream=None):
+    """Attention of the expanded form; returns (o [T, H, 128] bf16, lse [T, H]
+    fp32).
+
+    ``q`` [T, H, 192] bf16 (128 dims, then 64 rope dims), or the pair (q_nope
+    [T, H, 128], q_pe [T, H, 64]); ``k_nope`` and ``v`` [Tk, H, 128] as
+    :func:`expand_kv` gives them, ``k_pe`` [Tk, 64]; ``cu_seqlens_q`` and
+    ``cu_seqlens_k`` int32 [seqs + 1].  Causal rows are the last tokens of
+    their sequence's keys.  ``num_kv_splits``: parts of the key axis, from
+    ``mla_prefill_num_kv_splits``; the workspace they need is allocated here
+    when not given.
+    """
+    torch = _torch()
+    bf, i32 = torch.bfloat16, torch.int32
+    q, q_pe = q if isinstance(q, (tuple, list)) else (q, None)
+    dev = _cuda(stream, q=q, q_pe=q_pe, k_nope=k_nope, v=v, k_pe=k_pe, cu_seqlens_q=cu_seqlens_q,
+                cu_seqlens_k=cu_seqlens_k, workspace=workspace, out=out, lse=lse,
+                err_count=err_count)
+    _check(q.dim() == 3 and k_pe.dim() == 2, "q must be [tokens, heads, dims], k_pe [keys, 64]")
+    T, H, _ = q.shape
+    Tk, P = k_pe.shape
+    B = cu_seqlens_q.shape[0] - 1
+    if out is None:
+        out = _empty(stream, T, H, V_DIM, dtype=bf, device=dev)
+    if lse is None:
+        lse = _empty(stream, T, H, dtype=torch.float32, device=dev)
+    for t, d, shape, name in ((q, bf, (T, H, NOPE_DIM + (P if q_pe is None else 0)), "q"),
+                              (q_pe, bf, (T, H, P), "q_pe"),
+                              (k_nope, bf, (Tk, H, NOPE_DIM), "k_nope"),
+                              (v, bf, (Tk, H, V_DIM), "v"), (k_pe, bf, (Tk, P), "k_pe"),
+                              (cu_seqlens_q, i32, (B + 1,), "cu_seqlens_q"),
+                              (cu_seqlens_k, i32, (B + 1,), "cu_seqlens_k"),
+                              (out, bf, (T, H, V_DIM), "out"),
+                              (lse, torch.float32, (T, H), "lse"),
+                              (err_count, i32, (1,), "err_count")):
+        _typed(t, d, shape, name)
+    _check(B >= 0 and lse.is_contiguous(), "lse must be contiguous, cu_seqlens_q not empty")
+    need = mla_prefill_workspace_bytes(T, H, num_kv_splits, V_DIM)
+    if need and workspace is None:
+        workspace = _empty(stream, need, dtype=torch.uint8, device=dev)
+    _check(workspace is None or workspace.is_contiguous(), "workspace must be contiguous")
+    st = load().mla_prefill(
+        q.data_ptr(), *_strides(q), _ptr(q_pe), *(_strides(q_pe) if q_pe is not None else (0, 0)),
+        T, H, k_nope.data_ptr(), *_strides(k_nope), v.data_ptr(), *_strides(v), k_pe.data_ptr(),
+        k_pe.stride(0) if Tk > 1 else P, Tk, NOPE_DIM, P, V_DIM, cu_seqlens_q.data_ptr(),
+        cu_seqlens_k.data_ptr(), B, int(bool(causal)), float(sm_scale), int(num_kv_splits),
+        _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0,
+        out.data_ptr(), *_strides(out), lse.data_ptr(), _ptr(err_count), _stream_ptr(stream))
+    _lib.check(st, "mla_prefill")
+    return out, lse

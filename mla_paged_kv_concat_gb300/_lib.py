@@ -101,6 +101,11 @@ SIGNATURES = {
                             _I64, _P, _P]),
     "mla_project_v": (_I32, [_P, _I64, _I64, _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _I64,
                              _I64, _P, _P]),
+    "mla_prefill_num_kv_splits": (_I32, [_I32, _I32, _I32, _I64, _I32]),
+    "mla_prefill_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "mla_prefill": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _I64, _I64, _P, _I64,
+                           _I64, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _I32, _F32,
+                           _I32, _P, _SZ, _P, _I64, _I64, _P, _P, _P]),
     "mla_status_string": (ctypes.c_char_p, [_I32]),
     "mla_last_cuda_error": (ctypes.c_char_p, []),
 }

@@ -236,4 +236,30 @@ int proj_tile_cols(int tokens, int heads, int cols, int sm_count);
 cudaError_t launch_latent_proj(const ProjParams& p, const ProjMaps& m, int mode, int sm_count,
                                cudaStream_t stream);
 
+// Prompt attention of the expanded form (prefill.cu).
+struct PrefillParams {
+  int num_tokens, num_kv, heads, num_seqs;
+  const int32_t *cu_q, *cu_k;  // [num_seqs + 1]
+  bool causal;
+  float sm_scale;
+  int num_splits;
+  const uint16_t* v;  // for the rare values that are not finite
+  int64_t v_row_stride, v_head_stride;
+  uint16_t* o;
+  int64_t o_row_stride, o_head_stride;
+  float* lse;     // [num_tokens][heads]
+  float* ws_o;    // [splits][num_tokens][heads][128]
+  float* ws_lse;  // [splits][num_tokens][heads]
+  int* err_count;
+  // set by the launch
+  int slots, head_group;
+  int64_t units;
+};
+// {dims, heads (k_pe: 1), rows}, box {64, 1, 128}, 128-byte swizzled bf16.
+struct PrefillMaps {
+  CUtensorMap q, q_pe, k, k_pe, v;
+};
+cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, int sm_count,
+                           cudaStream_t stream);
+
 }  // namespace mla

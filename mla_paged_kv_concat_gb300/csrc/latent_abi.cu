@@ -350,4 +350,108 @@ mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_str
                      {y, y_row_stride, y_head_stride, v_dim}, {}, err_count, stream);
 }
 
+int mla_prefill_num_kv_splits(int num_tokens, int num_seqs, int num_heads, int64_t max_kv_len,
+                              int sm_count) {
+  if (num_tokens < 1 || num_seqs < 1 || num_heads < 1 || max_kv_len < 1 || sm_count < 1) return 1;
+  // 256-row blocks there can be, a CTA each
+  const int64_t blocks = num_tokens / 256 + (num_seqs < num_tokens ? num_seqs : num_tokens);
+  const int64_t units = blocks * num_heads;
+  if (units >= 2 * static_cast<int64_t>(sm_count)) return 1;
+  int64_t s = (4 * static_cast<int64_t>(sm_count) + units - 1) / units;
+  const int64_t most = (max_kv_len + 511) / 512;
+  if (s > most) s = most;
+  if (s > 64) s = 64;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+size_t mla_prefill_workspace_bytes(int num_tokens, int num_heads, int num_kv_splits, int v_dim) {
+  if (num_tokens <= 0 || num_heads <= 0 || num_kv_splits <= 1 || v_dim <= 0) return 0;
+  size_t n = static_cast<size_t>(num_tokens);
+  const size_t f[4] = {static_cast<size_t>(num_heads), static_cast<size_t>(num_kv_splits),
+                       static_cast<size_t>(v_dim) + 1, sizeof(float)};
+  for (size_t x : f)
+    if (__builtin_mul_overflow(n, x, &n)) return SIZE_MAX;
+  return n;
+}
+
+mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                       const void* q_pe, int64_t q_pe_row_stride, int64_t q_pe_head_stride,
+                       int num_tokens, int num_heads, const void* k_nope, int64_t k_row_stride,
+                       int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                       int64_t v_head_stride, const void* k_pe, int64_t k_pe_row_stride,
+                       int num_kv_tokens, int nope_dim, int rope_dim, int v_dim,
+                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int num_seqs,
+                       int causal, float sm_scale, int num_kv_splits, void* workspace,
+                       size_t workspace_bytes, void* o, int64_t o_row_stride,
+                       int64_t o_head_stride, float* lse, int* err_count, void* stream) {
+  if (num_tokens < 0 || num_kv_tokens < 0 || num_seqs < 0 || num_heads < 1 || num_heads > 1024 ||
+      num_kv_splits < 1 || num_kv_splits > 64 || nope_dim < 1 || rope_dim < 1 || v_dim < 1 ||
+      !(sm_scale >= 1e-30f && sm_scale <= 1e30f))
+    return MLA_ERR_INVALID_ARG;
+  if (nope_dim != kNopeDim || v_dim != kVDim || rope_dim != 64 || num_seqs > 65535 ||
+      num_tokens > (1 << 30) || num_kv_tokens > (1 << 30))
+    return MLA_ERR_UNSUPPORTED;
+  if (num_tokens == 0 || num_seqs == 0) return MLA_OK;
+  const Heads hq{q, q_row_stride, q_head_stride, q_pe ? nope_dim : nope_dim + rope_dim};
+  const Heads hqp = q_pe ? Heads{q_pe, q_pe_row_stride, q_pe_head_stride, rope_dim}
+                         : Heads{q ? static_cast<const uint16_t*>(q) + nope_dim : nullptr,
+                                 q_row_stride, q_head_stride, rope_dim};
+  const Heads hk{k_nope, k_row_stride, k_head_stride, nope_dim};
+  const Heads hv{v, v_row_stride, v_head_stride, v_dim};
+  const Heads hkp{k_pe, k_pe_row_stride, 0, rope_dim};
+  const Heads ho{o, o_row_stride, o_head_stride, v_dim};
+  if (!heads_ok(hq, num_tokens, num_heads) || !heads_ok(hqp, num_tokens, num_heads) ||
+      !heads_ok(ho, num_tokens, num_heads) || !heads_disjoint(ho, num_tokens, num_heads))
+    return MLA_ERR_INVALID_ARG;
+  if (num_kv_tokens > 0 &&
+      (!heads_ok(hk, num_kv_tokens, num_heads) || !heads_ok(hv, num_kv_tokens, num_heads) ||
+       !heads_ok(hkp, num_kv_tokens, 1)))
+    return MLA_ERR_INVALID_ARG;
+  if (!cu_seqlens_q || !cu_seqlens_k || !lse || !aligned4(cu_seqlens_q) ||
+      !aligned4(cu_seqlens_k) || !aligned4(lse) || !aligned4(err_count) || o == q || o == q_pe ||
+      o == k_nope || o == v)
+    return MLA_ERR_INVALID_ARG;
+  const size_t need = mla_prefill_workspace_bytes(num_tokens, num_heads, num_kv_splits, v_dim);
+  if (need > 0) {
+    if (!workspace || !aligned16(workspace)) return MLA_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  }
+  int sms = 0;
+  cudaError_t e = mla::device_sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  mla::PrefillParams p = {};
+  p.num_tokens = num_tokens;
+  p.num_kv = num_kv_tokens;
+  p.heads = num_heads;
+  p.num_seqs = num_seqs;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.causal = causal != 0;
+  p.sm_scale = sm_scale;
+  p.num_splits = num_kv_splits;
+  p.v = static_cast<const uint16_t*>(v);
+  p.v_row_stride = v_row_stride;
+  p.v_head_stride = num_heads > 1 ? v_head_stride : 0;
+  p.o = static_cast<uint16_t*>(o);
+  p.o_row_stride = o_row_stride;
+  p.o_head_stride = num_heads > 1 ? o_head_stride : 0;
+  p.lse = lse;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_lse = need ? p.ws_o + static_cast<size_t>(num_tokens) * num_heads * num_kv_splits * v_dim
+                  : nullptr;
+  p.err_count = err_count;
+  mla::PrefillMaps m;
+  memset(&m, 0, sizeof m);
+  mla_status st = heads_map(&m.q, hq, num_tokens, num_heads, 128);
+  if (st == MLA_OK) st = heads_map(&m.q_pe, hqp, num_tokens, num_heads, 128);
+  if (num_kv_tokens > 0) {
+    if (st == MLA_OK) st = heads_map(&m.k, hk, num_kv_tokens, num_heads, 128);
+    if (st == MLA_OK) st = heads_map(&m.k_pe, hkp, num_kv_tokens, 1, 128);
+    if (st == MLA_OK) st = heads_map(&m.v, hv, num_kv_tokens, num_heads, 128);
+  }
+  if (st != MLA_OK) return st;
+  e = mla::launch_prefill(p, m, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
 }  // extern "C"

@@ -1,0 +1,720 @@
+// Prompt attention of the expanded form: every head has its own keys (128
+// dims, plus 64 rope dims that all heads share) and values (128 dims), ragged
+// sequences, causal or not.
+//
+//   s_ij  = sm_scale * (q_nope_i . k_nope_j + q_pe_i . k_pe_j),
+//           j <= i + Lk - Lq when causal (queries are the last tokens)
+//   o_i   = sum_j softmax(s_i)_j v_j,   lse_i = ln sum_j exp(s_ij)
+//
+// One pass over the keys with the running maximum and sum of the softmax; O
+// is rescaled only when a row's maximum has grown by more than 2^8, so the
+// unnormalised P stays below 2^8 and fp32 sums lose nothing.  P is rounded to
+// bf16 for the second product; the sum adds the fp32 values.
+//
+// Work.  A unit is 256 query rows of one sequence and head (two tiles of 128)
+// and a range of its keys; persistent CTAs, one per SM.  Per 128 keys the
+// tensor core has 2 x (768 + 512) cycles of work (M = 128: 192 dims of Q.K
+// at N = 128, then 128 keys of P.V at N = 128), the exponentials 1024: with
+// two query tiles in turn, one tile's softmax runs under the other's
+// products and the tensor core is the bound.
+//   TMEM (512 columns): S0, S1 (128 each; P as packed bf16 over the first 64
+//     of its S), O0, O1 (128 each).
+//   Shared memory: Q 2 x 48 KiB, a ring of eight 16 KiB boxes (64 dims x 128
+//     keys) in the order K K K V V of each key tile: the box is what is filled
+//     and freed, so loads run ahead as far as the ring allows.
+//
+// Roles: warps 0-3 and 4-7 the softmax of query tiles 0 and 1 (thread = TMEM
+// lane = query row), warp 8 TMA producer and unit scheduler, warp 9 MMA
+// issuer and TMEM owner, warps 10-11 value keepers.
+//
+// Masked keys.  Scores of masked keys are replaced by -inf, whatever K held.
+// V of a masked key would still meet a zero of P, and 0 * NaN is NaN: in the
+// tiles that a mask cuts, the keepers zero the rows past the sequence's end
+// and any value that is not finite, and note the keys these were found in;
+// the epilogue adds them back for the rows that do attend to those keys.
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace mla {
+
+namespace {
+
+constexpr int kDv = 128;               // value dims
+constexpr int kTile = 128;             // query rows of a tile, keys of a tile
+constexpr int kUnitRows = 2 * kTile;
+constexpr int kBox = 16384;            // 64 dims x 128 rows of bf16
+constexpr int kRing = 8;
+constexpr int kUnits = 4;              // unit descriptions in flight
+constexpr int kThreads = 384;
+constexpr int OFF_Q = 0;
+constexpr int OFF_RING = OFF_Q + 6 * kBox;
+constexpr int OFF_UNIT = OFF_RING + kRing * kBox;
+constexpr int OFF_FLAG = OFF_UNIT + kUnits * 64;
+constexpr int OFF_BAR = OFF_FLAG + kUnits * 64;
+constexpr int kBars = 2 * kRing + 2 * kUnits + 14;
+constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
+constexpr int kSmem = OFF_TMEM + 16 + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+constexpr uint32_t O_COL = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;  // log2 units
+
+struct Unit {
+  int q_row;   // first query row (of all tokens); -1: no more units
+  int rows;    // query rows, 1 .. 256
+  int k_row;   // first key row of the sequence
+  int h;
+  int split;
+  int lk;      // keys of the sequence
+  int lim0;    // keys the first row may attend to (lk when not causal)
+  int ks, ke;  // this unit's keys [ks, ke)
+  int n0, n1;  // key tiles of each query tile
+  __device__ __forceinline__ int n(int t) const { return t == 0 ? n0 : n1; }
+  __device__ __forceinline__ int most() const { return max(n0, n1); }
+};
+static_assert(sizeof(Unit) <= 64, "unit slot");
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  const bool ok = mbar_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) {
+  return x < lo ? lo : (x > hi ? hi : x);
+}
+
+// Keys that row r (0 .. 255) of the unit may attend to, counted from the
+// sequence's first.
+__device__ __forceinline__ int row_limit(const Unit& u, int r, bool causal) {
+  return causal ? min(u.lk, u.lim0 + r) : u.lk;
+}
+
+// First key tile that a mask cuts (for some row of some tile).
+__device__ __forceinline__ int first_masked(const Unit& u, int row0, bool causal) {
+  const int bound = min(u.ke, row_limit(u, row0, causal));
+  return bound <= u.ks ? 0 : (bound - u.ks) / kTile;
+}
+
+// Unit `x` of the launch; false when it is empty.  Sequence b owns the block
+// slots from cu_q[b] / 256 + b on, at least as many as it has blocks, so
+// that a slot is found by one binary search with no sums.  Blocks run from
+// the last to the first (with a causal mask the longest come first); the
+// heads of a group share a block's turn, so that the CTAs at work together
+// read few heads' keys, from L2.
+__device__ bool unit_at(const PrefillParams& p, int64_t x, Unit& u) {
+  u.split = static_cast<int>(x % p.num_splits);
+  x /= p.num_splits;
+  const int hh = static_cast<int>(x % p.head_group);
+  x /= p.head_group;
+  const int slot = p.slots - 1 - static_cast<int>(x % p.slots);
+  u.h = static_cast<int>(x / p.slots) * p.head_group + hh;
+  if (u.h >= p.heads) return false;
+  int a = 0, z = p.num_seqs - 1;
+  while (a < z) {
+    const int m = (a + z + 1) >> 1;
+    const int c = clampi(__ldg(p.cu_q + m), 0, p.num_tokens);
+    if (c / kUnitRows + m <= slot) a = m; else z = m - 1;
+  }
+  const int q0 = __ldg(p.cu_q + a), q1 = __ldg(p.cu_q + a + 1);
+  const int k0 = __ldg(p.cu_k + a), k1 = __ldg(p.cu_k + a + 1);
+  const int qa = clampi(q0, 0, p.num_tokens), qz = clampi(q1, qa, p.num_tokens);
+  const int ka = clampi(k0, 0, p.num_kv), kz = clampi(k1, ka, p.num_kv);
+  const int blk = slot - (qa / kUnitRows + a);
+  if (blk == 0 && u.h == 0 && u.split == 0 && p.err_count &&
+      (qa != q0 || qz != q1 || ka != k0 || kz != k1))
+    atomicAdd(p.err_count, 1);
+  const int lq = qz - qa;
+  u.lk = kz - ka;
+  const int r0 = blk * kUnitRows;
+  if (blk < 0 || r0 >= lq) return false;
+  u.q_row = qa + r0;
+  u.k_row = ka;
+  u.rows = min(kUnitRows, lq - r0);
+  u.lim0 = p.causal ? r0 + (u.lk - lq) + 1 : u.lk;
+  const int per = ((u.lk + p.num_splits - 1) / p.num_splits + kTile - 1) / kTile * kTile;
+  const int64_t ks = static_cast<int64_t>(u.split) * per;
+  u.ks = ks < u.lk ? static_cast<int>(ks) : u.lk;
+  u.ke = ks + per < u.lk ? static_cast<int>(ks + per) : u.lk;
+  auto tiles = [&](int t) {
+    const int last = min(u.rows, (t + 1) * kTile) - 1;
+    const int keys = min(u.ke, row_limit(u, last, p.causal)) - u.ks;
+    return u.rows > t * kTile && keys > 0 ? (keys + kTile - 1) / kTile : 0;
+  };
+  u.n0 = tiles(0);
+  u.n1 = tiles(1);
+  return true;
+}
+
+// Packed fp32 pairs.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7F80u) != 0x7F80u; }
+
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const PrefillParams p, const __grid_constant__ PrefillMaps maps) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* full = bars;                     // [kRing] box landed
+  uint64_t* empty = full + kRing;            // [kRing] box read by its last product
+  uint64_t* unit_full = empty + kRing;       // [kUnits]
+  uint64_t* unit_empty = unit_full + kUnits; // [kUnits] 11 reading warps
+  uint64_t* q_full = unit_empty + kUnits;    // [2]
+  uint64_t* q_empty = q_full + 2;            // [2]
+  uint64_t* s_full = q_full + 4;             // [2]
+  uint64_t* p_full = q_full + 6;             // [2] P written, O rescaled
+  uint64_t* o_full = q_full + 8;             // [2] the unit's last P.V done
+  uint64_t* cut_full = q_full + 12;          // [2] a cut tile's values landed (the keepers do not
+                                             // follow the ring box by box)
+  uint64_t* v_ok = q_full + 10;              // [2] a cut tile's values are clean (in turn: the
+                                             // ring holds two tiles' values)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
+  auto unit_slot = [&](int i) { return reinterpret_cast<Unit*>(smem + OFF_UNIT + (i % kUnits) * 64); };
+  // keys with values that are not finite: 4 words for each of a unit's cut tiles
+  auto flags = [&](int i) { return reinterpret_cast<uint32_t*>(smem + OFF_FLAG + (i % kUnits) * 64); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&unit_full[i], 1);
+      mbar_init(&unit_empty[i], 11);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&cut_full[i], 1);
+      mbar_init(&v_ok[i], 64);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // One reading warp's walk over the units: f(unit, index) until the end
+  // mark or a failed wait.
+  auto for_each_unit = [&](auto&& f) -> bool {
+    for (int i = 0;; ++i) {
+      if (!warp_wait(&unit_full[i % kUnits], (i / kUnits) & 1)) return false;
+      const Unit u = *unit_slot(i);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&unit_empty[i % kUnits]);
+      if (u.q_row < 0) return true;
+      if (!f(u, i)) return false;
+    }
+  };
+
+  bool ok = true;
+  if (warp >= 8) {
+    reg_dec<104>();
+    if (warp == 8) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        int i = 0, pos = 0, cut = 0, qn[2] = {0, 0};
+        auto box = [&](const CUtensorMap* m, int c, int h, int row, uint64_t* bar) {
+          const int s = pos % kRing;
+          if (ok) ok = mbar_wait(&empty[s], ((pos / kRing) & 1) ^ 1);
+          if (!ok) return;
+          if (bar) {
+            mbar_arrive(&full[s]);  // keeps the ring's count; v_ok follows
+          } else {
+            bar = &full[s];
+            mbar_arrive_expect_tx(bar, kBox);
+          }
+          tma_load_3d(smem + OFF_RING + s * kBox, m, bar, c, h, row);
+          ++pos;
+        };
+        auto load_q = [&](const Unit& u, int t) {
+          if (u.n(t) == 0) return;
+          if (ok) ok = mbar_wait(&q_empty[t], (qn[t] & 1) ^ 1);
+          if (!ok) return;
+          ++qn[t];
+          mbar_arrive_expect_tx(&q_full[t], 3 * kBox);
+          uint8_t* dst = smem + OFF_Q + t * 3 * kBox;
+          const int row = u.q_row + t * kTile;
+          tma_load_3d(dst, &maps.q, &q_full[t], 0, u.h, row);
+          tma_load_3d(dst + kBox, &maps.q, &q_full[t], 64, u.h, row);
+          tma_load_3d(dst + 2 * kBox, &maps.q_pe, &q_full[t], 0, u.h, row);
+        };
+        auto load_k = [&](const Unit& u, int j) {
+          const int row = u.k_row + u.ks + j * kTile;
+          box(&maps.k, 0, u.h, row, nullptr);
+          box(&maps.k, 64, u.h, row, nullptr);
+          box(&maps.k_pe, 0, 0, row, nullptr);
+        };
+        auto load_v = [&](const Unit& u, int j) {
+          const int row = u.k_row + u.ks + j * kTile;
+          uint64_t* bar = nullptr;
+          if (j >= first_masked(u, 0, p.causal)) {
+            bar = &cut_full[cut & 1];
+            ++cut;
+            if (ok) mbar_arrive_expect_tx(bar, 2 * kBox);
+          }
+          box(&maps.v, 0, u.h, row, bar);
+          box(&maps.v, 64, u.h, row, bar);
+        };
+        for (int64_t x = blockIdx.x;; x += gridDim.x) {
+          Unit u;
+          const bool end = x >= p.units;
+          if (end) u.q_row = -1;
+          else if (!unit_at(p, x, u)) continue;
+          if (ok) ok = mbar_wait(&unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
+          if (!ok) break;
+          *unit_slot(i) = u;
+          mbar_arrive(&unit_full[i % kUnits]);
+          ++i;
+          if (end) break;
+          const int n = u.most();
+          if (n == 0) continue;
+          load_q(u, 0);
+          load_k(u, 0);
+          load_q(u, 1);
+          load_v(u, 0);
+          for (int j = 1; j < n && ok; ++j) {
+            load_k(u, j);
+            load_v(u, j);
+          }
+        }
+      }
+    } else if (warp == 9) {
+      // -------------------------------------------------------- MMA issuer
+      constexpr uint32_t id128 = tc::idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t idPV = tc::idesc_bf16(128, 128, 0, 1);
+      constexpr uint32_t idPVh = tc::idesc_bf16(128, 64, 0, 1);
+      const uint32_t q_base = smem_u32(smem + OFF_Q), ring = smem_u32(smem + OFF_RING);
+      int pos = 0;                // first box of the unit in the ring's count
+      int qn[2] = {0, 0}, pn[2] = {0, 0}, vn = 0;
+      ok = for_each_unit([&](const Unit& u, int) -> bool {
+        const int n = u.most();
+        if (n == 0) return true;
+        const int im = first_masked(u, 0, p.causal);
+        // S_t = Q_t K_j^T; `free_k`: the last product to read these boxes
+        auto qk = [&](int t, int j, bool free_k) -> bool {
+          if (j == 0) {
+            if (!warp_wait(&q_full[t], qn[t] & 1)) return false;
+            ++qn[t];
+          }
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const int b = pos + 5 * j + c, s = b % kRing;
+            if (!warp_wait(&full[s], (b / kRing) & 1)) return false;
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+              const uint64_t da =
+                  tc::smem_desc(q_base + (t * 3 + c) * kBox, 16, 1024, tc::kLayoutSw128);
+              const uint64_t db = tc::smem_desc(ring + s * kBox, 16, 1024, tc::kLayoutSw128);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc::mma_ss(tmem + t * 128, da + static_cast<uint64_t>(k * 2),
+                           db + static_cast<uint64_t>(k * 2), id128, (c > 0 || k > 0) ? 1u : 0u);
+              if (free_k) tc::commit(&empty[s]);
+              if (c == 2) {
+                tc::commit(&s_full[t]);
+                if (j == u.n(t) - 1) tc::commit(&q_empty[t]);
+              }
+            }
+            __syncwarp();
+          }
+          return true;
+        };
+        // O_t (+)= P_t V_j
+        auto pv = [&](int t, int j, bool free_v) -> bool {
+          const int b = pos + 5 * j + 3, s0 = b % kRing, s1 = (b + 1) % kRing;
+          if (!warp_wait(&p_full[t], pn[t] & 1)) return false;
+          ++pn[t];
+          if (!warp_wait(&full[s0], (b / kRing) & 1) ||
+              !warp_wait(&full[s1], ((b + 1) / kRing) & 1))
+            return false;
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            const uint32_t o = tmem + O_COL + t * 128, a = tmem + t * 128;
+            const uint32_t acc = j > 0 ? 1u : 0u;
+            const uint64_t d0 = tc::smem_desc(ring + s0 * kBox, kBox, 1024, tc::kLayoutSw128);
+            if (s1 == s0 + 1) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tc::mma_ts(o, a + k * 8, d0 + static_cast<uint64_t>(k * 128), idPV,
+                           k > 0 ? 1u : acc);
+            } else {  // the two boxes lie at the ring's two ends
+              const uint64_t d1 = tc::smem_desc(ring + s1 * kBox, kBox, 1024, tc::kLayoutSw128);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tc::mma_ts(o, a + k * 8, d0 + static_cast<uint64_t>(k * 128), idPVh,
+                           k > 0 ? 1u : acc);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tc::mma_ts(o + 64, a + k * 8, d1 + static_cast<uint64_t>(k * 128), idPVh,
+                           k > 0 ? 1u : acc);
+            }
+            if (free_v) {
+              tc::commit(&empty[s0]);
+              tc::commit(&empty[s1]);
+            }
+            if (j == u.n(t) - 1) tc::commit(&o_full[t]);
+          }
+          __syncwarp();
+          return true;
+        };
+        if (u.n0 > 0 && !qk(0, 0, u.n1 == 0)) return false;
+        if (u.n1 > 0 && !qk(1, 0, true)) return false;
+        for (int j = 0; j < n; ++j) {
+          if (j >= im) {
+            if (!warp_wait(&v_ok[vn & 1], (vn >> 1) & 1)) return false;
+            ++vn;
+          }
+          if (j < u.n0 && !pv(0, j, j >= u.n1)) return false;
+          if (j + 1 < u.n0 && !qk(0, j + 1, j + 1 >= u.n1)) return false;
+          if (j < u.n1 && !pv(1, j, true)) return false;
+          if (j + 1 < u.n1 && !qk(1, j + 1, true)) return false;
+        }
+        pos += 5 * n;
+        return true;
+      });
+    } else {
+      // ----------------------------------------------------- value keepers
+      const int row0 = (warp - 10) * 64 + lane;
+      int pos = 0, vn = 0;
+      ok = for_each_unit([&](const Unit& u, int i) -> bool {
+        const int n = u.most();
+        if (n == 0) return true;
+        for (int j = first_masked(u, 0, p.causal); j < n; ++j) {
+          const int b = pos + 5 * j + 3;
+          if (!warp_wait(&cut_full[vn & 1], (vn >> 1) & 1)) return false;
+          const int valid = u.lk - (u.ks + j * kTile);  // keys of the sequence in this tile
+          uint32_t* fl = flags(i) + (j - first_masked(u, 0, p.causal)) * 4 + (warp - 10) * 2;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const int r = row0 + half * 32;
+            __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
+            const __nv_bfloat162 zero = z;
+#pragma unroll 4
+            for (int c = 0; c < 16; ++c) {
+              uint4* a = reinterpret_cast<uint4*>(smem + OFF_RING + ((b + (c >> 3)) % kRing) * kBox +
+                                                  sw128(r, c & 7));
+              if (r < valid) {
+                const uint4 x = *a;  // 0 * x stays 0 unless x is not finite
+                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, z);
+                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, z);
+                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, z);
+                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, z);
+              } else {
+                *a = make_uint4(0, 0, 0, 0);
+              }
+            }
+            const uint32_t zb = *reinterpret_cast<uint32_t*>(&z);
+            const bool bad = (zb & 0x7FFF7FFFu) != 0;
+            if (bad) {
+#pragma unroll 1
+              for (int c = 0; c < 64; ++c) {
+                uint32_t* a = reinterpret_cast<uint32_t*>(
+                    smem + OFF_RING + ((b + (c >> 5)) % kRing) * kBox + sw128(r, (c >> 2) & 7) +
+                    (c & 3) * 4);
+                uint32_t x = *a;
+                if (!finite_bf16(x)) x &= 0xFFFF0000u;
+                if (!finite_bf16(x >> 16)) x &= 0xFFFFu;
+                *a = x;
+              }
+            }
+            const uint32_t word = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) fl[half] = word;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&v_ok[vn & 1]);
+          ++vn;
+        }
+        pos += 5 * n;
+        return true;
+      });
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    reg_inc<200>();
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;         // row of the tile, TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + O_COL + t * 128;
+    const float c = p.sm_scale * kLog2e;
+    const uint64_t c2 = pack2(c, c);
+    int sn = 0, on = 0;
+    ok = for_each_unit([&](const Unit& u, int i) -> bool {
+      const int row = t * kTile + r;         // row of the unit
+      const int n = u.n(t);
+      const bool live = row < u.rows;
+      const int lim = min(u.ke, row_limit(u, row, p.causal)) - u.ks;  // keys of this unit
+      const int im = first_masked(u, t * kTile, p.causal);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++sn) {
+        if (!warp_wait(&s_full[t], sn & 1)) return false;
+        tc::fence_after_sync();
+        uint32_t s[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          tc::ld_32x32b_x32(s_col + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[q * 32]));
+        tc::wait_ld();
+        tc::reg_fence(s);
+        if (j >= im) {
+          const int left = lim - j * kTile;
+#pragma unroll
+          for (int q = 0; q < 128; ++q)
+            if (q >= left) s[q] = 0xFF800000u;  // -inf
+        }
+        float mx[4] = {m, m, m, m};
+#pragma unroll
+        for (int q = 0; q < 128; q += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[q + 2 * e]), __uint_as_float(s[q + 2 * e + 1])));
+        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // O is rescaled only when the maximum has grown by more than 2^8
+        // (-inf - -inf is NaN: no)
+        const bool grow = (m_new - m) * c > kRescale;
+        if (j > 0 && __any_sync(0xffffffffu, grow)) {
+          // this tile's S was issued after the last P.V: O is complete
+          const float alpha = grow ? ex2((m - m_new) * c) : 1.f;
+          l *= alpha;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            tc::ld_32x32b_x32(o_col + q * 32, o);
+            tc::wait_ld();
+            tc::reg_fence(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::st_32x32b_x32(o_col + q * 32, o);
+          }
+        }
+        if (grow) m = m_new;
+        const float mc = m == -INFINITY ? 0.f : -m * c;
+        const uint64_t mc2 = pack2(mc, mc);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int q = 0; q < 64; ++q) {
+          float a, b;
+          unpack2(fma2(pack2(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1])), c2, mc2), a,
+                  b);
+          a = ex2(a);
+          b = ex2(b);
+          sum[q & 1] = add2(sum[q & 1], pack2(a, b));
+          s[q] = pack_bf16x2(a, b);
+          if ((q & 31) == 31)
+            tc::st_32x32b_x32(s_col + (q - 31), *reinterpret_cast<uint32_t(*)[32]>(&s[q - 31]));
+        }
+        float a0, a1, b0, b1;
+        unpack2(sum[0], a0, a1);
+        unpack2(sum[1], b0, b1);
+        l += (a0 + a1) + (b0 + b1);
+        tc::wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&p_full[t]);
+      }
+      // ---- this row of O, and its lse
+      if (n > 0) {
+        if (!warp_wait(&o_full[t], on & 1)) return false;
+        ++on;
+        tc::fence_after_sync();
+      }
+      const int64_t q_row = u.q_row + row;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // flagged keys of the cut tiles that this row attends to
+      uint32_t any = 0;
+      const int um = first_masked(u, 0, p.causal), nm = u.n(t) - um;
+      if (n > 0) {
+        for (int k = 0; k < nm; ++k)
+          for (int w = 0; w < 4; ++w) any |= flags(i)[k * 4 + w];
+      }
+      const int64_t part = (static_cast<int64_t>(u.split) * p.num_tokens + q_row) * p.heads + u.h;
+#pragma unroll 1
+      for (int q = 0; q < kDv; q += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        if (n > 0) {
+          tc::ld_32x32b_x32(o_col + q, o);
+          tc::wait_ld();
+          tc::reg_fence(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (live && any) {
+          for (int k = 0; k < nm; ++k) {
+            for (int w = 0; w < 4; ++w) {
+              uint32_t bits = flags(i)[k * 4 + w];
+              while (bits) {
+                const int key = (um + k) * kTile + w * 32 + __ffs(bits) - 1;
+                bits &= bits - 1;
+                if (key >= lim) continue;
+                const uint16_t* v =
+                    p.v + (static_cast<int64_t>(u.k_row) + u.ks + key) * p.v_row_stride +
+                    u.h * p.v_head_stride + q;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const uint32_t x = __ldg(v + e);
+                  if (!finite_bf16(x))
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(x << 16));
+                }
+              }
+            }
+          }
+        }
+        if (live && p.num_splits == 1) {
+          uint16_t* dst = p.o + q_row * p.o_row_stride + u.h * p.o_head_stride + q;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+              w[f] = pack_bf16x2(__uint_as_float(o[e + 2 * f]) * inv,
+                                 __uint_as_float(o[e + 2 * f + 1]) * inv);
+            *reinterpret_cast<uint4*>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (live && n > 0) {
+          float* dst = p.ws_o + part * kDv + q;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(dst + e) =
+                make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                            __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+        }
+      }
+      if (live) {
+        float lg;
+        asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(l));
+        const float lse = l == 0.f ? -INFINITY : (m * c + lg) * kLn2;
+        if (p.num_splits == 1)
+          p.lse[q_row * p.heads + u.h] = lse;
+        else
+          p.ws_lse[part] = lse;
+      }
+      // the reads of O are done before the next unit's first P opens the
+      // way for a P.V that overwrites it
+      __syncwarp();
+      tc::fence_before_sync();
+      return true;
+    });
+  }
+  if (!ok && lane == 0 && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// The splits of a row and head joined: M = max lse_s, o = sum e^{lse_s - M}
+// o_s / sum e^{lse_s - M}, in split order.  One warp each, four dims a lane.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const PrefillParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t rec = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  const int64_t records = static_cast<int64_t>(p.num_tokens) * p.heads;
+  if (rec >= records) return;
+  const int64_t row = rec / p.heads;
+  const int h = static_cast<int>(rec % p.heads);
+  // rows of no sequence are left as they were
+  if (row < __ldg(p.cu_q) || row >= __ldg(p.cu_q + p.num_seqs)) return;
+  const int S = p.num_splits;
+  float M = -INFINITY;
+  for (int s = lane; s < S; s += 32) M = fmaxf(M, p.ws_lse[s * records + rec]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f;
+  for (int s0 = 0; s0 < S; s0 += 32) {
+    const float ls = s0 + lane < S ? p.ws_lse[(s0 + lane) * records + rec] : -INFINITY;
+    const float w = ls == -INFINITY ? 0.f : ex2((ls - M) * kLog2e);
+    uint32_t mask = __ballot_sync(0xffffffffu, ls != -INFINITY);
+    while (mask) {
+      const int j = __ffs(mask) - 1;
+      mask &= mask - 1;
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const float4 x = *reinterpret_cast<const float4*>(p.ws_o + ((s0 + j) * records + rec) * kDv +
+                                                        lane * 4);
+      acc.x += wj * x.x;
+      acc.y += wj * x.y;
+      acc.z += wj * x.z;
+      acc.w += wj * x.w;
+      den += wj;
+    }
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  uint2 out;
+  out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.o + row * p.o_row_stride + h * p.o_head_stride + lane * 4) = out;
+  if (lane == 0) p.lse[rec] = den == 0.f ? -INFINITY : M + logf(den);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const PrefillParams& p_in, const PrefillMaps& maps, int sm_count,
+                           cudaStream_t stream) {
+  PrefillParams p = p_in;
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = set_smem_attr_once(prefill_kernel, kSmem, attr_done);
+  if (e != cudaSuccess) return e;
+  p.slots = p.num_tokens / kUnitRows + p.num_seqs;
+  p.head_group = p.heads < 8 ? p.heads : 8;
+  const int groups = (p.heads + p.head_group - 1) / p.head_group;
+  p.units = static_cast<int64_t>(groups) * p.slots * p.head_group * p.num_splits;
+  const int grid = p.units < sm_count ? static_cast<int>(p.units) : sm_count;
+  e = launch_overlapped(prefill_kernel, dim3(grid), dim3(kThreads), kSmem, stream, p, maps);
+  if (e != cudaSuccess || p.num_splits == 1) return e;
+  const int64_t records = static_cast<int64_t>(p.num_tokens) * p.heads;
+  return launch_overlapped(prefill_merge_kernel,
+                           dim3(static_cast<unsigned>((records + kMergeWarps - 1) / kMergeWarps)),
+                           dim3(kMergeWarps * 32), 0, stream, p);
+}
+
+}  // namespace mla
