@@ -374,46 +374,20 @@ def lse_merge(o_parts, lse_parts, *, out=None, lse=None, stream=None):
 
 
 # ------------------------------------------------------- prompts and batches
-def _check(cond: bool, what: str) -> None:
-    if not cond:
-        raise ValueError(what)
+_bind_module = None
 
 
-def _cuda(stream, **tensors):
-    """Checks that every tensor given is on the current CUDA device (where the
-    kernels run); returns that device."""
-    torch = _torch()
-    for name, t in tensors.items():
-        _check(t is None or t.is_cuda, f"{name} must be a CUDA tensor")
-    dev = torch.device("cuda", torch.cuda.current_device())
-    for name, t in tensors.items():
-        _check(t is None or t.device == dev, f"{name} is not on the current device {dev}")
-    _check(stream is None or stream.device == dev, f"the stream is not on the current device {dev}")
-    return dev
-
-
-def _empty(stream, *shape, dtype, device):
-    """A new tensor for a kernel that runs on `stream`."""
-    torch = _torch()
-    t = torch.empty(*shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
-def _typed(t, dtype, shape, name):
-    """Checks dtype and shape (None: any size) and unit last stride."""
-    if t is None:
-        return
-    _check(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _check(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)),
-           f"{name} has shape {tuple(t.shape)}, not {shape}")
-    _check(t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1,
-           f"{name} must have unit last stride")
-
-
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
+def _bind():
+    """The compiled binding (csrc/bind.cpp): it checks the tensors (dtype,
+    shape, unit last stride, on the current device; ValueError), allocates
+    outputs that are not given and calls the library (MlaError)."""
+    global _bind_module
+    if _bind_module is None:
+        _torch()
+        load()
+        from . import _calls
+        _bind_module = _calls
+    return _bind_module
 
 
 class BatchTables(NamedTuple):
@@ -443,51 +417,10 @@ def batch_build(query_lens, context_lens, req_block_table, free_blocks, free_cou
     not given; a block table allocated here starts as zeros.
     ``free_count_out`` may be ``free_count`` (updated in place).
     """
-    torch = _torch()
-    i32, i64 = torch.int32, torch.int64
-    dev = _cuda(stream, query_lens=query_lens, context_lens=context_lens,
-                req_block_table=req_block_table, free_blocks=free_blocks, free_count=free_count,
-                req_ids=req_ids, block_table=block_table, seq_lens=seq_lens,
-                cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, positions=positions,
-                slot_mapping=slot_mapping, free_count_out=free_count_out, err_count=err_count)
-    _check(query_lens.dim() == 1, "query_lens must have one dimension")
-    B = query_lens.shape[0]
-    if num_tokens is None:
-        given = positions if positions is not None else slot_mapping
-        _check(given is not None, "num_tokens is needed when no token output is given")
-        num_tokens = given.shape[0]
-    _typed(req_block_table, i32, (None, None), "req_block_table")
-    rows, maxb = req_block_table.shape
-    if block_table is None:
-        with torch.cuda.stream(stream):
-            block_table = torch.zeros(B, maxb, dtype=i32, device=dev)
-    mk = lambda t, n, d: t if t is not None else _empty(stream, n, dtype=d, device=dev)  # noqa: E731
-    seq_lens = mk(seq_lens, B, i32)
-    cu_seqlens_q, cu_seqlens_k = mk(cu_seqlens_q, B + 1, i32), mk(cu_seqlens_k, B + 1, i32)
-    positions, slot_mapping = mk(positions, num_tokens, i64), mk(slot_mapping, num_tokens, i64)
-    free_count_out = mk(free_count_out, 1, i32)
-    for t, d, shape, name in (
-            (query_lens, i32, (B,), "query_lens"), (context_lens, i32, (B,), "context_lens"),
-            (req_ids, i32, (B,), "req_ids"), (free_blocks, i32, (None,), "free_blocks"),
-            (free_count, i32, (1,), "free_count"), (free_count_out, i32, (1,), "free_count_out"),
-            (block_table, i32, (B, maxb), "block_table"), (seq_lens, i32, (B,), "seq_lens"),
-            (cu_seqlens_q, i32, (B + 1,), "cu_seqlens_q"),
-            (cu_seqlens_k, i32, (B + 1,), "cu_seqlens_k"),
-            (positions, i64, (num_tokens,), "positions"),
-            (slot_mapping, i64, (num_tokens,), "slot_mapping"),
-            (err_count, i32, (1,), "err_count")):
-        _typed(t, d, shape, name)
-    st = load().mla_batch_build(
-        _ptr(req_ids), query_lens.data_ptr(), context_lens.data_ptr(), B,
-        req_block_table.data_ptr(), req_block_table.stride(0), rows, maxb, int(block_size),
-        int(num_blocks), free_blocks.data_ptr(), free_blocks.numel(), free_count.data_ptr(),
-        free_count_out.data_ptr(), int(num_tokens), block_table.data_ptr(),
-        block_table.stride(0), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
-        cu_seqlens_k.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), _ptr(err_count),
-        _stream_ptr(stream))
-    _lib.check(st, "mla_batch_build")
-    return BatchTables(block_table, seq_lens, cu_seqlens_q, cu_seqlens_k, positions,
-                       slot_mapping, free_count_out)
+    return BatchTables(*_bind().batch_build(
+        query_lens, context_lens, req_block_table, free_blocks, free_count, block_size,
+        num_blocks, -1 if num_tokens is None else num_tokens, req_ids, block_table, seq_lens,
+        cu_seqlens_q, cu_seqlens_k, positions, slot_mapping, free_count_out, err_count, stream))
 
 
 def blocks_release(held_lens, req_block_table, free_blocks, free_count, block_size: int,
@@ -497,29 +430,8 @@ def blocks_release(held_lens, req_block_table, free_blocks, free_count, block_si
     rows ``req_ids`` of ``req_block_table``) back onto the stack
     ``free_blocks``; returns the new height (``free_count_out``, by default
     ``free_count`` updated in place)."""
-    torch = _torch()
-    i32 = torch.int32
-    if free_count_out is None:
-        free_count_out = free_count
-    _cuda(stream, held_lens=held_lens, req_block_table=req_block_table, free_blocks=free_blocks,
-          free_count=free_count, req_ids=req_ids, free_count_out=free_count_out,
-          err_count=err_count)
-    _typed(held_lens, i32, (None,), "held_lens")
-    B = held_lens.shape[0]
-    for t, shape, name in ((req_block_table, (None, None), "req_block_table"),
-                           (req_ids, (B,), "req_ids"), (free_blocks, (None,), "free_blocks"),
-                           (free_count, (1,), "free_count"),
-                           (free_count_out, (1,), "free_count_out"),
-                           (err_count, (1,), "err_count")):
-        _typed(t, i32, shape, name)
-    rows, maxb = req_block_table.shape
-    st = load().mla_blocks_release(
-        _ptr(req_ids), held_lens.data_ptr(), B, req_block_table.data_ptr(),
-        req_block_table.stride(0), rows, maxb, int(block_size), int(num_blocks),
-        free_blocks.data_ptr(), free_blocks.numel(), free_count.data_ptr(),
-        free_count_out.data_ptr(), _ptr(err_count), _stream_ptr(stream))
-    _lib.check(st, "mla_blocks_release")
-    return free_count_out
+    return _bind().blocks_release(held_lens, req_block_table, free_blocks, free_count, block_size,
+                                  num_blocks, req_ids, free_count_out, err_count, stream)
 
 
 def gather_cache(kv_cache, block_table, cu_seqlens, num_tokens: int | None = None, *,
@@ -534,61 +446,11 @@ def gather_cache(kv_cache, block_table, cu_seqlens, num_tokens: int | None = Non
     given; rows past ``cu_seqlens[B]`` are left as they were.  fp8 caches are
     multiplied by the device scalar ``kv_scale``.
     """
-    torch = _torch()
-    bf, i32 = torch.bfloat16, torch.int32
-    dev = _cuda(stream, kv_cache=kv_cache, block_table=block_table, cu_seqlens=cu_seqlens,
-                seq_starts=seq_starts, kv_scale=kv_scale, kv_c=kv_c, k_pe=k_pe,
-                err_count=err_count)
-    kvd = _kv_dtype(kv_cache, kv_cache_dtype)
-    _check(kv_cache.element_size() == (2 if kvd == MLA_KV_BF16 else 1),
-           "kv_cache_dtype does not fit the cache")
-    nb, bs, d, bstride = _cache_geom(kv_cache)
-    R = kv_lora_rank if kv_lora_rank is not None else d - 64
-    P = d - R
-    _typed(block_table, i32, (None, None), "block_table")
-    B = block_table.shape[0]
-    if num_tokens is None:
-        _check(kv_c is not None, "num_tokens is needed when kv_c is not given")
-        num_tokens = kv_c.shape[0]
-    if kv_c is None:
-        kv_c = _empty(stream, num_tokens, R, dtype=bf, device=dev)
-    if k_pe is None:
-        k_pe = _empty(stream, num_tokens, P, dtype=bf, device=dev)
-    for t, dt, shape, name in ((cu_seqlens, i32, (B + 1,), "cu_seqlens"),
-                               (seq_starts, i32, (B,), "seq_starts"),
-                               (kv_c, bf, (num_tokens, R), "kv_c"),
-                               (k_pe, bf, (num_tokens, P), "k_pe"),
-                               (err_count, i32, (1,), "err_count")):
-        _typed(t, dt, shape, name)
-    _check(kv_scale is None or (kv_scale.dtype == torch.float32 and kv_scale.numel() == 1),
-           "kv_scale must be one float32")
-    st = load().mla_gather_cache(
-        kv_cache.data_ptr(), kvd, nb, bs, bstride, R, P, block_table.data_ptr(),
-        block_table.stride(0), block_table.shape[1], cu_seqlens.data_ptr(), _ptr(seq_starts), B,
-        int(num_tokens), _ptr(kv_scale), kv_c.data_ptr(), kv_c.stride(0), k_pe.data_ptr(),
-        k_pe.stride(0), _ptr(err_count), _stream_ptr(stream))
-    _lib.check(st, "mla_gather_cache")
-    return kv_c, k_pe
-
-
-NOPE_DIM = 128  # head dims of the expanded form: keys without the rope part
-V_DIM = 128     # and values
-
-
-def _strides(t):
-    """(row, head) strides of a [T, H, D] tensor; those of dimensions of size
-    1, which torch leaves arbitrary, as in a dense tensor."""
-    T, H, D = t.shape
-    hs = t.stride(1) if H > 1 else D
-    rs = t.stride(0) if T > 1 else (H * hs if H > 1 else D)
-    return rs, hs
-
-
-def _kv_b(w_kv_b, num_heads: int):
-    """Checks the kv_b weight [H * 256, R]; returns R."""
-    torch = _torch()
-    _typed(w_kv_b, torch.bfloat16, (num_heads * (NOPE_DIM + V_DIM), None), "w_kv_b")
-    return w_kv_b.shape[1]
+    return _bind().gather_cache(
+        kv_cache, -1 if kv_cache_dtype is None else _kv_dtype(kv_cache, kv_cache_dtype),
+        block_table, cu_seqlens, -1 if num_tokens is None else num_tokens,
+        -1 if kv_lora_rank is None else kv_lora_rank, seq_starts, kv_scale, kv_c, k_pe,
+        err_count, stream)
 
 
 def expand_kv(kv_c, w_kv_b, num_heads: int, *, k_nope=None, v=None, err_count=None,
@@ -597,58 +459,20 @@ def expand_kv(kv_c, w_kv_b, num_heads: int, *, k_nope=None, v=None, err_count=No
     [T, H, 128] each; ``w_kv_b`` [H * 256, R] is the kv_b projection's weight
     (per head 128 rows of W_UK, then 128 of W_UV).  Allocated as the two
     halves of one [T, H, 256] buffer unless both are given."""
-    torch = _torch()
-    bf = torch.bfloat16
-    dev = _cuda(stream, kv_c=kv_c, w_kv_b=w_kv_b, k_nope=k_nope, v=v, err_count=err_count)
-    R = _kv_b(w_kv_b, num_heads)
-    _typed(kv_c, bf, (None, R), "kv_c")
-    T = kv_c.shape[0]
-    _check((k_nope is None) == (v is None), "give both k_nope and v, or neither")
-    if k_nope is None:
-        kv = _empty(stream, T, num_heads, NOPE_DIM + V_DIM, dtype=bf, device=dev)
-        k_nope, v = kv[..., :NOPE_DIM], kv[..., NOPE_DIM:]
-    _typed(k_nope, bf, (T, num_heads, NOPE_DIM), "k_nope")
-    _typed(v, bf, (T, num_heads, V_DIM), "v")
-    _typed(err_count, torch.int32, (1,), "err_count")
-    st = load().mla_expand_kv(
-        kv_c.data_ptr(), kv_c.stride(0) if T > 1 else R, T, w_kv_b.data_ptr(), w_kv_b.stride(0),
-        num_heads, R, NOPE_DIM, V_DIM, k_nope.data_ptr(), *_strides(k_nope), v.data_ptr(),
-        *_strides(v), _ptr(err_count), _stream_ptr(stream))
-    _lib.check(st, "mla_expand_kv")
-    return k_nope, v
-
-
-def _head_product(fn, x, w_kv_b, n_in, n_out, out, err_count, stream):
-    torch = _torch()
-    bf = torch.bfloat16
-    dev = _cuda(stream, x=x, w_kv_b=w_kv_b, out=out, err_count=err_count)
-    _check(x.dim() == 3, "the input must be [tokens, heads, dims]")
-    T, H, _ = x.shape
-    R = _kv_b(w_kv_b, H)
-    n_in, n_out = n_in or R, n_out or R
-    _typed(x, bf, (T, H, n_in), "the input")
-    if out is None:
-        out = _empty(stream, T, H, n_out, dtype=bf, device=dev)
-    _typed(out, bf, (T, H, n_out), "out")
-    _typed(err_count, torch.int32, (1,), "err_count")
-    st = getattr(load(), fn)(
-        x.data_ptr(), *_strides(x), T, w_kv_b.data_ptr(), w_kv_b.stride(0), H, R, NOPE_DIM,
-        V_DIM, out.data_ptr(), *_strides(out), _ptr(err_count), _stream_ptr(stream))
-    _lib.check(st, fn)
-    return out
+    return _bind().expand_kv(kv_c, w_kv_b, num_heads, k_nope, v, err_count, stream)
 
 
 def absorb_q(q_nope, w_kv_b, *, out=None, err_count=None, stream=None):
     """The latent query ql_nope [T, H, R] of ``q_nope`` [T, H, 128] (any row
     and head strides: a column slice of q will do): ``decode``'s query is then
     the pair (ql_nope, q_pe).  ``w_kv_b`` as in :func:`expand_kv`."""
-    return _head_product("mla_absorb_q", q_nope, w_kv_b, NOPE_DIM, None, out, err_count, stream)
+    return _bind().absorb_q(q_nope, w_kv_b, out, err_count, stream)
 
 
 def project_v(o, w_kv_b, *, out=None, err_count=None, stream=None):
     """Values [T, H, 128] of ``decode``'s latent output ``o`` [T, H, R];
     ``w_kv_b`` as in :func:`expand_kv`."""
-    return _head_product("mla_project_v", o, w_kv_b, None, V_DIM, out, err_count, stream)
+    return _bind().project_v(o, w_kv_b, out, err_count, stream)
 
 
 def prefill(q, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, sm_scale: float, *,
@@ -665,41 +489,6 @@ def prefill(q, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, sm_scale: float, *,
     ``mla_prefill_num_kv_splits``; the workspace they need is allocated here
     when not given.
     """
-    torch = _torch()
-    bf, i32 = torch.bfloat16, torch.int32
     q, q_pe = q if isinstance(q, (tuple, list)) else (q, None)
-    dev = _cuda(stream, q=q, q_pe=q_pe, k_nope=k_nope, v=v, k_pe=k_pe, cu_seqlens_q=cu_seqlens_q,
-                cu_seqlens_k=cu_seqlens_k, workspace=workspace, out=out, lse=lse,
-                err_count=err_count)
-    _check(q.dim() == 3 and k_pe.dim() == 2, "q must be [tokens, heads, dims], k_pe [keys, 64]")
-    T, H, _ = q.shape
-    Tk, P = k_pe.shape
-    B = cu_seqlens_q.shape[0] - 1
-    if out is None:
-        out = _empty(stream, T, H, V_DIM, dtype=bf, device=dev)
-    if lse is None:
-        lse = _empty(stream, T, H, dtype=torch.float32, device=dev)
-    for t, d, shape, name in ((q, bf, (T, H, NOPE_DIM + (P if q_pe is None else 0)), "q"),
-                              (q_pe, bf, (T, H, P), "q_pe"),
-                              (k_nope, bf, (Tk, H, NOPE_DIM), "k_nope"),
-                              (v, bf, (Tk, H, V_DIM), "v"), (k_pe, bf, (Tk, P), "k_pe"),
-                              (cu_seqlens_q, i32, (B + 1,), "cu_seqlens_q"),
-                              (cu_seqlens_k, i32, (B + 1,), "cu_seqlens_k"),
-                              (out, bf, (T, H, V_DIM), "out"),
-                              (lse, torch.float32, (T, H), "lse"),
-                              (err_count, i32, (1,), "err_count")):
-        _typed(t, d, shape, name)
-    _check(B >= 0 and lse.is_contiguous(), "lse must be contiguous, cu_seqlens_q not empty")
-    need = mla_prefill_workspace_bytes(T, H, num_kv_splits, V_DIM)
-    if need and workspace is None:
-        workspace = _empty(stream, need, dtype=torch.uint8, device=dev)
-    _check(workspace is None or workspace.is_contiguous(), "workspace must be contiguous")
-    st = load().mla_prefill(
-        q.data_ptr(), *_strides(q), _ptr(q_pe), *(_strides(q_pe) if q_pe is not None else (0, 0)),
-        T, H, k_nope.data_ptr(), *_strides(k_nope), v.data_ptr(), *_strides(v), k_pe.data_ptr(),
-        k_pe.stride(0) if Tk > 1 else P, Tk, NOPE_DIM, P, V_DIM, cu_seqlens_q.data_ptr(),
-        cu_seqlens_k.data_ptr(), B, int(bool(causal)), float(sm_scale), int(num_kv_splits),
-        _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0,
-        out.data_ptr(), *_strides(out), lse.data_ptr(), _ptr(err_count), _stream_ptr(stream))
-    _lib.check(st, "mla_prefill")
-    return out, lse
+    return _bind().prefill(q, q_pe, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, sm_scale, causal,
+                           num_kv_splits, workspace, out, lse, err_count, stream)

@@ -1,8 +1,10 @@
-"""Build libmla.so (the C-ABI CUDA library) in-tree for sm_103a with nvcc.
+"""Build libmla.so (the C-ABI CUDA library) in-tree for sm_103a with nvcc, and
+_calls.so (the compiled part of the Python binding) with g++.
 
 Each ``csrc/*.cu`` compiles to an object in ``_build/`` in parallel, then the
-objects link into ``mla_paged_kv_concat_gb300/libmla.so``.  ptxas resource
-usage (``-Xptxas -v``) goes to ``_build/ptxas.log``.  Run ``python -m
+objects link into ``mla_paged_kv_concat_gb300/libmla.so``; ``csrc/bind.cpp``
+compiles beside them and links against it and torch.  ptxas resource usage
+(``-Xptxas -v``) goes to ``_build/ptxas.log``.  Run ``python -m
 mla_paged_kv_concat_gb300.build`` or call :func:`build`.
 """
 from __future__ import annotations
@@ -19,6 +21,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmla.so")
+BIND = os.path.join(PKG, "_calls.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-Xptxas", "-v", "-I" + os.path.join(ROOT, "include")]
@@ -36,14 +40,14 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (_sources() + [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -56,23 +60,58 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stdout + r.stderr
 
 
+def _compile_bind() -> str:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "bind.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", BIND_SRC, "-o", obj,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for inc in (os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"],
+                os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")):
+        cmd += ["-isystem", inc]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BIND + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN", "-L" + lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libmla.so if any source changed; returns its path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        bind = ex.submit(_compile_bind)
         results = list(ex.map(_compile, srcs))
+        bind_obj = bind.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for (obj, log), src in zip(results, srcs):
             f.write(f"==== {os.path.basename(src)}\n{log}\n")
     tmp = LIB + ".tmp"
-    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *[o for o, _ in results], "-lcudart"]
+    cmd = [_nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=libmla.so", "-o", tmp,
+           *[o for o, _ in results], "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_bind(bind_obj)
     if verbose:
         print(f"built {LIB}")
     return LIB
