@@ -253,13 +253,11 @@ struct PrefillParams {
   int* err_count;
   // set by the launch
   int slots, head_group;
-  int64_t units;
 };
 // {dims, heads (k_pe: 1), rows}, box {64, 1, 128}, 128-byte swizzled bf16.
 struct PrefillMaps {
   CUtensorMap q, q_pe, k, k_pe, v;
 };
-cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, int sm_count,
-                           cudaStream_t stream);
+cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream);
 
 }  // namespace mla

@@ -416,9 +416,10 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
     if (!workspace || !aligned16(workspace)) return MLA_ERR_INVALID_ARG;
     if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
   }
-  int sms = 0;
-  cudaError_t e = mla::device_sm_count(&sms);
-  if (e != cudaSuccess) return cuda_fail(e);
+  // one CTA per 256-row block slot, head and split
+  if ((num_tokens / 256 + static_cast<int64_t>(num_seqs)) * 2 * num_heads * num_kv_splits >
+      INT32_MAX)
+    return MLA_ERR_UNSUPPORTED;
   mla::PrefillParams p = {};
   p.num_tokens = num_tokens;
   p.num_kv = num_kv_tokens;
@@ -450,7 +451,7 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
     if (st == MLA_OK) st = heads_map(&m.v, hv, num_kv_tokens, num_heads, 128);
   }
   if (st != MLA_OK) return st;
-  e = mla::launch_prefill(p, m, sms, static_cast<cudaStream_t>(stream));
+  cudaError_t e = mla::launch_prefill(p, m, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
 }
 

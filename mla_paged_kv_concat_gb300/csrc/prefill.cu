@@ -12,7 +12,10 @@
 // bf16 for the second product; the sum adds the fp32 values.
 //
 // Work.  A unit is 256 query rows of one sequence and head (two tiles of 128)
-// and a range of its keys; persistent CTAs, one per SM.  Per 128 keys the
+// and a range of its keys.  The grid has one CTA per unit, longest first; one
+// CTA runs on an SM and, instead of ending, takes over the next CTA that has
+// not started (cluster launch control), so that the work is shared out as
+// it goes, without a counter in memory.  Per 128 keys the
 // tensor core has 2 x (768 + 512) cycles of work (M = 128: 192 dims of Q.K
 // at N = 128, then 128 keys of P.V at N = 128), the exponentials 1024: with
 // two query tiles in turn, one tile's softmax runs under the other's
@@ -55,8 +58,9 @@ constexpr int OFF_RING = OFF_Q + 6 * kBox;
 constexpr int OFF_UNIT = OFF_RING + kRing * kBox;
 constexpr int OFF_FLAG = OFF_UNIT + kUnits * 64;
 constexpr int OFF_BAR = OFF_FLAG + kUnits * 64;
-constexpr int kBars = 2 * kRing + 2 * kUnits + 14;
-constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
+constexpr int kBars = 2 * kRing + 2 * kUnits + 15;
+constexpr int OFF_NEXT = (OFF_BAR + kBars * 8 + 15) & ~15;
+constexpr int OFF_TMEM = OFF_NEXT + 16;
 constexpr int kSmem = OFF_TMEM + 16 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t O_COL = 256;
@@ -170,6 +174,32 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// Cluster launch control: asks to cancel a CTA of this grid that has not been
+// started, to run it here; the answer (16 bytes) arrives in `dst` on `bar`.
+__device__ __forceinline__ void next_cta_ask(void* dst, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];" ::"r"(smem_u32(dst)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The answer: the cancelled CTA's index, or -1 when none was left.
+__device__ __forceinline__ int64_t next_cta_answer(const void* src) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(src);
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "mov.b128 h, {%2, %3};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "l"(a.x), "l"(a.y)
+      : "memory");
+  return got ? static_cast<int64_t>(x) : -1;
+}
+
 __device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7F80u) != 0x7F80u; }
 
 template <int N>
@@ -196,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = q_full + 4;             // [2]
   uint64_t* p_full = q_full + 6;             // [2] P written, O rescaled
   uint64_t* o_full = q_full + 8;             // [2] the unit's last P.V done
+  uint64_t* next_full = q_full + 14;         // the next CTA's index arrived
   uint64_t* cut_full = q_full + 12;          // [2] a cut tile's values landed (the keepers do not
                                              // follow the ring box by box)
   uint64_t* v_ok = q_full + 10;              // [2] a cut tile's values are clean (in turn: the
@@ -226,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&cut_full[i], 1);
       mbar_init(&v_ok[i], 64);
     }
+    mbar_init(next_full, 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -301,27 +333,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           box(&maps.v, 0, u.h, row, bar);
           box(&maps.v, 64, u.h, row, bar);
         };
-        for (int64_t x = blockIdx.x;; x += gridDim.x) {
+        int64_t x = blockIdx.x;
+        for (int asked = 0;; ++asked) {
+          // the next unit's index comes in while this one is loaded
+          if (x >= 0) next_cta_ask(smem + OFF_NEXT, next_full);
           Unit u;
-          const bool end = x >= p.units;
-          if (end) u.q_row = -1;
-          else if (!unit_at(p, x, u)) continue;
-          if (ok) ok = mbar_wait(&unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
-          if (!ok) break;
-          *unit_slot(i) = u;
-          mbar_arrive(&unit_full[i % kUnits]);
-          ++i;
-          if (end) break;
-          const int n = u.most();
-          if (n == 0) continue;
-          load_q(u, 0);
-          load_k(u, 0);
-          load_q(u, 1);
-          load_v(u, 0);
-          for (int j = 1; j < n && ok; ++j) {
-            load_k(u, j);
-            load_v(u, j);
+          if (x < 0) u.q_row = -1;
+          // after a wait that gave up, the CTAs left are taken over and dropped
+          if (ok && (x < 0 || unit_at(p, x, u))) {
+            ok = mbar_wait(&unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
+            if (ok) {
+              *unit_slot(i) = u;
+              mbar_arrive(&unit_full[i % kUnits]);
+              ++i;
+              const int n = x < 0 ? 0 : u.most();
+              if (n > 0) {
+                load_q(u, 0);
+                load_k(u, 0);
+                load_q(u, 1);
+                load_v(u, 0);
+              }
+              for (int j = 1; j < n && ok; ++j) {
+                load_k(u, j);
+                load_v(u, j);
+              }
+            }
           }
+          if (x < 0 || !mbar_wait(next_full, asked & 1)) break;
+          x = next_cta_answer(smem + OFF_NEXT);
+          fence_proxy_async_smem();  // read before the next answer is written
         }
       }
     } else if (warp == 9) {
@@ -698,17 +738,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const P
 
 }  // namespace
 
-cudaError_t launch_prefill(const PrefillParams& p_in, const PrefillMaps& maps, int sm_count,
+cudaError_t launch_prefill(const PrefillParams& p_in, const PrefillMaps& maps,
                            cudaStream_t stream) {
   PrefillParams p = p_in;
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e = set_smem_attr_once(prefill_kernel, kSmem, attr_done);
   if (e != cudaSuccess) return e;
   p.slots = p.num_tokens / kUnitRows + p.num_seqs;
-  p.head_group = p.heads < 8 ? p.heads : 8;
+  // heads side by side in the order of units: as many as keep their keys and
+  // values (512 bytes a key and head) in half of L2, at least eight
+  const int64_t fit = (int64_t{64} << 20) / (512 * static_cast<int64_t>(p.num_kv > 0 ? p.num_kv : 1));
+  p.head_group = static_cast<int>(fit < 8 ? 8 : fit > p.heads ? p.heads : fit);
+  if (p.head_group > p.heads) p.head_group = p.heads;
   const int groups = (p.heads + p.head_group - 1) / p.head_group;
-  p.units = static_cast<int64_t>(groups) * p.slots * p.head_group * p.num_splits;
-  const int grid = p.units < sm_count ? static_cast<int>(p.units) : sm_count;
+  const int64_t units = static_cast<int64_t>(groups) * p.slots * p.head_group * p.num_splits;
+  if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int grid = static_cast<int>(units);
   e = launch_overlapped(prefill_kernel, dim3(grid), dim3(kThreads), kSmem, stream, p, maps);
   if (e != cudaSuccess || p.num_splits == 1) return e;
   const int64_t records = static_cast<int64_t>(p.num_tokens) * p.heads;
