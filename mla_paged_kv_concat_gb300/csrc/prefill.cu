@@ -23,8 +23,13 @@
 //   TMEM (512 columns): S0, S1 (128 each; P as packed bf16 over the first 64
 //     of its S), O0, O1 (128 each).
 //   Shared memory: Q 2 x 48 KiB, a ring of eight 16 KiB boxes (64 dims x 128
-//     keys) in the order K K K V V of each key tile: the box is what is filled
-//     and freed, so loads run ahead as far as the ring allows.
+//     keys) in the order K K K V V of each key tile, K and V filled and freed
+//     as one group each.
+// The MMA warp's own instructions must stay under the tensor core's time: a
+// barrier that is already complete costs it about 100 cycles, so it waits
+// once per group (not per box, nor again for the second query tile) and
+// issues one tile's P.V and next Q.K from one elected block (waits, votes and
+// commits per box: 2500 cycles a step, the tensor core 50 % busy).
 //
 // Roles: warps 0-3 and 4-7 the softmax of query tiles 0 and 1 (thread = TMEM
 // lane = query row), warp 8 TMA producer and unit scheduler, warp 9 MMA
@@ -38,6 +43,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "ptx.cuh"
 #include "tc.cuh"
@@ -50,7 +57,8 @@ constexpr int kDv = 128;               // value dims
 constexpr int kTile = 128;             // query rows of a tile, keys of a tile
 constexpr int kUnitRows = 2 * kTile;
 constexpr int kBox = 16384;            // 64 dims x 128 rows of bf16
-constexpr int kRing = 8;
+constexpr int kRing = 8;               // boxes
+constexpr int kGroups = 4;             // more than fit: 3 + 2 + 3 + 2 boxes
 constexpr int kUnits = 4;              // unit descriptions in flight
 constexpr int kThreads = 384;
 constexpr int OFF_Q = 0;
@@ -58,7 +66,7 @@ constexpr int OFF_RING = OFF_Q + 6 * kBox;
 constexpr int OFF_UNIT = OFF_RING + kRing * kBox;
 constexpr int OFF_FLAG = OFF_UNIT + kUnits * 64;
 constexpr int OFF_BAR = OFF_FLAG + kUnits * 64;
-constexpr int kBars = 2 * kRing + 2 * kUnits + 15;
+constexpr int kBars = 2 * kGroups + 2 * kUnits + 15;
 constexpr int OFF_NEXT = (OFF_BAR + kBars * 8 + 15) & ~15;
 constexpr int OFF_TMEM = OFF_NEXT + 16;
 constexpr int kSmem = OFF_TMEM + 16 + 1024;
@@ -217,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-  uint64_t* full = bars;                     // [kRing] box landed
-  uint64_t* empty = full + kRing;            // [kRing] box read by its last product
-  uint64_t* unit_full = empty + kRing;       // [kUnits]
+  uint64_t* full = bars;                     // [kGroups] K or V of a tile landed
+  uint64_t* empty = full + kGroups;          // [kGroups] read by its last product
+  uint64_t* unit_full = empty + kGroups;     // [kUnits]
   uint64_t* unit_empty = unit_full + kUnits; // [kUnits] 11 reading warps
   uint64_t* q_full = unit_empty + kUnits;    // [2]
   uint64_t* q_empty = q_full + 2;            // [2]
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRing; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -290,18 +298,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
-        int i = 0, pos = 0, cut = 0, qn[2] = {0, 0};
-        auto box = [&](const CUtensorMap* m, int c, int h, int row, uint64_t* bar) {
-          const int s = pos % kRing;
-          if (ok) ok = mbar_wait(&empty[s], ((pos / kRing) & 1) ^ 1);
-          if (!ok) return;
-          if (bar) {
-            mbar_arrive(&full[s]);  // keeps the ring's count; v_ok follows
-          } else {
-            bar = &full[s];
-            mbar_arrive_expect_tx(bar, kBox);
+        int i = 0, cut = 0, qn[2] = {0, 0};
+        int grp = 0, pos = 0;    // groups (K and V in turn) and boxes issued
+        int fgrp = 0, fpos = 0;  // and known to be free again
+        // Room in the ring for the next group of `len` boxes.
+        auto reserve = [&](int len) {
+          while (ok && pos + len - fpos > kRing) {
+            ok = mbar_wait(&empty[fgrp % kGroups], (fgrp / kGroups) & 1);
+            fpos += fgrp & 1 ? 2 : 3;
+            ++fgrp;
           }
-          tma_load_3d(smem + OFF_RING + s * kBox, m, bar, c, h, row);
+        };
+        auto box = [&](const CUtensorMap* m, int c, int h, int row, uint64_t* bar) {
+          tma_load_3d(smem + OFF_RING + (pos % kRing) * kBox, m, bar, c, h, row);
           ++pos;
         };
         auto load_q = [&](const Unit& u, int t) {
@@ -317,19 +326,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(dst + 2 * kBox, &maps.q_pe, &q_full[t], 0, u.h, row);
         };
         auto load_k = [&](const Unit& u, int j) {
+          reserve(3);
+          if (!ok) return;
           const int row = u.k_row + u.ks + j * kTile;
-          box(&maps.k, 0, u.h, row, nullptr);
-          box(&maps.k, 64, u.h, row, nullptr);
-          box(&maps.k_pe, 0, 0, row, nullptr);
+          uint64_t* bar = &full[grp++ % kGroups];
+          mbar_arrive_expect_tx(bar, 3 * kBox);
+          box(&maps.k, 0, u.h, row, bar);
+          box(&maps.k, 64, u.h, row, bar);
+          box(&maps.k_pe, 0, 0, row, bar);
         };
         auto load_v = [&](const Unit& u, int j) {
+          reserve(2);
+          if (!ok) return;
           const int row = u.k_row + u.ks + j * kTile;
-          uint64_t* bar = nullptr;
+          uint64_t* bar = &full[grp++ % kGroups];
           if (j >= first_masked(u, 0, p.causal)) {
-            bar = &cut_full[cut & 1];
-            ++cut;
-            if (ok) mbar_arrive_expect_tx(bar, 2 * kBox);
+            mbar_arrive(bar);  // keeps the groups' count; v_ok follows
+            bar = &cut_full[cut++ & 1];
           }
+          mbar_arrive_expect_tx(bar, 2 * kBox);
           box(&maps.v, 0, u.h, row, bar);
           box(&maps.v, 64, u.h, row, bar);
         };
@@ -369,92 +384,116 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id128 = tc::idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t idPV = tc::idesc_bf16(128, 128, 0, 1);
       constexpr uint32_t idPVh = tc::idesc_bf16(128, 64, 0, 1);
-      const uint32_t q_base = smem_u32(smem + OFF_Q), ring = smem_u32(smem + OFF_RING);
-      int pos = 0;                // first box of the unit in the ring's count
-      int qn[2] = {0, 0}, pn[2] = {0, 0}, vn = 0;
+      const uint64_t q_desc = tc::smem_desc(smem_u32(smem + OFF_Q), 16, 1024, tc::kLayoutSw128);
+      const uint64_t k_desc = tc::smem_desc(smem_u32(smem + OFF_RING), 16, 1024, tc::kLayoutSw128);
+      // V is MN-major: the next 64 dims are one box on, 16 keys 2 KiB
+      const uint64_t v_desc = tc::smem_desc(smem_u32(smem + OFF_RING), kBox, 1024, tc::kLayoutSw128);
+      constexpr uint64_t kBoxStep = kBox >> 4;  // a box, in a descriptor's address field
+      int grp = 0, pos = 0;       // first group and box of the unit
+      int qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0, vn = 0;
+      // S_t = Q_t K^T, the tile's first box at ring position `b`
+      auto issue_qk = [&](auto tc_, int b) {
+        constexpr int t = decltype(tc_)::value;
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          const uint64_t db = k_desc + static_cast<uint64_t>((b + c) % kRing) * kBoxStep;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_ss(tmem + t * 128, q_desc + (t * 3 + c) * kBoxStep + static_cast<uint64_t>(k * 2),
+                       db + static_cast<uint64_t>(k * 2), id128, (c > 0 || k > 0) ? 1u : 0u);
+        }
+      };
+      // O_t (+)= P_t V
+      auto issue_pv = [&](auto tc_, int b, uint32_t acc) {
+        constexpr int t = decltype(tc_)::value;
+        const uint32_t o = tmem + O_COL + t * 128, a = tmem + t * 128;
+        const uint64_t d0 = v_desc + static_cast<uint64_t>(b % kRing) * kBoxStep;
+        if (b % kRing != kRing - 1) {
+          tc::mma_ts(o, a, d0, idPV, acc);
+#pragma unroll
+          for (int k = 1; k < 8; ++k)
+            tc::mma_ts(o, a + k * 8, d0 + static_cast<uint64_t>(k * 128), idPV, 1u);
+        } else {  // the two boxes lie at the ring's two ends
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc::mma_ts(o, a + k * 8, d0 + static_cast<uint64_t>(k * 128), idPVh, k > 0 ? 1u : acc);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc::mma_ts(o + 64, a + k * 8, v_desc + static_cast<uint64_t>(k * 128), idPVh,
+                       k > 0 ? 1u : acc);
+        }
+      };
       ok = for_each_unit([&](const Unit& u, int) -> bool {
         const int n = u.most();
         if (n == 0) return true;
         const int im = first_masked(u, 0, p.causal);
-        // S_t = Q_t K_j^T; `free_k`: the last product to read these boxes
-        auto qk = [&](int t, int j, bool free_k) -> bool {
-          if (j == 0) {
-            if (!warp_wait(&q_full[t], qn[t] & 1)) return false;
-            ++qn[t];
-          }
-#pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const int b = pos + 5 * j + c, s = b % kRing;
-            if (!warp_wait(&full[s], (b / kRing) & 1)) return false;
-            tc::fence_after_sync();
-            if (tc::elect_one()) {
-              const uint64_t da =
-                  tc::smem_desc(q_base + (t * 3 + c) * kBox, 16, 1024, tc::kLayoutSw128);
-              const uint64_t db = tc::smem_desc(ring + s * kBox, 16, 1024, tc::kLayoutSw128);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tc::mma_ss(tmem + t * 128, da + static_cast<uint64_t>(k * 2),
-                           db + static_cast<uint64_t>(k * 2), id128, (c > 0 || k > 0) ? 1u : 0u);
-              if (free_k) tc::commit(&empty[s]);
-              if (c == 2) {
-                tc::commit(&s_full[t]);
-                if (j == u.n(t) - 1) tc::commit(&q_empty[t]);
-              }
-            }
-            __syncwarp();
-          }
-          return true;
+        // whether query tile t is the first / the last to read key tile j
+        auto first = [&](int t, int j) { return t == 0 ? j < u.n0 : j >= u.n0; };
+        auto last = [&](int t, int j) { return t == 1 ? j < u.n1 : j >= u.n1; };
+        auto k_wait = [&](int j) {
+          const int g = grp + 2 * j;
+          return mbar_wait(&full[g % kGroups], (g / kGroups) & 1);
         };
-        // O_t (+)= P_t V_j
-        auto pv = [&](int t, int j, bool free_v) -> bool {
-          const int b = pos + 5 * j + 3, s0 = b % kRing, s1 = (b + 1) % kRing;
-          if (!warp_wait(&p_full[t], pn[t] & 1)) return false;
-          ++pn[t];
-          if (!warp_wait(&full[s0], (b / kRing) & 1) ||
-              !warp_wait(&full[s1], ((b + 1) / kRing) & 1))
-            return false;
+        // after Q.K of key tile j is issued
+        auto qk_commits = [&](int t, int j) {
+          if (last(t, j)) tc::commit(&empty[(grp + 2 * j) % kGroups]);
+          tc::commit(&s_full[t]);
+          if (j == u.n(t) - 1) tc::commit(&q_empty[t]);
+        };
+        auto start = [&](auto tc_, int& qn) -> bool {
+          constexpr int t = decltype(tc_)::value;
+          bool r = mbar_wait(&q_full[t], qn & 1);
+          ++qn;
+          if (first(t, 0)) r = k_wait(0) && r;
+          if (!__all_sync(0xffffffffu, r)) return false;
           tc::fence_after_sync();
           if (tc::elect_one()) {
-            const uint32_t o = tmem + O_COL + t * 128, a = tmem + t * 128;
-            const uint32_t acc = j > 0 ? 1u : 0u;
-            const uint64_t d0 = tc::smem_desc(ring + s0 * kBox, kBox, 1024, tc::kLayoutSw128);
-            if (s1 == s0 + 1) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                tc::mma_ts(o, a + k * 8, d0 + static_cast<uint64_t>(k * 128), idPV,
-                           k > 0 ? 1u : acc);
-            } else {  // the two boxes lie at the ring's two ends
-              const uint64_t d1 = tc::smem_desc(ring + s1 * kBox, kBox, 1024, tc::kLayoutSw128);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                tc::mma_ts(o, a + k * 8, d0 + static_cast<uint64_t>(k * 128), idPVh,
-                           k > 0 ? 1u : acc);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                tc::mma_ts(o + 64, a + k * 8, d1 + static_cast<uint64_t>(k * 128), idPVh,
-                           k > 0 ? 1u : acc);
-            }
-            if (free_v) {
-              tc::commit(&empty[s0]);
-              tc::commit(&empty[s1]);
-            }
-            if (j == u.n(t) - 1) tc::commit(&o_full[t]);
+            issue_qk(tc_, pos);
+            qk_commits(t, 0);
           }
           __syncwarp();
           return true;
         };
-        if (u.n0 > 0 && !qk(0, 0, u.n1 == 0)) return false;
-        if (u.n1 > 0 && !qk(1, 0, true)) return false;
-        for (int j = 0; j < n; ++j) {
-          if (j >= im) {
-            if (!warp_wait(&v_ok[vn & 1], (vn >> 1) & 1)) return false;
-            ++vn;
+        // P.V of key tile j, then Q.K of the next one
+        auto step = [&](auto tc_, int j, int& pn) -> bool {
+          constexpr int t = decltype(tc_)::value;
+          const bool more = j + 1 < u.n(t);
+          bool r = true;
+          if (first(t, j)) {
+            const int g = grp + 2 * j + 1;
+            r = mbar_wait(&full[g % kGroups], (g / kGroups) & 1);
+            if (j >= im) {
+              r = mbar_wait(&v_ok[vn & 1], (vn >> 1) & 1) && r;
+              ++vn;
+            }
           }
-          if (j < u.n0 && !pv(0, j, j >= u.n1)) return false;
-          if (j + 1 < u.n0 && !qk(0, j + 1, j + 1 >= u.n1)) return false;
-          if (j < u.n1 && !pv(1, j, true)) return false;
-          if (j + 1 < u.n1 && !qk(1, j + 1, true)) return false;
+          if (more && first(t, j + 1)) r = k_wait(j + 1) && r;
+          r = mbar_wait(&p_full[t], pn & 1) && r;
+          ++pn;
+          if (!__all_sync(0xffffffffu, r)) return false;
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            issue_pv(tc_, pos + 5 * j + 3, j > 0 ? 1u : 0u);
+            if (last(t, j)) tc::commit(&empty[(grp + 2 * j + 1) % kGroups]);
+            if (more) {
+              issue_qk(tc_, pos + 5 * (j + 1));
+              qk_commits(t, j + 1);
+            } else {
+              tc::commit(&o_full[t]);
+            }
+          }
+          __syncwarp();
+          return true;
+        };
+        constexpr std::integral_constant<int, 0> t0{};
+        constexpr std::integral_constant<int, 1> t1{};
+        if (u.n0 > 0 && !start(t0, qn0)) return false;
+        if (u.n1 > 0 && !start(t1, qn1)) return false;
+        for (int j = 0; j < n; ++j) {
+          if (j < u.n0 && !step(t0, j, pn0)) return false;
+          if (j < u.n1 && !step(t1, j, pn1)) return false;
         }
+        grp += 2 * n;
         pos += 5 * n;
         return true;
       });
