@@ -25,25 +25,23 @@
 //   Shared memory: Q 2 x 48 KiB, a ring of eight 16 KiB boxes (64 dims x 128
 //     keys) in the order K K K V V of each key tile, K and V filled and freed
 //     as one group each.
-// The MMA warp's own instructions must stay under the tensor core's time: a
-// barrier that is already complete costs it about 100 cycles, so it waits
-// once per group (not per box, nor again for the second query tile) and
-// issues one tile's P.V and next Q.K from one elected block (waits, votes and
-// commits per box: 2500 cycles a step, the tensor core 50 % busy).
+// The tensor core is kept busy only if its instructions arrive in time: one
+// issuing warp spent ~2000 cycles on a step (P.V of a tile, then Q.K of its
+// next one: 20 instructions at 25-45 cycles, and ~100 for each wait, vote and
+// commit), so each query tile has an issuing warp of its own, which
+// waits once per K or V group and issues a step from one elected block.
 //
 // Roles: warps 0-3 and 4-7 the softmax of query tiles 0 and 1 (thread = TMEM
-// lane = query row), warp 8 TMA producer and unit scheduler, warp 9 MMA
-// issuer and TMEM owner, warps 10-11 value keepers.
+// lane = query row), warp 8 TMA producer and unit scheduler, warps 9 and 10
+// MMA issuers of query tiles 0 and 1, warp 11 value keeper.
 //
 // Masked keys.  Scores of masked keys are replaced by -inf, whatever K held.
 // V of a masked key would still meet a zero of P, and 0 * NaN is NaN: in the
-// tiles that a mask cuts, the keepers zero the rows past the sequence's end
-// and any value that is not finite, and note the keys these were found in;
+// tiles that a mask cuts, the keeper zeroes the rows past the sequence's end
+// and any value that is not finite, and notes the keys these were found in;
 // the epilogue adds them back for the rows that do attend to those keys.
 #include <cuda_bf16.h>
 #include <stdint.h>
-
-#include <type_traits>
 
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -235,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = q_full + 6;             // [2] P written, O rescaled
   uint64_t* o_full = q_full + 8;             // [2] the unit's last P.V done
   uint64_t* next_full = q_full + 14;         // the next CTA's index arrived
-  uint64_t* cut_full = q_full + 12;          // [2] a cut tile's values landed (the keepers do not
+  uint64_t* cut_full = q_full + 12;          // [2] a cut tile's values landed (the keeper does not
                                              // follow the ring box by box)
   uint64_t* v_ok = q_full + 10;              // [2] a cut tile's values are clean (in turn: the
                                              // ring holds two tiles' values)
@@ -248,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);  // both query tiles
     }
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&unit_full[i], 1);
@@ -263,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&cut_full[i], 1);
-      mbar_init(&v_ok[i], 64);
+      mbar_init(&v_ok[i], 32);
     }
     mbar_init(next_full, 1);
     fence_mbar_init();
@@ -345,8 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar = &cut_full[cut++ & 1];
           }
           mbar_arrive_expect_tx(bar, 2 * kBox);
-          box(&maps.v, 0, u.h, row, bar);
-          box(&maps.v, 64, u.h, row, bar);
+          // at the ring's two ends the second half comes first: the product
+          // then starts at slot 0 and finds the other half seven boxes on
+          const int c0 = pos % kRing == kRing - 1 ? 64 : 0;
+          box(&maps.v, c0, u.h, row, bar);
+          box(&maps.v, 64 - c0, u.h, row, bar);
         };
         int64_t x = blockIdx.x;
         for (int asked = 0;; ++asked) {
@@ -379,163 +380,140 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();  // read before the next answer is written
         }
       }
-    } else if (warp == 9) {
-      // -------------------------------------------------------- MMA issuer
-      constexpr uint32_t id128 = tc::idesc_bf16(128, 128, 0, 0);
-      constexpr uint32_t idPV = tc::idesc_bf16(128, 128, 0, 1);
-      constexpr uint32_t idPVh = tc::idesc_bf16(128, 64, 0, 1);
-      const uint64_t q_desc = tc::smem_desc(smem_u32(smem + OFF_Q), 16, 1024, tc::kLayoutSw128);
-      const uint64_t k_desc = tc::smem_desc(smem_u32(smem + OFF_RING), 16, 1024, tc::kLayoutSw128);
-      // V is MN-major: the next 64 dims are one box on, 16 keys 2 KiB
-      const uint64_t v_desc = tc::smem_desc(smem_u32(smem + OFF_RING), kBox, 1024, tc::kLayoutSw128);
+    } else if (warp < 11) {
+      // ------------------------------------------------------- MMA issuers
+      constexpr uint32_t id_qk = tc::idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t id_pv = tc::idesc_bf16(128, 128, 0, 1);
       constexpr uint64_t kBoxStep = kBox >> 4;  // a box, in a descriptor's address field
+      const int t = warp - 9;
+      const uint32_t s_tm = tmem + t * 128, o_tm = tmem + O_COL + t * 128;
+      const uint64_t q_desc =
+          tc::smem_desc(smem_u32(smem + OFF_Q + t * 3 * kBox), 16, 1024, tc::kLayoutSw128);
+      const uint32_t ring = smem_u32(smem + OFF_RING);
+      const uint64_t k_desc = tc::smem_desc(ring, 16, 1024, tc::kLayoutSw128);
+      // V is MN-major: the other 64 dims are one box on (at the ring's ends
+      // seven), 16 keys 2 KiB
+      const uint64_t v_desc = tc::smem_desc(ring, kBox, 1024, tc::kLayoutSw128);
+      const uint64_t v_desc_ends = tc::smem_desc(ring, (kRing - 1) * kBox, 1024, tc::kLayoutSw128);
       int grp = 0, pos = 0;       // first group and box of the unit
-      int qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0, vn = 0;
-      // S_t = Q_t K^T, the tile's first box at ring position `b`
-      auto issue_qk = [&](auto tc_, int b) {
-        constexpr int t = decltype(tc_)::value;
+      int qn = 0, pn = 0, vn = 0;
+      auto ready = [&](int g) { return mbar_try_wait(&full[g % kGroups], (g / kGroups) & 1); };
+      auto await = [&](int g) { return mbar_wait(&full[g % kGroups], (g / kGroups) & 1); };
+      // S = Q K^T, the tile's first box at ring position `b`
+      auto issue_qk = [&](int b) {
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
           const uint64_t db = k_desc + static_cast<uint64_t>((b + c) % kRing) * kBoxStep;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc::mma_ss(tmem + t * 128, q_desc + (t * 3 + c) * kBoxStep + static_cast<uint64_t>(k * 2),
-                       db + static_cast<uint64_t>(k * 2), id128, (c > 0 || k > 0) ? 1u : 0u);
-        }
-      };
-      // O_t (+)= P_t V
-      auto issue_pv = [&](auto tc_, int b, uint32_t acc) {
-        constexpr int t = decltype(tc_)::value;
-        const uint32_t o = tmem + O_COL + t * 128, a = tmem + t * 128;
-        const uint64_t d0 = v_desc + static_cast<uint64_t>(b % kRing) * kBoxStep;
-        if (b % kRing != kRing - 1) {
-          tc::mma_ts(o, a, d0, idPV, acc);
-#pragma unroll
-          for (int k = 1; k < 8; ++k)
-            tc::mma_ts(o, a + k * 8, d0 + static_cast<uint64_t>(k * 128), idPV, 1u);
-        } else {  // the two boxes lie at the ring's two ends
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc::mma_ts(o, a + k * 8, d0 + static_cast<uint64_t>(k * 128), idPVh, k > 0 ? 1u : acc);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc::mma_ts(o + 64, a + k * 8, v_desc + static_cast<uint64_t>(k * 128), idPVh,
-                       k > 0 ? 1u : acc);
+            tc::mma_ss(s_tm, q_desc + c * kBoxStep + static_cast<uint64_t>(k * 2),
+                       db + static_cast<uint64_t>(k * 2), id_qk, (c > 0 || k > 0) ? 1u : 0u);
         }
       };
       ok = for_each_unit([&](const Unit& u, int) -> bool {
-        const int n = u.most();
+        const int n = u.most(), nt = u.n(t);
         if (n == 0) return true;
         const int im = first_masked(u, 0, p.causal);
-        // whether query tile t is the first / the last to read key tile j
-        auto first = [&](int t, int j) { return t == 0 ? j < u.n0 : j >= u.n0; };
-        auto last = [&](int t, int j) { return t == 1 ? j < u.n1 : j >= u.n1; };
-        auto k_wait = [&](int j) {
-          const int g = grp + 2 * j;
-          return mbar_wait(&full[g % kGroups], (g / kGroups) & 1);
-        };
-        // after Q.K of key tile j is issued
-        auto qk_commits = [&](int t, int j) {
-          if (last(t, j)) tc::commit(&empty[(grp + 2 * j) % kGroups]);
-          tc::commit(&s_full[t]);
-          if (j == u.n(t) - 1) tc::commit(&q_empty[t]);
-        };
-        auto start = [&](auto tc_, int& qn) -> bool {
-          constexpr int t = decltype(tc_)::value;
+        if (nt > 0) {
           bool r = mbar_wait(&q_full[t], qn & 1);
           ++qn;
-          if (first(t, 0)) r = k_wait(0) && r;
+          r = await(grp) && r;
           if (!__all_sync(0xffffffffu, r)) return false;
           tc::fence_after_sync();
           if (tc::elect_one()) {
-            issue_qk(tc_, pos);
-            qk_commits(t, 0);
+            issue_qk(pos);
+            tc::commit(&s_full[t]);
+            tc::commit(&empty[grp % kGroups]);
+            if (nt == 1) tc::commit(&q_empty[t]);
           }
           __syncwarp();
-          return true;
-        };
-        // P.V of key tile j, then Q.K of the next one
-        auto step = [&](auto tc_, int j, int& pn) -> bool {
-          constexpr int t = decltype(tc_)::value;
-          const bool more = j + 1 < u.n(t);
-          bool r = true;
-          if (first(t, j)) {
-            const int g = grp + 2 * j + 1;
-            r = mbar_wait(&full[g % kGroups], (g / kGroups) & 1);
-            if (j >= im) {
-              r = mbar_wait(&v_ok[vn & 1], (vn >> 1) & 1) && r;
-              ++vn;
-            }
+        }
+        // O (+)= P V of key tile j, then S of the next one
+        for (int j = 0; j < nt; ++j, ++pn) {
+          const int gv = grp + 2 * j + 1, b = pos + 5 * j + 3;
+          const bool more = j + 1 < nt, cut = j >= im;
+          bool r = ready(gv);
+          if (more) r = ready(gv + 1) && r;
+          if (cut) r = mbar_try_wait(&v_ok[vn & 1], (vn >> 1) & 1) && r;
+          r = mbar_try_wait(&p_full[t], pn & 1) && r;
+          if (!__all_sync(0xffffffffu, r)) {
+            r = await(gv);
+            if (more) r = await(gv + 1) && r;
+            if (cut) r = mbar_wait(&v_ok[vn & 1], (vn >> 1) & 1) && r;
+            r = mbar_wait(&p_full[t], pn & 1) && r;
+            if (!__all_sync(0xffffffffu, r)) return false;
           }
-          if (more && first(t, j + 1)) r = k_wait(j + 1) && r;
-          r = mbar_wait(&p_full[t], pn & 1) && r;
-          ++pn;
-          if (!__all_sync(0xffffffffu, r)) return false;
+          if (cut) ++vn;
           tc::fence_after_sync();
           if (tc::elect_one()) {
-            issue_pv(tc_, pos + 5 * j + 3, j > 0 ? 1u : 0u);
-            if (last(t, j)) tc::commit(&empty[(grp + 2 * j + 1) % kGroups]);
+            const uint64_t dv =
+                b % kRing == kRing - 1 ? v_desc_ends : v_desc + (b % kRing) * kBoxStep;
+            tc::mma_ts(o_tm, s_tm, dv, id_pv, j > 0 ? 1u : 0u);
+#pragma unroll
+            for (int k = 1; k < 8; ++k)
+              tc::mma_ts(o_tm, s_tm + k * 8, dv + static_cast<uint64_t>(k * 128), id_pv, 1u);
+            tc::commit(&empty[gv % kGroups]);
             if (more) {
-              issue_qk(tc_, pos + 5 * (j + 1));
-              qk_commits(t, j + 1);
+              issue_qk(b + 2);
+              tc::commit(&s_full[t]);
+              tc::commit(&empty[(gv + 1) % kGroups]);
+              if (j + 2 == nt) tc::commit(&q_empty[t]);
             } else {
               tc::commit(&o_full[t]);
             }
           }
           __syncwarp();
-          return true;
-        };
-        constexpr std::integral_constant<int, 0> t0{};
-        constexpr std::integral_constant<int, 1> t1{};
-        if (u.n0 > 0 && !start(t0, qn0)) return false;
-        if (u.n1 > 0 && !start(t1, qn1)) return false;
-        for (int j = 0; j < n; ++j) {
-          if (j < u.n0 && !step(t0, j, pn0)) return false;
-          if (j < u.n1 && !step(t1, j, pn1)) return false;
+        }
+        // key tiles that only the other query tile reads
+        for (int g = grp + 2 * nt; g < grp + 2 * n; ++g) {
+          if (g & 1 && (g - grp) / 2 >= im) ++vn;
+          if (!__all_sync(0xffffffffu, await(g))) return false;
+          if (lane == 0) mbar_arrive(&empty[g % kGroups]);
         }
         grp += 2 * n;
         pos += 5 * n;
         return true;
       });
     } else {
-      // ----------------------------------------------------- value keepers
-      const int row0 = (warp - 10) * 64 + lane;
+      // ------------------------------------------------------ value keeper
       int pos = 0, vn = 0;
       ok = for_each_unit([&](const Unit& u, int i) -> bool {
-        const int n = u.most();
-        if (n == 0) return true;
-        for (int j = first_masked(u, 0, p.causal); j < n; ++j) {
+        const int n = u.most(), im = first_masked(u, 0, p.causal);
+        for (int j = im; j < n; ++j, ++vn) {
+          // the dims' halves may be swapped: it does not matter here
           const int b = pos + 5 * j + 3;
+          const uint8_t* box0 = smem + OFF_RING + (b % kRing) * kBox;
+          const uint8_t* box1 = smem + OFF_RING + ((b + 1) % kRing) * kBox;
           if (!warp_wait(&cut_full[vn & 1], (vn >> 1) & 1)) return false;
           const int valid = u.lk - (u.ks + j * kTile);  // keys of the sequence in this tile
-          uint32_t* fl = flags(i) + (j - first_masked(u, 0, p.causal)) * 4 + (warp - 10) * 2;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            const int r = row0 + half * 32;
-            __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
-            const __nv_bfloat162 zero = z;
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-              uint4* a = reinterpret_cast<uint4*>(smem + OFF_RING + ((b + (c >> 3)) % kRing) * kBox +
-                                                  sw128(r, c & 7));
-              if (r < valid) {
-                const uint4 x = *a;  // 0 * x stays 0 unless x is not finite
-                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, z);
-                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, z);
-                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, z);
-                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, z);
-              } else {
-                *a = make_uint4(0, 0, 0, 0);
+          for (int q = 0; q < 4; ++q) {
+            const int r = q * 32 + lane;
+            const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+            __nv_bfloat162 z[4] = {zero, zero, zero, zero};
+            if (r < valid) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                // 0 * x stays 0 unless x is not finite
+                const uint4 x = *reinterpret_cast<const uint4*>((c < 8 ? box0 : box1) + sw128(r, c & 7));
+                z[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, z[0]);
+                z[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, z[1]);
+                z[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, z[2]);
+                z[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, z[3]);
               }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                *reinterpret_cast<uint4*>(const_cast<uint8_t*>(c < 8 ? box0 : box1) +
+                                          sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
             }
-            const uint32_t zb = *reinterpret_cast<uint32_t*>(&z);
-            const bool bad = (zb & 0x7FFF7FFFu) != 0;
+            z[0] = __hadd2(__hadd2(z[0], z[1]), __hadd2(z[2], z[3]));
+            const bool bad = (*reinterpret_cast<uint32_t*>(&z[0]) & 0x7FFF7FFFu) != 0;
             if (bad) {
 #pragma unroll 1
               for (int c = 0; c < 64; ++c) {
                 uint32_t* a = reinterpret_cast<uint32_t*>(
-                    smem + OFF_RING + ((b + (c >> 5)) % kRing) * kBox + sw128(r, (c >> 2) & 7) +
-                    (c & 3) * 4);
+                    const_cast<uint8_t*>(c < 32 ? box0 : box1) + sw128(r, (c >> 2) & 7) + (c & 3) * 4);
                 uint32_t x = *a;
                 if (!finite_bf16(x)) x &= 0xFFFF0000u;
                 if (!finite_bf16(x >> 16)) x &= 0xFFFFu;
@@ -543,11 +521,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const uint32_t word = __ballot_sync(0xffffffffu, bad);
-            if (lane == 0) fl[half] = word;
+            if (lane == 0) flags(i)[(j - im) * 4 + q] = word;
           }
           fence_proxy_async_smem();
           mbar_arrive(&v_ok[vn & 1]);
-          ++vn;
         }
         pos += 5 * n;
         return true;
