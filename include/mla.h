@@ -515,7 +515,7 @@ void mla_plan_destroy(mla_decode_plan* plan);
  *
  *   req_ids         int32 [num_reqs], or NULL.  Different entries have
  *                   different rows (else the row's new pages are unspecified).
- *   num_reqs        0 .. 16384.
+ *   num_reqs        0 .. 8192.
  *   req_block_table int32 [num_table_rows][max_blocks_per_req] at row stride
  *                   req_block_table_stride (elements); max_blocks_per_req *
  *                   block_size <= 2^30.
@@ -523,7 +523,7 @@ void mla_plan_destroy(mla_decode_plan* plan);
  *   free_blocks     int32 [free_capacity], the stack, bottom first.
  *   free_count      int32 [1], its height (clamped to [0, free_capacity]).
  *   free_count_out  int32 [1]; may be free_count itself (costs one more small
- *                   launch when the batch is larger than one CTA).
+ *                   launch).
  *   block_table     int32 [num_reqs][>= max_blocks_per_req] at row stride
  *                   block_table_stride.
  *   positions, slot_mapping   int64 [num_tokens].

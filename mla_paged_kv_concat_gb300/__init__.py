@@ -457,8 +457,8 @@ def expand_kv(kv_c, w_kv_b, num_heads: int, *, k_nope=None, v=None, err_count=No
               stream=None):
     """Keys and values of latents ``kv_c`` [T, R]: (k_nope, v), bf16
     [T, H, 128] each; ``w_kv_b`` [H * 256, R] is the kv_b projection's weight
-    (per head 128 rows of W_UK, then 128 of W_UV).  Allocated as the two
-    halves of one [T, H, 256] buffer unless both are given."""
+    (per head 128 rows of W_UK, then 128 of W_UV).  Allocated unless both are
+    given (they may be the halves of one [T, H, 256] buffer)."""
     return _bind().expand_kv(kv_c, w_kv_b, num_heads, k_nope, v, err_count, stream)
 
 

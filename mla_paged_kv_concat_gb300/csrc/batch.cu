@@ -10,12 +10,16 @@
 // page * bs + (c + j) % bs.
 //
 // What bounds it: launch and memory latency for a decode step (a few KB),
-// the copy of the page ids for large batches.  So it is one launch with no
-// pass between its CTAs: every CTA forms the prefix sums of all requests
-// itself (12 bytes a request, from L2), then takes whole requests' table rows
-// and 256-token pieces of the slot map in turn.  A token's page is looked up
-// where it comes from (the request's old row or the stack), never where
-// another CTA writes it, so no order between CTAs matters.
+// for large batches the latency of the page ids' copy on top.  So it is one
+// launch with no pass between its CTAs: each forms the prefix sums of all
+// requests itself (12 bytes a request, from L2) and its warps then take units:
+// 1024 ids of a request's row (eight 16-byte loads of a lane in flight, or 16
+// of one id where a row is not aligned), or 32 token rows.  A token's page is
+// looked up where it comes from (the request's old row or the stack), never
+// where another warp writes it, so no order between units matters.  1000
+// requests of up to 65536 tokens in pages of 16 (17 MB moved): 7.4 us (a CTA
+// per row, with its own sums: 10-16; four CTAs of 64 registers on an SM, which
+// spill: 10.4); a decode step of 64 requests 3.7 us.
 #include <stdint.h>
 
 #include "kernels.cuh"
@@ -28,11 +32,19 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPiece = 1024;  // ids of a table row in one unit
 constexpr int kRelThreads = 512;
 constexpr int kRelCtas = 8;  // one portable cluster
 
-__device__ __forceinline__ int cdiv_pos(int a, int b) {  // a >= 0; no overflow near INT_MAX
-  return a / b + (a % b != 0);
+// a / block_size and its round-up for 0 <= a < 2^31, as a product with a
+// reciprocal (see page_reciprocal): a division by a variable took half of the
+// kernel's instructions.
+__device__ __forceinline__ int page_of(const BatchParams& p, int a) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(a)) * p.page_mul) >>
+                          p.page_shift);
+}
+__device__ __forceinline__ int pages_of(const BatchParams& p, int a) {
+  return a == 0 ? 0 : page_of(p, a - 1) + 1;
 }
 
 __device__ __forceinline__ int sat32(long long x) {
@@ -48,10 +60,8 @@ struct Req {
   bool bad;   // something was clamped
 };
 
-__device__ __forceinline__ Req load_req(const BatchParams& p, int b) {
+__device__ __forceinline__ Req make_req(const BatchParams& p, int q, int c, int id) {
   Req r;
-  const int q = p.query_lens ? __ldg(p.query_lens + b) : 0, c = __ldg(p.context_lens + b);
-  const int id = p.req_ids ? __ldg(p.req_ids + b) : b;
   r.row = id >= 0 && id < p.num_table_rows ? id : -1;
   r.n = q < 0 ? 0 : q;
   r.ctx = c < 0 ? 0 : (c > p.capacity ? p.capacity : c);
@@ -59,6 +69,31 @@ __device__ __forceinline__ Req load_req(const BatchParams& p, int b) {
   r.seq = s > p.capacity ? p.capacity : static_cast<int>(s);
   r.bad = q < 0 || r.ctx != c || s > p.capacity;
   return r;
+}
+
+__device__ __forceinline__ Req load_req(const BatchParams& p, int b) {
+  return make_req(p, p.query_lens ? __ldg(p.query_lens + b) : 0, __ldg(p.context_lens + b),
+                  p.req_ids ? __ldg(p.req_ids + b) : b);
+}
+
+// f(b, request) for four requests of [from, to) at b = first, first + step,
+// ..., all loads in flight before the first is used.
+template <typename F>
+__device__ __forceinline__ void four_reqs(const BatchParams& p, int first, int step, int to, F&& f) {
+  int q[4], c[4], id[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int b = first + k * step;
+    const bool in = b < to;
+    q[k] = in && p.query_lens ? __ldg(p.query_lens + b) : 0;
+    c[k] = in ? __ldg(p.context_lens + b) : 0;
+    id[k] = in && p.req_ids ? __ldg(p.req_ids + b) : b;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int b = first + k * step;
+    if (b < to) f(b, make_req(p, q[k], c[k], id[k]));
+  }
 }
 
 // Turns a[1..n] into inclusive sums with a[0] = 0 (64-bit sums, stored
@@ -127,102 +162,210 @@ __device__ __forceinline__ int pop_page(const BatchParams& p, int count, long lo
   return id >= 0 && id < p.num_blocks ? id : -1;
 }
 
-__global__ void __launch_bounds__(kThreads) batch_build_kernel(const BatchParams p) {
+__device__ __forceinline__ int new_pages(const BatchParams& p, const Req& r) {
+  return r.row < 0 ? 0 : pages_of(p, r.seq) - pages_of(p, r.ctx);
+}
+
+// Prefix sums over all requests in one pass, four neighbouring requests a
+// thread and 1024 a step: g(b, request), then f(b, tokens before, X before)
+// with X the new pages, or the lengths with kSeq.  Returns (all tokens, all X).
+template <bool kSeq, typename G, typename F>
+__device__ __forceinline__ longlong2 scan_reqs(const BatchParams& p, long long (*part)[kWarps],
+                                               G&& g, F&& f) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  longlong2 total = make_longlong2(0, 0);
+  for (int base = 0; base < p.num_reqs; base += 4 * kThreads) {
+    const int b0 = base + 4 * tid;
+    int n[4] = {0, 0, 0, 0}, x[4] = {0, 0, 0, 0};
+    four_reqs(p, b0, 1, p.num_reqs, [&](int b, const Req& r) {
+      n[b - b0] = r.n;
+      x[b - b0] = kSeq ? r.seq : new_pages(p, r);
+      g(b, r);
+    });
+    long long own_n = 0, own_x = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      own_n += n[k];
+      own_x += x[k];
+    }
+    long long sn = own_n, sx = own_x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long un = __shfl_up_sync(0xffffffffu, sn, o);
+      const long long ux = __shfl_up_sync(0xffffffffu, sx, o);
+      if (lane >= o) {
+        sn += un;
+        sx += ux;
+      }
+    }
+    if (lane == 31) {
+      part[0][warp] = sn;
+      part[1][warp] = sx;
+    }
+    __syncthreads();
+    long long cn = total.x + sn - own_n, cx = total.y + sx - own_x;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const long long wn = part[0][w], wx = part[1][w];
+      if (w < warp) {
+        cn += wn;
+        cx += wx;
+      }
+      total.x += wn;
+      total.y += wx;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (b0 + k < p.num_reqs) {
+        f(b0 + k, cn, cx);
+        cn += n[k];
+        cx += x[k];
+      }
+    }
+    __syncthreads();  // part[] may be written again
+  }
+  return total;
+}
+
+// Sum over the block of one value per thread.
+__device__ long long block_sum(long long s, long long* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  __syncthreads();  // part[] may still be read from the last call
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += part[w];
+  return total;
+}
+
+__global__ void __launch_bounds__(kThreads, 3) batch_build_kernel(const BatchParams p) {
   extern __shared__ int sm[];
-  __shared__ long long part[kWarps];
+  __shared__ long long part[2][kWarps];
   griddep_wait();
   griddep_launch_dependents();
-  const int B = p.num_reqs, tid = threadIdx.x;
-  const bool first = blockIdx.x == 0;
-  int* cuq = sm;              // [B + 1] first token row of each request
-  int* off = sm + B + 1;      // [B + 1] new pages before each request
-  int* cuk = sm + 2 * (B + 1);  // [B + 1] cumulative lengths (CTA 0 only)
+  const int B = p.num_reqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int errs = 0;
-  for (int b = tid; b < B; b += kThreads) {
-    const Req r = load_req(p, b);
-    cuq[b + 1] = r.n;
-    off[b + 1] =
-        r.row < 0 ? 0 : cdiv_pos(r.seq, p.block_size) - cdiv_pos(r.ctx, p.block_size);
-    if (first) {
-      cuk[b + 1] = r.seq;
-      p.seq_lens[b] = r.seq;
-      errs += r.bad ? 1 : 0;
-    }
-  }
-  const int count = stack_count(p);
-  __syncthreads();
-  const long long total_q = block_scan<kThreads>(cuq, B, part);
-  const long long total_new = block_scan<kThreads>(off, B, part);
-  if (first) {
-    block_scan<kThreads>(cuk, B, part);
-    for (int b = tid; b <= B; b += kThreads) {
-      p.cu_q[b] = cuq[b];
-      p.cu_k[b] = cuk[b];
-    }
+  if (blockIdx.x == 0) {
+    // ---- lengths and their sums
+    const longlong2 total = scan_reqs<true>(
+        p, part,
+        [&](int b, const Req& r) {
+          p.seq_lens[b] = r.seq;
+          errs += r.bad ? 1 : 0;
+        },
+        [&](int b, long long n, long long seq) {
+          p.cu_q[b] = sat32(n);
+          p.cu_k[b] = sat32(seq);
+        });
     if (tid == 0) {
-      if (total_q > p.num_tokens) ++errs;
-      // with the same address for both counts another CTA may still have to
-      // read the old one: a launch of its own writes it then
-      if (!p.defer_count)
-        *p.free_count_out = total_new > count ? 0 : count - static_cast<int>(total_new);
+      p.cu_q[B] = sat32(total.x);
+      p.cu_k[B] = sat32(total.y);
+      if (total.x > p.num_tokens) ++errs;
     }
+    count_errors(p.err_count, errs);
+    return;
   }
-
-  // ---- table rows: old pages from the request's row, new ones off the stack
-  for (int b = blockIdx.x; b < B; b += gridDim.x) {
-    const Req r = load_req(p, b);
-    const int pages = cdiv_pos(r.seq, p.block_size);
-    const int old = r.row < 0 ? 0 : cdiv_pos(r.ctx, p.block_size);
-    int32_t* dst = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
-    int32_t* req = r.row < 0 ? nullptr : p.req_table + static_cast<int64_t>(r.row) * p.rt_stride;
-    int done = 0;
-    if (((reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(req)) & 15u) == 0) {
-      const int n4 = old >> 2;
-      for (int i = tid; i < n4; i += kThreads)
-        reinterpret_cast<int4*>(dst)[i] = reinterpret_cast<const int4*>(req)[i];
-      done = n4 << 2;
-    }
-    const long long k0 = off[b];
-    for (int i = done + tid; i < pages; i += kThreads) {
-      int id;
-      if (i < old) {
-        id = req[i];
+  int* cuq = sm;          // [B] first token row of each request
+  int* off = sm + B;      // [B] new pages before each request
+  int* ctx = sm + 2 * B;  // [B]
+  int* row = sm + 3 * B;  // [B]
+  const int count = stack_count(p);
+  const longlong2 total = scan_reqs<false>(
+      p, part,
+      [&](int b, const Req& r) {
+        ctx[b] = r.ctx;
+        row[b] = r.row;
+      },
+      [&](int b, long long n, long long pages) {
+        cuq[b] = sat32(n);
+        off[b] = sat32(pages);
+      });
+  // With the same address for both counts another CTA may still have to read
+  // the old one: a launch of its own writes it then.
+  if (blockIdx.x == 1 && tid == 0 && !p.defer_count)
+    *p.free_count_out = total.y > count ? 0 : count - static_cast<int>(total.y);
+  const int64_t warps = static_cast<int64_t>(gridDim.x - 1) * kWarps;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x - 1) * kWarps + warp; u < p.units; u += warps) {
+    if (u < p.row_units) {
+      // ---- a piece of a table row: old pages from the request's row, new
+      // ones off the stack
+      const int b = static_cast<int>(u / p.row_pieces);
+      const int i0 = static_cast<int>(u % p.row_pieces) * kPiece;
+      const long long n = (b + 1 < B ? cuq[b + 1] : total.x) - cuq[b];
+      const int c = ctx[b], rw = row[b];
+      const int seq = c + n > p.capacity ? p.capacity : static_cast<int>(c + n);
+      const int end = min(pages_of(p, seq), i0 + kPiece);
+      const int old_all = rw < 0 ? 0 : pages_of(p, c), old = min(old_all, end);
+      int32_t* dst = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
+      int32_t* req = rw < 0 ? nullptr : p.req_table + static_cast<int64_t>(rw) * p.rt_stride;
+      int done = min(i0, end);
+      if (((reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(req)) & 15u) == 0) {
+        const int n4 = old >> 2;
+        int4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if ((i0 >> 2) + lane + k * 32 < n4)
+            x[k] = reinterpret_cast<const int4*>(req)[(i0 >> 2) + lane + k * 32];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if ((i0 >> 2) + lane + k * 32 < n4)
+            reinterpret_cast<int4*>(dst)[(i0 >> 2) + lane + k * 32] = x[k];
+        done = max(done, n4 << 2);
       } else {
-        id = r.row < 0 ? -1 : pop_page(p, count, k0 + (i - old));
-        if (id < 0 && r.row >= 0) ++errs;
-        if (req) req[i] = id;
+#pragma unroll 1
+        for (; done < old; done += 512) {
+          int x[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (done + lane + k * 32 < old) x[k] = req[done + lane + k * 32];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (done + lane + k * 32 < old) dst[done + lane + k * 32] = x[k];
+        }
+        done = min(done, max(old, i0));
       }
-      dst[i] = id;
+      for (int i = done + lane; i < end; i += 32) {
+        int id;
+        if (i < old) {
+          id = req[i];
+        } else {
+          id = rw < 0 ? -1 : pop_page(p, count, static_cast<long long>(off[b]) + (i - old_all));
+          if (id < 0 && rw >= 0) ++errs;
+          if (req) req[i] = id;
+        }
+        dst[i] = id;
+      }
+    } else {
+      // ---- token rows
+      const int64_t t = (u - p.row_units) * 32 + lane;
+      if (t >= p.num_tokens) continue;
+      int64_t pos = 0, slot = -1;
+      if (t < total.x) {
+        int a = 0, z = B - 1;  // the last request whose first row is <= t
+        while (a < z) {
+          const int m = (a + z + 1) >> 1;
+          if (cuq[m] <= t) a = m; else z = m - 1;
+        }
+        const int c = ctx[a], rw = row[a];
+        pos = static_cast<int64_t>(c) + (t - cuq[a]);
+        if (rw >= 0 && pos < p.capacity) {
+          const int page = page_of(p, static_cast<int>(pos)), old = pages_of(p, c);
+          const int id = page < old
+                             ? p.req_table[static_cast<int64_t>(rw) * p.rt_stride + page]
+                             : pop_page(p, count, static_cast<long long>(off[a]) + (page - old));
+          if (id >= 0 && id < p.num_blocks)
+            slot = static_cast<int64_t>(id) * p.block_size +
+                   (static_cast<int>(pos) - page * p.block_size);
+        }
+        if (slot < 0) ++errs;
+      }
+      p.positions[t] = pos;
+      p.slot_mapping[t] = slot;
     }
   }
-
-  // ---- token rows
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + tid; t < p.num_tokens;
-       t += static_cast<int64_t>(gridDim.x) * kThreads) {
-    int64_t pos = 0, slot = -1;
-    if (t < total_q) {
-      int a = 0, z = B - 1;  // the last request whose first row is <= t
-      while (a < z) {
-        const int m = (a + z + 1) >> 1;
-        if (cuq[m] <= t) a = m; else z = m - 1;
-      }
-      const Req r = load_req(p, a);
-      pos = static_cast<int64_t>(r.ctx) + (t - cuq[a]);
-      if (r.row >= 0 && pos < r.seq) {
-        const int page = static_cast<int>(pos) / p.block_size;
-        const int old = cdiv_pos(r.ctx, p.block_size);
-        const int id =
-            page < old ? p.req_table[static_cast<int64_t>(r.row) * p.rt_stride + page]
-                       : pop_page(p, count, static_cast<long long>(off[a]) + (page - old));
-        if (id >= 0 && id < p.num_blocks)
-          slot = static_cast<int64_t>(id) * p.block_size +
-                 (static_cast<int>(pos) - page * p.block_size);
-      }
-      if (slot < 0) ++errs;
-    }
-    p.positions[t] = pos;
-    p.slot_mapping[t] = slot;
-  }
+  __syncwarp();
   count_errors(p.err_count, errs);
 }
 
@@ -232,17 +375,10 @@ __global__ void __launch_bounds__(kThreads) batch_count_kernel(const BatchParams
   griddep_wait();
   griddep_launch_dependents();
   long long s = 0;
-  for (int b = threadIdx.x; b < p.num_reqs; b += kThreads) {
-    const Req r = load_req(p, b);
-    if (r.row >= 0) s += cdiv_pos(r.seq, p.block_size) - cdiv_pos(r.ctx, p.block_size);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-  __syncthreads();
+  for (int i = threadIdx.x; i < p.num_reqs; i += 4 * kThreads)
+    four_reqs(p, i, kThreads, p.num_reqs, [&](int, const Req& r) { s += new_pages(p, r); });
+  const long long total = block_sum(s, part);
   if (threadIdx.x == 0) {
-    long long total = 0;
-    for (int w = 0; w < kWarps; ++w) total += part[w];
     const int count = *p.free_count_out;
     const int c = count < 0 ? 0 : (count > p.free_capacity ? p.free_capacity : count);
     *p.free_count_out = total > c ? 0 : c - static_cast<int>(total);
@@ -269,7 +405,7 @@ __global__ void __cluster_dims__(kRelCtas, 1, 1) __launch_bounds__(kRelThreads)
   int errs = 0;
   for (int b = tid; b < B; b += kRelThreads) {
     const Req r = load_req(p, b);
-    pre[b + 1] = r.row < 0 ? 0 : cdiv_pos(r.ctx, p.block_size);
+    pre[b + 1] = r.row < 0 ? 0 : pages_of(p, r.ctx);
     if (rank == 0 && (r.bad || r.row < 0)) ++errs;
   }
   if (tid == 0) valid_here = 0;
@@ -329,25 +465,40 @@ __global__ void __cluster_dims__(kRelCtas, 1, 1) __launch_bounds__(kRelThreads)
   count_errors(p.err_count, errs);
 }
 
+// With s = ceil(log2 d) and m = floor(2^(31+s) / d) + 1: m d = 2^(31+s) + e,
+// 0 < e <= d <= 2^s, so a m / 2^(31+s) exceeds a / d by less than 1 / d for
+// a < 2^31 and the floors are equal.
+void page_reciprocal(BatchParams* p) {
+  int s = 0;
+  while ((1 << s) < p->block_size) ++s;
+  p->page_shift = 31 + s;
+  p->page_mul = static_cast<uint32_t>((uint64_t{1} << (31 + s)) / p->block_size + 1);
+}
+
 }  // namespace
 
 cudaError_t launch_batch_build(const BatchParams& p_in, int sm_count, cudaStream_t stream) {
   BatchParams p = p_in;
+  page_reciprocal(&p);
   static std::atomic<uint64_t> attr_done{0};
-  cudaError_t e = set_smem_attr_once(batch_build_kernel, 3 * (kMaxBatchReqs + 1) * 4, attr_done);
+  cudaError_t e = set_smem_attr_once(batch_build_kernel, 4 * kMaxBatchReqs * 4, attr_done);
   if (e != cudaSuccess) return e;
-  const int pieces = p.num_tokens / kThreads + (p.num_tokens % kThreads != 0);
-  int grid = p.num_reqs > pieces ? p.num_reqs : pieces;
-  if (grid > 4 * sm_count) grid = 4 * sm_count;
-  if (grid < 1) grid = 1;
-  p.defer_count = p.free_count == p.free_count_out && grid > 1;
+  // max_blocks is capacity / block_size
+  p.row_pieces = (p.capacity / p.block_size + kPiece - 1) / kPiece;
+  p.row_units = static_cast<int64_t>(p.num_reqs) * p.row_pieces;
+  p.units = p.row_units + (static_cast<int64_t>(p.num_tokens) + 31) / 32;
+  const int64_t ctas = (p.units + kWarps - 1) / kWarps, most = 3 * sm_count - 1;
+  const int grid = 1 + static_cast<int>(ctas < 1 ? 1 : ctas < most ? ctas : most);
+  p.defer_count = p.free_count == p.free_count_out;
   e = launch_overlapped(batch_build_kernel, dim3(grid), dim3(kThreads),
-                        3 * (static_cast<size_t>(p.num_reqs) + 1) * 4, stream, p);
+                        4 * static_cast<size_t>(p.num_reqs) * 4, stream, p);
   if (e != cudaSuccess || !p.defer_count) return e;
   return launch_overlapped(batch_count_kernel, dim3(1), dim3(kThreads), 0, stream, p);
 }
 
-cudaError_t launch_blocks_release(const BatchParams& p, cudaStream_t stream) {
+cudaError_t launch_blocks_release(const BatchParams& p_in, cudaStream_t stream) {
+  BatchParams p = p_in;
+  page_reciprocal(&p);
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e = set_smem_attr_once(blocks_release_kernel, (kMaxBatchReqs + 1) * 4, attr_done);
   if (e != cudaSuccess) return e;

@@ -383,9 +383,8 @@ PyObject* expand_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t T = x.size(0);
     check(k.defined() == v.defined(), "give both k_nope and v, or neither");
     if (!k.defined()) {
-      const Tensor kv = c.empty({T, H, kNope + kV}, kBf16);
-      k = kv.slice(2, 0, kNope);
-      v = kv.slice(2, kNope);
+      k = c.empty({T, H, kNope}, kBf16);
+      v = c.empty({T, H, kV}, kBf16);
     }
     typed(k, kBf16, {T, H, kNope}, "k_nope");
     typed(v, kBf16, {T, H, kV}, "v");

@@ -164,7 +164,7 @@ cudaError_t launch_lse_merge(const void* o_parts, int64_t o_part_stride, const f
 // ---------------------------------------------------------------- prompts
 // Largest number of requests mla_batch_build and mla_blocks_release take
 // (their prefix sums live in shared memory).
-constexpr int kMaxBatchReqs = 16384;
+constexpr int kMaxBatchReqs = 8192;
 
 // Arguments of the batch tables after host validation (device pointers).
 struct BatchParams {
@@ -183,6 +183,10 @@ struct BatchParams {
   const int32_t* free_count;
   int32_t* free_count_out;
   bool defer_count;             // set by the launch
+  int row_pieces;               // units of a table row; set by the launch, as what follows
+  int64_t row_units, units;
+  uint32_t page_mul;            // x / block_size = x * page_mul >> page_shift
+  int page_shift;
   int num_tokens;
   int32_t* block_table;
   int64_t bt_stride;
