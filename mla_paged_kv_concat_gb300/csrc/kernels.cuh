@@ -226,17 +226,20 @@ struct ProjParams {
   int k;       // length of the sum: R (expand, project) or 128 (absorb)
   int cols;    // output columns of a head: 256, R or 128
   int bn;      // columns of a tile, from proj_tile_cols
+  bool pair;   // tiles of CTA pairs, from proj_pairs
   int w_row0;  // first of the head's 256 weight rows that the product reads
   int* err_count;
 };
 // a: {K, heads or 1, tokens}, box {64, 1, 128}.  b: the weight as
-// {R, 256, heads}, box {64, bn, 1}, or {64, 64, 1} for absorb.  c0, c1:
+// {R, 256, heads}, box {64, bn, 1}, or {64, 64, 1} for absorb, {64, 128, 1} for
+// pairs.  c0, c1:
 // {cols, heads, tokens}, box {64, 1, 32}; c1 is expand's v.  All 128-byte
 // swizzled bf16.
 struct ProjMaps {
   CUtensorMap a, b, c0, c1;
 };
 int proj_tile_cols(int tokens, int heads, int cols, int sm_count);
+bool proj_pairs(int mode, int tokens, int heads, int k, int sm_count);
 cudaError_t launch_latent_proj(const ProjParams& p, const ProjMaps& m, int mode, int sm_count,
                                cudaStream_t stream);
 
@@ -258,7 +261,8 @@ struct PrefillParams {
   // set by the launch
   int slots, head_group;
 };
-// {dims, heads (k_pe: 1), rows}, box {64, 1, 128}, 128-byte swizzled bf16.
+// {dims, heads (k_pe: 1), rows}, box {64, 1, 128} (v: {64, 1, 64}), 128-byte
+// swizzled bf16.
 struct PrefillMaps {
   CUtensorMap q, q_pe, k, k_pe, v;
 };

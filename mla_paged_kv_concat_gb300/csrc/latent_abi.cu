@@ -152,12 +152,13 @@ mla_status latent_proj(int mode, Heads in, int in_heads, int tokens, const void*
   p.cols = two ? nope + vdim : out0.cols;
   p.w_row0 = mode == mla::kProjProject ? nope : 0;
   p.bn = mla::proj_tile_cols(tokens, heads, p.cols, sms);
+  p.pair = mla::proj_pairs(mode, tokens, heads, p.k, sms);
   p.err_count = err_count;
   mla::ProjMaps m;
   mla_status st = heads_map(&m.a, in, tokens, in_heads, 128);
   if (st == MLA_OK)
     st = make_map(&m.b, w, R, nope + vdim, heads, w_stride, w_stride * (nope + vdim),
-                  mode == mla::kProjAbsorb ? 64 : p.bn, 1);
+                  p.pair ? 128 : mode == mla::kProjAbsorb ? 64 : p.bn, 1);
   if (st == MLA_OK) st = heads_map(&m.c0, out0, tokens, heads, 32);
   if (st == MLA_OK) st = heads_map(&m.c1, two ? out1 : out0, tokens, heads, 32);
   if (st != MLA_OK) return st;
@@ -448,7 +449,7 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
   if (num_kv_tokens > 0) {
     if (st == MLA_OK) st = heads_map(&m.k, hk, num_kv_tokens, num_heads, 128);
     if (st == MLA_OK) st = heads_map(&m.k_pe, hkp, num_kv_tokens, 1, 128);
-    if (st == MLA_OK) st = heads_map(&m.v, hv, num_kv_tokens, num_heads, 128);
+    if (st == MLA_OK) st = heads_map(&m.v, hv, num_kv_tokens, num_heads, 64);
   }
   if (st != MLA_OK) return st;
   cudaError_t e = mla::launch_prefill(p, m, static_cast<cudaStream_t>(stream));

@@ -61,6 +61,30 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       : "memory");
 }
 
+// One epilogue warp's 32 rows x 64 columns: fp32 registers (a row a lane) to
+// bf16 in the swizzled box `dst` and from there to the tensor, rows past its
+// end left out by the TMA (`some`: not all of them are).
+__device__ __forceinline__ void store_box(uint8_t* dst, const uint32_t (&r)[64], int lane, bool some,
+                                          const CUtensorMap* map, int c, int h, int row0) {
+  // the store that last used this box, the one before the last, has read it
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack_bf16x2(__uint_as_float(r[q * 8 + 2 * e]), __uint_as_float(r[q * 8 + 2 * e + 1]));
+    *reinterpret_cast<uint4*>(dst + sw128(lane, q)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (some) tma_store_3d(map, dst, c, h, row0);
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
 template <int MODE, int BN>
 __global__ void __launch_bounds__(192, 1)
     latent_proj_kernel(const ProjParams p, const __grid_constant__ CUtensorMap ma,
@@ -216,31 +240,10 @@ __global__ void __launch_bounds__(192, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&acc_empty[a]);
         }
-        uint8_t* dst = box + (nb & 1) * STORE_BYTES;
-        // the store that last used this box has read it
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(r[q * 8 + 2 * e]),
-                               __uint_as_float(r[q * 8 + 2 * e + 1]));
-          *reinterpret_cast<uint4*>(dst + sw128(lane, q)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (row0 < p.tokens) {
-            const int c = n * BN + j * 64;
-            if (MODE == kProjExpand && c >= 128)
-              tma_store_3d(&mc1, dst, c - 128, h, row0);
-            else
-              tma_store_3d(&mc0, dst, c, h, row0);
-          }
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+        const int c = n * BN + j * 64;
+        const bool second = MODE == kProjExpand && c >= 128;
+        store_box(box + (nb & 1) * STORE_BYTES, r, lane, row0 < p.tokens, second ? &mc1 : &mc0,
+                  second ? c - 128 : c, h, row0);
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -252,6 +255,186 @@ __global__ void __launch_bounds__(192, 1)
   if (warp == 5) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::COLS);
+  }
+}
+
+// ---------------------------------------------------------------- CTA pairs
+// expand with a long sum (R = 512) for many tokens, which the tensor core
+// bounds.  Two CTAs of a cluster share a tile of 256 tokens x 256 columns (one
+// head's W_UK | W_UV): each holds its 128 tokens of A and half of the columns
+// of B, and cta_group::2 products read both halves, so a CTA takes in 32 KiB
+// per 552 cycles of products instead of 48.  Rank 0 issues for both; the ring's
+// "landed" barrier is rank 0's and counts both CTAs' bytes; "read" and
+// "accumulator ready" arrive in both.  Eight epilogue warps, four per output.
+// 8192 tokens, 16 heads: 24.8 us (1386 TFLOP/s) against 27.6 for single CTAs;
+// with four epilogue warps no faster than those.  With R = 256 the writes bound
+// expand (256 flops a byte written: 1040 TFLOP/s at the 4.07 TB/s that a plain
+// fill of the same buffer reaches) and pairs, which drain together, lose:
+// 5001 tokens, 128 heads 100 us against 77.
+constexpr int kPairStages = 5;
+constexpr int kPairHalf = A_BYTES;  // A, and the half of B, of one stage
+constexpr int PP_STORE = kPairStages * 2 * kPairHalf;
+constexpr int PP_BAR = PP_STORE + 8 * 2 * STORE_BYTES;
+constexpr int PP_TMEM = PP_BAR + (2 * kPairStages + 4) * 8;
+constexpr int PP_SMEM = PP_TMEM + 16 + 1024;
+static_assert(PP_SMEM <= 227 * 1024, "shared memory");
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
+    expand_pair_kernel(const ProjParams p, const __grid_constant__ CUtensorMap ma,
+                       const __grid_constant__ CUtensorMap mb,
+                       const __grid_constant__ CUtensorMap mc0,
+                       const __grid_constant__ CUtensorMap mc1) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + PP_BAR);  // [stages] rank 0's: both landed
+  uint64_t* empty = full + kPairStages;                         // [stages]
+  uint64_t* acc_full = empty + kPairStages;                     // [2]
+  uint64_t* acc_empty = acc_full + 2;                           // [2] rank 0's: eight warps
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PP_TMEM);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_ctarank();
+
+  if (threadIdx.x == 128) {
+    tma_prefetch_desc(&ma);
+    tma_prefetch_desc(&mb);
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 16);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tc::pair_tmem_alloc(tmem_slot, 512);
+    tc::pair_tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int nk = p.k / KC;
+  // heads fastest, then blocks of 256 tokens
+  const int64_t total = static_cast<int64_t>((p.tokens + 2 * TM - 1) / (2 * TM)) * p.heads;
+  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int64_t t = first; t < total && ok; t += step) {
+        const int h = static_cast<int>(t % p.heads), m = static_cast<int>(t / p.heads);
+        for (int kc = 0; kc < nk; ++kc, ++it) {
+          const int st = it % kPairStages;
+          if (!mbar_wait(&empty[st], ((it / kPairStages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + st * 2 * kPairHalf;
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 4 * kPairHalf);
+          const uint32_t bar = tc::map_peer(smem_u32(&full[st]), 0);
+          tc::pair_tma_load_3d(dst, &ma, bar, kc * KC, 0, m * 2 * TM + rank * TM);
+          tc::pair_tma_load_3d(dst + kPairHalf, &mb, bar, kc * KC, rank * 128, h);
+        }
+      }
+      if (!ok && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+    }
+  } else if (warp == 5) {
+    bool ok = true;
+    int it = 0, ta = 0;
+    if (rank == 0) {
+      constexpr uint32_t idesc = tc::idesc_bf16(2 * TM, 256, 0, 0);
+      for (int64_t t = first; t < total && ok; t += step, ++ta) {
+        const int a = ta & 1;
+        const bool free = tc::mbar_wait_cluster(&acc_empty[a], ((ta >> 1) & 1) ^ 1);
+        if (!__all_sync(0xffffffffu, free)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        for (int kc = 0; kc < nk; ++kc, ++it) {
+          const int st = it % kPairStages;
+          if (!warp_wait(&full[st], (it / kPairStages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            const uint32_t base = smem_u32(smem + st * 2 * kPairHalf);
+            const uint64_t da = tc::smem_desc(base, 16, 1024, tc::kLayoutSw128);
+            const uint64_t db = tc::smem_desc(base + kPairHalf, 16, 1024, tc::kLayoutSw128);
+#pragma unroll
+            for (int k = 0; k < KC / 16; ++k)
+              tc::pair_mma_ss(tmem + a * 256, da + static_cast<uint64_t>(k * 2),
+                              db + static_cast<uint64_t>(k * 2), idesc,
+                              (kc > 0 || k > 0) ? 1u : 0u);
+            tc::pair_commit(&empty[st], 3);
+            if (kc == nk - 1) tc::pair_commit(&acc_full[a], 3);
+          }
+          __syncwarp();
+        }
+      }
+      for (int j = 0; ok && j < 2 && j < ta; ++j) {
+        const int u = ta - 1 - j;
+        warp_wait(&acc_full[u & 1], (u >> 1) & 1);
+      }
+      if (!ok && lane == 0 && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+    }
+  } else {
+    // warps 0-3 k_nope's columns, 6-9 v's; a warp reads the TMEM lanes of its
+    // quarter (warp % 4)
+    const int half = warp >= 6, ew = half ? warp - 2 : warp, qd = warp & 3;
+    uint8_t* box = smem + PP_STORE + ew * 2 * STORE_BYTES;
+    const uint32_t lanes = static_cast<uint32_t>(qd * 32) << 16;
+    int ta = 0, nb = 0;
+    bool ok = true;
+    for (int64_t t = first; t < total; t += step, ++ta) {
+      const int h = static_cast<int>(t % p.heads), m = static_cast<int>(t / p.heads);
+      const int a = ta & 1;
+      if (!warp_wait(&acc_full[a], (ta >> 1) & 1)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      const int row0 = m * 2 * TM + rank * TM + qd * STORE_ROWS;
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj, ++nb) {
+        const int j = half * 2 + jj;
+        uint32_t r[64];
+        tc::ld_32x32b_x32(tmem + lanes + a * 256 + j * 64,
+                          *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+        tc::ld_32x32b_x32(tmem + lanes + a * 256 + j * 64 + 32,
+                          *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+        tc::wait_ld();
+        tc::reg_fence(r);
+        if (jj == 1) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::arrive_peer(tc::map_peer(smem_u32(&acc_empty[a]), 0));
+        }
+        store_box(box + (nb & 1) * STORE_BYTES, r, lane, row0 < p.tokens, j < 2 ? &mc0 : &mc1,
+                  (j & 1) * 64, h, row0);
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (!ok && lane == 0 && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();  // the peer's barriers and operands are used to the end
+  if (warp == 5) {
+    tc::fence_after_sync();
+    tc::pair_tmem_dealloc(tmem, 512);
   }
 }
 
@@ -278,6 +461,14 @@ cudaError_t launch_mode(const ProjParams& p, const ProjMaps& m, int sm_count, cu
 
 }  // namespace
 
+// Pairs where the products bound the work and their tiles, twice as high,
+// still come several to an SM (R = 512: 1000 tokens, 128 heads 27.7 us against
+// 30.1; 300 tokens, 128 heads, 256 tiles, 15.1 against 13.8).
+bool proj_pairs(int mode, int tokens, int heads, int k, int sm_count) {
+  return mode == kProjExpand && k > 256 && tokens > TM &&
+         static_cast<int64_t>((tokens + 2 * TM - 1) / (2 * TM)) * heads >= 2 * sm_count;
+}
+
 int proj_tile_cols(int tokens, int heads, int cols, int sm_count) {
   const int64_t units = static_cast<int64_t>((tokens + TM - 1) / TM) * heads;
   int bn = cols < 256 ? cols : 256;
@@ -287,6 +478,15 @@ int proj_tile_cols(int tokens, int heads, int cols, int sm_count) {
 
 cudaError_t launch_latent_proj(const ProjParams& p, const ProjMaps& m, int mode, int sm_count,
                                cudaStream_t stream) {
+  if (p.pair) {
+    static std::atomic<uint64_t> attr_done{0};
+    cudaError_t e = set_smem_attr_once(expand_pair_kernel, PP_SMEM, attr_done);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = static_cast<int64_t>((p.tokens + 2 * TM - 1) / (2 * TM)) * p.heads;
+    const int pairs = tiles < sm_count / 2 ? static_cast<int>(tiles) : sm_count / 2;
+    return launch_overlapped(expand_pair_kernel, dim3(2 * pairs), dim3(320), PP_SMEM, stream, p, m.a,
+                             m.b, m.c0, m.c1);
+  }
   switch (mode) {
     case kProjExpand: return launch_mode<kProjExpand>(p, m, sm_count, stream);
     case kProjAbsorb: return launch_mode<kProjAbsorb>(p, m, sm_count, stream);

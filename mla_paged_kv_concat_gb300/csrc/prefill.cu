@@ -22,14 +22,17 @@
 // products and the tensor core is the bound.
 //   TMEM (512 columns): S0, S1 (128 each; P as packed bf16 over the first 64
 //     of its S), O0, O1 (128 each).
-//   Shared memory: Q 2 x 48 KiB, a ring of eight 16 KiB boxes (64 dims x 128
-//     keys) in the order K K K V V of each key tile, K and V filled and freed
-//     as one group each.
+//   Shared memory: Q 2 x 48 KiB, a ring of eight 16 KiB boxes in the order K
+//     K K (64 dims x 128 keys each) V V (128 dims x 64 keys each) of every key
+//     tile, filled and freed box by box in the order of their use: a box is
+//     asked for 1800 to 3000 cycles before its product (K and V waited for
+//     together, freed as groups: 770 cycles, less than a load takes).
 // The tensor core is kept busy only if its instructions arrive in time: one
 // issuing warp spent ~2000 cycles on a step (P.V of a tile, then Q.K of its
 // next one: 20 instructions at 25-45 cycles, and ~100 for each wait, vote and
-// commit), so each query tile has an issuing warp of its own, which
-// waits once per K or V group and issues a step from one elected block.
+// commit), so each query tile has an issuing warp of its own, with one vote
+// and one elected block for P.V and one for Q.K; the commits follow the
+// products (between them they cost 3 %).
 //
 // Roles: warps 0-3 and 4-7 the softmax of query tiles 0 and 1 (thread = TMEM
 // lane = query row), warp 8 TMA producer and unit scheduler, warps 9 and 10
@@ -56,7 +59,6 @@ constexpr int kTile = 128;             // query rows of a tile, keys of a tile
 constexpr int kUnitRows = 2 * kTile;
 constexpr int kBox = 16384;            // 64 dims x 128 rows of bf16
 constexpr int kRing = 8;               // boxes
-constexpr int kGroups = 4;             // more than fit: 3 + 2 + 3 + 2 boxes
 constexpr int kUnits = 4;              // unit descriptions in flight
 constexpr int kThreads = 384;
 constexpr int OFF_Q = 0;
@@ -64,7 +66,7 @@ constexpr int OFF_RING = OFF_Q + 6 * kBox;
 constexpr int OFF_UNIT = OFF_RING + kRing * kBox;
 constexpr int OFF_FLAG = OFF_UNIT + kUnits * 64;
 constexpr int OFF_BAR = OFF_FLAG + kUnits * 64;
-constexpr int kBars = 2 * kGroups + 2 * kUnits + 15;
+constexpr int kBars = 2 * kRing + 2 * kUnits + 15;
 constexpr int OFF_NEXT = (OFF_BAR + kBars * 8 + 15) & ~15;
 constexpr int OFF_TMEM = OFF_NEXT + 16;
 constexpr int kSmem = OFF_TMEM + 16 + 1024;
@@ -223,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-  uint64_t* full = bars;                     // [kGroups] K or V of a tile landed
-  uint64_t* empty = full + kGroups;          // [kGroups] read by its last product
-  uint64_t* unit_full = empty + kGroups;     // [kUnits]
+  uint64_t* full = bars;                     // [kRing] box landed
+  uint64_t* empty = full + kRing;            // [kRing] read by both query tiles
+  uint64_t* unit_full = empty + kRing;       // [kUnits]
   uint64_t* unit_empty = unit_full + kUnits; // [kUnits] 11 reading warps
   uint64_t* q_full = unit_empty + kUnits;    // [2]
   uint64_t* q_empty = q_full + 2;            // [2]
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kGroups; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 2);  // both query tiles
     }
@@ -296,20 +298,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
-        int i = 0, cut = 0, qn[2] = {0, 0};
-        int grp = 0, pos = 0;    // groups (K and V in turn) and boxes issued
-        int fgrp = 0, fpos = 0;  // and known to be free again
-        // Room in the ring for the next group of `len` boxes.
-        auto reserve = [&](int len) {
-          while (ok && pos + len - fpos > kRing) {
-            ok = mbar_wait(&empty[fgrp % kGroups], (fgrp / kGroups) & 1);
-            fpos += fgrp & 1 ? 2 : 3;
-            ++fgrp;
-          }
-        };
-        auto box = [&](const CUtensorMap* m, int c, int h, int row, uint64_t* bar) {
-          tma_load_3d(smem + OFF_RING + (pos % kRing) * kBox, m, bar, c, h, row);
+        int i = 0, cut = 0, pos = 0, qn[2] = {0, 0};
+        // The next box of the ring, once it is free.
+        auto slot = [&]() -> int {
+          const int b = pos % kRing;
+          if (ok) ok = mbar_wait(&empty[b], ((pos / kRing) & 1) ^ 1);
           ++pos;
+          return b;
         };
         auto load_q = [&](const Unit& u, int t) {
           if (u.n(t) == 0) return;
@@ -324,30 +319,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(dst + 2 * kBox, &maps.q_pe, &q_full[t], 0, u.h, row);
         };
         auto load_k = [&](const Unit& u, int j) {
-          reserve(3);
-          if (!ok) return;
           const int row = u.k_row + u.ks + j * kTile;
-          uint64_t* bar = &full[grp++ % kGroups];
-          mbar_arrive_expect_tx(bar, 3 * kBox);
-          box(&maps.k, 0, u.h, row, bar);
-          box(&maps.k, 64, u.h, row, bar);
-          box(&maps.k_pe, 0, 0, row, bar);
+          for (int c = 0; c < 3; ++c) {
+            const int b = slot();
+            if (!ok) return;
+            mbar_arrive_expect_tx(&full[b], kBox);
+            tma_load_3d(smem + OFF_RING + b * kBox, c < 2 ? &maps.k : &maps.k_pe, &full[b],
+                        c < 2 ? c * 64 : 0, c < 2 ? u.h : 0, row);
+          }
         };
         auto load_v = [&](const Unit& u, int j) {
-          reserve(2);
-          if (!ok) return;
           const int row = u.k_row + u.ks + j * kTile;
-          uint64_t* bar = &full[grp++ % kGroups];
-          if (j >= first_masked(u, 0, p.causal)) {
-            mbar_arrive(bar);  // keeps the groups' count; v_ok follows
-            bar = &cut_full[cut++ & 1];
+          uint64_t* cut_bar = nullptr;
+          if (j >= first_masked(u, 0, p.causal)) cut_bar = &cut_full[cut++ & 1];
+          for (int c = 0; c < 2; ++c) {
+            const int b = slot();
+            if (!ok) return;
+            uint64_t* bar = &full[b];
+            if (cut_bar) {
+              mbar_arrive(bar);  // keeps the ring's count; v_ok follows
+              bar = cut_bar;
+              if (c == 0) mbar_arrive_expect_tx(bar, 2 * kBox);
+            } else {
+              mbar_arrive_expect_tx(bar, kBox);
+            }
+            uint8_t* dst = smem + OFF_RING + b * kBox;
+            tma_load_3d(dst, &maps.v, bar, 0, u.h, row + c * 64);
+            tma_load_3d(dst + kBox / 2, &maps.v, bar, 64, u.h, row + c * 64);
           }
-          mbar_arrive_expect_tx(bar, 2 * kBox);
-          // at the ring's two ends the second half comes first: the product
-          // then starts at slot 0 and finds the other half seven boxes on
-          const int c0 = pos % kRing == kRing - 1 ? 64 : 0;
-          box(&maps.v, c0, u.h, row, bar);
-          box(&maps.v, 64 - c0, u.h, row, bar);
         };
         int64_t x = blockIdx.x;
         for (int asked = 0;; ++asked) {
@@ -391,54 +390,61 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::smem_desc(smem_u32(smem + OFF_Q + t * 3 * kBox), 16, 1024, tc::kLayoutSw128);
       const uint32_t ring = smem_u32(smem + OFF_RING);
       const uint64_t k_desc = tc::smem_desc(ring, 16, 1024, tc::kLayoutSw128);
-      // V is MN-major: the other 64 dims are one box on (at the ring's ends
-      // seven), 16 keys 2 KiB
-      const uint64_t v_desc = tc::smem_desc(ring, kBox, 1024, tc::kLayoutSw128);
-      const uint64_t v_desc_ends = tc::smem_desc(ring, (kRing - 1) * kBox, 1024, tc::kLayoutSw128);
-      int grp = 0, pos = 0;       // first group and box of the unit
+      // V is MN-major: the other 64 dims are half a box on, 16 keys 2 KiB
+      const uint64_t v_desc = tc::smem_desc(ring, kBox / 2, 1024, tc::kLayoutSw128);
+      int pos = 0;                // first box of the unit
       int qn = 0, pn = 0, vn = 0;
-      auto ready = [&](int g) { return mbar_try_wait(&full[g % kGroups], (g / kGroups) & 1); };
-      auto await = [&](int g) { return mbar_wait(&full[g % kGroups], (g / kGroups) & 1); };
+      auto ready = [&](int b) { return mbar_try_wait(&full[b % kRing], (b / kRing) & 1); };
+      auto await = [&](int b) { return mbar_wait(&full[b % kRing], (b / kRing) & 1); };
       // S = Q K^T, the tile's first box at ring position `b`
-      auto issue_qk = [&](int b) {
-#pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          const uint64_t db = k_desc + static_cast<uint64_t>((b + c) % kRing) * kBoxStep;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_ss(s_tm, q_desc + c * kBoxStep + static_cast<uint64_t>(k * 2),
-                       db + static_cast<uint64_t>(k * 2), id_qk, (c > 0 || k > 0) ? 1u : 0u);
+      auto qk = [&](int b, bool last) -> bool {
+        bool r = ready(b);
+        r = ready(b + 1) && r;
+        r = ready(b + 2) && r;
+        if (!__all_sync(0xffffffffu, r)) {
+          r = await(b);
+          r = await(b + 1) && r;
+          r = await(b + 2) && r;
+          if (!__all_sync(0xffffffffu, r)) return false;
         }
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const uint64_t db = k_desc + static_cast<uint64_t>((b + c) % kRing) * kBoxStep;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::mma_ss(s_tm, q_desc + c * kBoxStep + static_cast<uint64_t>(k * 2),
+                         db + static_cast<uint64_t>(k * 2), id_qk, (c > 0 || k > 0) ? 1u : 0u);
+            if (c == 2) tc::commit(&s_full[t]);
+          }
+#pragma unroll
+          for (int c = 0; c < 3; ++c) tc::commit(&empty[(b + c) % kRing]);
+          if (last) tc::commit(&q_empty[t]);
+        }
+        __syncwarp();
+        return true;
       };
       ok = for_each_unit([&](const Unit& u, int) -> bool {
         const int n = u.most(), nt = u.n(t);
         if (n == 0) return true;
         const int im = first_masked(u, 0, p.causal);
         if (nt > 0) {
-          bool r = mbar_wait(&q_full[t], qn & 1);
+          if (!warp_wait(&q_full[t], qn & 1)) return false;
           ++qn;
-          r = await(grp) && r;
-          if (!__all_sync(0xffffffffu, r)) return false;
-          tc::fence_after_sync();
-          if (tc::elect_one()) {
-            issue_qk(pos);
-            tc::commit(&s_full[t]);
-            tc::commit(&empty[grp % kGroups]);
-            if (nt == 1) tc::commit(&q_empty[t]);
-          }
-          __syncwarp();
+          if (!qk(pos, nt == 1)) return false;
         }
-        // O (+)= P V of key tile j, then S of the next one
         for (int j = 0; j < nt; ++j, ++pn) {
-          const int gv = grp + 2 * j + 1, b = pos + 5 * j + 3;
-          const bool more = j + 1 < nt, cut = j >= im;
-          bool r = ready(gv);
-          if (more) r = ready(gv + 1) && r;
+          // O (+)= P V of key tile j
+          int b = pos + 5 * j + 3;
+          const bool cut = j >= im;
+          bool r = ready(b);
+          r = ready(b + 1) && r;
           if (cut) r = mbar_try_wait(&v_ok[vn & 1], (vn >> 1) & 1) && r;
           r = mbar_try_wait(&p_full[t], pn & 1) && r;
           if (!__all_sync(0xffffffffu, r)) {
-            r = await(gv);
-            if (more) r = await(gv + 1) && r;
+            r = await(b);
+            r = await(b + 1) && r;
             if (cut) r = mbar_wait(&v_ok[vn & 1], (vn >> 1) & 1) && r;
             r = mbar_wait(&p_full[t], pn & 1) && r;
             if (!__all_sync(0xffffffffu, r)) return false;
@@ -446,31 +452,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (cut) ++vn;
           tc::fence_after_sync();
           if (tc::elect_one()) {
-            const uint64_t dv =
-                b % kRing == kRing - 1 ? v_desc_ends : v_desc + (b % kRing) * kBoxStep;
-            tc::mma_ts(o_tm, s_tm, dv, id_pv, j > 0 ? 1u : 0u);
 #pragma unroll
-            for (int k = 1; k < 8; ++k)
-              tc::mma_ts(o_tm, s_tm + k * 8, dv + static_cast<uint64_t>(k * 128), id_pv, 1u);
-            tc::commit(&empty[gv % kGroups]);
-            if (more) {
-              issue_qk(b + 2);
-              tc::commit(&s_full[t]);
-              tc::commit(&empty[(gv + 1) % kGroups]);
-              if (j + 2 == nt) tc::commit(&q_empty[t]);
-            } else {
-              tc::commit(&o_full[t]);
+            for (int c = 0; c < 2; ++c) {
+              const uint64_t dv = v_desc + static_cast<uint64_t>((b + c) % kRing) * kBoxStep;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc::mma_ts(o_tm, s_tm + (c * 4 + k) * 8, dv + static_cast<uint64_t>(k * 128), id_pv,
+                           (c > 0 || k > 0 || j > 0) ? 1u : 0u);
+              tc::commit(&empty[(b + c) % kRing]);
             }
+            if (j + 1 == nt) tc::commit(&o_full[t]);
           }
           __syncwarp();
+          // S of the next one, whose keys may still be on their way
+          if (j + 1 < nt && !qk(b + 2, j + 2 == nt)) return false;
         }
         // key tiles that only the other query tile reads
-        for (int g = grp + 2 * nt; g < grp + 2 * n; ++g) {
-          if (g & 1 && (g - grp) / 2 >= im) ++vn;
-          if (!__all_sync(0xffffffffu, await(g))) return false;
-          if (lane == 0) mbar_arrive(&empty[g % kGroups]);
+        for (int b = pos + 5 * nt; b < pos + 5 * n; ++b) {
+          if ((b - pos) % 5 == 3 && (b - pos) / 5 >= im) ++vn;
+          if (!__all_sync(0xffffffffu, await(b))) return false;
+          if (lane == 0) mbar_arrive(&empty[b % kRing]);
         }
-        grp += 2 * n;
         pos += 5 * n;
         return true;
       });
@@ -480,22 +482,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = for_each_unit([&](const Unit& u, int i) -> bool {
         const int n = u.most(), im = first_masked(u, 0, p.causal);
         for (int j = im; j < n; ++j, ++vn) {
-          // the dims' halves may be swapped: it does not matter here
           const int b = pos + 5 * j + 3;
-          const uint8_t* box0 = smem + OFF_RING + (b % kRing) * kBox;
-          const uint8_t* box1 = smem + OFF_RING + ((b + 1) % kRing) * kBox;
           if (!warp_wait(&cut_full[vn & 1], (vn >> 1) & 1)) return false;
           const int valid = u.lk - (u.ks + j * kTile);  // keys of the sequence in this tile
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            const int r = q * 32 + lane;
+            const int r = q * 32 + lane;  // key of the tile
+            uint8_t* box = smem + OFF_RING + ((b + (r >> 6)) % kRing) * kBox;
+            auto at = [&](int c) { return box + (c >> 3) * (kBox / 2) + sw128(r & 63, c & 7); };
             const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
             __nv_bfloat162 z[4] = {zero, zero, zero, zero};
             if (r < valid) {
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
                 // 0 * x stays 0 unless x is not finite
-                const uint4 x = *reinterpret_cast<const uint4*>((c < 8 ? box0 : box1) + sw128(r, c & 7));
+                const uint4 x = *reinterpret_cast<const uint4*>(at(c));
                 z[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, z[0]);
                 z[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, z[1]);
                 z[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, z[2]);
@@ -504,16 +505,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
               for (int c = 0; c < 16; ++c)
-                *reinterpret_cast<uint4*>(const_cast<uint8_t*>(c < 8 ? box0 : box1) +
-                                          sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(at(c)) = make_uint4(0, 0, 0, 0);
             }
             z[0] = __hadd2(__hadd2(z[0], z[1]), __hadd2(z[2], z[3]));
             const bool bad = (*reinterpret_cast<uint32_t*>(&z[0]) & 0x7FFF7FFFu) != 0;
             if (bad) {
 #pragma unroll 1
               for (int c = 0; c < 64; ++c) {
-                uint32_t* a = reinterpret_cast<uint32_t*>(
-                    const_cast<uint8_t*>(c < 32 ? box0 : box1) + sw128(r, (c >> 2) & 7) + (c & 3) * 4);
+                uint32_t* a = reinterpret_cast<uint32_t*>(at(c >> 2) + (c & 3) * 4);
                 uint32_t x = *a;
                 if (!finite_bf16(x)) x &= 0xFFFF0000u;
                 if (!finite_bf16(x >> 16)) x &= 0xFFFFu;
