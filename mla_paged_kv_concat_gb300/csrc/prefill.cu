@@ -280,15 +280,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
 
   // One reading warp's walk over the units: f(unit, index) until the end
-  // mark or a failed wait.
-  auto for_each_unit = [&](auto&& f) -> bool {
+  // mark or a failed wait.  The softmax warps give the unit's slot back when
+  // they are done with it, flags included.
+  auto for_each_unit = [&](bool keep, auto&& f) -> bool {
     for (int i = 0;; ++i) {
       if (!warp_wait(&unit_full[i % kUnits], (i / kUnits) & 1)) return false;
       const Unit u = *unit_slot(i);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&unit_empty[i % kUnits]);
+      if (!keep && lane == 0) mbar_arrive(&unit_empty[i % kUnits]);
       if (u.q_row < 0) return true;
       if (!f(u, i)) return false;
+      if (keep) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&unit_empty[i % kUnits]);
+      }
     }
   };
 
@@ -425,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         return true;
       };
-      ok = for_each_unit([&](const Unit& u, int) -> bool {
+      ok = for_each_unit(false, [&](const Unit& u, int) -> bool {
         const int n = u.most(), nt = u.n(t);
         if (n == 0) return true;
         const int im = first_masked(u, 0, p.causal);
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ------------------------------------------------------ value keeper
       int pos = 0, vn = 0;
-      ok = for_each_unit([&](const Unit& u, int i) -> bool {
+      ok = for_each_unit(false, [&](const Unit& u, int i) -> bool {
         const int n = u.most(), im = first_masked(u, 0, p.causal);
         for (int j = im; j < n; ++j, ++vn) {
           const int b = pos + 5 * j + 3;
@@ -539,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.sm_scale * kLog2e;
     const uint64_t c2 = pack2(c, c);
     int sn = 0, on = 0;
-    ok = for_each_unit([&](const Unit& u, int i) -> bool {
+    ok = for_each_unit(true, [&](const Unit& u, int i) -> bool {
       const int row = t * kTile + r;         // row of the unit
       const int n = u.n(t);
       const bool live = row < u.rows;
