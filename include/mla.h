@@ -647,10 +647,12 @@ mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_str
 
 /*
  * mla_prefill_num_kv_splits - how many parts mla_prefill should cut the key
- * axis into: 1 when the 256-row query blocks of all heads fill the SMs, else
- * enough parts to fill them, none shorter than 512 keys of the longest
- * sequence; at most 64.  max_kv_len: longest sequence's keys (an upper bound
- * will do).
+ * axis into: as many as give every SM one part where the 256-row query blocks
+ * of all heads leave SMs idle (no part shorter than 1024 keys of the longest
+ * sequence), a few more where sequences have at most 64 rows on average and
+ * there are fewer than four blocks for every SM (their lengths may differ; no
+ * part shorter than 2048 keys), else 1; at most 64.  max_kv_len: longest
+ * sequence's keys (an upper bound will do).
  */
 int mla_prefill_num_kv_splits(int num_tokens, int num_seqs, int num_heads, int64_t max_kv_len,
                               int sm_count);

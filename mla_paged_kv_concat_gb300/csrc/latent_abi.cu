@@ -351,15 +351,27 @@ mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_str
                      {y, y_row_stride, y_head_stride, v_dim}, {}, err_count, stream);
 }
 
+// Measured on GB300, 16 heads (us at S = 1 / the rule's S / twice that): one
+// sequence of 256 rows, 32768 keys: 438 / 80 (8) / 98; two of 500 rows, 4596 keys:
+// 72 / 53 (2) / 63; eight of 1 to 5 rows, 4096 to 32768 keys: 381 / 225 (5) / 225;
+// 64 of one row, 4096 keys: 363 (1) / 384; 1000 rows, 1000 keys: 23 (1) / 26.
 int mla_prefill_num_kv_splits(int num_tokens, int num_seqs, int num_heads, int64_t max_kv_len,
                               int sm_count) {
   if (num_tokens < 1 || num_seqs < 1 || num_heads < 1 || max_kv_len < 1 || sm_count < 1) return 1;
-  // 256-row blocks there can be, a CTA each
-  const int64_t blocks = num_tokens / 256 + (num_seqs < num_tokens ? num_seqs : num_tokens);
+  // 256-row blocks there are at least, one CTA each per head
+  const int64_t by_rows = (static_cast<int64_t>(num_tokens) + 255) / 256;
+  const int64_t blocks = num_seqs > by_rows && num_seqs <= num_tokens ? num_seqs : by_rows;
   const int64_t units = blocks * num_heads;
-  if (units >= 2 * static_cast<int64_t>(sm_count)) return 1;
-  int64_t s = (4 * static_cast<int64_t>(sm_count) + units - 1) / units;
-  const int64_t most = (max_kv_len + 511) / 512;
+  int64_t s = sm_count / units, most = max_kv_len / 1024;
+  if (s < 2) {
+    // Nearly every SM has a unit.  With few rows a sequence its length is what
+    // a unit takes; parts of it even out lengths that differ.
+    s = 1;
+    if (num_tokens <= 64 * static_cast<int64_t>(num_seqs) && units < 4 * static_cast<int64_t>(sm_count)) {
+      s = (4 * static_cast<int64_t>(sm_count) + units - 1) / units;
+      most = max_kv_len / 2048;
+    }
+  }
   if (s > most) s = most;
   if (s > 64) s = 64;
   return s < 1 ? 1 : static_cast<int>(s);

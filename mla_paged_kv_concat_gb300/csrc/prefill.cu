@@ -355,8 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int64_t x = blockIdx.x;
         for (int asked = 0;; ++asked) {
-          // the next unit's index comes in while this one is loaded
-          if (x >= 0) next_cta_ask(smem + OFF_NEXT, next_full);
+          // The next unit is asked for when this one's last key tiles are to be
+          // loaded: early enough to be there, and no unit waits here while
+          // another CTA has nothing to do (asked for at a unit's start, 128
+          // units of one sequence's splits took as long as twice as many).
+          bool ask = x >= 0;
           Unit u;
           if (x < 0) u.q_row = -1;
           // after a wait that gave up, the CTAs left are taken over and dropped
@@ -374,11 +377,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_v(u, 0);
               }
               for (int j = 1; j < n && ok; ++j) {
+                if (ask && j >= n - 2) {
+                  next_cta_ask(smem + OFF_NEXT, next_full);
+                  ask = false;
+                }
                 load_k(u, j);
                 load_v(u, j);
               }
             }
           }
+          if (ask) next_cta_ask(smem + OFF_NEXT, next_full);
           if (x < 0 || !mbar_wait(next_full, asked & 1)) break;
           x = next_cta_answer(smem + OFF_NEXT);
           fence_proxy_async_smem();  // read before the next answer is written
