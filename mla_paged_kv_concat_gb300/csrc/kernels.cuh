@@ -247,6 +247,7 @@ cudaError_t launch_latent_proj(const ProjParams& p, const ProjMaps& m, int mode,
 struct PrefillParams {
   int num_tokens, num_kv, heads, num_seqs;
   const int32_t *cu_q, *cu_k;  // [num_seqs + 1]
+  int pe_col;      // column of q's rope part, or 0 when it has a map of its own
   bool causal;
   float sm_scale;
   int num_splits;

@@ -440,6 +440,7 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
   p.num_seqs = num_seqs;
   p.cu_q = cu_seqlens_q;
   p.cu_k = cu_seqlens_k;
+  p.pe_col = q_pe ? 0 : nope_dim;
   p.causal = causal != 0;
   p.sm_scale = sm_scale;
   p.num_splits = num_kv_splits;
@@ -457,7 +458,7 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
   mla::PrefillMaps m;
   memset(&m, 0, sizeof m);
   mla_status st = heads_map(&m.q, hq, num_tokens, num_heads, 128);
-  if (st == MLA_OK) st = heads_map(&m.q_pe, hqp, num_tokens, num_heads, 128);
+  if (st == MLA_OK && q_pe) st = heads_map(&m.q_pe, hqp, num_tokens, num_heads, 128);
   if (num_kv_tokens > 0) {
     if (st == MLA_OK) st = heads_map(&m.k, hk, num_kv_tokens, num_heads, 128);
     if (st == MLA_OK) st = heads_map(&m.k_pe, hkp, num_kv_tokens, 1, 128);

@@ -65,7 +65,9 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_RING = OFF_Q + 6 * kBox;
 constexpr int OFF_UNIT = OFF_RING + kRing * kBox;
 constexpr int OFF_FLAG = OFF_UNIT + kUnits * 64;
-constexpr int OFF_BAR = OFF_FLAG + kUnits * 64;
+constexpr int kCuCached = 64;          // cumulative lengths kept in shared memory
+constexpr int OFF_CU = OFF_FLAG + kUnits * 64;
+constexpr int OFF_BAR = OFF_CU + 2 * kCuCached * 4;
 constexpr int kBars = 2 * kRing + 2 * kUnits + 15;
 constexpr int OFF_NEXT = (OFF_BAR + kBars * 8 + 15) & ~15;
 constexpr int OFF_TMEM = OFF_NEXT + 16;
@@ -118,7 +120,9 @@ __device__ __forceinline__ int first_masked(const Unit& u, int row0, bool causal
 // the last to the first (with a causal mask the longest come first); the
 // heads of a group share a block's turn, so that the CTAs at work together
 // read few heads' keys, from L2.
-__device__ bool unit_at(const PrefillParams& p, int64_t x, Unit& u) {
+// `cu_q`, `cu_k`: p's, or their copies in shared memory.
+__device__ bool unit_at(const PrefillParams& p, const int32_t* cu_q, const int32_t* cu_k, int64_t x,
+                        Unit& u) {
   u.split = static_cast<int>(x % p.num_splits);
   x /= p.num_splits;
   const int hh = static_cast<int>(x % p.head_group);
@@ -129,11 +133,11 @@ __device__ bool unit_at(const PrefillParams& p, int64_t x, Unit& u) {
   int a = 0, z = p.num_seqs - 1;
   while (a < z) {
     const int m = (a + z + 1) >> 1;
-    const int c = clampi(__ldg(p.cu_q + m), 0, p.num_tokens);
+    const int c = clampi(cu_q[m], 0, p.num_tokens);
     if (c / kUnitRows + m <= slot) a = m; else z = m - 1;
   }
-  const int q0 = __ldg(p.cu_q + a), q1 = __ldg(p.cu_q + a + 1);
-  const int k0 = __ldg(p.cu_k + a), k1 = __ldg(p.cu_k + a + 1);
+  const int q0 = cu_q[a], q1 = cu_q[a + 1];
+  const int k0 = cu_k[a], k1 = cu_k[a + 1];
   const int qa = clampi(q0, 0, p.num_tokens), qz = clampi(q1, qa, p.num_tokens);
   const int ka = clampi(k0, 0, p.num_kv), kz = clampi(k1, ka, p.num_kv);
   const int blk = slot - (qa / kUnitRows + a);
@@ -302,6 +306,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     reg_dec<104>();
     if (warp == 8) {
       // ---------------------------------------------------------- producer
+      // a few sequences' lengths come in at once, not one search step after
+      // the other
+      const int32_t *cu_q = p.cu_q, *cu_k = p.cu_k;
+      if (p.num_seqs < kCuCached) {
+        int32_t* cu = reinterpret_cast<int32_t*>(smem + OFF_CU);
+        for (int b = lane; b <= p.num_seqs; b += 32) {
+          cu[b] = __ldg(p.cu_q + b);
+          cu[kCuCached + b] = __ldg(p.cu_k + b);
+        }
+        __syncwarp();
+        cu_q = cu;
+        cu_k = cu + kCuCached;
+      }
       if (lane == 0) {
         int i = 0, cut = 0, pos = 0, qn[2] = {0, 0};
         // The next box of the ring, once it is free.
@@ -321,7 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = u.q_row + t * kTile;
           tma_load_3d(dst, &maps.q, &q_full[t], 0, u.h, row);
           tma_load_3d(dst + kBox, &maps.q, &q_full[t], 64, u.h, row);
-          tma_load_3d(dst + 2 * kBox, &maps.q_pe, &q_full[t], 0, u.h, row);
+          if (p.pe_col)
+            tma_load_3d(dst + 2 * kBox, &maps.q, &q_full[t], p.pe_col, u.h, row);
+          else
+            tma_load_3d(dst + 2 * kBox, &maps.q_pe, &q_full[t], 0, u.h, row);
         };
         auto load_k = [&](const Unit& u, int j) {
           const int row = u.k_row + u.ks + j * kTile;
@@ -363,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Unit u;
           if (x < 0) u.q_row = -1;
           // after a wait that gave up, the CTAs left are taken over and dropped
-          if (ok && (x < 0 || unit_at(p, x, u))) {
+          if (ok && (x < 0 || unit_at(p, cu_q, cu_k, x, u))) {
             ok = mbar_wait(&unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
             if (ok) {
               *unit_slot(i) = u;
