@@ -699,7 +699,7 @@ size_t mla_prefill_workspace_bytes(int num_tokens, int num_heads, int num_kv_spl
  *   sm_scale        1e-30 .. 1e30.
  *   num_kv_splits   1 .. 64 parts of the key axis, joined by a second kernel
  *                   (see mla_prefill_num_kv_splits); 1 needs no workspace.
- *   workspace       >= mla_prefill_workspace_bytes(...), 16-byte aligned.
+ *   workspace       >= mla_prefill_workspace_bytes(...), 32-byte aligned.
  *   o               bf16 [num_tokens][num_heads][v_dim] at its strides; must
  *                   not overlap an input.  lse fp32 [num_tokens][num_heads],
  *                   contiguous.  Rows of no sequence are left as they were.

@@ -255,6 +255,7 @@ struct PrefillParams {
   int64_t v_row_stride, v_head_stride;
   uint16_t* o;
   int64_t o_row_stride, o_head_stride;
+  bool o_aligned32;  // every row of a head starts on a 32-byte boundary
   float* lse;     // [num_tokens][heads]
   float* ws_o;    // [splits][num_tokens][heads][128]
   float* ws_lse;  // [splits][num_tokens][heads]

@@ -426,7 +426,8 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
     return MLA_ERR_INVALID_ARG;
   const size_t need = mla_prefill_workspace_bytes(num_tokens, num_heads, num_kv_splits, v_dim);
   if (need > 0) {
-    if (!workspace || !aligned16(workspace)) return MLA_ERR_INVALID_ARG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 31u) != 0)
+      return MLA_ERR_INVALID_ARG;
     if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
   }
   // one CTA per 256-row block slot, head and split
@@ -450,6 +451,8 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
   p.o = static_cast<uint16_t*>(o);
   p.o_row_stride = o_row_stride;
   p.o_head_stride = num_heads > 1 ? o_head_stride : 0;
+  p.o_aligned32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0 && o_row_stride % 16 == 0 &&
+                  p.o_head_stride % 16 == 0;
   p.lse = lse;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_lse = need ? p.ws_o + static_cast<size_t>(num_tokens) * num_heads * num_kv_splits * v_dim

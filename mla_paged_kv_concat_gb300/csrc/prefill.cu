@@ -121,14 +121,12 @@ __device__ __forceinline__ int first_masked(const Unit& u, int row0, bool causal
 // heads of a group share a block's turn, so that the CTAs at work together
 // read few heads' keys, from L2.
 // `cu_q`, `cu_k`: p's, or their copies in shared memory.
-__device__ bool unit_at(const PrefillParams& p, const int32_t* cu_q, const int32_t* cu_k, int64_t x,
-                        Unit& u) {
-  u.split = static_cast<int>(x % p.num_splits);
-  x /= p.num_splits;
-  const int hh = static_cast<int>(x % p.head_group);
-  x /= p.head_group;
-  const int slot = p.slots - 1 - static_cast<int>(x % p.slots);
-  u.h = static_cast<int>(x / p.slots) * p.head_group + hh;
+__device__ bool unit_at(const PrefillParams& p, const int32_t* cu_q, const int32_t* cu_k,
+                        uint32_t x, Unit& u) {
+  const uint32_t x1 = x / p.num_splits, x2 = x1 / p.head_group, x3 = x2 / p.slots;
+  u.split = static_cast<int>(x - x1 * p.num_splits);
+  u.h = static_cast<int>(x3 * p.head_group + (x1 - x2 * p.head_group));
+  const int slot = p.slots - 1 - static_cast<int>(x2 - x3 * p.slots);
   if (u.h >= p.heads) return false;
   int a = 0, z = p.num_seqs - 1;
   while (a < z) {
@@ -210,6 +208,13 @@ __device__ __forceinline__ int64_t next_cta_answer(const void* src) {
       : "l"(a.x), "l"(a.y)
       : "memory");
   return got ? static_cast<int64_t>(x) : -1;
+}
+
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void store32(void* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
 }
 
 __device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7F80u) != 0x7F80u; }
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Unit u;
           if (x < 0) u.q_row = -1;
           // after a wait that gave up, the CTAs left are taken over and dropped
-          if (ok && (x < 0 || unit_at(p, cu_q, cu_k, x, u))) {
+          if (ok && (x < 0 || unit_at(p, cu_q, cu_k, static_cast<uint32_t>(x), u))) {
             ok = mbar_wait(&unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
             if (ok) {
               *unit_slot(i) = u;
@@ -693,23 +698,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (live && p.num_splits == 1) {
+          // rows of different lanes lie far apart, so a store costs a cycle for
+          // each lane: 32 bytes at once where the output is aligned for it
           uint16_t* dst = p.o + q_row * p.o_row_stride + u.h * p.o_head_stride + q;
+          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t w[4];
+          for (int f = 0; f < 16; ++f)
+            w[f] = pack_bf16x2(__uint_as_float(o[2 * f]) * inv, __uint_as_float(o[2 * f + 1]) * inv);
+          if (p.o_aligned32) {
+            store32(dst, &w[0]);
+            store32(dst + 16, &w[8]);
+          } else {
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
-              w[f] = pack_bf16x2(__uint_as_float(o[e + 2 * f]) * inv,
-                                 __uint_as_float(o[e + 2 * f + 1]) * inv);
-            *reinterpret_cast<uint4*>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int f = 0; f < 16; f += 4)
+              *reinterpret_cast<uint4*>(dst + 2 * f) = make_uint4(w[f], w[f + 1], w[f + 2], w[f + 3]);
           }
         } else if (live && n > 0) {
           float* dst = p.ws_o + part * kDv + q;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(dst + e) =
-                make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                            __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) store32(dst + e, &o[e]);
         }
       }
       if (live) {

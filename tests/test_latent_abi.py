@@ -135,7 +135,7 @@ PREFILL = dict(q=at(1), qrs=16 * 192, qhs=192, qpe=None, qprs=0, qphs=0, T=10, H
     (dict(khs=100), 1), (dict(vrs=12), 1), (dict(kps=60), 1), (dict(kps=68), 1),
     (dict(q=at(1) + 8), 1), (dict(kpe=at(3) + 8), 1), (dict(o=at(7) + 8), 1), (dict(lse=at(8) + 2), 1),
     (dict(ors=64, ohs=128), 1), (dict(ors=1024, ohs=128), 1), (dict(o=at(1)), 1), (dict(o=at(2)), 1),
-    (dict(ws=None), 1), (dict(ws=at(6) + 8), 1), (dict(wsb=100), 3),
+    (dict(ws=None), 1), (dict(ws=at(6) + 16), 1), (dict(wsb=100), 3),
     (dict(T=1 << 29, seqs=1000, H=1024, qrs=1024 * 192, ors=1024 * 128), 1),
 ])
 def test_prefill_refusals(lib, over, code):
