@@ -227,10 +227,11 @@ struct ProjParams {
   int cols;    // output columns of a head: 256, R or 128
   int bn;      // columns of a tile, from proj_tile_cols
   bool pair;   // tiles of CTA pairs, from proj_pairs
+  int a_rows;  // token rows of a's box: 128, or all there are
   int w_row0;  // first of the head's 256 weight rows that the product reads
   int* err_count;
 };
-// a: {K, heads or 1, tokens}, box {64, 1, 128}.  b: the weight as
+// a: {K, heads or 1, tokens}, box {64, 1, a_rows}.  b: the weight as
 // {R, 256, heads}, box {64, bn, 1}, or {64, 64, 1} for absorb, {64, 128, 1} for
 // pairs.  c0, c1:
 // {cols, heads, tokens}, box {64, 1, 32}; c1 is expand's v.  All 128-byte

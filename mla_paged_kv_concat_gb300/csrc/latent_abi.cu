@@ -153,9 +153,10 @@ mla_status latent_proj(int mode, Heads in, int in_heads, int tokens, const void*
   p.w_row0 = mode == mla::kProjProject ? nope : 0;
   p.bn = mla::proj_tile_cols(tokens, heads, p.cols, sms);
   p.pair = mla::proj_pairs(mode, tokens, heads, p.k, sms);
+  p.a_rows = tokens < 128 ? tokens : 128;
   p.err_count = err_count;
   mla::ProjMaps m;
-  mla_status st = heads_map(&m.a, in, tokens, in_heads, 128);
+  mla_status st = heads_map(&m.a, in, tokens, in_heads, p.a_rows);
   if (st == MLA_OK)
     st = make_map(&m.b, w, R, nope + vdim, heads, w_stride, w_stride * (nope + vdim),
                   p.pair ? 128 : mode == mla::kProjAbsorb ? 64 : p.bn, 1);

@@ -156,7 +156,9 @@ __global__ void __launch_bounds__(192, 1)
             break;
           }
           uint8_t* dst = smem + st * C::STAGE;
-          mbar_arrive_expect_tx(&full[st], C::STAGE);
+          // fewer than 128 tokens: the tile's other rows hold what was there; an
+          // accumulator's row depends on its own row of A only
+          mbar_arrive_expect_tx(&full[st], p.a_rows * 128 + C::B_BYTES);
           tma_load_3d(dst, &ma, &full[st], kc * KC, MODE == kProjExpand ? 0 : h, m * TM);
           if (kBMn) {
 #pragma unroll
@@ -469,11 +471,24 @@ bool proj_pairs(int mode, int tokens, int heads, int k, int sm_count) {
          static_cast<int64_t>((tokens + 2 * TM - 1) / (2 * TM)) * heads >= 2 * sm_count;
 }
 
+// Columns of a tile: those for which the CTA with the most tiles takes in the
+// fewest operand rows (tokens and columns; K is the same).  project, 128 tokens,
+// 128 heads: 128 columns, one tile a CTA 6.0 us, 64 columns, two, 7.4; absorb, 64
+// tokens, 16 heads: 64 columns 3.6 us, 256 4.8.
 int proj_tile_cols(int tokens, int heads, int cols, int sm_count) {
-  const int64_t units = static_cast<int64_t>((tokens + TM - 1) / TM) * heads;
-  int bn = cols < 256 ? cols : 256;
-  while (bn > 64 && units * (cols / bn) < sm_count) bn /= 2;
-  return bn;
+  const int64_t blocks = static_cast<int64_t>((tokens + TM - 1) / TM) * heads;
+  const int rows = tokens < TM ? tokens : TM;
+  int best = 0;
+  int64_t best_cost = 0;
+  for (int bn = cols < 256 ? cols : 256; bn >= 64; bn /= 2) {
+    const int64_t rounds = (blocks * (cols / bn) + sm_count - 1) / sm_count;
+    const int64_t cost = rounds * (rows + bn);
+    if (best == 0 || cost < best_cost) {
+      best = bn;
+      best_cost = cost;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_latent_proj(const ProjParams& p, const ProjMaps& m, int mode, int sm_count,
