@@ -4,7 +4,8 @@
 // include/mla.h.  Nothing is computed here.
 //
 // Compiled, because these calls are short: through ctypes and Python checks
-// one took 34 to 74 us of host time, more than most of the kernels.
+// one took 34 to 74 us of host time, more than most of the kernels; now 3.5 to
+// 9.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -34,9 +35,12 @@ struct BadValue : std::runtime_error {
 };
 struct PyError {};  // a Python exception is set
 
-void check(bool ok, const std::string& what) {
-  if (!ok) throw BadValue(what);
-}
+// The text is put together only when the check fails: for every check of a
+// call it took longer than the rest of the call.
+#define CHECK(ok, what)                \
+  do {                                 \
+    if (!(ok)) throw BadValue(what);   \
+  } while (0)
 
 // The arguments of one call in order, with the device and stream they run on.
 struct Call {
@@ -59,9 +63,9 @@ struct Call {
       throw PyError();
     }
     const Tensor& t = THPVariable_Unpack(o);
-    check(t.is_cuda(), std::string(name) + " must be a CUDA tensor");
+    CHECK(t.is_cuda(), std::string(name) + " must be a CUDA tensor");
     if (dev < 0) dev = c10::cuda::current_device();
-    check(t.device().index() == dev,
+    CHECK(t.device().index() == dev,
           std::string(name) + " is not on the current device cuda:" + std::to_string(dev));
     return t;
   }
@@ -77,7 +81,7 @@ struct Call {
   }
   int small(const char* name) {
     const int64_t v = integer();
-    check(v >= INT32_MIN && v <= INT32_MAX, std::string(name) + " does not fit 32 bits");
+    CHECK(v >= INT32_MIN && v <= INT32_MAX, std::string(name) + " does not fit 32 bits");
     return static_cast<int>(v);
   }
   double real() {
@@ -104,7 +108,7 @@ struct Call {
     }
     stream = c10::cuda::CUDAStream(c10::Stream::unpack3(
         v[0], static_cast<c10::DeviceIndex>(v[1]), static_cast<c10::DeviceType>(v[2])));
-    check(stream->device_index() == dev,
+    CHECK(stream->device_index() == dev,
           "the stream is not on the current device cuda:" + std::to_string(dev));
     own_stream = true;
   }
@@ -126,7 +130,7 @@ std::string dims(at::IntArrayRef s) {
 void typed(const Tensor& t, at::ScalarType dtype, std::initializer_list<int64_t> shape,
            const char* name) {
   if (!t.defined()) return;
-  check(t.scalar_type() == dtype, std::string(name) + " must be " + c10::toString(dtype) +
+  CHECK(t.scalar_type() == dtype, std::string(name) + " must be " + c10::toString(dtype) +
                                       ", not " + c10::toString(t.scalar_type()));
   const auto s = t.sizes();
   bool ok = s.size() == shape.size();
@@ -137,8 +141,8 @@ void typed(const Tensor& t, at::ScalarType dtype, std::initializer_list<int64_t>
       ++k;
     }
   }
-  check(ok, std::string(name) + " has the wrong shape " + dims(s));
-  check(t.numel() == 0 || s.back() == 1 || t.stride(-1) == 1,
+  CHECK(ok, std::string(name) + " has the wrong shape " + dims(s));
+  CHECK(t.numel() == 0 || s.back() == 1 || t.stride(-1) == 1,
         std::string(name) + " must have unit last stride");
 }
 
@@ -161,7 +165,7 @@ struct Strides {
 };
 int64_t row_stride(const Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
 int as_int(int64_t x, const char* name) {
-  check(x <= INT32_MAX, std::string(name) + " does not fit 32 bits");
+  CHECK(x <= INT32_MAX, std::string(name) + " does not fit 32 bits");
   return static_cast<int>(x);
 }
 
@@ -235,7 +239,7 @@ PyObject* batch_build(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t rows = table.size(0), maxb = table.size(1);
     if (tokens < 0) {
       const Tensor& given = pos.defined() ? pos : slot;
-      check(given.defined() && given.dim() == 1,
+      CHECK(given.defined() && given.dim() == 1,
             "num_tokens is needed when no token output is given");
       tokens = given.size(0);
     }
@@ -328,9 +332,9 @@ PyObject* gather_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
         default: throw BadValue("unsupported cache dtype");
       }
     }
-    check(cache.element_size() == (fmt == MLA_KV_BF16 ? 2u : 1u),
+    CHECK(cache.element_size() == (fmt == MLA_KV_BF16 ? 2u : 1u),
           "kv_cache_dtype does not fit the cache");
-    check(cache.dim() == 3 && cache.stride(2) == 1 && cache.stride(1) == cache.size(2),
+    CHECK(cache.dim() == 3 && cache.stride(2) == 1 && cache.stride(1) == cache.size(2),
           "cache rows must be dense");
     const int64_t nb = cache.size(0), bs = cache.size(1), d = cache.size(2);
     if (R < 0) R = d - kRope;
@@ -338,10 +342,10 @@ PyObject* gather_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     typed(table, kI32, {-1, -1}, "block_table");
     const int64_t B = table.size(0);
     if (tokens < 0) {
-      check(kv_c.defined() && kv_c.dim() == 2, "num_tokens is needed when kv_c is not given");
+      CHECK(kv_c.defined() && kv_c.dim() == 2, "num_tokens is needed when kv_c is not given");
       tokens = kv_c.size(0);
     }
-    check(R > 0 && P > 0, "kv_lora_rank does not fit the cache");
+    CHECK(R > 0 && P > 0, "kv_lora_rank does not fit the cache");
     if (!kv_c.defined()) kv_c = c.empty({tokens, R}, kBf16);
     if (!k_pe.defined()) k_pe = c.empty({tokens, P}, kBf16);
     typed(cu, kI32, {B + 1}, "cu_seqlens");
@@ -349,7 +353,7 @@ PyObject* gather_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     typed(kv_c, kBf16, {tokens, R}, "kv_c");
     typed(k_pe, kBf16, {tokens, P}, "k_pe");
     typed(err, kI32, {1}, "err_count");
-    check(!scale.defined() || (scale.scalar_type() == at::kFloat && scale.numel() == 1),
+    CHECK(!scale.defined() || (scale.scalar_type() == at::kFloat && scale.numel() == 1),
           "kv_scale must be one float32");
     done(mla_gather_cache(ptr(cache), static_cast<mla_kv_dtype>(fmt), as_int(nb, "the cache"),
                           as_int(bs, "the block size"), nb > 1 ? cache.stride(0) : bs * d,
@@ -377,11 +381,11 @@ PyObject* expand_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int H = c.small("num_heads");
     Tensor k = c.maybe("k_nope"), v = c.maybe("v"), err = c.maybe("err_count");
     c.take_stream();
-    check(H > 0, "num_heads must be positive");
+    CHECK(H > 0, "num_heads must be positive");
     const int64_t R = kv_b(w, H);
     typed(x, kBf16, {-1, R}, "kv_c");
     const int64_t T = x.size(0);
-    check(k.defined() == v.defined(), "give both k_nope and v, or neither");
+    CHECK(k.defined() == v.defined(), "give both k_nope and v, or neither");
     if (!k.defined()) {
       k = c.empty({T, H, kNope}, kBf16);
       v = c.empty({T, H, kV}, kBf16);
@@ -405,7 +409,7 @@ PyObject* head_product(PyObject* const* a, Py_ssize_t n, bool absorb) {
     Tensor x = c.tensor(absorb ? "q_nope" : "o"), w = c.tensor("w_kv_b");
     Tensor out = c.maybe("out"), err = c.maybe("err_count");
     c.take_stream();
-    check(x.dim() == 3, "the input must be [tokens, heads, dims]");
+    CHECK(x.dim() == 3, "the input must be [tokens, heads, dims]");
     const int64_t T = x.size(0), H = x.size(1);
     const int64_t R = kv_b(w, H);
     const int64_t in = absorb ? kNope : R, cols = absorb ? R : kV;
@@ -439,11 +443,11 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor ws = c.maybe("workspace"), out = c.maybe("out"), lse = c.maybe("lse");
     Tensor err = c.maybe("err_count");
     c.take_stream();
-    check(q.dim() == 3 && k_pe.dim() == 2, "q must be [tokens, heads, dims], k_pe [keys, 64]");
+    CHECK(q.dim() == 3 && k_pe.dim() == 2, "q must be [tokens, heads, dims], k_pe [keys, 64]");
     const int64_t T = q.size(0), H = q.size(1), Tk = k_pe.size(0), P = k_pe.size(1);
     typed(cu_q, kI32, {-1}, "cu_seqlens_q");
     const int64_t B = cu_q.size(0) - 1;
-    check(B >= 0, "cu_seqlens_q must not be empty");
+    CHECK(B >= 0, "cu_seqlens_q must not be empty");
     if (!out.defined()) out = c.empty({T, H, kV}, kBf16);
     if (!lse.defined()) lse = c.empty({T, H}, at::kFloat);
     typed(q, kBf16, {T, H, kNope + (q_pe.defined() ? 0 : P)}, "q");
@@ -455,14 +459,14 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     typed(out, kBf16, {T, H, kV}, "out");
     typed(lse, at::kFloat, {T, H}, "lse");
     typed(err, kI32, {1}, "err_count");
-    check(lse.is_contiguous(), "lse must be contiguous");
+    CHECK(lse.is_contiguous(), "lse must be contiguous");
     const int Ti = as_int(T, "the number of tokens"), Hi = as_int(H, "the number of heads");
     const size_t need = mla_prefill_workspace_bytes(Ti, Hi, splits, kV);
     if (need && !ws.defined()) {
-      check(need <= static_cast<size_t>(INT64_MAX), "the workspace does not fit");
+      CHECK(need <= static_cast<size_t>(INT64_MAX), "the workspace does not fit");
       ws = c.empty({static_cast<int64_t>(need)}, at::kByte);
     }
-    check(!ws.defined() || ws.is_contiguous(), "workspace must be contiguous");
+    CHECK(!ws.defined() || ws.is_contiguous(), "workspace must be contiguous");
     const Strides sq(q), sk(k), sv(v), so(out), sp = q_pe.defined() ? Strides(q_pe) : Strides();
     done(mla_prefill(ptr(q), sq.row, sq.head, ptr(q_pe), sp.row, sp.head, Ti, Hi, ptr(k), sk.row,
                      sk.head, ptr(v), sv.row, sv.head, ptr(k_pe), row_stride(k_pe),
