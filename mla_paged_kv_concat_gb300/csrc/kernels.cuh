@@ -239,7 +239,7 @@ struct ProjParams {
 struct ProjMaps {
   CUtensorMap a, b, c0, c1;
 };
-int proj_tile_cols(int tokens, int heads, int cols, int sm_count);
+int proj_tile_cols(int mode, int tokens, int heads, int cols, int sm_count);
 bool proj_pairs(int mode, int tokens, int heads, int k, int sm_count);
 cudaError_t launch_latent_proj(const ProjParams& p, const ProjMaps& m, int mode, int sm_count,
                                cudaStream_t stream);

@@ -151,7 +151,7 @@ mla_status latent_proj(int mode, Heads in, int in_heads, int tokens, const void*
   p.k = in.cols;
   p.cols = two ? nope + vdim : out0.cols;
   p.w_row0 = mode == mla::kProjProject ? nope : 0;
-  p.bn = mla::proj_tile_cols(tokens, heads, p.cols, sms);
+  p.bn = mla::proj_tile_cols(mode, tokens, heads, p.cols, sms);
   p.pair = mla::proj_pairs(mode, tokens, heads, p.k, sms);
   p.a_rows = tokens < 128 ? tokens : 128;
   p.err_count = err_count;

@@ -18,7 +18,7 @@
 // which also clips the rows past the last token.  Roles: warps 0-3 epilogue,
 // warp 4 TMA producer, warp 5 MMA issuer and TMEM owner.
 // Measured: expand, 5001 tokens, 128 heads, R = 256, 77 us (4.25 TB/s written; a
-// plain fill reaches 4.02); absorb, 2048 tokens, 128 heads, 72 us; project, the
+// plain fill reaches 4.02); absorb, 2048 tokens, 128 heads, 64 us; project, the
 // same, 56 us (5.9 TB/s); absorb, 64 tokens, 16 heads, 3.5 us, launch and latency.
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -477,9 +477,14 @@ bool proj_pairs(int mode, int tokens, int heads, int k, int sm_count) {
 // Columns of a tile: those for which the CTA with the most tiles takes in the
 // fewest operand rows (tokens and columns; K is the same).  project, 128 tokens,
 // 128 heads: 128 columns, one tile a CTA 6.0 us, 64 columns, two, 7.4; absorb, 64
-// tokens, 16 heads: 64 columns 3.6 us, 256 4.8.
-int proj_tile_cols(int tokens, int heads, int cols, int sm_count) {
+// tokens, 16 heads: 64 columns 3.6 us, 256 4.8.  Large absorbs, which are bound
+// by their writes (a sum of 128 terms an element), do better with narrower
+// tiles once there are many: 2048 tokens, 128 heads, R = 512 64 us at 128 columns,
+// 72 at 256 (a plain fill 67); 4096 tokens, 32 heads 32.1 and 33.3; but 500 tokens,
+// 128 heads 18.6 and 17.1; expand, R = 256, 5001 tokens, 128 heads 88 and 78.
+int proj_tile_cols(int mode, int tokens, int heads, int cols, int sm_count) {
   const int64_t blocks = static_cast<int64_t>((tokens + TM - 1) / TM) * heads;
+  if (mode == kProjAbsorb && blocks * (cols / 128) >= 24 * static_cast<int64_t>(sm_count)) return 128;
   const int rows = tokens < TM ? tokens : TM;
   int best = 0;
   int64_t best_cost = 0;

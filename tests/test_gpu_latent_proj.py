@@ -131,3 +131,17 @@ def test_no_tokens(cuda_dev):
     w = torch.zeros(4 * 256, 256, dtype=torch.bfloat16, device="cuda")
     k, v = mla.expand_kv(torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"), w, 4)
     assert k.shape == v.shape == (0, 4, 128)
+
+
+@pytest.mark.parametrize("T,H,R", [(2047, 128, 256), (1537, 64, 512)])
+def test_many_tiles(cuda_dev, T, H, R):
+    """Sizes past the changes of tile width and of CTA pairs, sampled heads."""
+    g = torch.Generator("cuda").manual_seed(8)
+    w = normal(g, H * 256, R)
+    W = w.view(H, 256, R)
+    for op, shape in (("absorb", (T, H, 128)), ("expand", (T, R)), ("project", (T, H, R))):
+        x = normal(g, *shape)
+        y = call(op, x, w, H)
+        for h in (0, H // 2, H - 1):
+            xs = x if op == "expand" else x[:, h:h + 1]
+            check(op, y[:, h:h + 1], xs, W[h].contiguous(), 1, R)
