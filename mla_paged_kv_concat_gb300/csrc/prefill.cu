@@ -660,70 +660,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int64_t q_row = u.q_row + row;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      // flagged keys of the cut tiles that this row attends to
+      // keys of the cut tiles with values that are not finite
       uint32_t any = 0;
       const int um = first_masked(u, 0, p.causal), nm = u.n(t) - um;
       if (n > 0) {
-        for (int k = 0; k < nm; ++k)
-          for (int w = 0; w < 4; ++w) any |= flags(i)[k * 4 + w];
+        for (int k = 0; k < nm; ++k) {
+          const uint4 x = *reinterpret_cast<const uint4*>(flags(i) + k * 4);
+          any |= x.x | x.y | x.z | x.w;
+        }
       }
-      const int64_t part = (static_cast<int64_t>(u.split) * p.num_tokens + q_row) * p.heads + u.h;
+      if (any) {  // the whole tile: those values into O for the rows that attend to their keys
 #pragma unroll 1
-      for (int q = 0; q < kDv; q += 32) {
-        uint32_t o[32];
-        __syncwarp();
-        if (n > 0) {
+        for (int q = 0; q < kDv; q += 32) {
+          uint32_t o[32];
           tc::ld_32x32b_x32(o_col + q, o);
           tc::wait_ld();
           tc::reg_fence(o);
-        } else {
+          for (int k = 0; k < nm * 4; ++k) {
+            uint32_t bits = flags(i)[k];
+            while (bits) {
+              const int key = um * kTile + k * 32 + __ffs(bits) - 1;
+              bits &= bits - 1;
+              if (key >= lim || !live) continue;
+              const uint16_t* v = p.v + (static_cast<int64_t>(u.k_row) + u.ks + key) * p.v_row_stride +
+                                  u.h * p.v_head_stride + q;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0;
-        }
-        if (live && any) {
-          for (int k = 0; k < nm; ++k) {
-            for (int w = 0; w < 4; ++w) {
-              uint32_t bits = flags(i)[k * 4 + w];
-              while (bits) {
-                const int key = (um + k) * kTile + w * 32 + __ffs(bits) - 1;
-                bits &= bits - 1;
-                if (key >= lim) continue;
-                const uint16_t* v =
-                    p.v + (static_cast<int64_t>(u.k_row) + u.ks + key) * p.v_row_stride +
-                    u.h * p.v_head_stride + q;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const uint32_t x = __ldg(v + e);
-                  if (!finite_bf16(x))
-                    o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(x << 16));
-                }
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t x = __ldg(v + e);
+                if (!finite_bf16(x))
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(x << 16));
               }
             }
           }
+          __syncwarp();
+          tc::st_32x32b_x32(o_col + q, o);
         }
-        if (live && p.num_splits == 1) {
-          // rows of different lanes lie far apart, so a store costs a cycle for
-          // each lane: 32 bytes at once where the output is aligned for it
-          uint16_t* dst = p.o + q_row * p.o_row_stride + u.h * p.o_head_stride + q;
-          uint32_t w[16];
+        tc::wait_st();
+      }
+      const int64_t part = (static_cast<int64_t>(u.split) * p.num_tokens + q_row) * p.heads + u.h;
+      uint32_t o[kDv];
+      if (n > 0) {
 #pragma unroll
-          for (int f = 0; f < 16; ++f)
-            w[f] = pack_bf16x2(__uint_as_float(o[2 * f]) * inv, __uint_as_float(o[2 * f + 1]) * inv);
-          if (p.o_aligned32) {
-            store32(dst, &w[0]);
-            store32(dst + 16, &w[8]);
-          } else {
+        for (int q = 0; q < 4; ++q)
+          tc::ld_32x32b_x32(o_col + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[q * 32]));
+        tc::wait_ld();
+        tc::reg_fence(o);
+      } else {
 #pragma unroll
-            for (int f = 0; f < 16; f += 4)
-              *reinterpret_cast<uint4*>(dst + 2 * f) = make_uint4(w[f], w[f + 1], w[f + 2], w[f + 3]);
-          }
-        } else if (live && n > 0) {
-          float* dst = p.ws_o + part * kDv + q;
+        for (int e = 0; e < kDv; ++e) o[e] = 0;
+      }
+      // Rows of different lanes lie far apart, so a store costs a cycle for
+      // each lane: 32 bytes at once where the output is aligned for it.
+      if (live && p.num_splits == 1) {
+        uint16_t* dst = p.o + q_row * p.o_row_stride + u.h * p.o_head_stride;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+        for (int f = 0; f < kDv / 2; ++f)
+          o[f] = pack_bf16x2(__uint_as_float(o[2 * f]) * inv, __uint_as_float(o[2 * f + 1]) * inv);
+        if (p.o_aligned32) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) store32(dst + e, &o[e]);
+          for (int f = 0; f < kDv / 2; f += 8) store32(dst + 2 * f, &o[f]);
+        } else {
+#pragma unroll
+          for (int f = 0; f < kDv / 2; f += 4)
+            *reinterpret_cast<uint4*>(dst + 2 * f) = make_uint4(o[f], o[f + 1], o[f + 2], o[f + 3]);
         }
+      } else if (live && n > 0) {
+        float* dst = p.ws_o + part * kDv;
+#pragma unroll
+        for (int e = 0; e < kDv; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+#pragma unroll
+        for (int e = 0; e < kDv; e += 8) store32(dst + e, &o[e]);
       }
       if (live) {
         float lg;
