@@ -7,7 +7,10 @@
  * step's new tokens (plain, or fused with the RMSNorm of the latent and the
  * rotary embedding), the split-KV attention pass over the paged latent cache
  * and the log-sum-exp merge -- plus the cross-shard merge of decode context
- * parallelism and prepared, CUDA-graph-safe plans of a whole step:
+ * parallelism, prepared, CUDA-graph-safe plans of a whole step, and the calls
+ * that make a layer of it: a step's block tables and slot map from request
+ * lengths, the gather of cached rows, the products with the kv_b weight and
+ * the expanded form's attention over prompts:
  *
  *   [diff] "frozenleaves/vllm compare v0.11.0...mla_cuda_graphs" ("fix TP"),
  *          a unified diff of vLLM, cited by file section;

@@ -24,7 +24,7 @@
 
 #include "kernels.cuh"
 #include "ptx.cuh"
-#include "tc.cuh"
+#include "tc.cuh"  // cluster helpers
 
 namespace mla {
 

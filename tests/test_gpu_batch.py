@@ -94,7 +94,9 @@ def run(pool, ids, new, ctx, T, alias, stream=None):
 @pytest.mark.parametrize("B,bs,max_new,max_ctx,pad,seed", [
     (1, 64, 1, 0, 0, 1), (1, 1, 7, 3, 5, 2), (3, 16, 40, 70, 0, 3), (64, 64, 1, 4096, 0, 4),
     (257, 16, 33, 300, 100, 5), (300, 128, 3, 5000, 1, 6), (2, 1024, 5000, 3000, 9, 7),
-    (1000, 48, 2, 400, 0, 8),
+    (1000, 48, 2, 400, 0, 8), (8192, 16, 2, 50, 3, 9),
+    # rows of several pieces, 16-byte aligned and not
+    (5, 1, 1000, 4000, 7, 10), (5, 1, 1001, 4000, 0, 11),
 ])
 def test_matches_the_walk(cuda_dev, B, bs, max_new, max_ctx, pad, seed, alias):
     rng = np.random.default_rng(seed)
@@ -167,7 +169,7 @@ def test_steps_in_place_then_release(cuda_dev):
     assert free.tolist() == want
 
 
-@pytest.mark.parametrize("B,pages,seed", [(1, 1, 1), (7, 40, 2), (600, 30, 3)])
+@pytest.mark.parametrize("B,pages,seed", [(1, 1, 1), (7, 40, 2), (600, 30, 3), (8192, 3, 4)])
 def test_release_leaves_bad_entries_out(cuda_dev, B, pages, seed):
     rng = np.random.default_rng(seed)
     bs, nb = 16, 100000
