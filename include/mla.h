@@ -653,7 +653,7 @@ mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_str
  * axis into: as many as give every SM one part where the 256-row query blocks
  * of all heads leave SMs idle (no part shorter than 1024 keys of the longest
  * sequence), a few more where sequences have at most 64 rows on average and
- * there are fewer than four blocks for every SM (their lengths may differ; no
+ * there are fewer than six blocks for every SM (their lengths may differ; no
  * part shorter than 2048 keys), else 1; at most 64.  max_kv_len: longest
  * sequence's keys (an upper bound will do).
  */

@@ -23,7 +23,7 @@
 // own chain - softmax, barriers, its products - comes to ~3050 and is the
 // bound.  Measured: a prompt of 8192 tokens, 16 heads, 217 us, 1580 TFLOP/s of
 // the causal half, tensor core 70 % busy (176 us without softmax and loads);
-// 17 rows against eight contexts of up to 32768 keys, 225 us, 5.5 TB/s.
+// 17 rows against eight contexts of up to 32768 keys, 218 us, 5.7 TB/s.
 //   TMEM (512 columns): S0, S1 (128 each; P as packed bf16 over the first 64
 //     of its S), O0, O1 (128 each).
 //   Shared memory: Q 2 x 48 KiB, a ring of eight 16 KiB boxes in the order K

@@ -164,7 +164,7 @@ def test_split_rule_and_workspace():
     assert f(8192, 1, 16, 8192, 152) == 1          # the blocks fill the SMs
     assert f(256, 1, 16, 32768, 152) == 9          # 16 units: nine parts each
     assert f(16, 1, 16, 4096, 152) == 4            # none under 1024 keys
-    assert f(24, 8, 16, 32768, 152) == 5           # few rows: lengths evened out
+    assert f(24, 8, 16, 32768, 152) == 8           # few rows: lengths evened out
     assert f(24, 8, 16, 4096, 152) == 2
     assert f(64, 64, 16, 4096, 152) == 1
     assert f(1000, 1, 16, 1000, 152) == 1
