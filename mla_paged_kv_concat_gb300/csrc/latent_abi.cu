@@ -354,10 +354,13 @@ mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_str
 
 // Measured on GB300, 16 heads (us at S = 1 / the rule's S / twice that): one
 // sequence of 256 rows, 32768 keys: 438 / 80 (8) / 98; two of 500 rows, 4596 keys:
-// 72 / 53 (2) / 63; eight of 1 to 5 rows, 4096 to 32768 keys: 381 / 218 (8) / 233;
-// 16 of 1 to 8 rows, 1000 to 30000 keys: 466 / 326 (4) / 321 (6); 32 of one row, 500
-// to 16000 keys: 388 / 351 (2) / 345; 64 of one row, 4096 keys: 363 (1) / 384; 1000
-// rows, 1000 keys: 23 (1) / 26.
+// 72 / 53 (2) / 63; contexts of 4096 to 32768 keys, eight of 1 to 5 rows: 382 / 218 (8)
+// / 228; of 1000 to 30000 keys, 16 of 1 to 8 rows: 465 / 325 (4) / 323; of 500 to 16000
+// keys, one row each, 32: 388 / 351 (2) / 344, 40: 469 / 437 (2) / 434, 56: 659 / 629 (2)
+// / 630; of 4096 keys each, one row, 48: 309 / 299 (2) / 292, 56: 315 / 337 (2) / 338 (the
+// rule's worst, it does not see that the lengths are equal), 64: 364 (1) / 383; 1000
+// rows, 1000 keys: 23 (1) / 26.  With 4 for 6 below the first three ragged ones took
+// 225 (5), 336 (3) and 351 (2).
 int mla_prefill_num_kv_splits(int num_tokens, int num_seqs, int num_heads, int64_t max_kv_len,
                               int sm_count) {
   if (num_tokens < 1 || num_seqs < 1 || num_heads < 1 || max_kv_len < 1 || sm_count < 1) return 1;
@@ -370,8 +373,9 @@ int mla_prefill_num_kv_splits(int num_tokens, int num_seqs, int num_heads, int64
     // Nearly every SM has a unit.  With few rows a sequence its length is what
     // a unit takes; parts of it even out lengths that differ.
     s = 1;
-    if (num_tokens <= 64 * static_cast<int64_t>(num_seqs) && units < 6 * static_cast<int64_t>(sm_count)) {
-      s = (6 * static_cast<int64_t>(sm_count) + units - 1) / units;
+    const int64_t parts = 6 * static_cast<int64_t>(sm_count);
+    if (num_tokens <= 64 * static_cast<int64_t>(num_seqs) && units < parts) {
+      s = (parts + units - 1) / units;
       most = max_kv_len / 2048;
     }
   }
