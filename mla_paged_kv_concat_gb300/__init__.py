@@ -380,7 +380,12 @@ _bind_module = None
 def _bind():
     """The compiled binding (csrc/bind.cpp): it checks the tensors (dtype,
     shape, unit last stride, on the current device; ValueError), allocates
-    outputs that are not given and calls the library (MlaError)."""
+    outputs that are not given and calls the library (MlaError).
+
+    A call runs on ``stream``, by default the current one, and what it
+    allocates (outputs, workspace) is that stream's memory.  With another
+    stream than the current one the caller makes it wait for the inputs, and
+    the current one wait for it before the outputs are used there."""
     global _bind_module
     if _bind_module is None:
         _torch()

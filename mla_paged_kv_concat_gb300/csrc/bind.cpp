@@ -113,10 +113,28 @@ struct Call {
     own_stream = true;
   }
   void* s() const { return stream->stream(); }
-  Tensor empty(at::IntArrayRef size, at::ScalarType dtype) const {
-    Tensor t = at::empty(size, at::TensorOptions().dtype(dtype).device(at::kCUDA, dev));
-    if (own_stream) t.record_stream(*stream);
+  // Memory of the stream that the kernels run on.  A block of the current
+  // stream's pool may still be in use by work queued there, which a kernel on
+  // another stream does not wait for.  The caller may use what it gets on its
+  // own current stream too, so a block is not given out again before that.
+  template <typename F>
+  Tensor allocate(F&& f) const {
+    if (!own_stream) return f();
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(dev);
+    const c10::cuda::CUDAStreamGuard guard(*stream);
+    Tensor t = f();
+    if (current != *stream) t.record_stream(current);
     return t;
+  }
+  Tensor empty(at::IntArrayRef size, at::ScalarType dtype) const {
+    return allocate([&] {
+      return at::empty(size, at::TensorOptions().dtype(dtype).device(at::kCUDA, dev));
+    });
+  }
+  Tensor zeros(at::IntArrayRef size, at::ScalarType dtype) const {
+    return allocate([&] {
+      return at::zeros(size, at::TensorOptions().dtype(dtype).device(at::kCUDA, dev));
+    });
   }
 };
 
@@ -243,11 +261,7 @@ PyObject* batch_build(PyObject*, PyObject* const* a, Py_ssize_t n) {
             "num_tokens is needed when no token output is given");
       tokens = given.size(0);
     }
-    if (!bt.defined()) {
-      // the zeros are written on the stream that the kernel runs on
-      c10::cuda::CUDAStreamGuard guard(*c.stream);
-      bt = at::zeros({B, maxb}, table.options());
-    }
+    if (!bt.defined()) bt = c.zeros({B, maxb}, kI32);
     if (!seq.defined()) seq = c.empty({B}, kI32);
     if (!cu_q.defined()) cu_q = c.empty({B + 1}, kI32);
     if (!cu_k.defined()) cu_k = c.empty({B + 1}, kI32);
