@@ -127,6 +127,25 @@ def _stream_ptr(stream=None) -> int:
     return int(s.cuda_stream)
 
 
+def _empty(stream, *shape, dtype, device, returned=True):
+    """Memory of the stream that a call runs on.  A block of the current
+    stream's pool may still be in use by work queued there, which a kernel on
+    another stream does not wait for.  What is returned may be used on the
+    caller's own current stream too, so its block is not given out again
+    before that."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(*shape, dtype=dtype, device=device)
+    if returned and current != stream:
+        t.record_stream(current)
+    return t
+
+
 def _kv_dtype(kv_cache, kv_cache_dtype: str | None) -> int:
     torch = _torch()
     if kv_cache_dtype in (None, "auto"):
@@ -216,14 +235,15 @@ def decode(q, kv_cache, block_table, seq_lens, sm_scale: float, num_kv_splits: i
     ``block_table`` int32 [seqs, max_blocks]; ``seq_lens`` int32 [seqs];
     ``kv_scale`` device fp32 tensor for fp8 caches; ``workspace`` a device
     buffer of at least ``mla_decode_workspace_bytes`` bytes (allocated here
-    when omitted and needed).
+    when omitted and needed).  What is allocated here is memory of the stream
+    that the call runs on (``stream``, by default the current one).
     """
     if isinstance(q, (tuple, list)):
         q_nope, q_pe = q
         plan = DecodePlan(q_nope, kv_cache, block_table, seq_lens, sm_scale, num_kv_splits,
                           q_pe=q_pe, kv_cache_dtype=kv_cache_dtype, kv_scale=kv_scale,
                           workspace=workspace, out=out, lse=lse, err_count=err_count,
-                          path=path)
+                          path=path, _stream=stream)
         try:
             plan.run(stream)
         finally:
@@ -238,12 +258,12 @@ def decode(q, kv_cache, block_table, seq_lens, sm_scale: float, num_kv_splits: i
     P = d - R
     seqs = seq_lens.numel()
     if out is None:
-        out = torch.empty(rows, H, R, dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, rows, H, R, dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty(rows, H, dtype=torch.float32, device=q.device)
+        lse = _empty(stream, rows, H, dtype=torch.float32, device=q.device)
     need = mla_decode_workspace_bytes(rows, H, num_kv_splits, R)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, need, dtype=torch.uint8, device=q.device, returned=False)
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = load().mla_decode_ex(
@@ -263,7 +283,9 @@ class DecodePlan:
 
     ``run()`` only launches kernels, so it can be captured into a CUDA graph
     and replayed after new values are copied into the same tensors.  The
-    tensors are kept referenced for the plan's life.
+    tensors are kept referenced for the plan's life; those not given are
+    allocated here, on the current stream: another stream waits for that one
+    before its first ``run``.
 
     ``q``: [rows, H, R+P] bf16, or dims [0, R) when ``q_pe`` [rows, H, P] is
     given.  ``write``: optional dict(kv_c, k_pe, slot_mapping) of the step's
@@ -276,7 +298,7 @@ class DecodePlan:
     def __init__(self, q, kv_cache, block_table, seq_lens, sm_scale: float, num_kv_splits: int,
                  *, q_pe=None, kv_cache_dtype: str | None = None, kv_scale=None,
                  workspace=None, out=None, lse=None, err_count=None,
-                 path: int = MLA_PATH_AUTO, write=None, norm_rope=None):
+                 path: int = MLA_PATH_AUTO, write=None, norm_rope=None, _stream=None):
         import ctypes
         torch = _torch()
         kvd = _kv_dtype(kv_cache, kv_cache_dtype)
@@ -291,12 +313,12 @@ class DecodePlan:
             assert dq == d
         assert R + P == d
         if out is None:
-            out = torch.empty(rows, H, R, dtype=torch.bfloat16, device=q.device)
+            out = _empty(_stream, rows, H, R, dtype=torch.bfloat16, device=q.device)
         if lse is None:
-            lse = torch.empty(rows, H, dtype=torch.float32, device=q.device)
+            lse = _empty(_stream, rows, H, dtype=torch.float32, device=q.device)
         need = mla_decode_workspace_bytes(rows, H, num_kv_splits, R)
         if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _empty(_stream, need, dtype=torch.uint8, device=q.device, returned=False)
         self.out, self.lse = out, lse
         self._keep = [q, q_pe, kv_cache, block_table, seq_lens, kv_scale, workspace, out, lse,
                       err_count, write, norm_rope]
@@ -357,15 +379,16 @@ def lse_merge(o_parts, lse_parts, *, out=None, lse=None, stream=None):
     ``o_parts`` bf16 [G, rows, H, R] and ``lse_parts`` fp32 [G, rows, H]: the
     (o, lse) of G disjoint KV token shards of the same query vectors, each
     part dense in (rows, H, R) / (rows, H); lse = -inf marks an empty part.
+    What is allocated here is memory of the stream that the call runs on.
     """
     torch = _torch()
     G, rows, H, R = o_parts.shape
     assert lse_parts.shape == (G, rows, H)
     assert o_parts.stride()[1:] == (H * R, R, 1) and lse_parts.stride()[1:] == (H, 1)
     if out is None:
-        out = torch.empty(rows, H, R, dtype=torch.bfloat16, device=o_parts.device)
+        out = _empty(stream, rows, H, R, dtype=torch.bfloat16, device=o_parts.device)
     if lse is None:
-        lse = torch.empty(rows, H, dtype=torch.float32, device=o_parts.device)
+        lse = _empty(stream, rows, H, dtype=torch.float32, device=o_parts.device)
     st = load().mla_lse_merge(
         o_parts.data_ptr(), o_parts.stride(0), lse_parts.data_ptr(), lse_parts.stride(0), G,
         rows, H, R, out.data_ptr(), lse.data_ptr(), _stream_ptr(stream))

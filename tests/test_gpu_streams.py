@@ -30,6 +30,8 @@ def make_calls():
     table = i32([list(range(nb))])
     rows, free, count = i32([[-1] * nb]), i32(list(range(nb))), i32([nb])
     new, old = i32([T]), i32([0])
+    ql, lens = normal(g, T, H, R + 64), i32([4000] * T)
+    tables, parts, lses = table.repeat(T, 1), normal(g, 3, T, H, R), normal(g, 3, T, H).float()
     return {
         "batch_build": lambda s: mla.batch_build(new, old, rows, free, count, bs, nb, T, stream=s),
         "gather_cache": lambda s: mla.gather_cache(cache, table, cu, T, stream=s),
@@ -38,10 +40,15 @@ def make_calls():
         "project_v": lambda s: (mla.project_v(o, w, stream=s),),
         "prefill": lambda s: mla.prefill(q, kv[..., :128], kv[..., 128:], k_pe, cu, cu, SCALE,
                                          num_kv_splits=3, stream=s),
+        "decode": lambda s: mla.decode(ql, cache, tables, lens, SCALE, 4, stream=s),
+        "decode_pair": lambda s: mla.decode((ql[..., :R], ql[..., R:]), cache, tables, lens, SCALE,
+                                            4, stream=s),
+        "lse_merge": lambda s: mla.lse_merge(parts, lses, stream=s),
     }
 
 
-NAMES = ["batch_build", "gather_cache", "expand_kv", "absorb_q", "project_v", "prefill"]
+NAMES = ["batch_build", "gather_cache", "expand_kv", "absorb_q", "project_v", "prefill",
+         "decode", "decode_pair", "lse_merge"]
 
 
 def wait_inputs(side):
@@ -110,3 +117,46 @@ def test_two_split_attentions_on_two_streams(cuda_dev):
         torch.cuda.synchronize()
         for (o, lse), (_, want) in zip(got, cases):
             assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_captured_on_a_forked_stream(cuda_dev, name):
+    """A call on a stream that joins a capture: its memory is the graph's."""
+    call = make_calls()[name]
+    ref = [x.clone() for x in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        wait_inputs(side)
+        out = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for x in out:
+        x.zero_()
+    gr.replay()
+    other = call(None)  # nothing of the graph's memory
+    gr.replay()
+    torch.cuda.synchronize()
+    for x, y, r in zip(out, other, ref):
+        assert torch.equal(x, r) and torch.equal(y, r)
+
+
+@pytest.mark.parametrize("split_call", ["decode", "decode_pair"])
+def test_workspaces_do_not_pile_up(cuda_dev, split_call):
+    """Calls one after the other on a stream use one workspace, however long
+    the current stream is busy."""
+    call = make_calls()[split_call]
+    side = torch.cuda.Stream()
+    wait_inputs(side)
+    active = lambda: torch.cuda.memory_stats()["active_bytes.all.current"]  # noqa: E731
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    keep = [call(side)]
+    used = sum(x.nbytes for x in keep[0])
+    torch.cuda._sleep(400_000_000)
+    start = active()
+    for _ in range(8):
+        keep.append(call(side))
+    grown = active() - start
+    torch.cuda.synchronize()
+    assert grown <= 8 * (used + 8 * 512), (grown, used)
