@@ -115,24 +115,25 @@ struct Call {
   void* s() const { return stream->stream(); }
   // Memory of the stream that the kernels run on.  A block of the current
   // stream's pool may still be in use by work queued there, which a kernel on
-  // another stream does not wait for.  The caller may use what it gets on its
-  // own current stream too, so a block is not given out again before that.
+  // another stream does not wait for.  The caller may use what is returned on
+  // its own current stream too, so such a block is not given out again before
+  // that.
   template <typename F>
-  Tensor allocate(F&& f) const {
+  Tensor allocate(bool returned, F&& f) const {
     if (!own_stream) return f();
     const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(dev);
     const c10::cuda::CUDAStreamGuard guard(*stream);
     Tensor t = f();
-    if (current != *stream) t.record_stream(current);
+    if (returned && current != *stream) t.record_stream(current);
     return t;
   }
-  Tensor empty(at::IntArrayRef size, at::ScalarType dtype) const {
-    return allocate([&] {
+  Tensor empty(at::IntArrayRef size, at::ScalarType dtype, bool returned = true) const {
+    return allocate(returned, [&] {
       return at::empty(size, at::TensorOptions().dtype(dtype).device(at::kCUDA, dev));
     });
   }
   Tensor zeros(at::IntArrayRef size, at::ScalarType dtype) const {
-    return allocate([&] {
+    return allocate(true, [&] {
       return at::zeros(size, at::TensorOptions().dtype(dtype).device(at::kCUDA, dev));
     });
   }
@@ -478,7 +479,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const size_t need = mla_prefill_workspace_bytes(Ti, Hi, splits, kV);
     if (need && !ws.defined()) {
       CHECK(need <= static_cast<size_t>(INT64_MAX), "the workspace does not fit");
-      ws = c.empty({static_cast<int64_t>(need)}, at::kByte);
+      ws = c.empty({static_cast<int64_t>(need)}, at::kByte, false);
     }
     CHECK(!ws.defined() || ws.is_contiguous(), "workspace must be contiguous");
     const Strides sq(q), sk(k), sv(v), so(out), sp = q_pe.defined() ? Strides(q_pe) : Strides();

@@ -141,7 +141,7 @@ def test_captured_on_a_forked_stream(cuda_dev, name):
         assert torch.equal(x, r) and torch.equal(y, r)
 
 
-@pytest.mark.parametrize("split_call", ["decode", "decode_pair"])
+@pytest.mark.parametrize("split_call", ["prefill", "decode", "decode_pair"])
 def test_workspaces_do_not_pile_up(cuda_dev, split_call):
     """Calls one after the other on a stream use one workspace, however long
     the current stream is busy."""
