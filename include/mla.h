@@ -503,7 +503,8 @@ void mla_plan_destroy(mla_decode_plan* plan);
  * order.  For batch entry b with row r = req_ids[b] (b without req_ids),
  * c = context_lens[b] tokens cached and n = query_lens[b] new ones:
  *   seq_lens[b] = c + n;  cu_seqlens_q / cu_seqlens_k: sums of n / of c + n
- *               over the entries before b (num_reqs + 1 values);
+ *               over the entries before b (num_reqs + 1 values, each at most
+ *               INT32_MAX);
  *   pages       the row holds ceil(c / bs) pages and gets ceil((c + n) / bs);
  *               new page k of the batch (entries in order, pages in order) is
  *               free_blocks[*free_count - 1 - k], written into the row;

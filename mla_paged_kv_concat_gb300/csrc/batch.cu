@@ -271,12 +271,14 @@ __global__ void __launch_bounds__(kThreads, 3) batch_build_kernel(const BatchPar
   int* off = sm + B;      // [B] new pages before each request
   int* ctx = sm + 2 * B;  // [B]
   int* row = sm + 3 * B;  // [B]
+  int* seq = sm + 4 * B;  // [B] cached + new; not ctx + a step of cuq, which saturates
   const int count = stack_count(p);
   const longlong2 total = scan_reqs<false>(
       p, part,
       [&](int b, const Req& r) {
         ctx[b] = r.ctx;
         row[b] = r.row;
+        seq[b] = r.seq;
       },
       [&](int b, long long n, long long pages) {
         cuq[b] = sat32(n);
@@ -293,10 +295,8 @@ __global__ void __launch_bounds__(kThreads, 3) batch_build_kernel(const BatchPar
       // ones off the stack
       const int b = static_cast<int>(u / p.row_pieces);
       const int i0 = static_cast<int>(u % p.row_pieces) * kPiece;
-      const long long n = (b + 1 < B ? cuq[b + 1] : total.x) - cuq[b];
       const int c = ctx[b], rw = row[b];
-      const int seq = c + n > p.capacity ? p.capacity : static_cast<int>(c + n);
-      const int end = min(pages_of(p, seq), i0 + kPiece);
+      const int end = min(pages_of(p, seq[b]), i0 + kPiece);
       const int old_all = rw < 0 ? 0 : pages_of(p, c), old = min(old_all, end);
       int32_t* dst = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
       int32_t* req = rw < 0 ? nullptr : p.req_table + static_cast<int64_t>(rw) * p.rt_stride;
@@ -481,7 +481,7 @@ cudaError_t launch_batch_build(const BatchParams& p_in, int sm_count, cudaStream
   BatchParams p = p_in;
   page_reciprocal(&p);
   static std::atomic<uint64_t> attr_done{0};
-  cudaError_t e = set_smem_attr_once(batch_build_kernel, 4 * kMaxBatchReqs * 4, attr_done);
+  cudaError_t e = set_smem_attr_once(batch_build_kernel, 5 * kMaxBatchReqs * 4, attr_done);
   if (e != cudaSuccess) return e;
   // max_blocks is capacity / block_size
   p.row_pieces = (p.capacity / p.block_size + kPiece - 1) / kPiece;
@@ -491,7 +491,7 @@ cudaError_t launch_batch_build(const BatchParams& p_in, int sm_count, cudaStream
   const int grid = 1 + static_cast<int>(ctas < 1 ? 1 : ctas < most ? ctas : most);
   p.defer_count = p.free_count == p.free_count_out;
   e = launch_overlapped(batch_build_kernel, dim3(grid), dim3(kThreads),
-                        4 * static_cast<size_t>(p.num_reqs) * 4, stream, p);
+                        5 * static_cast<size_t>(p.num_reqs) * 4, stream, p);
   if (e != cudaSuccess || !p.defer_count) return e;
   return launch_overlapped(batch_count_kernel, dim3(1), dim3(kThreads), 0, stream, p);
 }
