@@ -139,8 +139,9 @@ __device__ __forceinline__ void count_errors(int* err_count, int errs) {
   if ((threadIdx.x & 31) == 0 && errs) atomicAdd(err_count, errs);
 }
 
+// A plain load: blocks_release_kernel may write this address before it ends.
 __device__ __forceinline__ int stack_count(const BatchParams& p) {
-  const int c = __ldg(p.free_count);
+  const int c = *p.free_count;
   return c < 0 ? 0 : (c > p.free_capacity ? p.free_capacity : c);
 }
 

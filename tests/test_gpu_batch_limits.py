@@ -1,5 +1,5 @@
-"""GPU tests of the batch tables beyond what a sound caller passes: sums of
-lengths past 32 bits."""
+"""GPU tests of the batch tables at their limits: sums of lengths past 32 bits,
+the stack's height read and written by one release."""
 import numpy as np
 import pytest
 import torch
@@ -43,3 +43,22 @@ def test_query_lengths_that_sum_past_32_bits(cuda_dev, new, ctx, ids, alias):
     held = np.concatenate([table[r, :-(-int(n) // bs)].cpu().numpy() for r, n in zip(rows, seq)])
     live = np.concatenate([held, pool.free[:pool.count]])
     assert len(set(live.tolist())) == len(live)
+
+
+@pytest.mark.parametrize("B,pages", [(1, 1), (64, 100), (8192, 60)])
+def test_release_in_place_is_release_apart(cuda_dev, B, pages):
+    """The height is read by every CTA and written by one before the others
+    end: the same stack as with an output of its own, however it is run."""
+    bs, nb = 16, B * pages + 50
+    perm = torch.randperm(nb, device="cuda", dtype=torch.int32)
+    table, held = perm[:B * pages].view(B, pages).contiguous(), i32([pages * bs] * B)
+    free0 = torch.full((nb,), -9, dtype=torch.int32, device="cuda")
+    free0[:50] = perm[B * pages:]
+    want = torch.cat([perm[B * pages:], perm[:B * pages]])
+    for _ in range(20):
+        for apart in (False, True):
+            free, count = free0.clone(), i32([50])
+            out = mla.blocks_release(held, table, free, count, bs, nb,
+                                     free_count_out=torch.empty_like(count) if apart else None)
+            assert torch.equal(free, want) and out.item() == nb
+            assert count.item() == (50 if apart else nb)
