@@ -624,8 +624,9 @@ mla_status mla_gather_cache(const void* kv_cache, mla_kv_dtype kv_dtype, int num
  * strides; fp32 accumulation, one rounding to bf16.  Every pointer is 16-byte
  * aligned, every stride a positive multiple of 8 (a head stride is not read
  * when num_heads is 1).  Outputs [num_tokens][num_heads][columns]: the
- * elements of one must not overlap each other or an input; k_nope and v may
- * be column ranges of one buffer.
+ * elements of one must not overlap each other, the other output or an input
+ * (refused where two tensors have rows at the same distance, or one has no
+ * gaps); columns of one buffer are fine, for k_nope and v as well.
  *   kv_lora_rank    512 or 256; nope_dim = v_dim = 128 (else
  *                   MLA_ERR_UNSUPPORTED).  num_heads 1 .. 1024.
  *   err_count       device int, may be NULL: +(1 << 20) if a pipeline wait

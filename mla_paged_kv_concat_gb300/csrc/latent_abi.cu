@@ -107,9 +107,69 @@ bool heads_disjoint(const Heads& t, int tokens, int heads) {
          t.hs >= (tokens - 1) * t.rs + t.cols;
 }
 
-// Bytes from the first to the last element.
-int64_t heads_bytes(const Heads& t, int tokens, int heads) {
-  return 2 * ((tokens - 1) * t.rs + (heads > 1 ? (heads - 1) * t.hs : 0) + t.cols);
+// The bytes of a tensor: runs of `len` at p + i * s[0] + j * s[1], the larger
+// stride first.
+struct Runs {
+  uintptr_t p;
+  int64_t n[2], s[2], len;
+  int64_t inner() const { return (n[1] - 1) * s[1] + len; }
+  int64_t span() const { return (n[0] - 1) * s[0] + inner(); }
+};
+Runs runs(const Heads& t, int tokens, int heads) {
+  Runs r{reinterpret_cast<uintptr_t>(t.p), {tokens, heads}, {2 * t.rs, 2 * t.hs},
+         2 * int64_t{t.cols}};
+  if (r.n[0] == 1 || (r.n[1] > 1 && r.s[1] > r.s[0])) {
+    const int64_t n = r.n[0], s = r.s[0];
+    r.n[0] = r.n[1];
+    r.s[0] = r.s[1];
+    r.n[1] = n;
+    r.s[1] = s;
+  }
+  for (int k = 1; k >= 0; --k) {  // runs that join are one
+    if (r.n[k] > 1 && r.s[k] == r.len && (k == 1 || r.n[1] == 1)) {
+      r.len *= r.n[k];
+      r.n[k] = 1;
+    }
+    if (r.n[k] == 1) r.s[k] = 0;
+  }
+  return r;
+}
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
+
+// The m of [lo, hi] with -lb < x + m * s < la, from first to last.
+struct Steps {
+  int64_t first, last;
+};
+Steps steps(int64_t x, int64_t s, int64_t lo, int64_t hi, int64_t la, int64_t lb) {
+  if (s == 0) return -lb < x && x < la ? Steps{lo, lo} : Steps{0, -1};
+  const int64_t a = floor_div(-lb - x, s) + 1, z = -floor_div(x - la, s) - 1;
+  return {a > lo ? a : lo, z < hi ? z : hi};
+}
+
+// Whether two tensors share a byte.  Exact but for two that both have rows
+// apart from each other, at different distances: those count as sharing one
+// only where they start at the same address.
+bool intersect(const Runs& a, const Runs& b) {
+  if (a.span() <= 0 || b.span() <= 0 || a.p + a.span() <= b.p || b.p + b.span() <= a.p)
+    return false;
+  if (a.p == b.p) return true;
+  if (a.s[0] && b.s[0] && a.s[0] != b.s[0]) return false;
+  const int64_t d = static_cast<int64_t>(b.p - a.p), s0 = a.s[0] ? a.s[0] : b.s[0];
+  const Steps k = steps(d, s0, 1 - a.n[0], b.n[0] - 1, a.inner(), b.inner());
+  for (int64_t m = k.first; m <= k.last; ++m) {
+    const int64_t x = d + m * s0;
+    if (!a.s[1] || !b.s[1] || a.s[1] == b.s[1]) {
+      const Steps j = steps(x, a.s[1] ? a.s[1] : b.s[1], 1 - a.n[1], b.n[1] - 1, a.len, b.len);
+      if (j.first <= j.last) return true;
+      continue;
+    }
+    for (int64_t i = 0; i < a.n[1]; ++i) {
+      const Steps j = steps(x - i * a.s[1], b.s[1], 0, b.n[1] - 1, a.len, b.len);
+      if (j.first <= j.last) return true;
+    }
+  }
+  return false;
 }
 
 mla_status heads_map(CUtensorMap* m, const Heads& t, int tokens, int heads, int box_rows) {
@@ -131,17 +191,13 @@ mla_status latent_proj(int mode, Heads in, int in_heads, int tokens, const void*
   if (!heads_disjoint(out0, tokens, heads) || (two && !heads_disjoint(out1, tokens, heads)))
     return MLA_ERR_INVALID_ARG;
   const int64_t wb = 2 * ((static_cast<int64_t>(heads) * (nope + vdim) - 1) * w_stride + R);
-  const int64_t ib = heads_bytes(in, tokens, in_heads);
-  for (int i = 0; i < (two ? 2 : 1); ++i) {
-    const Heads& o = i ? out1 : out0;
-    const int64_t ob = heads_bytes(o, tokens, heads);
-    if (overlap(o.p, ob, w, wb)) return MLA_ERR_INVALID_ARG;
-    // an output between an input's rows (columns of one buffer) is fine;
-    // only a dense overlap is refused
-    if (o.p == in.p || (ib == 2 * static_cast<int64_t>(tokens) * in_heads * in.cols &&
-                        overlap(o.p, ob, in.p, ib)))
-      return MLA_ERR_INVALID_ARG;
-  }
+  // outputs may lie between an input's rows or each other's (columns of one
+  // buffer)
+  const Runs r_in = runs(in, tokens, in_heads), r0 = runs(out0, tokens, heads);
+  const Runs r1 = two ? runs(out1, tokens, heads) : r0;
+  if (overlap(out0.p, r0.span(), w, wb) || intersect(r0, r_in) ||
+      (two && (overlap(out1.p, r1.span(), w, wb) || intersect(r1, r_in) || intersect(r0, r1))))
+    return MLA_ERR_INVALID_ARG;
   int sms = 0;
   cudaError_t e = mla::device_sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);

@@ -1,0 +1,68 @@
+"""Outputs of the calls around the decode that would lie over an input or each
+other are refused on the host before any launch (so those run without a GPU);
+columns of one buffer that do not meet are taken and hold the same bits."""
+import pytest
+import torch
+
+import mla_paged_kv_concat_gb300 as mla
+from test_latent_abi import ABSORB, EXPAND, PROJECT, args, at, lib  # noqa: F401
+
+# strides in elements, addresses in bytes: at(5) holds [10][16][256] of bf16
+ROW, HEAD = 16 * 256, 256
+
+
+@pytest.mark.parametrize("over", [
+    dict(v=at(5)),                                    # one buffer for both
+    dict(v=at(5) + 2 * 120),                          # columns that meet
+    dict(v=at(5) + 2 * HEAD),                         # the next head's k_nope
+    dict(v=at(5) + 2 * (3 * ROW + 2 * HEAD)),
+    dict(v=at(5) - 2 * (2 * ROW + HEAD)),
+    dict(v=at(5) + 2 * ROW, vhs=512, vrs=2 * 16 * 256, krs=2 * 16 * 256),   # other head strides
+    dict(k=at(5), krs=16 * 128, khs=128, v=at(5) + 2 * 4096),   # k_nope dense
+    dict(H=1, khs=0, vhs=0, v=at(5) + 2 * 64),
+    dict(T=1, v=at(5) + 2 * HEAD),
+    dict(khs=10 * 256, krs=256, vhs=10 * 256, vrs=256, v=at(5) + 2 * 256),  # head-major
+    # over rows of kv_c that lie apart
+    dict(c=at(1), cs=ROW, k=at(1) + 2 * 512, v=at(1) + 2 * 384, krs=ROW, khs=128, vrs=ROW, vhs=128, H=1),
+    dict(c=at(1), cs=1024, k=at(1) + 2 * 256, krs=1024, khs=128, H=1),
+    dict(c=at(1), cs=ROW, k=at(1) + 2 * (ROW - 128), krs=ROW, khs=256, H=2),
+])
+def test_expand_outputs(lib, over):  # noqa: F811
+    assert lib.mla_expand_kv(*args(EXPAND, over)) == 1
+
+
+@pytest.mark.parametrize("fn,base,over", [
+    # out among q_nope's columns [10][16][192], and among o's [10][16][512]
+    ("mla_absorb_q", ABSORB, dict(hs=1024, rs=16 * 1024, out=at(1) + 2 * 64, ohs=1024, ors=16 * 1024)),
+    ("mla_absorb_q", ABSORB, dict(hs=1024, rs=16 * 1024, out=at(1) - 2 * 504, ohs=1024, ors=16 * 1024)),
+    ("mla_project_v", PROJECT, dict(out=at(1) + 2 * 384, ohs=512, ors=16 * 512)),
+    ("mla_project_v", PROJECT, dict(out=at(1) + 2 * 512 * 16)),
+    ("mla_project_v", PROJECT, dict(hs=640, rs=16 * 640, out=at(1) + 2 * 632, ohs=640, ors=16 * 640)),
+])
+def test_head_product_outputs(lib, fn, base, over):  # noqa: F811
+    assert getattr(lib, fn)(*args(base, over)) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [(1, 1), (1, 16), (37, 1), (200, 5), (1000, 16)])
+def test_products_into_columns_of_one_buffer(cuda_dev, T, H):
+    g = torch.Generator("cuda").manual_seed(T + H)
+    normal = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    R = 512
+    c, w = normal(T, R), normal(H * 256, R)
+    k, v = mla.expand_kv(c, w, H)
+    halves = torch.zeros(T, H, 256, dtype=torch.bfloat16, device="cuda")
+    flat = torch.zeros(T, R + 2 * H * 128, dtype=torch.bfloat16, device="cuda")  # kv_c too
+    flat[:, :R] = c
+    heads = torch.zeros(H, T, 256, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    f = flat[:, R:].view(T, 2, H, 128) if T == 1 else flat[:, R:].unflatten(1, (2, H, 128))
+    for x, kk, vv in ((c, halves[..., :128], halves[..., 128:]), (flat[:, :R], f[:, 0], f[:, 1]),
+                      (c, heads[..., :128], heads[..., 128:]), (c, heads[..., 128:], heads[..., :128])):
+        mla.expand_kv(x, w, H, k_nope=kk, v=vv)
+        assert torch.equal(kk, k) and torch.equal(vv, v)
+    buf = torch.zeros(T, H, 192 + R + 128, dtype=torch.bfloat16, device="cuda")
+    buf[..., :192] = normal(T, H, 192)
+    ql = mla.absorb_q(buf[..., :128], w, out=buf[..., 192:192 + R])
+    y = mla.project_v(ql, w, out=buf[..., 192 + R:])
+    assert torch.equal(ql, mla.absorb_q(buf[..., :128].contiguous(), w))
+    assert torch.equal(y, mla.project_v(ql.contiguous(), w))
