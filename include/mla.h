@@ -705,9 +705,11 @@ size_t mla_prefill_workspace_bytes(int num_tokens, int num_heads, int num_kv_spl
  *   num_kv_splits   1 .. 64 parts of the key axis, joined by a second kernel
  *                   (see mla_prefill_num_kv_splits); 1 needs no workspace.
  *   workspace       >= mla_prefill_workspace_bytes(...), 32-byte aligned.
- *   o               bf16 [num_tokens][num_heads][v_dim] at its strides; must
- *                   not overlap an input.  lse fp32 [num_tokens][num_heads],
- *                   contiguous.  Rows of no sequence are left as they were.
+ *   o               bf16 [num_tokens][num_heads][v_dim] at its strides.  lse
+ *                   fp32 [num_tokens][num_heads], contiguous.  Rows of no
+ *                   sequence are left as they were.  o, lse and workspace must
+ *                   not overlap each other or an input (refused as for the
+ *                   products above).
  *   err_count       device int, may be NULL: clamped cu_seqlens; +(1 << 20)
  *                   if a pipeline wait timed out.
  * Run-to-run deterministic; a row's result depends on num_kv_splits but not on

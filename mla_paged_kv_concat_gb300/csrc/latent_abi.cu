@@ -115,6 +115,9 @@ struct Runs {
   int64_t inner() const { return (n[1] - 1) * s[1] + len; }
   int64_t span() const { return (n[0] - 1) * s[0] + inner(); }
 };
+Runs runs(const void* p, int64_t bytes) {
+  return {reinterpret_cast<uintptr_t>(p), {1, 1}, {0, 0}, p ? bytes : 0};
+}
 Runs runs(const Heads& t, int tokens, int heads) {
   Runs r{reinterpret_cast<uintptr_t>(t.p), {tokens, heads}, {2 * t.rs, 2 * t.hs},
          2 * int64_t{t.cols}};
@@ -484,8 +487,7 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
        !heads_ok(hkp, num_kv_tokens, 1)))
     return MLA_ERR_INVALID_ARG;
   if (!cu_seqlens_q || !cu_seqlens_k || !lse || !aligned4(cu_seqlens_q) ||
-      !aligned4(cu_seqlens_k) || !aligned4(lse) || !aligned4(err_count) || o == q || o == q_pe ||
-      o == k_nope || o == v)
+      !aligned4(cu_seqlens_k) || !aligned4(lse) || !aligned4(err_count))
     return MLA_ERR_INVALID_ARG;
   const size_t need = mla_prefill_workspace_bytes(num_tokens, num_heads, num_kv_splits, v_dim);
   if (need > 0) {
@@ -497,6 +499,25 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
   if ((num_tokens / 256 + static_cast<int64_t>(num_seqs)) * 2 * num_heads * num_kv_splits >
       INT32_MAX)
     return MLA_ERR_UNSUPPORTED;
+  const int64_t n_cu = (static_cast<int64_t>(num_seqs) + 1) * 4;
+  Runs in[7] = {runs(hq, num_tokens, num_heads), runs(hqp, num_tokens, num_heads),
+                runs(cu_seqlens_q, n_cu), runs(cu_seqlens_k, n_cu)};
+  int n_in = 4;
+  if (num_kv_tokens > 0) {
+    in[n_in++] = runs(hk, num_kv_tokens, num_heads);
+    in[n_in++] = runs(hv, num_kv_tokens, num_heads);
+    in[n_in++] = runs(hkp, num_kv_tokens, 1);
+  }
+  // what is not written (a workspace that is not needed) overlaps nothing
+  const Runs out[3] = {runs(ho, num_tokens, num_heads),
+                       runs(lse, static_cast<int64_t>(num_tokens) * num_heads * 4),
+                       runs(workspace, need > INT64_MAX ? INT64_MAX : static_cast<int64_t>(need))};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (intersect(out[i], in[j])) return MLA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (intersect(out[i], out[j])) return MLA_ERR_INVALID_ARG;
+  }
   mla::PrefillParams p = {};
   p.num_tokens = num_tokens;
   p.num_kv = num_kv_tokens;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import mla_paged_kv_concat_gb300 as mla
-from test_latent_abi import ABSORB, EXPAND, PROJECT, args, at, lib  # noqa: F401
+from test_latent_abi import ABSORB, EXPAND, PREFILL, PROJECT, args, at, lib  # noqa: F401
 
 # strides in elements, addresses in bytes: at(5) holds [10][16][256] of bf16
 ROW, HEAD = 16 * 256, 256
@@ -41,6 +41,48 @@ def test_expand_outputs(lib, over):  # noqa: F811
 ])
 def test_head_product_outputs(lib, fn, base, over):  # noqa: F811
     assert getattr(lib, fn)(*args(base, over)) == 1
+
+
+QROW = 16 * 192
+
+
+@pytest.mark.parametrize("over", [
+    # o in q's columns, at another offset and in other rows; in q_pe's
+    dict(o=at(1) + 2 * 32, ors=QROW, ohs=192), dict(o=at(1) + 2 * (2 * QROW + 128), ors=QROW, ohs=192),
+    dict(o=at(1) + 2 * QROW), dict(o=at(1) - 2 * 1024),
+    dict(qpe=at(9), qprs=QROW, qphs=192, o=at(9) + 2 * 48, ors=QROW, ohs=192),
+    # among the keys and values [30][16][256], over k_pe and the lengths
+    dict(o=at(2) + 2 * ROW, ors=ROW, ohs=HEAD), dict(o=at(2) + 2 * (5 * ROW + 120), ors=ROW, ohs=HEAD),
+    dict(o=at(2) + 2 * 4096), dict(o=at(3)), dict(o=at(3) + 2 * 64 * 29), dict(o=at(4)),
+    dict(o=at(5) - 2 * 2048), dict(o=at(8)), dict(o=at(6)), dict(o=at(6) + 10 * 16 * 2 * 129 * 4 - 16),
+    # lse and the workspace
+    dict(lse=at(1) + 64), dict(lse=at(2) + 4), dict(lse=at(3)), dict(lse=at(4) + 8), dict(lse=at(5) + 8),
+    dict(lse=at(6) + 400), dict(lse=at(7) + 10 * 16 * 256 - 4), dict(lse=at(7) - 636),
+    dict(ws=at(1) + 32), dict(ws=at(2)), dict(ws=at(3)), dict(ws=at(4)), dict(ws=at(5) - 160000),
+    dict(ws=at(7) + 32), dict(ws=at(8)),
+])
+def test_prefill_outputs(lib, over):  # noqa: F811
+    assert lib.mla_prefill(*args(PREFILL, over)) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("splits", [1, 3])
+def test_prefill_into_columns_of_its_inputs(cuda_dev, splits):
+    """q, k, v and o as columns of one buffer; a workspace that is not needed
+    may be anything."""
+    g = torch.Generator("cuda").manual_seed(3)
+    T, H = 200, 5
+    buf = torch.randn(T, H, 192 + 256 + 128, generator=g, device="cuda").to(torch.bfloat16)
+    kp = torch.randn(T, 64, generator=g, device="cuda").to(torch.bfloat16)
+    cu = torch.tensor([0, 70, T], dtype=torch.int32, device="cuda")
+    q, k, v, o = buf[..., :192], buf[..., 192:320], buf[..., 320:448], buf[..., 448:]
+    want = mla.prefill(q.contiguous(), k.contiguous(), v.contiguous(), kp, cu, cu, 0.07,
+                       num_kv_splits=splits)
+    ws = torch.empty(mla.mla_prefill_workspace_bytes(T, H, splits, 128), dtype=torch.uint8,
+                     device="cuda") if splits > 1 else q.contiguous()
+    got = mla.prefill(q, k, v, kp, cu, cu, 0.07, num_kv_splits=splits, out=o, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 @pytest.mark.gpu
