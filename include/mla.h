@@ -559,8 +559,8 @@ mla_status mla_batch_build(const int32_t* req_ids, const int32_t* query_lens,
  * outside [0, num_blocks) are left out and counted, and so are pages beyond
  * free_capacity.  The rows themselves are not changed.  Arguments as
  * mla_batch_build; num_reqs * max_blocks_per_req <= INT32_MAX; free_count_out
- * may be free_count.  Releasing one row twice in one call puts its pages on
- * the stack twice.
+ * may be free_count, else neither it nor the stack may overlap an input.
+ * Releasing one row twice in one call puts its pages on the stack twice.
  */
 mla_status mla_blocks_release(const int32_t* req_ids, const int32_t* held_lens, int num_reqs,
                               const int32_t* req_block_table, int64_t req_block_table_stride,

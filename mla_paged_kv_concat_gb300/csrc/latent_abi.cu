@@ -313,15 +313,19 @@ mla_status mla_blocks_release(const int32_t* req_ids, const int32_t* held_lens, 
   if (static_cast<int64_t>(num_reqs) * max_blocks_per_req > INT32_MAX)
     return MLA_ERR_UNSUPPORTED;
   const int64_t n4 = static_cast<int64_t>(num_reqs) * 4;
+  // the stack is written while other CTAs still read the rows, and the new
+  // height before the last of them ends
   const int64_t stack = static_cast<int64_t>(free_capacity) * 4;
-  if (overlap(free_blocks, stack, free_count, 4) ||
-      overlap(free_blocks, stack, free_count_out, 4) ||
-      overlap(free_blocks, stack, held_lens, n4) ||
-      overlap(free_blocks, stack, req_ids, req_ids ? n4 : 0) ||
-      overlap(free_blocks, stack, req_block_table,
-              num_reqs ? ((num_table_rows - 1) * req_block_table_stride + max_blocks_per_req) * 4
-                       : 0))
-    return MLA_ERR_INVALID_ARG;
+  const struct { const void* p; int64_t n; } in[] = {
+      {free_count, free_count == free_count_out ? 0 : 4},
+      {held_lens, n4},
+      {req_ids, req_ids ? n4 : 0},
+      {req_block_table,
+       num_reqs ? ((num_table_rows - 1) * req_block_table_stride + max_blocks_per_req) * 4 : 0}};
+  if (overlap(free_blocks, stack, free_count_out, 4)) return MLA_ERR_INVALID_ARG;
+  for (const auto& x : in)
+    if (overlap(free_blocks, stack, x.p, x.n) || overlap(free_count_out, 4, x.p, x.n))
+      return MLA_ERR_INVALID_ARG;
   p.free_out = free_blocks;
   cudaError_t e = mla::launch_blocks_release(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import mla_paged_kv_concat_gb300 as mla
-from test_latent_abi import ABSORB, EXPAND, PREFILL, PROJECT, args, at, lib  # noqa: F401
+from test_latent_abi import ABSORB, EXPAND, PREFILL, PROJECT, RELEASE, args, at, lib  # noqa: F401
 
 # strides in elements, addresses in bytes: at(5) holds [10][16][256] of bf16
 ROW, HEAD = 16 * 256, 256
@@ -41,6 +41,15 @@ def test_expand_outputs(lib, over):  # noqa: F811
 ])
 def test_head_product_outputs(lib, fn, base, over):  # noqa: F811
     assert getattr(lib, fn)(*args(base, over)) == 1
+
+
+@pytest.mark.parametrize("over", [
+    dict(cnt_out=at(2)), dict(cnt_out=at(2) + 12), dict(cnt_out=at(1) + 4), dict(cnt_out=at(4)),
+    dict(cnt_out=at(4) + (9 * 8 + 7) * 4), dict(cnt_out=at(5)), dict(cnt_out=at(5) + 196),
+    dict(ids=at(5) + 100),
+])
+def test_release_outputs(lib, over):  # noqa: F811
+    assert lib.mla_blocks_release(*args(RELEASE, over)) == 1
 
 
 QROW = 16 * 192
