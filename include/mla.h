@@ -587,7 +587,9 @@ mla_status mla_blocks_release(const int32_t* req_ids, const int32_t* held_lens, 
  *                   cu_seqlens[num_seqs] are left as they were.
  *   kv_c            bf16 [num_tokens][kv_lora_rank], k_pe bf16
  *                   [num_tokens][rope_dim] at the given row strides (multiples
- *                   of 8); both 16-byte aligned.
+ *                   of 8); both 16-byte aligned.  They may be columns of one
+ *                   buffer, but must not overlap each other or an input
+ *                   (refused as for the products below).
  *   kv_scale        device float, read only for the fp8 formats.
  *   err_count       device int, may be NULL: counts the rows whose position
  *                   lies outside the block table or whose block id lies

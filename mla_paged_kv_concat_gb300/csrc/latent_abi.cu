@@ -118,17 +118,9 @@ struct Runs {
 Runs runs(const void* p, int64_t bytes) {
   return {reinterpret_cast<uintptr_t>(p), {1, 1}, {0, 0}, p ? bytes : 0};
 }
-Runs runs(const Heads& t, int tokens, int heads) {
-  Runs r{reinterpret_cast<uintptr_t>(t.p), {tokens, heads}, {2 * t.rs, 2 * t.hs},
-         2 * int64_t{t.cols}};
-  if (r.n[0] == 1 || (r.n[1] > 1 && r.s[1] > r.s[0])) {
-    const int64_t n = r.n[0], s = r.s[0];
-    r.n[0] = r.n[1];
-    r.s[0] = r.s[1];
-    r.n[1] = n;
-    r.s[1] = s;
-  }
-  for (int k = 1; k >= 0; --k) {  // runs that join are one
+// Runs that join are one, and a stride that no step takes is 0.
+Runs joined(Runs r) {
+  for (int k = 1; k >= 0; --k) {
     if (r.n[k] > 1 && r.s[k] == r.len && (k == 1 || r.n[1] == 1)) {
       r.len *= r.n[k];
       r.n[k] = 1;
@@ -136,6 +128,15 @@ Runs runs(const Heads& t, int tokens, int heads) {
     if (r.n[k] == 1) r.s[k] = 0;
   }
   return r;
+}
+Runs runs(const void* p, int64_t n, int64_t stride, int64_t len) {
+  return joined({reinterpret_cast<uintptr_t>(p), {n, 1}, {stride, 0}, len});
+}
+Runs runs(const Heads& t, int tokens, int heads) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(t.p);
+  const int64_t rs = 2 * t.rs, hs = 2 * t.hs, len = 2 * int64_t{t.cols};
+  return tokens == 1 || (heads > 1 && hs > rs) ? joined({p, {heads, tokens}, {hs, rs}, len})
+                                               : joined({p, {tokens, heads}, {rs, hs}, len});
 }
 
 int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
@@ -359,6 +360,18 @@ mla_status mla_gather_cache(const void* kv_cache, mla_kv_dtype kv_dtype, int num
       !aligned4(block_table) || !aligned4(cu_seqlens) || !aligned4(seq_starts) ||
       !aligned4(kv_scale) || !aligned4(err_count))
     return MLA_ERR_INVALID_ARG;
+  const Runs out[2] = {runs(kv_c, num_tokens, kv_c_row_stride * 2, int64_t{kv_lora_rank} * 2),
+                       runs(k_pe, num_tokens, k_pe_row_stride * 2, int64_t{rope_dim} * 2)};
+  const Runs in[5] = {
+      runs(kv_cache, num_blocks, block_stride * elt,
+           static_cast<int64_t>(block_size) * (kv_lora_rank + rope_dim) * elt),
+      runs(block_table, num_seqs, block_table_stride * 4, int64_t{max_blocks_per_seq} * 4),
+      runs(cu_seqlens, (static_cast<int64_t>(num_seqs) + 1) * 4),
+      runs(seq_starts, static_cast<int64_t>(num_seqs) * 4), runs(fp8 ? kv_scale : nullptr, 4)};
+  if (intersect(out[0], out[1])) return MLA_ERR_INVALID_ARG;
+  for (const Runs& o : out)
+    for (const Runs& x : in)
+      if (intersect(o, x)) return MLA_ERR_INVALID_ARG;
   mla::GatherParams p = {};
   p.cache = kv_cache;
   p.block_stride = block_stride;

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import mla_paged_kv_concat_gb300 as mla
-from test_latent_abi import ABSORB, EXPAND, PREFILL, PROJECT, RELEASE, args, at, lib  # noqa: F401
+from test_latent_abi import (ABSORB, EXPAND, GATHER, PREFILL, PROJECT, RELEASE, args, at,
+                             lib)  # noqa: F401
 
 # strides in elements, addresses in bytes: at(5) holds [10][16][256] of bf16
 ROW, HEAD = 16 * 256, 256
@@ -50,6 +51,19 @@ def test_head_product_outputs(lib, fn, base, over):  # noqa: F811
 ])
 def test_release_outputs(lib, over):  # noqa: F811
     assert lib.mla_blocks_release(*args(RELEASE, over)) == 1
+
+
+@pytest.mark.parametrize("over", [
+    # kv_c and k_pe over each other: rows of one buffer, columns that meet
+    dict(k_pe=at(4)), dict(k_pe=at(4) + 2 * 512 * 99), dict(cs=576, k_pe=at(4) + 2 * 504, ps=576),
+    dict(cs=576, k_pe=at(4) + 2 * (576 * 3 + 64), ps=576),
+    # over the cache's blocks, dense and with room between them, and over what names the rows
+    dict(kv_c=at(1)), dict(kv_c=at(1) + 2 * 64 * 576 * 5), dict(k_pe=at(1) + 2 * 64 * 576 * 8 - 16),
+    dict(bstride=2 * 64 * 576, kv_c=at(1) + 2 * 64 * 576, cs=512), dict(k_pe=at(2)),
+    dict(kv_c=at(2) + 16), dict(k_pe=at(3)), dict(starts=at(4) + 1024), dict(kvd=1, scale=at(5) + 4),
+])
+def test_gather_outputs(lib, over):  # noqa: F811
+    assert lib.mla_gather_cache(*args(GATHER, over)) == 1
 
 
 QROW = 16 * 192
