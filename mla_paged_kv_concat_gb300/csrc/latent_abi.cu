@@ -108,35 +108,35 @@ bool heads_disjoint(const Heads& t, int tokens, int heads) {
 }
 
 // The bytes of a tensor: runs of `len` at p + i * s[0] + j * s[1], the larger
-// stride first.
+// stride first, up to `end`.
 struct Runs {
-  uintptr_t p;
+  uintptr_t p, end;
   int64_t n[2], s[2], len;
   int64_t inner() const { return (n[1] - 1) * s[1] + len; }
-  int64_t span() const { return (n[0] - 1) * s[0] + inner(); }
 };
+// One run; none, which meets nothing, without a pointer or bytes.
 Runs runs(const void* p, int64_t bytes) {
-  return {reinterpret_cast<uintptr_t>(p), {1, 1}, {0, 0}, p ? bytes : 0};
+  const uintptr_t x = bytes > 0 ? reinterpret_cast<uintptr_t>(p) : 0;
+  return {x, x ? x + bytes : 0, {1, 1}, {0, 0}, bytes};
 }
 // Runs that join are one, and a stride that no step takes is 0.
-Runs joined(Runs r) {
-  for (int k = 1; k >= 0; --k) {
-    if (r.n[k] > 1 && r.s[k] == r.len && (k == 1 || r.n[1] == 1)) {
-      r.len *= r.n[k];
-      r.n[k] = 1;
-    }
-    if (r.n[k] == 1) r.s[k] = 0;
+Runs runs(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t len) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+  const uintptr_t end = x + (n0 - 1) * s0 + (n1 - 1) * s1 + len;
+  if (n1 > 1 && s1 == len) {
+    len *= n1;
+    n1 = 1;
   }
-  return r;
-}
-Runs runs(const void* p, int64_t n, int64_t stride, int64_t len) {
-  return joined({reinterpret_cast<uintptr_t>(p), {n, 1}, {stride, 0}, len});
+  if (n1 == 1 && n0 > 1 && s0 == len) {
+    len *= n0;
+    n0 = 1;
+  }
+  return {x, end, {n0, n1}, {n0 > 1 ? s0 : 0, n1 > 1 ? s1 : 0}, len};
 }
 Runs runs(const Heads& t, int tokens, int heads) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(t.p);
-  const int64_t rs = 2 * t.rs, hs = 2 * t.hs, len = 2 * int64_t{t.cols};
-  return tokens == 1 || (heads > 1 && hs > rs) ? joined({p, {heads, tokens}, {hs, rs}, len})
-                                               : joined({p, {tokens, heads}, {rs, hs}, len});
+  const int64_t rs = tokens > 1 ? 2 * t.rs : 0, hs = heads > 1 ? 2 * t.hs : 0;
+  return hs > rs ? runs(t.p, heads, hs, tokens, rs, 2 * int64_t{t.cols})
+                 : runs(t.p, tokens, rs, heads, hs, 2 * int64_t{t.cols});
 }
 
 int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
@@ -154,9 +154,7 @@ Steps steps(int64_t x, int64_t s, int64_t lo, int64_t hi, int64_t la, int64_t lb
 // Whether two tensors share a byte.  Exact but for two that both have rows
 // apart from each other, at different distances: those count as sharing one
 // only where they start at the same address.
-bool intersect(const Runs& a, const Runs& b) {
-  if (a.span() <= 0 || b.span() <= 0 || a.p + a.span() <= b.p || b.p + b.span() <= a.p)
-    return false;
+bool meet(const Runs& a, const Runs& b) {
   if (a.p == b.p) return true;
   if (a.s[0] && b.s[0] && a.s[0] != b.s[0]) return false;
   const int64_t d = static_cast<int64_t>(b.p - a.p), s0 = a.s[0] ? a.s[0] : b.s[0];
@@ -175,6 +173,7 @@ bool intersect(const Runs& a, const Runs& b) {
   }
   return false;
 }
+bool intersect(const Runs& a, const Runs& b) { return a.p < b.end && b.p < a.end && meet(a, b); }
 
 mla_status heads_map(CUtensorMap* m, const Heads& t, int tokens, int heads, int box_rows) {
   // the stride of a dimension of size 1 is never used but has to be valid
@@ -194,13 +193,14 @@ mla_status latent_proj(int mode, Heads in, int in_heads, int tokens, const void*
     return MLA_ERR_INVALID_ARG;
   if (!heads_disjoint(out0, tokens, heads) || (two && !heads_disjoint(out1, tokens, heads)))
     return MLA_ERR_INVALID_ARG;
-  const int64_t wb = 2 * ((static_cast<int64_t>(heads) * (nope + vdim) - 1) * w_stride + R);
+  // the rows the product leaves out count as well
+  const Runs r_w = runs(w, 2 * ((static_cast<int64_t>(heads) * (nope + vdim) - 1) * w_stride + R));
   // outputs may lie between an input's rows or each other's (columns of one
   // buffer)
   const Runs r_in = runs(in, tokens, in_heads), r0 = runs(out0, tokens, heads);
   const Runs r1 = two ? runs(out1, tokens, heads) : r0;
-  if (overlap(out0.p, r0.span(), w, wb) || intersect(r0, r_in) ||
-      (two && (overlap(out1.p, r1.span(), w, wb) || intersect(r1, r_in) || intersect(r0, r1))))
+  if (intersect(r0, r_w) || intersect(r0, r_in) ||
+      (two && (intersect(r1, r_w) || intersect(r1, r_in) || intersect(r0, r1))))
     return MLA_ERR_INVALID_ARG;
   int sms = 0;
   cudaError_t e = mla::device_sm_count(&sms);
@@ -360,12 +360,12 @@ mla_status mla_gather_cache(const void* kv_cache, mla_kv_dtype kv_dtype, int num
       !aligned4(block_table) || !aligned4(cu_seqlens) || !aligned4(seq_starts) ||
       !aligned4(kv_scale) || !aligned4(err_count))
     return MLA_ERR_INVALID_ARG;
-  const Runs out[2] = {runs(kv_c, num_tokens, kv_c_row_stride * 2, int64_t{kv_lora_rank} * 2),
-                       runs(k_pe, num_tokens, k_pe_row_stride * 2, int64_t{rope_dim} * 2)};
+  const Runs out[2] = {runs(kv_c, num_tokens, kv_c_row_stride * 2, 1, 0, int64_t{kv_lora_rank} * 2),
+                       runs(k_pe, num_tokens, k_pe_row_stride * 2, 1, 0, int64_t{rope_dim} * 2)};
   const Runs in[5] = {
-      runs(kv_cache, num_blocks, block_stride * elt,
+      runs(kv_cache, num_blocks, block_stride * elt, 1, 0,
            static_cast<int64_t>(block_size) * (kv_lora_rank + rope_dim) * elt),
-      runs(block_table, num_seqs, block_table_stride * 4, int64_t{max_blocks_per_seq} * 4),
+      runs(block_table, num_seqs, block_table_stride * 4, 1, 0, int64_t{max_blocks_per_seq} * 4),
       runs(cu_seqlens, (static_cast<int64_t>(num_seqs) + 1) * 4),
       runs(seq_starts, static_cast<int64_t>(num_seqs) * 4), runs(fp8 ? kv_scale : nullptr, 4)};
   if (intersect(out[0], out[1])) return MLA_ERR_INVALID_ARG;

@@ -131,3 +131,14 @@ def test_products_into_columns_of_one_buffer(cuda_dev, T, H):
     y = mla.project_v(ql, w, out=buf[..., 192 + R:])
     assert torch.equal(ql, mla.absorb_q(buf[..., :128].contiguous(), w))
     assert torch.equal(y, mla.project_v(ql.contiguous(), w))
+
+
+@pytest.mark.gpu
+def test_an_unneeded_workspace_inside_an_input_is_taken(cuda_dev):
+    q = torch.randn(20, 3, 192, device="cuda").to(torch.bfloat16)
+    kv, kp = torch.randn(20, 3, 256, device="cuda").to(torch.bfloat16), q[:, 0, :64].contiguous()
+    cu = torch.tensor([0, 20], dtype=torch.int32, device="cuda")
+    want = mla.prefill(q, kv[..., :128], kv[..., 128:], kp, cu, cu, 0.07)
+    got = mla.prefill(q, kv[..., :128], kv[..., 128:], kp, cu, cu, 0.07, workspace=q[5:])
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
