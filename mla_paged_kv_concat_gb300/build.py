@@ -39,16 +39,25 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return (_sources() + [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__])
+def _newer(out: str, deps) -> bool:
+    """Whether ``out`` is there and no older than any of ``deps``."""
+    if not os.path.exists(out):
+        return False
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
+                  + glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__])
+
+
+def _bind_up_to_date() -> bool:
+    return _newer(BIND, [BIND_SRC, __file__] + glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _lib_up_to_date() and _bind_up_to_date()
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -91,27 +100,36 @@ def _link_bind(obj: str) -> None:
     os.replace(tmp, BIND)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libmla.so if any source changed; returns its path."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        bind = ex.submit(_compile_bind)
-        results = list(ex.map(_compile, srcs))
-        bind_obj = bind.result()
-    with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
-        for (obj, log), src in zip(results, srcs):
-            f.write(f"==== {os.path.basename(src)}\n{log}\n")
+def _link_lib(objs) -> None:
     tmp = LIB + ".tmp"
-    cmd = [_nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=libmla.so", "-o", tmp,
-           *[o for o, _ in results], "-lcudart"]
+    cmd = [_nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=libmla.so", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_bind(bind_obj)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link what changed; returns the path of libmla.so.
+
+    The library needs neither torch nor the binding: it is linked first, and
+    what goes wrong with the binding is raised after that.
+    """
+    lib, bind = force or not _lib_up_to_date(), force or not _bind_up_to_date()
+    if not lib and not bind:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    srcs = _sources()
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        bind_obj = ex.submit(_compile_bind) if bind else None
+        results = list(ex.map(_compile, srcs)) if lib else []
+    if lib:
+        with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
+            for (obj, log), src in zip(results, srcs):
+                f.write(f"==== {os.path.basename(src)}\n{log}\n")
+        _link_lib([o for o, _ in results])
+    if bind:
+        _link_bind(bind_obj.result())
     if verbose:
         print(f"built {LIB}")
     return LIB
