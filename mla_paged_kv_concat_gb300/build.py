@@ -3,7 +3,8 @@ _calls.so (the compiled part of the Python binding) with g++.
 
 Each ``csrc/*.cu`` compiles to an object in ``_build/`` in parallel, then the
 objects link into ``mla_paged_kv_concat_gb300/libmla.so``; ``csrc/bind.cpp``
-compiles beside them and links against it and torch.  ptxas resource usage
+compiles beside them and links against it and torch, and is made anew for
+another torch or Python.  ptxas resource usage
 (``-Xptxas -v``) goes to ``_build/ptxas.log``.  Run ``python -m
 mla_paged_kv_concat_gb300.build`` or call :func:`build`.
 """
@@ -12,6 +13,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -52,7 +54,28 @@ def _lib_up_to_date() -> bool:
                   + glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__])
 
 
+def _bind_versions() -> str:
+    """What the binding is compiled for; another torch or Python cannot load
+    it, or reads its tensors wrongly."""
+    import importlib.metadata as md
+    try:
+        torch = md.version("torch")
+    except md.PackageNotFoundError:
+        torch = "none"
+    return f"torch {torch}, {sys.implementation.cache_tag}, {platform.machine()}\n"
+
+
+def _bind_stamp() -> str:
+    return os.path.join(BUILD, os.path.basename(BIND) + ".versions")
+
+
 def _bind_up_to_date() -> bool:
+    try:
+        with open(_bind_stamp()) as f:
+            if f.read() != _bind_versions():
+                return False
+    except OSError:
+        return False
     return _newer(BIND, [BIND_SRC, __file__] + glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
@@ -129,7 +152,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 f.write(f"==== {os.path.basename(src)}\n{log}\n")
         _link_lib([o for o, _ in results])
     if bind:
-        _link_bind(bind_obj.result())
+        obj = bind_obj.result()
+        if os.path.exists(_bind_stamp()):
+            os.remove(_bind_stamp())  # no stamp beside a binding that is not its own
+        _link_bind(obj)
+        with open(_bind_stamp(), "w") as f:
+            f.write(_bind_versions())
     if verbose:
         print(f"built {LIB}")
     return LIB

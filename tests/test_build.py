@@ -68,3 +68,23 @@ def test_only_what_changed_is_built(tree):
     assert not build.up_to_date()
     build.build()
     assert made[2:] == ["bind"]
+
+
+@pytest.mark.parametrize("what", ["torch", "python", "stamp"])
+def test_binding_is_made_anew_for_another_torch_or_python(tree, monkeypatch, what):
+    """Its file times say nothing about the versions it was compiled for."""
+    root, made = tree
+    build.build()
+    assert build.up_to_date()
+    if what == "torch":
+        import importlib.metadata as md
+        old = md.version
+        monkeypatch.setattr(md, "version", lambda n: old(n) + ".post1")
+    elif what == "python":
+        monkeypatch.setattr(build.sys.implementation, "cache_tag", "cpython-999")
+    else:
+        for p in (root / "_build").glob("*.versions"):
+            p.unlink()
+    assert not build.up_to_date()
+    build.build()
+    assert made[2:] == ["bind"] and build.up_to_date()
