@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
@@ -83,6 +84,15 @@ struct Call {
     const int64_t v = integer();
     CHECK(v >= INT32_MIN && v <= INT32_MAX, std::string(name) + " does not fit 32 bits");
     return static_cast<int>(v);
+  }
+  // A truth value: a bool, an integer or NumPy's bool, which is no integer.
+  bool truth() {
+    if (i < n && std::strncmp(Py_TYPE(a[i])->tp_name, "numpy.bool", 10) == 0) {
+      const int v = PyObject_IsTrue(next());
+      if (v < 0) throw PyError();
+      return v != 0;
+    }
+    return integer() != 0;
   }
   double real() {
     const double v = PyFloat_AsDouble(next());
@@ -453,7 +463,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor q = c.tensor("q"), q_pe = c.maybe("q_pe"), k = c.tensor("k_nope"), v = c.tensor("v");
     Tensor k_pe = c.tensor("k_pe"), cu_q = c.tensor("cu_seqlens_q"), cu_k = c.tensor("cu_seqlens_k");
     const float sm_scale = static_cast<float>(c.real());
-    const int causal = c.integer() != 0;
+    const int causal = c.truth();
     const int splits = c.small("num_kv_splits");
     Tensor ws = c.maybe("workspace"), out = c.maybe("out"), lse = c.maybe("lse");
     Tensor err = c.maybe("err_count");
