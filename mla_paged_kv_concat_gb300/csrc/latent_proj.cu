@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(192, 1)
           }
         }
       }
-      if (!ok && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+      if (!ok) gave_up(p.err_count);
     }
   } else if (warp == 5) {
     constexpr uint32_t idesc = tc::idesc_bf16(TM, BN, 0, kBMn ? 1 : 0);
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(192, 1)
         __syncwarp();
       }
     }
-    if (!ok && lane == 0 && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+    if (!ok && lane == 0) gave_up(p.err_count);
     // nothing of this CTA's still runs on the tensor core when TMEM is freed
     for (int j = 0; ok && j < 2 && j < ta; ++j) {
       const int u = ta - 1 - j;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(192, 1)
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    if (!ok && lane == 0 && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+    if (!ok && lane == 0) gave_up(p.err_count);
   }
 
   tc::fence_before_sync();
@@ -351,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
           tc::pair_tma_load_3d(dst + kPairHalf, &mb, bar, kc * KC, rank * 128, h);
         }
       }
-      if (!ok && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+      if (!ok) gave_up(p.err_count);
     }
   } else if (warp == 5) {
     bool ok = true;
@@ -392,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
         const int u = ta - 1 - j;
         warp_wait(&acc_full[u & 1], (u >> 1) & 1);
       }
-      if (!ok && lane == 0 && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+      if (!ok && lane == 0) gave_up(p.err_count);
     }
   } else {
     // warps 0-3 k_nope's columns, 6-9 v's; a warp reads the TMEM lanes of its
@@ -431,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    if (!ok && lane == 0 && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+    if (!ok && lane == 0) gave_up(p.err_count);
   }
 
   tc::fence_before_sync();

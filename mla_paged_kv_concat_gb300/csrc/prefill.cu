@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     });
   }
-  if (!ok && lane == 0 && p.err_count) atomicAdd(p.err_count, kTimeoutErr);
+  if (!ok && lane == 0) gave_up(p.err_count);
 
   tc::fence_before_sync();
   __syncthreads();

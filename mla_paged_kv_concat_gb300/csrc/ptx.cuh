@@ -86,6 +86,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// For a role whose wait gave up, before it meets the others at the CTA's end,
+// where TMEM and shared memory are given back.  Copies and products in flight
+// can then not be told one by one; none takes a thousandth of this time, and a
+// role that goes on finds what it needs from this one missing within
+// microseconds and gives up itself.
+constexpr uint64_t kSettleNs = 20000000ull;  // 20 ms
+__device__ __forceinline__ void gave_up(int* err_count) {
+  if (err_count) atomicAdd(err_count, kTimeoutErr);
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < kSettleNs) __nanosleep(10000);
+}
+
 // ---------------------------------------------------------------- launch order
 // Programmatic dependent launch.  A kernel launched with programmatic stream
 // serialization may start while the previous kernel of the stream is still
