@@ -514,8 +514,9 @@ def prefill(q, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, sm_scale: float, *,
     :func:`expand_kv` gives them, ``k_pe`` [Tk, 64]; ``cu_seqlens_q`` and
     ``cu_seqlens_k`` int32 [seqs + 1].  Causal rows are the last tokens of
     their sequence's keys.  ``num_kv_splits``: parts of the key axis, from
-    ``mla_prefill_num_kv_splits``; the workspace they need is allocated here
-    when not given.
+    ``mla_prefill_num_kv_splits`` (few rows against long contexts take up to
+    six times as long in the one part of the default); the workspace they need
+    is allocated here when not given.
     """
     q, q_pe = q if isinstance(q, (tuple, list)) else (q, None)
     return _bind().prefill(q, q_pe, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, sm_scale, causal,

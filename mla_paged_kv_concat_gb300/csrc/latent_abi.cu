@@ -429,7 +429,7 @@ mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_str
 }
 
 // Measured on GB300, 16 heads (us at S = 1 / the rule's S / twice that): one
-// sequence of 256 rows, 32768 keys: 438 / 80 (8) / 98; two of 500 rows, 4596 keys:
+// sequence of 256 rows, 32768 keys: 437 / 75 (9) / 92; two of 500 rows, 4596 keys:
 // 72 / 53 (2) / 63; contexts of 4096 to 32768 keys, eight of 1 to 5 rows: 382 / 218 (8)
 // / 228; of 1000 to 30000 keys, 16 of 1 to 8 rows: 465 / 325 (4) / 323; of 500 to 16000
 // keys, one row each, 32: 388 / 351 (2) / 344, 40: 469 / 437 (2) / 434, 56: 659 / 629 (2)

@@ -17,9 +17,13 @@
 // TMEM -> registers -> bf16 in a swizzled 4 KiB staging box -> TMA store,
 // which also clips the rows past the last token.  Roles: warps 0-3 epilogue,
 // warp 4 TMA producer, warp 5 MMA issuer and TMEM owner.
-// Measured: expand, 5001 tokens, 128 heads, R = 256, 77 us (4.25 TB/s written; a
-// plain fill reaches 4.02); absorb, 2048 tokens, 128 heads, 64 us; project, the
-// same, 56 us (5.9 TB/s); absorb, 64 tokens, 16 heads, 3.5 us, launch and latency.
+// Measured: expand, 5001 tokens, 128 heads, R = 256, 77 us (4.28 TB/s written),
+// into two buffers or the halves of one; the library's product into one matrix
+// takes 70 and a plain fill 82, so neither memory nor the layout is the bound;
+// absorb, 2048 tokens, 128 heads, 64 us; project, the same, 56 us (5.9 TB/s);
+// absorb, 64 tokens, 16 heads, 3.3 us and project, 128 tokens, 128 heads, 5.7 us
+// (11.1 with L2 flushed): launch, first loads and epilogue around short work
+// (the library, to a head-major output: 2.2 and 4.2, flushed 10.3).
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -271,11 +275,10 @@ __global__ void __launch_bounds__(192, 1)
 // per 552 cycles of products instead of 48.  Rank 0 issues for both; the ring's
 // "landed" barrier is rank 0's and counts both CTAs' bytes; "read" and
 // "accumulator ready" arrive in both.  Eight epilogue warps, four per output.
-// 8192 tokens, 16 heads: 24.8 us (1386 TFLOP/s) against 27.6 for single CTAs;
-// with four epilogue warps no faster than those.  With R = 256 the writes bound
-// expand (256 flops a byte written: 1040 TFLOP/s at the 4.07 TB/s that a plain
-// fill of the same buffer reaches) and pairs, which drain together, lose:
-// 5001 tokens, 128 heads 100 us against 77.
+// 8192 tokens, 16 heads: 25.4 us (1353 TFLOP/s; the library's single matrix
+// 21.1) against 27.6 for single CTAs; with four epilogue warps no faster than
+// those.  With R = 256 there are half the products to the same bytes written and
+// pairs, which drain together, lose: 5001 tokens, 128 heads 100 us against 77.
 constexpr int kPairStages = 5;
 constexpr int kPairHalf = A_BYTES;  // A, and the half of B, of one stage
 constexpr int PP_STORE = kPairStages * 2 * kPairHalf;
@@ -477,10 +480,10 @@ bool proj_pairs(int mode, int tokens, int heads, int k, int sm_count) {
 // Columns of a tile: those for which the CTA with the most tiles takes in the
 // fewest operand rows (tokens and columns; K is the same).  project, 128 tokens,
 // 128 heads: 128 columns, one tile a CTA 6.0 us, 64 columns, two, 7.4; absorb, 64
-// tokens, 16 heads: 64 columns 3.6 us, 256 4.8.  Large absorbs, which are bound
-// by their writes (a sum of 128 terms an element), do better with narrower
+// tokens, 16 heads: 64 columns 3.6 us, 256 4.8.  Large absorbs, which write
+// much for their work (a sum of 128 terms an element), do better with narrower
 // tiles once there are many: 2048 tokens, 128 heads, R = 512 64 us at 128 columns,
-// 72 at 256 (a plain fill 67); 4096 tokens, 32 heads 32.1 and 33.3; but 500 tokens,
+// 72 at 256; 4096 tokens, 32 heads 32.1 and 33.3; but 500 tokens,
 // 128 heads 18.6 and 17.1; expand, R = 256, 5001 tokens, 128 heads 88 and 78.
 int proj_tile_cols(int mode, int tokens, int heads, int cols, int sm_count) {
   const int64_t blocks = static_cast<int64_t>((tokens + TM - 1) / TM) * heads;
