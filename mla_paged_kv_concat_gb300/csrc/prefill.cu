@@ -81,6 +81,12 @@ constexpr uint32_t O_COL = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // log2 units
+// Largest |m c| that is subtracted from s c in one operation.  What m c's own
+// rounding leaves, at most 2^4, is an exponent that P and the sum have in common:
+// a factor of 2^16.  With larger scores (whose step in fp32 is then 16 and more)
+// it would soon pass any range, so such a row takes |m c| = 2^28, as if c were
+// smaller: its scores below the maximum still weigh 2^-16 at most.
+constexpr float kLarge = 268435456.0f;  // 2^28, log2 units
 
 struct Unit {
   int q_row;   // first query row (of all tokens); -1: no more units
@@ -166,6 +172,12 @@ __device__ bool unit_at(const PrefillParams& p, const int32_t* cu_q, const int32
   u.n0 = tiles(0);
   u.n1 = tiles(1);
   return true;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Packed fp32 pairs.
@@ -579,7 +591,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + O_COL + t * 128;
     const float c = p.sm_scale * kLog2e;
-    const uint64_t c2 = pack2(c, c);
     int sn = 0, on = 0;
     ok = for_each_unit(true, [&](const Unit& u, int i) -> bool {
       const int row = t * kTile + r;         // row of the unit
@@ -587,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = row < u.rows;
       const int lim = min(u.ke, row_limit(u, row, p.causal)) - u.ks;  // keys of this unit
       const int im = first_masked(u, t * kTile, p.causal);
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, cr = c;  // cr: c, less for a row of large scores
       for (int j = 0; j < n; ++j, ++sn) {
         if (!warp_wait(&s_full[t], sn & 1)) return false;
         tc::fence_after_sync();
@@ -613,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O is rescaled only when the maximum has grown by more than 2^8
         // (-inf - -inf is NaN: no)
         const bool grow = (m_new - m) * c > kRescale;
+        const float c_new = fminf(c, fmaxf(kLarge * rcp(fabsf(m_new)), 0x1p-100f));
         if (j > 0 && __any_sync(0xffffffffu, grow)) {
           // this tile's S was issued after the last P.V: O is complete
           const float alpha = grow ? ex2((m - m_new) * c) : 1.f;
@@ -628,8 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::st_32x32b_x32(o_col + q * 32, o);
           }
         }
-        if (grow) m = m_new;
-        const float mc = m == -INFINITY ? 0.f : -m * c;
+        if (grow) {
+          m = m_new;
+          cr = c_new;
+        }
+        const float mc = m == -INFINITY ? 0.f : -m * cr;
+        const uint64_t c2 = pack2(cr, cr);
         const uint64_t mc2 = pack2(mc, mc);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -734,7 +750,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live) {
         float lg;
         asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(l));
-        const float lse = l == 0.f ? -INFINITY : (m * c + lg) * kLn2;
+        const float lse =
+            l == 0.f ? -INFINITY : cr < c ? m * p.sm_scale + lg * kLn2 : (m * c + lg) * kLn2;
         if (p.num_splits == 1)
           p.lse[q_row * p.heads + u.h] = lse;
         else
