@@ -407,8 +407,9 @@ def _bind():
 
     A call runs on ``stream``, by default the current one, and what it
     allocates (outputs, workspace) is that stream's memory.  With another
-    stream than the current one the caller makes it wait for the inputs, and
-    the current one wait for it before the outputs are used there."""
+    stream than the current one the caller makes it wait for the inputs, keeps
+    those until it is done with them, and makes the current one wait for it
+    before the outputs are used there."""
     global _bind_module
     if _bind_module is None:
         _torch()
