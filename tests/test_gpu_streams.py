@@ -160,3 +160,39 @@ def test_workspaces_do_not_pile_up(cuda_dev, split_call):
     grown = active() - start
     torch.cuda.synchronize()
     assert grown <= 8 * (used + 8 * 512), (grown, used)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_host_threads(cuda_dev, given):
+    """Four host threads, each with a stream of its own, current or given."""
+    import threading
+    sets = [make_calls() for _ in range(4)]
+    refs = [{n: [x.clone() for x in c[n](None)] for n in NAMES} for c in sets]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        try:
+            for _ in range(10):
+                for n in NAMES:
+                    if given:
+                        out = sets[i][n](s)
+                        torch.cuda.current_stream().wait_stream(s)
+                        ok = all(torch.equal(x, r) for x, r in zip(out, refs[i][n]))
+                    else:
+                        with torch.cuda.stream(s):
+                            out = sets[i][n](None)
+                            ok = all(torch.equal(x, r) for x, r in zip(out, refs[i][n]))
+                    if not ok:
+                        wrong.append((i, n))
+        except Exception as e:  # noqa: BLE001 - reported below
+            wrong.append((i, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong
