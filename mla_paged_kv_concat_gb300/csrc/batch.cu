@@ -268,17 +268,15 @@ __global__ void __launch_bounds__(kThreads, 3) batch_build_kernel(const BatchPar
     count_errors(p.err_count, errs);
     return;
   }
-  // [B] cached, and cached + new, tokens (not from cuq's steps, which saturate;
-  // as an array of its own the second costs 0.25 us)
-  int2* len = reinterpret_cast<int2*>(sm);
-  int* cuq = sm + 2 * B;                    // [B] first token row of each request
-  int* off = sm + 3 * B;                    // [B] new pages before each request
-  int* row = sm + 4 * B;                    // [B]
+  int* cuq = sm;          // [B] first token row of each request
+  int* off = sm + B;      // [B] new pages before each request
+  int* ctx = sm + 2 * B;  // [B]
+  int* row = sm + 3 * B;  // [B]
   const int count = stack_count(p);
   const longlong2 total = scan_reqs<false>(
       p, part,
       [&](int b, const Req& r) {
-        len[b] = make_int2(r.ctx, r.seq);
+        ctx[b] = r.ctx;
         row[b] = r.row;
       },
       [&](int b, long long n, long long pages) {
@@ -296,8 +294,14 @@ __global__ void __launch_bounds__(kThreads, 3) batch_build_kernel(const BatchPar
       // ones off the stack
       const int b = static_cast<int>(u / p.row_pieces);
       const int i0 = static_cast<int>(u % p.row_pieces) * kPiece;
-      const int c = len[b].x, rw = row[b];
-      const int end = min(pages_of(p, len[b].y), i0 + kPiece);
+      const int c = ctx[b], rw = row[b];
+      // New tokens: a step of cuq, unless its sums have saturated.  (The length
+      // kept beside ctx costs an SM its third CTA from 3800 requests on: 4500
+      // of them 22.7 us against 17.4.)
+      const long long n = total.x > INT32_MAX ? max(0, __ldg(p.query_lens + b))
+                                              : (b + 1 < B ? cuq[b + 1] : total.x) - cuq[b];
+      const int seq = c + n > p.capacity ? p.capacity : static_cast<int>(c + n);
+      const int end = min(pages_of(p, seq), i0 + kPiece);
       const int old_all = rw < 0 ? 0 : pages_of(p, c), old = min(old_all, end);
       int32_t* dst = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
       int32_t* req = rw < 0 ? nullptr : p.req_table + static_cast<int64_t>(rw) * p.rt_stride;
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 3) batch_build_kernel(const BatchPar
           const int m = (a + z + 1) >> 1;
           if (cuq[m] <= t) a = m; else z = m - 1;
         }
-        const int c = len[a].x, rw = row[a];
+        const int c = ctx[a], rw = row[a];
         pos = static_cast<int64_t>(c) + (t - cuq[a]);
         if (rw >= 0 && pos < p.capacity) {
           const int page = page_of(p, static_cast<int>(pos)), old = pages_of(p, c);
@@ -482,7 +486,7 @@ cudaError_t launch_batch_build(const BatchParams& p_in, int sm_count, cudaStream
   BatchParams p = p_in;
   page_reciprocal(&p);
   static std::atomic<uint64_t> attr_done{0};
-  cudaError_t e = set_smem_attr_once(batch_build_kernel, 5 * kMaxBatchReqs * 4, attr_done);
+  cudaError_t e = set_smem_attr_once(batch_build_kernel, 4 * kMaxBatchReqs * 4, attr_done);
   if (e != cudaSuccess) return e;
   // max_blocks is capacity / block_size
   p.row_pieces = (p.capacity / p.block_size + kPiece - 1) / kPiece;
@@ -492,7 +496,7 @@ cudaError_t launch_batch_build(const BatchParams& p_in, int sm_count, cudaStream
   const int grid = 1 + static_cast<int>(ctas < 1 ? 1 : ctas < most ? ctas : most);
   p.defer_count = p.free_count == p.free_count_out;
   e = launch_overlapped(batch_build_kernel, dim3(grid), dim3(kThreads),
-                        5 * static_cast<size_t>(p.num_reqs) * 4, stream, p);
+                        4 * static_cast<size_t>(p.num_reqs) * 4, stream, p);
   if (e != cudaSuccess || !p.defer_count) return e;
   return launch_overlapped(batch_count_kernel, dim3(1), dim3(kThreads), 0, stream, p);
 }
