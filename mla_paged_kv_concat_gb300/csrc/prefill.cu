@@ -81,12 +81,11 @@ constexpr uint32_t O_COL = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // log2 units
-// Largest |m c| that is subtracted from s c in one operation.  What m c's own
-// rounding leaves, at most 2^4, is an exponent that P and the sum have in common:
-// a factor of 2^16.  With larger scores (whose step in fp32 is then 16 and more)
-// it would soon pass any range, so such a row takes |m c| = 2^28, as if c were
-// smaller: its scores below the maximum still weigh 2^-16 at most.
-constexpr float kLarge = 268435456.0f;  // 2^28, log2 units
+// Largest |m c| that is subtracted from s c in one operation: what m c's own
+// rounding leaves, 2^-8 here, is a factor of P, and from 2^31 on passes any
+// range.  For a row of larger scores m is taken off S in TMEM and the tile read
+// again.
+constexpr float kLarge = 65536.0f;  // log2 units
 
 struct Unit {
   int q_row;   // first query row (of all tokens); -1: no more units
@@ -172,12 +171,6 @@ __device__ bool unit_at(const PrefillParams& p, const int32_t* cu_q, const int32
   u.n0 = tiles(0);
   u.n1 = tiles(1);
   return true;
-}
-
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // Packed fp32 pairs.
@@ -591,6 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + O_COL + t * 128;
     const float c = p.sm_scale * kLog2e;
+    const uint64_t c2 = pack2(c, c);
+    const float large = kLarge / c;
     int sn = 0, on = 0;
     ok = for_each_unit(true, [&](const Unit& u, int i) -> bool {
       const int row = t * kTile + r;         // row of the unit
@@ -598,10 +593,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = row < u.rows;
       const int lim = min(u.ke, row_limit(u, row, p.causal)) - u.ks;  // keys of this unit
       const int im = first_masked(u, t * kTile, p.causal);
-      float m = -INFINITY, l = 0.f, cr = c;  // cr: c, less for a row of large scores
+      float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++sn) {
         if (!warp_wait(&s_full[t], sn & 1)) return false;
         tc::fence_after_sync();
+        float off = 0.f;  // taken off this row's scores
+      again:
         uint32_t s[128];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -614,7 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 128; ++q)
             if (q >= left) s[q] = 0xFF800000u;  // -inf
         }
-        float mx[4] = {m, m, m, m};
+        const float mo = m - off;
+        float mx[4] = {mo, mo, mo, mo};
 #pragma unroll
         for (int q = 0; q < 128; q += 8)
 #pragma unroll
@@ -623,29 +621,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         // O is rescaled only when the maximum has grown by more than 2^8
         // (-inf - -inf is NaN: no)
-        const bool grow = (m_new - m) * c > kRescale;
-        const float c_new = fminf(c, fmaxf(kLarge * rcp(fabsf(m_new)), 0x1p-100f));
-        if (j > 0 && __any_sync(0xffffffffu, grow)) {
-          // this tile's S was issued after the last P.V: O is complete
+        const bool grow = (m_new - mo) * c > kRescale;
+        if (__any_sync(0xffffffffu, (j > 0 && grow) || fabsf(m_new) > large)) {
+          // This tile's S was issued after the last P.V: O is complete.  The loop
+          // does O and S alike, so that the rare case adds little code (64
+          // instructions more cost short prompts 4 %).
           const float alpha = grow ? ex2((m - m_new) * c) : 1.f;
           l *= alpha;
+          if (grow) m = m_new;
+          const bool wide = off == 0.f && fabsf(m) > large && m != -INFINITY;
+          const bool shift = __any_sync(0xffffffffu, wide);
+          if (wide) off = m;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = j > 0 ? 0 : 4; q < (shift ? 8 : 4); ++q) {
+            const uint32_t col = q < 4 ? o_col + q * 32 : s_col + (q - 4) * 32;
+            const float f = q < 4 ? alpha : 1.f, g = q < 4 ? 0.f : -off;
             uint32_t o[32];
-            tc::ld_32x32b_x32(o_col + q * 32, o);
+            tc::ld_32x32b_x32(col, o);
             tc::wait_ld();
             tc::reg_fence(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::st_32x32b_x32(o_col + q * 32, o);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f + g);
+            tc::st_32x32b_x32(col, o);
+          }
+          if (shift) {
+            tc::wait_st();
+            goto again;
           }
         }
-        if (grow) {
-          m = m_new;
-          cr = c_new;
-        }
-        const float mc = m == -INFINITY ? 0.f : -m * cr;
-        const uint64_t c2 = pack2(cr, cr);
+        if (grow) m = m_new;
+        const float mc = m == -INFINITY ? 0.f : (off - m) * c;
         const uint64_t mc2 = pack2(mc, mc);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -750,8 +755,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live) {
         float lg;
         asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(l));
-        const float lse =
-            l == 0.f ? -INFINITY : cr < c ? m * p.sm_scale + lg * kLn2 : (m * c + lg) * kLn2;
+        const float lse = l == 0.f            ? -INFINITY
+                          : fabsf(m) > large ? m * p.sm_scale + lg * kLn2
+                                             : (m * c + lg) * kLn2;
         if (p.num_splits == 1)
           p.lse[q_row * p.heads + u.h] = lse;
         else

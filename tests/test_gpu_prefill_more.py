@@ -72,9 +72,8 @@ def test_scores_beyond_any_range_of_their_weights(cuda_dev, sm, sign, splits):
 
     Tolerance: o as in test_gpu_prefill with no error of the scores, so e =
     2^-21: (1 + 2^-8) A (2^-8 + 2 e + 2 n 2^-23) + 2^-8 |ref|.  lse: c, m c (or m
-    sm), the sum and its product with ln 2 are rounded once each, the rounding
-    of m c that the sum carries is at most 2^-24 of it, and for a row of large
-    scores 2^4 ln 2 against |lse| >= 2^28 ln 2: below 2^-20 |ref| in all.
+    sm), the sum and its product with ln 2 are rounded once each, and so is the
+    m c that the weights and their sum carry: below 2^-20 |ref| in all.
     Joining splits sees no more than their lse holds, so rows whose largest
     keys lie in several of them are left out there."""
     g = torch.Generator("cuda").manual_seed(7)
