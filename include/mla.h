@@ -652,6 +652,44 @@ mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_str
                          int64_t y_row_stride, int64_t y_head_stride, int* err_count,
                          void* stream);
 
+/* What mla_linear applies to the sum with the bias.  GELU is x Phi(x), GELU_TANH
+ * its approximation by tanh, SILU x / (1 + e^-x). */
+typedef enum {
+  MLA_ACT_NONE = 0,
+  MLA_ACT_RELU = 1,
+  MLA_ACT_SILU = 2,
+  MLA_ACT_GELU = 3,
+  MLA_ACT_GELU_TANH = 4
+} mla_activation;
+
+/*
+ * mla_linear - a projection of the layer with what follows it: the query's and
+ * the latent's projections with their bias before mla_absorb_q, the output's
+ * with the residual stream behind mla_project_v.
+ *
+ *   y[t, n] = act(sum_k x[t, k] W[n, k] + bias[n]) + residual[t, n]
+ *
+ * bf16 tensors, fp32 sum and epilogue, one rounding to bf16.
+ *   x          bf16 [num_tokens][in_features], row stride x_row_stride.
+ *   w          bf16 [out_features][in_features], row stride w_row_stride.
+ *   bias       bf16 [out_features], or NULL.  residual  bf16 [num_tokens]
+ *              [out_features] at its row stride, or NULL.
+ *   y          bf16 [num_tokens][out_features] at its row stride.  It may be the
+ *              residual itself (same address, same stride), else it must not
+ *              overlap an input.
+ *   in_features, out_features  1 .. 2^20; every pointer 16-byte aligned, every
+ *              row stride a positive multiple of 8 and at least the row (that of
+ *              a single row, too).
+ *   num_tokens 0 .. 2^30; 0 is a no-op.
+ *   err_count  device int, may be NULL: +(1 << 20) if a pipeline wait timed out.
+ * Run-to-run deterministic.
+ */
+mla_status mla_linear(const void* x, int64_t x_row_stride, int num_tokens, int in_features,
+                      const void* w, int64_t w_row_stride, int out_features, const void* bias,
+                      mla_activation activation, const void* residual,
+                      int64_t residual_row_stride, void* y, int64_t y_row_stride,
+                      int* err_count, void* stream);
+
 /*
  * mla_prefill_num_kv_splits - how many parts mla_prefill should cut the key
  * axis into: as many as give every SM one part where the 256-row query blocks

@@ -17,6 +17,7 @@ Thin Python binding over the C ABI of ``libmla.so`` (``include/mla.h``):
 * ``gather_cache(...)`` — cached rows of a ragged batch as contiguous bf16.
 * ``expand_kv(...)``, ``absorb_q(...)`` and ``project_v(...)`` — the products
   with the kv_b weight of the expanded and the absorbed form.
+* ``linear(...)`` — a projection with bias, activation and residual.
 * ``prefill(...)`` — attention of the expanded form over ragged prompts.
 * ``cache_write(...)`` and ``decode(...)`` — torch-tensor conveniences that
   only marshal pointers, strides and the current CUDA stream; every step of
@@ -29,7 +30,8 @@ from __future__ import annotations
 from typing import NamedTuple
 
 from . import _lib
-from ._lib import (MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_FP8_E5M2, MLA_PATH_AUTO,
+from ._lib import (MLA_ACT_GELU, MLA_ACT_GELU_TANH, MLA_ACT_NONE, MLA_ACT_RELU, MLA_ACT_SILU,
+                   MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_FP8_E5M2, MLA_PATH_AUTO,
                    MLA_PATH_MMA_SYNC, MLA_PATH_TCGEN05, MlaError, load)
 
 __all__ = [
@@ -39,10 +41,11 @@ __all__ = [
     "mla_batch_build", "mla_blocks_release", "mla_gather_cache",
     "mla_expand_kv", "mla_absorb_q", "mla_project_v", "expand_kv", "absorb_q", "project_v",
     "mla_prefill", "mla_prefill_num_kv_splits", "mla_prefill_workspace_bytes", "prefill",
-    "batch_build", "blocks_release", "gather_cache", "BatchTables",
+    "batch_build", "blocks_release", "gather_cache", "BatchTables", "mla_linear", "linear",
     "MlaError", "load",
     "MLA_KV_BF16", "MLA_KV_FP8_E4M3", "MLA_KV_FP8_E5M2", "MLA_PATH_AUTO", "MLA_PATH_MMA_SYNC",
-    "MLA_PATH_TCGEN05",
+    "MLA_PATH_TCGEN05", "MLA_ACT_NONE", "MLA_ACT_RELU", "MLA_ACT_SILU", "MLA_ACT_GELU",
+    "MLA_ACT_GELU_TANH",
 ]
 
 
@@ -89,6 +92,10 @@ def mla_absorb_q(*args) -> int:
 
 def mla_project_v(*args) -> int:
     return load().mla_project_v(*args)
+
+
+def mla_linear(*args) -> int:
+    return load().mla_linear(*args)
 
 
 def mla_prefill(*args) -> int:
@@ -502,6 +509,25 @@ def project_v(o, w_kv_b, *, out=None, err_count=None, stream=None):
     """Values [T, H, 128] of ``decode``'s latent output ``o`` [T, H, R];
     ``w_kv_b`` as in :func:`expand_kv`."""
     return _bind().project_v(o, w_kv_b, out, err_count, stream)
+
+
+_ACTIVATIONS = {None: MLA_ACT_NONE, "relu": MLA_ACT_RELU, "silu": MLA_ACT_SILU,
+                "gelu": MLA_ACT_GELU, "gelu_tanh": MLA_ACT_GELU_TANH}
+
+
+def linear(x, weight, *, bias=None, activation: str | None = None, residual=None, out=None,
+           err_count=None, stream=None):
+    """``act(x @ weight.T + bias) + residual`` as bf16 [T, N], rounded once.
+
+    ``x`` bf16 [T, K], ``weight`` bf16 [N, K] as a linear layer stores it,
+    ``bias`` bf16 [N], ``residual`` bf16 [T, N] (any row strides that are
+    multiples of 8); ``activation``: None, "relu", "silu", "gelu" (x Phi(x)) or
+    "gelu_tanh".  ``out`` may be ``residual`` (updated in place).
+    """
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"unsupported activation {activation!r}")
+    return _bind().linear(x, weight, bias, _ACTIVATIONS[activation], residual, out, err_count,
+                          stream)
 
 
 def prefill(q, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, sm_scale: float, *,

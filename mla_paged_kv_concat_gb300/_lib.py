@@ -23,6 +23,12 @@ MLA_KV_BF16 = 0
 MLA_KV_FP8_E4M3 = 1
 MLA_KV_FP8_E5M2 = 2
 
+MLA_ACT_NONE = 0
+MLA_ACT_RELU = 1
+MLA_ACT_SILU = 2
+MLA_ACT_GELU = 3
+MLA_ACT_GELU_TANH = 4
+
 MLA_PATH_AUTO = 0
 MLA_PATH_MMA_SYNC = 1
 MLA_PATH_TCGEN05 = 2
@@ -101,6 +107,8 @@ SIGNATURES = {
                             _I64, _P, _P]),
     "mla_project_v": (_I32, [_P, _I64, _I64, _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _I64,
                              _I64, _P, _P]),
+    "mla_linear": (_I32, [_P, _I64, _I32, _I32, _P, _I64, _I32, _P, _I32, _P, _I64, _P, _I64, _P,
+                          _P]),
     "mla_prefill_num_kv_splits": (_I32, [_I32, _I32, _I32, _I64, _I32]),
     "mla_prefill_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
     "mla_prefill": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _I64, _I64, _P, _I64,

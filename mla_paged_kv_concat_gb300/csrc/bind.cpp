@@ -456,6 +456,43 @@ PyObject* project_v(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return head_product(a, n, false);
 }
 
+// Row stride of [rows][columns] for the calls that read it from a single row
+// too: rounded up to a multiple of 8 there, where torch leaves it arbitrary.
+int64_t row_stride8(const Tensor& t) {
+  return t.size(0) > 1 ? t.stride(0) : (t.size(1) + 7) / 8 * 8;
+}
+
+// (x, weight, bias, activation, residual, out, err_count, stream)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, [](Call& c) {
+    Tensor x = c.tensor("x"), w = c.tensor("weight"), bias = c.maybe("bias");
+    const int act = c.small("activation");
+    Tensor res = c.maybe("residual"), out = c.maybe("out"), err = c.maybe("err_count");
+    c.take_stream();
+    typed(w, kBf16, {-1, -1}, "weight");
+    const int64_t N = w.size(0), K = w.size(1);
+    CHECK(N > 0 && K > 0, "weight must not be empty");
+    typed(x, kBf16, {-1, K}, "x");
+    const int64_t T = x.size(0);
+    if (!out.defined()) {
+      // rows of an odd length start on 16 bytes all the same
+      out = c.empty({T, (N + 7) / 8 * 8}, kBf16);
+      if (N % 8) out = out.narrow(1, 0, N);
+    }
+    typed(bias, kBf16, {N}, "bias");
+    typed(res, kBf16, {T, N}, "residual");
+    typed(out, kBf16, {T, N}, "out");
+    typed(err, kI32, {1}, "err_count");
+    done(mla_linear(ptr(x), row_stride8(x), as_int(T, "the number of tokens"),
+                    as_int(K, "in_features"), ptr(w), row_stride8(w), as_int(N, "out_features"),
+                    ptr(bias), static_cast<mla_activation>(act), ptr(res),
+                    res.defined() ? row_stride8(res) : 0, ptr(out), row_stride8(out),
+                    ptr<int>(err), c.s()),
+         "mla_linear");
+    return wrap(out);
+  });
+}
+
 // (q, q_pe, k_nope, v, k_pe, cu_q, cu_k, sm_scale, causal, num_kv_splits,
 //  workspace, out, lse, err_count, stream)
 PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -514,7 +551,8 @@ PyMethodDef kMethods[] = {
     method<batch_build>("batch_build"),   method<blocks_release>("blocks_release"),
     method<gather_cache>("gather_cache"), method<expand_kv>("expand_kv"),
     method<absorb_q>("absorb_q"),         method<project_v>("project_v"),
-    method<prefill>("prefill"),           {nullptr, nullptr, 0, nullptr}};
+    method<linear>("linear"),             method<prefill>("prefill"),
+    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 

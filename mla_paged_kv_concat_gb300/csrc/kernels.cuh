@@ -244,6 +244,33 @@ bool proj_pairs(int mode, int tokens, int heads, int k, int sm_count);
 cudaError_t launch_latent_proj(const ProjParams& p, const ProjMaps& m, int mode, int sm_count,
                                cudaStream_t stream);
 
+// The product with bias, activation and residual (linear.cu).
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+struct LinearParams {
+  int tokens, n, k;
+  int act;
+  const uint16_t* bias;      // [n] or nullptr
+  const uint16_t* residual;  // [tokens][n] at res_stride, or nullptr; may be y
+  int64_t res_stride;
+  uint16_t* y;
+  int64_t y_stride;
+  int bn, a_rows;            // from the plan
+  int* err_count;
+};
+// How a product is cut: columns of a tile, and the rows of the boxes that the
+// tensor maps of x (`a`) and W (`b`) take.
+struct LinearPlan {
+  int bn, a_rows, b_rows;
+};
+LinearPlan linear_plan(int tokens, int n, int k, int sm_count);
+// a: x as {K, 1, tokens}, box {64, 1, a_rows}; b: W as {K, 1, N}, box {64, 1,
+// b_rows}; c: y as {N, 1, tokens}, box {64, 1, 32}.  All 128-byte swizzled bf16.
+struct LinearMaps {
+  CUtensorMap a, b, c;
+};
+cudaError_t launch_linear(const LinearParams& p, const LinearMaps& m, int sm_count,
+                          cudaStream_t stream);
+
 // Prompt attention of the expanded form (prefill.cu).
 struct PrefillParams {
   int num_tokens, num_kv, heads, num_seqs;

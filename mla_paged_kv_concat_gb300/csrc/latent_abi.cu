@@ -323,6 +323,62 @@ mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_str
                      {y, y_row_stride, y_head_stride, v_dim}, {}, err_count, stream);
 }
 
+mla_status mla_linear(const void* x, int64_t x_row_stride, int num_tokens, int in_features,
+                      const void* w, int64_t w_row_stride, int out_features, const void* bias,
+                      mla_activation activation, const void* residual,
+                      int64_t residual_row_stride, void* y, int64_t y_row_stride,
+                      int* err_count, void* stream) {
+  if (num_tokens < 0 || in_features < 1 || out_features < 1 || activation < MLA_ACT_NONE ||
+      activation > MLA_ACT_GELU_TANH)
+    return MLA_ERR_INVALID_ARG;
+  constexpr int kMost = 1 << 20;
+  if (num_tokens > (1 << 30) || in_features > kMost || out_features > kMost)
+    return MLA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return MLA_OK;
+  const Heads hx{x, x_row_stride, 0, in_features}, hw{w, w_row_stride, 0, in_features};
+  const Heads hr{residual, residual_row_stride, 0, out_features};
+  const Heads hy{y, y_row_stride, 0, out_features};
+  if (!heads_ok(hx, num_tokens, 1) || !heads_ok(hw, out_features, 1) ||
+      !heads_ok(hy, num_tokens, 1) || (residual && !heads_ok(hr, num_tokens, 1)) ||
+      !aligned16(bias) || !aligned4(err_count))
+    return MLA_ERR_INVALID_ARG;
+  const Runs ry = runs(hy, num_tokens, 1);
+  if (intersect(ry, runs(hx, num_tokens, 1)) || intersect(ry, runs(hw, out_features, 1)) ||
+      intersect(ry, runs(bias, 2 * int64_t{out_features})))
+    return MLA_ERR_INVALID_ARG;
+  // an element of the residual is read by the thread that writes y's there
+  const bool in_place = residual == y && (residual_row_stride == y_row_stride || num_tokens == 1);
+  if (residual && !in_place && intersect(ry, runs(hr, num_tokens, 1))) return MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  cudaError_t e = mla::device_sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const mla::LinearPlan plan = mla::linear_plan(num_tokens, out_features, in_features, sms);
+  mla::LinearParams p = {};
+  p.tokens = num_tokens;
+  p.n = out_features;
+  p.k = in_features;
+  p.act = activation;
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.residual = static_cast<const uint16_t*>(residual);
+  p.res_stride = residual_row_stride;
+  p.y = static_cast<uint16_t*>(y);
+  p.y_stride = y_row_stride;
+  p.bn = plan.bn;
+  p.a_rows = plan.a_rows;
+  p.err_count = err_count;
+  mla::LinearMaps m;
+  mla_status st = make_map(&m.a, x, in_features, 1, num_tokens, x_row_stride, x_row_stride, 1,
+                           plan.a_rows);
+  if (st == MLA_OK)
+    st = make_map(&m.b, w, in_features, 1, out_features, w_row_stride, w_row_stride, 1,
+                  plan.b_rows);
+  if (st == MLA_OK)
+    st = make_map(&m.c, y, out_features, 1, num_tokens, y_row_stride, y_row_stride, 1, 32);
+  if (st != MLA_OK) return st;
+  e = mla::launch_linear(p, m, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
 // Measured on GB300, 16 heads (us at S = 1 / the rule's S / twice that): one
 // sequence of 256 rows, 32768 keys: 437 / 75 (9) / 92; two of 500 rows, 4596 keys:
 // 72 / 53 (2) / 63; contexts of 4096 to 32768 keys, eight of 1 to 5 rows: 382 / 218 (8)
