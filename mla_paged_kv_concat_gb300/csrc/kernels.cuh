@@ -254,13 +254,16 @@ struct LinearParams {
   int64_t res_stride;
   uint16_t* y;
   int64_t y_stride;
-  int bn, a_rows;            // from the plan
+  int form, bn, splits;      // from the plan
+  int a_rows;
   int* err_count;
 };
-// How a product is cut: columns of a tile, and the rows of the boxes that the
-// tensor maps of x (`a`) and W (`b`) take.
+// How a product is cut: its kernel, the columns of a tile (few tokens: the padded
+// tokens), the CTAs that share a sum, and the rows of the boxes that the tensor
+// maps of x (`a`) and W (`b`) take.
+enum { kLinearTile = 0, kLinearPair = 1, kLinearFew = 2 };
 struct LinearPlan {
-  int bn, a_rows, b_rows;
+  int form, bn, splits, a_rows, b_rows;
 };
 LinearPlan linear_plan(int tokens, int n, int k, int sm_count);
 // a: x as {K, 1, tokens}, box {64, 1, a_rows}; b: W as {K, 1, N}, box {64, 1,

@@ -363,7 +363,9 @@ mla_status mla_linear(const void* x, int64_t x_row_stride, int num_tokens, int i
   p.res_stride = residual_row_stride;
   p.y = static_cast<uint16_t*>(y);
   p.y_stride = y_row_stride;
+  p.form = plan.form;
   p.bn = plan.bn;
+  p.splits = plan.splits;
   p.a_rows = plan.a_rows;
   p.err_count = err_count;
   mla::LinearMaps m;

@@ -99,54 +99,106 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int n) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One thread's 64 columns of the residual from column c on (zeros without one).
+// One thread's N columns of the residual from column c on (zeros without one).
+template <int N>
 __device__ __forceinline__ void load_residual(const LinearParams& p, int row, int c,
-                                              uint4 (&r)[8]) {
-  const bool there = p.residual && row < p.tokens;
+                                              uint4 (&r)[N / 8]) {
+  const bool there = p.residual && row < p.tokens && c < p.n;
   const uint16_t* src = p.residual + (there ? row * p.res_stride : 0);
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
+  for (int q = 0; q < N / 8; ++q)
     r[q] = there ? load8(src, c + 8 * q, p.n) : make_uint4(0, 0, 0, 0);
 }
 
-// One epilogue warp's 32 rows x 64 columns: the accumulator's fp32 (a row a
-// lane) through bias, activation and residual to bf16 in the swizzled box `dst`
-// and from there to y (`some`: not all rows are past its end).
-__device__ __forceinline__ void finish_box(const LinearParams& p, uint8_t* dst,
-                                           const uint32_t (&r)[64], const uint4 (&res)[8], int lane,
-                                           bool some, const CUtensorMap* map, int c, int row0) {
-  // the store that last used this box, the one before the last, has read it
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-  __syncwarp();
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 32)
+    tc::ld_32x32b_x32(addr, r);
+  else
+    tc::ld_32x32b_x16(addr, r);
+}
+
+// One epilogue warp's 32 rows x `cols` (a multiple of 64) columns of a tile from
+// TMEM column `acc` and y column c0 on: fp32 (a row a lane) through bias,
+// activation and residual to bf16 in swizzled boxes of 64 columns (two in turn,
+// `nb` counts them) and from there to y.  `before` waits for the accumulator,
+// `after` gives it back.  The loop is not unrolled, and products without an
+// activation have kernels of their own: with all activations in 32 copies of the
+// body 1001 x 1536 -> 6136 took 35 us, waiting for instructions, against 22.
+template <bool ACT, typename Before, typename After>
+__device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, int cols, int c0,
+                                         int row0, int lane, uint8_t* boxes, int& nb,
+                                         const CUtensorMap* map, Before&& before, After&& after) {
+  constexpr int N = ACT ? 16 : 32;  // columns of a step
+  uint4 res[N / 8];
+  load_residual<N>(p, row0 + lane, c0, res);
+  if (!before()) return false;
+  tc::fence_after_sync();
+#pragma unroll 1
+  for (int j = 0; j < cols; j += N) {
+    const int c = c0 + j;
+    uint32_t r[N];
+    tmem_load<N>(acc + j, r);
+    uint4 nxt[N / 8], bias[N / 8];
+    if (j + N < cols) load_residual<N>(p, row0 + lane, c + N, nxt);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    float x[8];
+    for (int q = 0; q < N / 8; ++q)
+      bias[q] = p.bias ? load8(p.bias, c + 8 * q, p.n) : make_uint4(0, 0, 0, 0);
+    tc::wait_ld();
+    tc::reg_fence(r);
+    if (j + N >= cols) {
+      tc::fence_before_sync();
+      __syncwarp();
+      after();
+    }
+    float x[N];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r[q * 8 + e]);
-    if (p.bias) {
-      const uint4 b = load8(p.bias, c + 8 * q, p.n);
-      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+    for (int q = 0; q < N / 8; ++q) {
+      const uint32_t w[4] = {bias[q].x, bias[q].y, bias[q].z, bias[q].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[2 * e] += lo_f(w[e]);
-        x[2 * e + 1] += hi_f(w[e]);
+        const int i = 8 * q + 2 * e;
+        x[i] = __uint_as_float(r[i]);
+        x[i + 1] = __uint_as_float(r[i + 1]);
+        if (p.bias) {
+          x[i] += lo_f(w[e]);
+          x[i + 1] += hi_f(w[e]);
+        }
       }
     }
-    activate(p.act, x);
-    const uint32_t w[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
-    uint32_t o[4];
+    if (ACT) activate(p.act, x);
+    uint8_t* dst = boxes + (nb & 1) * STORE_BYTES;
+    if ((j & 63) == 0) {
+      // the store that last used this box, the one before the last, has read it
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();
+    }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      o[e] = p.residual ? pack_bf16x2(x[2 * e] + lo_f(w[e]), x[2 * e + 1] + hi_f(w[e]))
-                        : pack_bf16x2(x[2 * e], x[2 * e + 1]);
-    *reinterpret_cast<uint4*>(dst + sw128(lane, q)) = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int q = 0; q < N / 8; ++q) {
+      const uint32_t w[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 8 * q + 2 * e;
+        o[e] = p.residual ? pack_bf16x2(x[i] + lo_f(w[e]), x[i + 1] + hi_f(w[e]))
+                          : pack_bf16x2(x[i], x[i + 1]);
+      }
+      *reinterpret_cast<uint4*>(dst + sw128(lane, (j & 63) / 8 + q)) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+      res[q] = nxt[q];
+    }
+    if ((j & 63) == 64 - N) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int cb = c0 + (j & ~63);
+        if (row0 < p.tokens && cb < p.n) tma_store_3d(map, dst, cb, 0, row0);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      ++nb;
+    }
   }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    if (some) tma_store_3d(map, dst, c, 0, row0);
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  }
+  return true;
 }
 
 // Tile t of `mt` x `nt`, token blocks in groups of kGroup, token blocks of a
@@ -160,7 +212,7 @@ __device__ __forceinline__ void tile_at(int64_t t, int mt, int nt, int& m, int& 
   m = g * kGroup + in % rows;
 }
 
-template <int BN>
+template <int BN, bool ACT>
 __global__ void __launch_bounds__(192, 1)
     linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap ma,
                   const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mc) {
@@ -271,37 +323,16 @@ __global__ void __launch_bounds__(192, 1)
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     int ta = 0, nb = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < total; t += gridDim.x, ++ta) {
+    for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x, ++ta) {
       int m, n;
       tile_at(t, mt, nt, m, n);
       const int a = ta & 1;
-      const int row0 = m * TM + warp * STORE_ROWS;
-      uint4 res[2][8];
-      load_residual(p, row0 + lane, n * BN, res[0]);
-      if (!warp_wait(&acc_full[a], (ta >> 1) & 1)) {
-        ok = false;
-        break;
-      }
-      tc::fence_after_sync();
-#pragma unroll
-      for (int j = 0; j < BN / 64; ++j, ++nb) {
-        uint32_t r[64];
-        tc::ld_32x32b_x32(tmem + lanes + a * BN + j * 64,
-                          *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-        tc::ld_32x32b_x32(tmem + lanes + a * BN + j * 64 + 32,
-                          *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-        const int c = n * BN + j * 64;
-        if (j + 1 < BN / 64) load_residual(p, row0 + lane, c + 64, res[(j + 1) & 1]);
-        tc::wait_ld();
-        tc::reg_fence(r);
-        if (j == BN / 64 - 1) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[a]);
-        }
-        finish_box(p, box + (nb & 1) * STORE_BYTES, r, res[j & 1], lane,
-                   row0 < p.tokens && c < p.n, &mc, c, row0);
-      }
+      ok = epilogue<ACT>(
+          p, tmem + lanes + a * BN, BN, n * BN, m * TM + warp * STORE_ROWS, lane, box, nb, &mc,
+          [&] { return warp_wait(&acc_full[a], (ta >> 1) & 1); },
+          [&] {
+            if (lane == 0) mbar_arrive(&acc_empty[a]);
+          });
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok && lane == 0) gave_up(p.err_count);
@@ -315,46 +346,492 @@ __global__ void __launch_bounds__(192, 1)
   }
 }
 
-template <int BN>
+// ---------------------------------------------------------------- CTA pairs
+// For many tokens, which the tensor core bounds: two CTAs of a cluster share a
+// tile of 256 tokens x BN columns, each holds its 128 tokens of A and half of
+// the columns of B, and cta_group::2 products read both halves.  Rank 0 issues
+// for both; the ring's "landed" barrier is rank 0's and counts both CTAs' bytes;
+// "read" and "accumulator ready" arrive in both.  Eight epilogue warps.
+constexpr int kPairStages = 5;
+constexpr int kPairHalf = A_BYTES;  // A, and room for the half of B, of one stage
+constexpr int PP_STORE = kPairStages * 2 * kPairHalf;
+constexpr int PP_BAR = PP_STORE + 8 * 2 * STORE_BYTES;
+constexpr int PP_TMEM = PP_BAR + (2 * kPairStages + 4) * 8;
+constexpr int PP_SMEM = PP_TMEM + 16 + 1024;
+static_assert(PP_SMEM <= 227 * 1024, "shared memory");
+
+template <int BN, bool ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
+    linear_pair_kernel(const LinearParams p, const __grid_constant__ CUtensorMap ma,
+                       const __grid_constant__ CUtensorMap mb,
+                       const __grid_constant__ CUtensorMap mc) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + PP_BAR);  // [stages] rank 0's: both landed
+  uint64_t* empty = full + kPairStages;                         // [stages]
+  uint64_t* acc_full = empty + kPairStages;                     // [2]
+  uint64_t* acc_empty = acc_full + 2;                           // [2] rank 0's: 16 warps
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PP_TMEM);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_ctarank();
+
+  if (threadIdx.x == 128) {
+    tma_prefetch_desc(&ma);
+    tma_prefetch_desc(&mb);
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 16);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tc::pair_tmem_alloc(tmem_slot, 512);
+    tc::pair_tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int nk = (p.k + KC - 1) / KC;
+  const int mt = (p.tokens + 2 * TM - 1) / (2 * TM), nt = (p.n + BN - 1) / BN;
+  const int64_t total = static_cast<int64_t>(mt) * nt;
+  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int64_t t = first; t < total && ok; t += step) {
+        int m, n;
+        tile_at(t, mt, nt, m, n);
+        for (int kc = 0; kc < nk; ++kc, ++it) {
+          const int st = it % kPairStages;
+          if (!mbar_wait(&empty[st], ((it / kPairStages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + st * 2 * kPairHalf;
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * (A_BYTES + BN / 2 * 128));
+          const uint32_t bar = tc::map_peer(smem_u32(&full[st]), 0);
+          tc::pair_tma_load_3d(dst, &ma, bar, kc * KC, 0, m * 2 * TM + rank * TM);
+          tc::pair_tma_load_3d(dst + kPairHalf, &mb, bar, kc * KC, 0, n * BN + rank * (BN / 2));
+        }
+      }
+      if (!ok) gave_up(p.err_count);
+    }
+  } else if (warp == 5) {
+    bool ok = true;
+    int it = 0, ta = 0;
+    if (rank == 0) {
+      constexpr uint32_t idesc = tc::idesc_bf16(2 * TM, BN, 0, 0);
+      for (int64_t t = first; t < total && ok; t += step, ++ta) {
+        const int a = ta & 1;
+        const bool free = tc::mbar_wait_cluster(&acc_empty[a], ((ta >> 1) & 1) ^ 1);
+        if (!__all_sync(0xffffffffu, free)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        for (int kc = 0; kc < nk; ++kc, ++it) {
+          const int st = it % kPairStages;
+          if (!warp_wait(&full[st], (it / kPairStages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            const uint32_t base = smem_u32(smem + st * 2 * kPairHalf);
+            const uint64_t da = tc::smem_desc(base, 16, 1024, tc::kLayoutSw128);
+            const uint64_t db = tc::smem_desc(base + kPairHalf, 16, 1024, tc::kLayoutSw128);
+#pragma unroll
+            for (int k = 0; k < KC / 16; ++k)
+              tc::pair_mma_ss(tmem + a * 256, da + static_cast<uint64_t>(k * 2),
+                              db + static_cast<uint64_t>(k * 2), idesc,
+                              (kc > 0 || k > 0) ? 1u : 0u);
+            tc::pair_commit(&empty[st], 3);
+            if (kc == nk - 1) tc::pair_commit(&acc_full[a], 3);
+          }
+          __syncwarp();
+        }
+      }
+      for (int j = 0; ok && j < 2 && j < ta; ++j) {
+        const int u = ta - 1 - j;
+        warp_wait(&acc_full[u & 1], (u >> 1) & 1);
+      }
+      if (!ok && lane == 0) gave_up(p.err_count);
+    }
+  } else {
+    // warps 0-3 the tile's first half of columns (128 of 192), 6-9 the others; a
+    // warp reads the TMEM lanes of its quarter (warp % 4)
+    constexpr int kFirst = (BN / 64 + 1) / 2 * 64;
+    const int half = warp >= 6, ew = half ? warp - 2 : warp, qd = warp & 3;
+    uint8_t* box = smem + PP_STORE + ew * 2 * STORE_BYTES;
+    const uint32_t lanes = static_cast<uint32_t>(qd * 32) << 16;
+    int ta = 0, nb = 0;
+    bool ok = true;
+    for (int64_t t = first; t < total && ok; t += step, ++ta) {
+      int m, n;
+      tile_at(t, mt, nt, m, n);
+      const int a = ta & 1;
+      ok = epilogue<ACT>(
+          p, tmem + lanes + a * 256 + half * kFirst, half ? BN - kFirst : kFirst, n * BN + half * kFirst,
+          m * 2 * TM + rank * TM + qd * STORE_ROWS, lane, box, nb, &mc,
+          [&] { return warp_wait(&acc_full[a], (ta >> 1) & 1); },
+          [&] {
+            if (lane == 0) tc::arrive_peer(tc::map_peer(smem_u32(&acc_empty[a]), 0));
+          });
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (!ok && lane == 0) gave_up(p.err_count);
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();  // the peer's barriers and operands are used to the end
+  if (warp == 5) {
+    tc::fence_after_sync();
+    tc::pair_tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- few tokens
+// Up to 128 tokens the weight is the work, and it has to come in at the rate of
+// memory: the operands change places (128 rows of W are A, the tokens B, padded
+// to TN), and the sum over K is split over a cluster of up to eight CTAs, so that
+// nearly every SM has its part of W under way whatever N is.  Each CTA keeps its
+// partial sums in TMEM and sends them, four tokens at a time, to the CTA of the
+// cluster that finishes those tokens, which adds the parts in rank order.  A
+// thread has one column of y: a warp stores 64 bytes of a token's row at once.
+constexpr int kAhead = 8;  // chunks of W asked for before the kernel before has ended
+
+__device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+template <int TN>
+struct FewCfg {
+  static constexpr int STAGE = A_BYTES + TN * KC * 2;
+  static constexpr int CTAS = TN >= 64 ? 1 : 2;  // an SM
+  // parts received: at most TN / 4 groups of four tokens from all ranks
+  static constexpr int RECV = 128 * 16 * (TN / 4 + 8);
+  static constexpr int STAGES = TN == 16 ? 4 : TN == 32 ? 3 : TN == 64 ? 7 : 4;
+  static constexpr int OFF_RECV = STAGES * STAGE;
+  static constexpr int OFF_BAR = OFF_RECV + RECV;
+  static constexpr int OFF_TMEM = OFF_BAR + (2 * STAGES + 2) * 8;
+  static constexpr int SMEM = OFF_TMEM + 16 + 1024;
+  static constexpr uint32_t COLS = TN < 32 ? 32 : TN;
+  static_assert(SMEM * CTAS <= 227 * 1024, "shared memory");
+};
+
+template <int TN, bool ACT>
+__global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
+    linear_few_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mx,
+                      const __grid_constant__ CUtensorMap mw) {
+  using C = FewCfg<TN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [STAGES]
+  uint64_t* empty = full + C::STAGES;                               // [STAGES]
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* recv_full = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.splits;
+  const int rank = static_cast<int>(tc::cluster_ctarank());
+  const int n0 = static_cast<int>(blockIdx.x / S) * 128;
+  const int t0 = static_cast<int>(blockIdx.y) * TN;
+  const int nt = min(TN, p.tokens - t0);  // tokens here
+  const int quads = (nt + 3) / 4, per = (quads + S - 1) / S;
+  const int q_lo = min(quads, rank * per), q_hi = min(quads, q_lo + per);
+
+  if (threadIdx.x == 128) {
+    tma_prefetch_desc(&mx);
+    tma_prefetch_desc(&mw);
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(recv_full, 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(recv_full, static_cast<uint32_t>(S * (q_hi - q_lo) * 128 * 16));
+  }
+  if (warp == 5) {
+    tc::tmem_alloc(tmem_slot, C::COLS);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();  // every CTA's barrier is there before parts are sent
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int nk = (p.k + KC - 1) / KC;
+  const int k_lo = static_cast<int>(static_cast<int64_t>(nk) * rank / S);
+  const int k_hi = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) / S);
+  bool ok = true;
+  // The first of this CTA's W comes on its way into L2 while the kernel before
+  // still runs: L2 holds what that one may write of it, so nothing stale is read.
+  if (threadIdx.x == 128)
+    for (int kc = k_lo; kc < min(k_hi, k_lo + kAhead); ++kc) tma_prefetch_l2(&mw, kc * KC, 0, n0);
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 4) {
+    if (lane == 0) {
+      for (int kc = k_lo; kc < k_hi; ++kc) {
+        const int it = kc - k_lo, st = it % C::STAGES;
+        if (!mbar_wait(&empty[st], ((it / C::STAGES) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = smem + st * C::STAGE;
+        mbar_arrive_expect_tx(&full[st], C::STAGE);
+        tma_load_3d(dst, &mw, &full[st], kc * KC, 0, n0);
+        tma_load_3d(dst + A_BYTES, &mx, &full[st], kc * KC, 0, t0);
+      }
+    }
+  } else if (warp == 5) {
+    constexpr uint32_t idesc = tc::idesc_bf16(128, TN, 0, 0);
+    for (int kc = k_lo; kc < k_hi; ++kc) {
+      const int it = kc - k_lo, st = it % C::STAGES;
+      if (!warp_wait(&full[st], (it / C::STAGES) & 1)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
+        const uint32_t base = smem_u32(smem + st * C::STAGE);
+        const uint64_t da = tc::smem_desc(base, 16, 1024, tc::kLayoutSw128);
+        const uint64_t db = tc::smem_desc(base + A_BYTES, 16, 1024, tc::kLayoutSw128);
+#pragma unroll
+        for (int k = 0; k < KC / 16; ++k)
+          tc::mma_ss(tmem, da + static_cast<uint64_t>(k * 2), db + static_cast<uint64_t>(k * 2),
+                     idesc, (it > 0 || k > 0) ? 1u : 0u);
+        tc::commit(&empty[st]);
+        if (kc == k_hi - 1) tc::commit(acc_full);
+      }
+      __syncwarp();
+    }
+    if (ok) ok = warp_wait(acc_full, 0);  // nothing is in flight when TMEM is freed
+  } else {
+    const int row = warp * 32 + lane;  // TMEM lane, row of W
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    ok = warp_wait(acc_full, 0);
+    if (ok) {
+      tc::fence_after_sync();
+      const uint32_t recv = smem_u32(smem + C::OFF_RECV);
+#pragma unroll 1
+      for (int c = 0; c < nt; c += 16) {
+        uint32_t r[16];
+        tc::ld_32x32b_x16(tmem + lanes + c, r);
+        tc::wait_ld();
+        tc::reg_fence(r);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int quad = c / 4 + q;
+          if (quad >= quads) break;
+          const int to = quad / per;
+          const uint32_t slot = static_cast<uint32_t>((rank * per + quad - to * per) * 128 + row) * 16;
+          tc::st_async_v4u(tc::map_peer(recv + slot, to), r[4 * q], r[4 * q + 1], r[4 * q + 2],
+                           r[4 * q + 3], tc::map_peer(smem_u32(recv_full), to));
+        }
+      }
+    }
+    if (q_hi > q_lo) {
+      const int n = n0 + row;
+      const bool mine = n < p.n;
+      const float bias = p.bias && mine ? lo_f(p.bias[n]) : 0.f;
+      // the residual of the next 16 tokens, under the wait or the last ones' work
+      float res[16];
+      auto load = [&](int quad) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int t = quad * 4 + e;
+          res[e] = p.residual && mine && t < nt && quad + e / 4 < q_hi
+                       ? lo_f(p.residual[(t0 + t) * p.res_stride + n])
+                       : 0.f;
+        }
+      };
+      load(q_lo);
+      const bool got = tc::mbar_wait_cluster(recv_full, 0);
+      ok = __all_sync(0xffffffffu, got) && ok;
+      if (ok && mine) {
+#pragma unroll 1
+        for (int quad = q_lo; quad < q_hi; quad += 4) {
+          float r[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[e] = res[e];
+          if (quad + 4 < q_hi) load(quad + 4);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (quad + q >= q_hi) break;
+            float x[4] = {bias, bias, bias, bias};
+            for (int s = 0; s < S; ++s) {
+              const float4 v = *reinterpret_cast<const float4*>(
+                  smem + C::OFF_RECV + ((s * per + quad + q - q_lo) * 128 + row) * 16);
+              x[0] += v.x;
+              x[1] += v.y;
+              x[2] += v.z;
+              x[3] += v.w;
+            }
+            if (ACT) activate(p.act, x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = (quad + q) * 4 + e;
+              if (t >= nt) break;
+              p.y[(t0 + t) * p.y_stride + n] =
+                  __bfloat16_as_ushort(__float2bfloat16_rn(p.residual ? x[e] + r[4 * q + e] : x[e]));
+            }
+          }
+        }
+      }
+    }
+  }
+  if (!ok && lane == 0) gave_up(p.err_count);
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 5) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, C::COLS);
+  }
+}
+
+template <int BN, bool ACT>
 cudaError_t launch(const LinearParams& p, const LinearMaps& m, int sm_count, cudaStream_t stream) {
   using C = Cfg<BN>;
   static std::atomic<uint64_t> attr_done{0};
-  cudaError_t e = set_smem_attr_once(linear_kernel<BN>, C::SMEM, attr_done);
+  cudaError_t e = set_smem_attr_once(linear_kernel<BN, ACT>, C::SMEM, attr_done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>((p.tokens + TM - 1) / TM) * ((p.n + BN - 1) / BN);
   const int grid = tiles < sm_count ? static_cast<int>(tiles) : sm_count;
-  return launch_overlapped(linear_kernel<BN>, dim3(grid), dim3(192), C::SMEM, stream, p, m.a, m.b,
-                           m.c);
+  return launch_overlapped(linear_kernel<BN, ACT>, dim3(grid), dim3(192), C::SMEM, stream, p, m.a,
+                           m.b, m.c);
 }
+
+template <int BN, bool ACT>
+cudaError_t launch_pair(const LinearParams& p, const LinearMaps& m, int sm_count,
+                        cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = set_smem_attr_once(linear_pair_kernel<BN, ACT>, PP_SMEM, attr_done);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((p.tokens + 255) / 256) * ((p.n + BN - 1) / BN);
+  const int pairs = tiles < sm_count / 2 ? static_cast<int>(tiles) : sm_count / 2;
+  return launch_overlapped(linear_pair_kernel<BN, ACT>, dim3(2 * pairs), dim3(320), PP_SMEM, stream, p,
+                           m.a, m.b, m.c);
+}
+
+template <int TN, bool ACT>
+cudaError_t launch_few(const LinearParams& p, const LinearMaps& m, cudaStream_t stream) {
+  using C = FewCfg<TN>;
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = set_smem_attr_once(linear_few_kernel<TN, ACT>, C::SMEM, attr_done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.n + 127) / 128 * p.splits),
+                     static_cast<unsigned>((p.tokens + TN - 1) / TN));
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.splits);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, linear_few_kernel<TN, ACT>, p, m.a, m.b);
+}
+
+template <bool ACT>
+cudaError_t launch_any(const LinearParams& p, const LinearMaps& m, int sm_count,
+                       cudaStream_t stream) {
+  if (p.form == kLinearFew) {
+    switch (p.bn) {
+      case 16: return launch_few<16, ACT>(p, m, stream);
+      case 32: return launch_few<32, ACT>(p, m, stream);
+      case 64: return launch_few<64, ACT>(p, m, stream);
+      default: return launch_few<128, ACT>(p, m, stream);
+    }
+  }
+  if (p.form == kLinearPair) {
+    switch (p.bn) {
+      case 256: return launch_pair<256, ACT>(p, m, sm_count, stream);
+      case 192: return launch_pair<192, ACT>(p, m, sm_count, stream);
+      default: return launch_pair<128, ACT>(p, m, sm_count, stream);
+    }
+  }
+  switch (p.bn) {
+    case 256: return launch<256, ACT>(p, m, sm_count, stream);
+    case 128: return launch<128, ACT>(p, m, sm_count, stream);
+    default: return launch<64, ACT>(p, m, sm_count, stream);
+  }
+}
+
+int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Columns of a tile: those for which the CTA with the most tiles takes in the
-// fewest operand rows (tokens and columns; K is the same).
+// The kernel and tile with the least estimated time, in cycles.  A chunk of K
+// takes what its operands' way through L2 does, about 55 bytes a cycle and SM
+// (7/3 cycles for a row of 128 bytes), or its products (2.16 cycles a column of
+// 128 rows); a tile's start and end come to about 4000, once for a persistent
+// CTA and for every CTA of the kernel for few tokens.
 LinearPlan linear_plan(int tokens, int n, int k, int sm_count) {
-  LinearPlan plan = {};
-  plan.a_rows = tokens < TM ? tokens : TM;
-  const int64_t blocks = (tokens + TM - 1) / TM;
-  int64_t best = 0;
-  for (int bn = 256; bn >= 64; bn /= 2) {
-    const int64_t rounds = (blocks * ((n + bn - 1) / bn) + sm_count - 1) / sm_count;
-    const int64_t cost = rounds * (plan.a_rows + bn);
-    if (plan.bn == 0 || cost < best) {
-      plan.bn = bn;
-      best = cost;
+  const int64_t nk = cdiv64(k, KC);
+  LinearPlan best = {};
+  int64_t least = 0;
+  auto take = [&](int64_t cost, const LinearPlan& plan) {
+    if (least == 0 || cost < least) {
+      least = cost;
+      best = plan;
     }
+  };
+  auto chunk = [](int rows, int cols) {
+    const int64_t loads = int64_t{rows} * 7 / 3, products = int64_t{cols} * 54 / 25;
+    return loads > products ? loads : products;
+  };
+  if (tokens <= 1024) {
+    const int tn = tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
+    const int64_t ctas = cdiv64(n, 128) * cdiv64(tokens, tn);
+    for (int s = 1; s <= 8 && s <= nk; ++s)
+      take(cdiv64(ctas * s, (tn >= 64 ? 1 : 2) * sm_count) *
+               (cdiv64(nk, s) * chunk(128 + tn, 128) + 4000),
+           {kLinearFew, tn, s, tn, 128});
   }
-  plan.b_rows = plan.bn;
-  return plan;
+  if (tokens > 128) {
+    for (int bn = 256; bn >= 128; bn -= 64)
+      take(cdiv64(cdiv64(tokens, 256) * cdiv64(n, bn), sm_count / 2) * nk *
+                   chunk(128 + bn / 2, bn) + 4000,
+           {kLinearPair, bn, 1, TM, bn / 2});
+    for (int bn = 256; bn >= 64; bn /= 2)
+      take(cdiv64(cdiv64(tokens, TM) * cdiv64(n, bn), sm_count) * nk * chunk(128 + bn, bn) + 4000,
+           {kLinearTile, bn, 1, TM, bn});
+  }
+  return best;
 }
 
 cudaError_t launch_linear(const LinearParams& p, const LinearMaps& m, int sm_count,
                           cudaStream_t stream) {
-  switch (p.bn) {
-    case 256: return launch<256>(p, m, sm_count, stream);
-    case 128: return launch<128>(p, m, sm_count, stream);
-    default: return launch<64>(p, m, sm_count, stream);
-  }
+  return p.act == kActNone ? launch_any<false>(p, m, sm_count, stream)
+                           : launch_any<true>(p, m, sm_count, stream);
 }
 
 }  // namespace mla
