@@ -677,6 +677,7 @@ typedef enum {
  *   y          bf16 [num_tokens][out_features] at its row stride.  It may be the
  *              residual itself (same address, same stride), else it must not
  *              overlap an input.
+ *   activation one of mla_activation.
  *   in_features, out_features  1 .. 2^20; every pointer 16-byte aligned, every
  *              row stride a positive multiple of 8 and at least the row (that of
  *              a single row, too).
@@ -686,7 +687,7 @@ typedef enum {
  */
 mla_status mla_linear(const void* x, int64_t x_row_stride, int num_tokens, int in_features,
                       const void* w, int64_t w_row_stride, int out_features, const void* bias,
-                      mla_activation activation, const void* residual,
+                      int activation, const void* residual,
                       int64_t residual_row_stride, void* y, int64_t y_row_stride,
                       int* err_count, void* stream);
 
@@ -765,6 +766,46 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
                        int causal, float sm_scale, int num_kv_splits, void* workspace,
                        size_t workspace_bytes, void* o, int64_t o_row_stride,
                        int64_t o_head_stride, float* lse, int* err_count, void* stream);
+
+/*
+ * mla_prefill_shared - mla_prefill for a batch whose sequences share prefixes:
+ * rows of all sequences of a group attend to the group's prefix keys together,
+ * so that those are read once for 256 rows instead of once for a sequence.
+ *
+ * Group g is the sequences [group_seqs[g], group_seqs[g + 1]), its prefix the
+ * key rows [cu_prefix[g], cu_prefix[g + 1]) of k_nope, v and k_pe, which also
+ * hold the sequences' own keys (cu_seqlens_k, behind the prefixes or anywhere):
+ * row i of sequence b attends to every key of its group's prefix and to those of
+ * its own keys that mla_prefill would let it attend to.  Sequences before
+ * group_seqs[0] or from group_seqs[num_groups] on have no prefix.
+ *
+ *   group_seqs, cu_prefix   device int32 [num_groups + 1], non-decreasing;
+ *                   values are clamped (cu_prefix counted).  num_groups 1 ..
+ *                   65535.
+ *   num_prefix_splits, num_kv_splits   1 .. 64 parts of a prefix's keys and of a
+ *                   sequence's own, joined by a second kernel (see
+ *                   mla_prefill_shared_num_kv_splits).
+ *   workspace       >= mla_prefill_workspace_bytes(num_tokens, num_heads,
+ *                   num_prefix_splits + num_kv_splits, v_dim).
+ * Otherwise as mla_prefill.
+ */
+mla_status mla_prefill_shared(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* q_pe,
+    int64_t q_pe_row_stride, int64_t q_pe_head_stride, int num_tokens, int num_heads,
+    const void* k_nope, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+    int64_t v_row_stride, int64_t v_head_stride, const void* k_pe, int64_t k_pe_row_stride,
+    int num_kv_tokens, int nope_dim, int rope_dim, int v_dim, const int32_t* cu_seqlens_q,
+    const int32_t* cu_seqlens_k, int num_seqs, const int32_t* group_seqs,
+    const int32_t* cu_prefix, int num_groups, int causal, float sm_scale, int num_prefix_splits,
+    int num_kv_splits, void* workspace, size_t workspace_bytes, void* o, int64_t o_row_stride,
+    int64_t o_head_stride, float* lse, int* err_count, void* stream);
+
+/* Parts that mla_prefill_shared should cut the prefixes' keys into (returned) and
+ * the sequences' own (*num_kv_splits, may be NULL).  max_prefix_len, max_kv_len:
+ * the longest prefix and the longest sequence's own keys (upper bounds will do). */
+int mla_prefill_shared_num_kv_splits(int num_tokens, int num_seqs, int num_groups, int num_heads,
+                                     int64_t max_prefix_len, int64_t max_kv_len, int sm_count,
+                                     int* num_kv_splits);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* mla_status_string(mla_status status);

@@ -19,6 +19,7 @@ Thin Python binding over the C ABI of ``libmla.so`` (``include/mla.h``):
   with the kv_b weight of the expanded and the absorbed form.
 * ``linear(...)`` — a projection with bias, activation and residual.
 * ``prefill(...)`` — attention of the expanded form over ragged prompts.
+* ``prefill_shared(...)`` — the same for sequences that share prefixes.
 * ``cache_write(...)`` and ``decode(...)`` — torch-tensor conveniences that
   only marshal pointers, strides and the current CUDA stream; every step of
   the computation runs in the library's CUDA kernels.
@@ -42,6 +43,7 @@ __all__ = [
     "mla_expand_kv", "mla_absorb_q", "mla_project_v", "expand_kv", "absorb_q", "project_v",
     "mla_prefill", "mla_prefill_num_kv_splits", "mla_prefill_workspace_bytes", "prefill",
     "batch_build", "blocks_release", "gather_cache", "BatchTables", "mla_linear", "linear",
+    "mla_prefill_shared", "mla_prefill_shared_num_kv_splits", "prefill_shared",
     "MlaError", "load",
     "MLA_KV_BF16", "MLA_KV_FP8_E4M3", "MLA_KV_FP8_E5M2", "MLA_PATH_AUTO", "MLA_PATH_MMA_SYNC",
     "MLA_PATH_TCGEN05", "MLA_ACT_NONE", "MLA_ACT_RELU", "MLA_ACT_SILU", "MLA_ACT_GELU",
@@ -105,6 +107,22 @@ def mla_prefill(*args) -> int:
 def mla_prefill_num_kv_splits(num_tokens: int, num_seqs: int, num_heads: int, max_kv_len: int,
                               sm_count: int) -> int:
     return load().mla_prefill_num_kv_splits(num_tokens, num_seqs, num_heads, max_kv_len, sm_count)
+
+
+def mla_prefill_shared(*args) -> int:
+    return load().mla_prefill_shared(*args)
+
+
+def mla_prefill_shared_num_kv_splits(num_tokens: int, num_seqs: int, num_groups: int,
+                                     num_heads: int, max_prefix_len: int, max_kv_len: int,
+                                     sm_count: int) -> tuple[int, int]:
+    """(parts of a prefix's keys, parts of a sequence's own keys)."""
+    import ctypes
+    own = ctypes.c_int()
+    pre = load().mla_prefill_shared_num_kv_splits(num_tokens, num_seqs, num_groups, num_heads,
+                                                  max_prefix_len, max_kv_len, sm_count,
+                                                  ctypes.byref(own))
+    return pre, own.value
 
 
 def mla_prefill_workspace_bytes(num_tokens: int, num_heads: int, num_kv_splits: int,
@@ -548,3 +566,22 @@ def prefill(q, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, sm_scale: float, *,
     q, q_pe = q if isinstance(q, (tuple, list)) else (q, None)
     return _bind().prefill(q, q_pe, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, sm_scale, causal,
                            num_kv_splits, workspace, out, lse, err_count, stream)
+
+
+def prefill_shared(q, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, group_seqs, cu_prefix,
+                   sm_scale: float, *, causal: bool = True, num_kv_splits=1, workspace=None,
+                   out=None, lse=None, err_count=None, stream=None):
+    """:func:`prefill` for sequences that share prefixes; returns (o, lse).
+
+    Group g is the sequences ``group_seqs[g]`` to ``group_seqs[g + 1]`` (int32
+    [groups + 1]); their rows all attend to the key rows ``cu_prefix[g]`` to
+    ``cu_prefix[g + 1]`` (int32 [groups + 1]) of ``k_nope``, ``v`` and ``k_pe``,
+    besides their own keys there (``cu_seqlens_k``, masked as by ``causal``).
+    ``num_kv_splits``: parts of the prefixes' keys and of the sequences' own, a
+    pair from ``mla_prefill_shared_num_kv_splits``, or the first of them.
+    """
+    q, q_pe = q if isinstance(q, (tuple, list)) else (q, None)
+    pre, own = num_kv_splits if isinstance(num_kv_splits, (tuple, list)) else (num_kv_splits, 1)
+    return _bind().prefill_shared(q, q_pe, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, group_seqs,
+                                  cu_prefix, sm_scale, causal, pre, own, workspace, out, lse,
+                                  err_count, stream)

@@ -485,7 +485,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     typed(err, kI32, {1}, "err_count");
     done(mla_linear(ptr(x), row_stride8(x), as_int(T, "the number of tokens"),
                     as_int(K, "in_features"), ptr(w), row_stride8(w), as_int(N, "out_features"),
-                    ptr(bias), static_cast<mla_activation>(act), ptr(res),
+                    ptr(bias), act, ptr(res),
                     res.defined() ? row_stride8(res) : 0, ptr(out), row_stride8(out),
                     ptr<int>(err), c.s()),
          "mla_linear");
@@ -494,13 +494,20 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (q, q_pe, k_nope, v, k_pe, cu_q, cu_k, sm_scale, causal, num_kv_splits,
-//  workspace, out, lse, err_count, stream)
-PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(a, n, [](Call& c) {
+//  workspace, out, lse, err_count, stream); shared: with group_seqs and
+//  cu_prefix behind cu_k, and the prefix's parts before num_kv_splits
+PyObject* prefill_call(PyObject* const* a, Py_ssize_t n, bool shared) {
+  return guarded(a, n, [shared](Call& c) {
     Tensor q = c.tensor("q"), q_pe = c.maybe("q_pe"), k = c.tensor("k_nope"), v = c.tensor("v");
     Tensor k_pe = c.tensor("k_pe"), cu_q = c.tensor("cu_seqlens_q"), cu_k = c.tensor("cu_seqlens_k");
+    Tensor gs, cu_p;
+    if (shared) {
+      gs = c.tensor("group_seqs");
+      cu_p = c.tensor("cu_prefix");
+    }
     const float sm_scale = static_cast<float>(c.real());
     const int causal = c.truth();
+    const int pre = shared ? c.small("num_prefix_splits") : 0;
     const int splits = c.small("num_kv_splits");
     Tensor ws = c.maybe("workspace"), out = c.maybe("out"), lse = c.maybe("lse");
     Tensor err = c.maybe("err_count");
@@ -518,27 +525,52 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     typed(v, kBf16, {Tk, H, kV}, "v");
     typed(k_pe, kBf16, {Tk, P}, "k_pe");
     typed(cu_k, kI32, {B + 1}, "cu_seqlens_k");
+    int64_t G = 0;
+    if (shared) {
+      typed(gs, kI32, {-1}, "group_seqs");
+      G = gs.size(0) - 1;
+      CHECK(G >= 1, "group_seqs must hold a group");
+      typed(cu_p, kI32, {G + 1}, "cu_prefix");
+      CHECK(pre >= 1 && pre <= 64 && splits >= 1 && splits <= 64, "1 to 64 parts of the keys");
+    }
     typed(out, kBf16, {T, H, kV}, "out");
     typed(lse, at::kFloat, {T, H}, "lse");
     typed(err, kI32, {1}, "err_count");
     CHECK(lse.is_contiguous(), "lse must be contiguous");
     const int Ti = as_int(T, "the number of tokens"), Hi = as_int(H, "the number of heads");
-    const size_t need = mla_prefill_workspace_bytes(Ti, Hi, splits, kV);
+    const size_t need = mla_prefill_workspace_bytes(Ti, Hi, splits + pre, kV);
     if (need && !ws.defined()) {
       CHECK(need <= static_cast<size_t>(INT64_MAX), "the workspace does not fit");
       ws = c.empty({static_cast<int64_t>(need)}, at::kByte, false);
     }
     CHECK(!ws.defined() || ws.is_contiguous(), "workspace must be contiguous");
     const Strides sq(q), sk(k), sv(v), so(out), sp = q_pe.defined() ? Strides(q_pe) : Strides();
-    done(mla_prefill(ptr(q), sq.row, sq.head, ptr(q_pe), sp.row, sp.head, Ti, Hi, ptr(k), sk.row,
-                     sk.head, ptr(v), sv.row, sv.head, ptr(k_pe), row_stride(k_pe),
-                     as_int(Tk, "the number of keys"), kNope, as_int(P, "rope_dim"), kV,
-                     ptr<int32_t>(cu_q), ptr<int32_t>(cu_k), as_int(B, "the number of sequences"),
-                     causal, sm_scale, splits, ptr(ws), ws.defined() ? ws.nbytes() : 0, ptr(out),
-                     so.row, so.head, ptr<float>(lse), ptr<int>(err), c.s()),
-         "mla_prefill");
+    const int Tk32 = as_int(Tk, "the number of keys"), P32 = as_int(P, "rope_dim");
+    const int B32 = as_int(B, "the number of sequences");
+    const size_t ws_bytes = ws.defined() ? ws.nbytes() : 0;
+    if (shared)
+      done(mla_prefill_shared(ptr(q), sq.row, sq.head, ptr(q_pe), sp.row, sp.head, Ti, Hi, ptr(k),
+                              sk.row, sk.head, ptr(v), sv.row, sv.head, ptr(k_pe),
+                              row_stride(k_pe), Tk32, kNope, P32, kV, ptr<int32_t>(cu_q),
+                              ptr<int32_t>(cu_k), B32, ptr<int32_t>(gs), ptr<int32_t>(cu_p),
+                              as_int(G, "the number of groups"), causal, sm_scale, pre, splits,
+                              ptr(ws), ws_bytes, ptr(out), so.row, so.head, ptr<float>(lse),
+                              ptr<int>(err), c.s()),
+           "mla_prefill_shared");
+    else
+      done(mla_prefill(ptr(q), sq.row, sq.head, ptr(q_pe), sp.row, sp.head, Ti, Hi, ptr(k), sk.row,
+                       sk.head, ptr(v), sv.row, sv.head, ptr(k_pe), row_stride(k_pe), Tk32, kNope,
+                       P32, kV, ptr<int32_t>(cu_q), ptr<int32_t>(cu_k), B32, causal, sm_scale,
+                       splits, ptr(ws), ws_bytes, ptr(out), so.row, so.head, ptr<float>(lse),
+                       ptr<int>(err), c.s()),
+           "mla_prefill");
     return tuple({out, lse});
   });
+}
+
+PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) { return prefill_call(a, n, false); }
+PyObject* prefill_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return prefill_call(a, n, true);
 }
 
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
@@ -552,7 +584,7 @@ PyMethodDef kMethods[] = {
     method<gather_cache>("gather_cache"), method<expand_kv>("expand_kv"),
     method<absorb_q>("absorb_q"),         method<project_v>("project_v"),
     method<linear>("linear"),             method<prefill>("prefill"),
-    {nullptr, nullptr, 0, nullptr}};
+    method<prefill_shared>("prefill_shared"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 

@@ -291,8 +291,13 @@ struct PrefillParams {
   float* ws_o;    // [splits][num_tokens][heads][128]
   float* ws_lse;  // [splits][num_tokens][heads]
   int* err_count;
+  // groups of sequences that share a prefix (num_groups > 0): prefix_splits of
+  // the num_splits parts are the prefix's
+  int num_groups, prefix_splits;
+  const int32_t *group_seqs, *cu_prefix;  // [num_groups + 1]
   // set by the launch
-  int slots, head_group;
+  int slots, head_group, prefix_slots;
+  uint32_t prefix_units;
 };
 // {dims, heads (k_pe: 1), rows}, box {64, 1, 128} (v: {64, 1, 64}), 128-byte
 // swizzled bf16.

@@ -122,6 +122,127 @@ mla_status latent_proj(int mode, Heads in, int in_heads, int tokens, const void*
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
 }
 
+// Groups of sequences that share a prefix, for the prompt attention.
+struct Groups {
+  const int32_t *seqs = nullptr, *cu_prefix = nullptr;
+  int num = 0, splits = 0;
+};
+
+mla_status prefill(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* q_pe,
+                   int64_t q_pe_row_stride, int64_t q_pe_head_stride, int num_tokens,
+                   int num_heads, const void* k_nope, int64_t k_row_stride, int64_t k_head_stride,
+                   const void* v, int64_t v_row_stride, int64_t v_head_stride, const void* k_pe,
+                   int64_t k_pe_row_stride, int num_kv_tokens, int nope_dim, int rope_dim,
+                   int v_dim, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                   int num_seqs, const Groups& groups, int causal, float sm_scale,
+                   int num_kv_splits, void* workspace, size_t workspace_bytes, void* o,
+                   int64_t o_row_stride, int64_t o_head_stride, float* lse, int* err_count,
+                   void* stream) {
+  const int parts = num_kv_splits + groups.splits;
+  if (num_tokens < 0 || num_kv_tokens < 0 || num_seqs < 0 || num_heads < 1 || num_heads > 1024 ||
+      num_kv_splits < 1 || num_kv_splits > 64 || groups.num < 0 ||
+      (groups.num > 0 && (groups.splits < 1 || groups.splits > 64)) || nope_dim < 1 || rope_dim < 1 || v_dim < 1 ||
+      !(sm_scale >= 1e-30f && sm_scale <= 1e30f))
+    return MLA_ERR_INVALID_ARG;
+  if (nope_dim != kNopeDim || v_dim != kVDim || rope_dim != 64 || num_seqs > 65535 ||
+      groups.num > 65535 ||
+      num_tokens > (1 << 30) || num_kv_tokens > (1 << 30))
+    return MLA_ERR_UNSUPPORTED;
+  if (num_tokens == 0 || num_seqs == 0) return MLA_OK;
+  const Heads hq{q, q_row_stride, q_head_stride, q_pe ? nope_dim : nope_dim + rope_dim};
+  const Heads hqp = q_pe ? Heads{q_pe, q_pe_row_stride, q_pe_head_stride, rope_dim}
+                         : Heads{q ? static_cast<const uint16_t*>(q) + nope_dim : nullptr,
+                                 q_row_stride, q_head_stride, rope_dim};
+  const Heads hk{k_nope, k_row_stride, k_head_stride, nope_dim};
+  const Heads hv{v, v_row_stride, v_head_stride, v_dim};
+  const Heads hkp{k_pe, k_pe_row_stride, 0, rope_dim};
+  const Heads ho{o, o_row_stride, o_head_stride, v_dim};
+  if (!heads_ok(hq, num_tokens, num_heads) || !heads_ok(hqp, num_tokens, num_heads) ||
+      !heads_ok(ho, num_tokens, num_heads) || !heads_disjoint(ho, num_tokens, num_heads))
+    return MLA_ERR_INVALID_ARG;
+  if (num_kv_tokens > 0 &&
+      (!heads_ok(hk, num_kv_tokens, num_heads) || !heads_ok(hv, num_kv_tokens, num_heads) ||
+       !heads_ok(hkp, num_kv_tokens, 1)))
+    return MLA_ERR_INVALID_ARG;
+  if (!cu_seqlens_q || !cu_seqlens_k || !lse || !aligned4(cu_seqlens_q) ||
+      !aligned4(cu_seqlens_k) || !aligned4(lse) || !aligned4(err_count) ||
+      (groups.num > 0 && (!groups.seqs || !groups.cu_prefix || !aligned4(groups.seqs) ||
+                          !aligned4(groups.cu_prefix))))
+    return MLA_ERR_INVALID_ARG;
+  const size_t need = mla_prefill_workspace_bytes(num_tokens, num_heads, parts, v_dim);
+  if (need > 0) {
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 31u) != 0)
+      return MLA_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  }
+  // one CTA per 256-row block slot, head and split
+  if ((num_tokens / 256 + static_cast<int64_t>(num_seqs)) * 2 * num_heads * num_kv_splits +
+          (num_tokens / 256 + static_cast<int64_t>(groups.num)) * 2 * num_heads * groups.splits >
+      INT32_MAX)
+    return MLA_ERR_UNSUPPORTED;
+  const int64_t n_cu = (static_cast<int64_t>(num_seqs) + 1) * 4;
+  const int64_t n_groups = groups.num > 0 ? (static_cast<int64_t>(groups.num) + 1) * 4 : 0;
+  Runs in[9] = {runs(hq, num_tokens, num_heads),  runs(hqp, num_tokens, num_heads),
+                runs(cu_seqlens_q, n_cu),         runs(cu_seqlens_k, n_cu),
+                runs(groups.seqs, n_groups),      runs(groups.cu_prefix, n_groups)};
+  int n_in = 6;
+  if (num_kv_tokens > 0) {
+    in[n_in++] = runs(hk, num_kv_tokens, num_heads);
+    in[n_in++] = runs(hv, num_kv_tokens, num_heads);
+    in[n_in++] = runs(hkp, num_kv_tokens, 1);
+  }
+  // what is not written (a workspace that is not needed) overlaps nothing
+  const Runs out[3] = {runs(ho, num_tokens, num_heads),
+                       runs(lse, static_cast<int64_t>(num_tokens) * num_heads * 4),
+                       runs(workspace, need > INT64_MAX ? INT64_MAX : static_cast<int64_t>(need))};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (intersect(out[i], in[j])) return MLA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (intersect(out[i], out[j])) return MLA_ERR_INVALID_ARG;
+  }
+  mla::PrefillParams p = {};
+  p.num_tokens = num_tokens;
+  p.num_kv = num_kv_tokens;
+  p.heads = num_heads;
+  p.num_seqs = num_seqs;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.pe_col = q_pe ? 0 : nope_dim;
+  p.causal = causal != 0;
+  p.sm_scale = sm_scale;
+  p.num_splits = parts;
+  p.num_groups = groups.num;
+  p.prefix_splits = groups.splits;
+  p.group_seqs = groups.seqs;
+  p.cu_prefix = groups.cu_prefix;
+  p.v = static_cast<const uint16_t*>(v);
+  p.v_row_stride = v_row_stride;
+  p.v_head_stride = num_heads > 1 ? v_head_stride : 0;
+  p.o = static_cast<uint16_t*>(o);
+  p.o_row_stride = o_row_stride;
+  p.o_head_stride = num_heads > 1 ? o_head_stride : 0;
+  p.o_aligned32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0 && o_row_stride % 16 == 0 &&
+                  p.o_head_stride % 16 == 0;
+  p.lse = lse;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_lse = need ? p.ws_o + static_cast<size_t>(num_tokens) * num_heads * parts * v_dim
+                  : nullptr;
+  p.err_count = err_count;
+  mla::PrefillMaps m;
+  memset(&m, 0, sizeof m);
+  mla_status st = heads_map(&m.q, hq, num_tokens, num_heads, 128);
+  if (st == MLA_OK && q_pe) st = heads_map(&m.q_pe, hqp, num_tokens, num_heads, 128);
+  if (num_kv_tokens > 0) {
+    if (st == MLA_OK) st = heads_map(&m.k, hk, num_kv_tokens, num_heads, 128);
+    if (st == MLA_OK) st = heads_map(&m.k_pe, hkp, num_kv_tokens, 1, 128);
+    if (st == MLA_OK) st = heads_map(&m.v, hv, num_kv_tokens, num_heads, 64);
+  }
+  if (st != MLA_OK) return st;
+  cudaError_t e = mla::launch_prefill(p, m, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -325,7 +446,7 @@ mla_status mla_project_v(const void* o, int64_t o_row_stride, int64_t o_head_str
 
 mla_status mla_linear(const void* x, int64_t x_row_stride, int num_tokens, int in_features,
                       const void* w, int64_t w_row_stride, int out_features, const void* bias,
-                      mla_activation activation, const void* residual,
+                      int activation, const void* residual,
                       int64_t residual_row_stride, void* y, int64_t y_row_stride,
                       int* err_count, void* stream) {
   if (num_tokens < 0 || in_features < 1 || out_features < 1 || activation < MLA_ACT_NONE ||
@@ -433,97 +554,50 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
                        int causal, float sm_scale, int num_kv_splits, void* workspace,
                        size_t workspace_bytes, void* o, int64_t o_row_stride,
                        int64_t o_head_stride, float* lse, int* err_count, void* stream) {
-  if (num_tokens < 0 || num_kv_tokens < 0 || num_seqs < 0 || num_heads < 1 || num_heads > 1024 ||
-      num_kv_splits < 1 || num_kv_splits > 64 || nope_dim < 1 || rope_dim < 1 || v_dim < 1 ||
-      !(sm_scale >= 1e-30f && sm_scale <= 1e30f))
-    return MLA_ERR_INVALID_ARG;
-  if (nope_dim != kNopeDim || v_dim != kVDim || rope_dim != 64 || num_seqs > 65535 ||
-      num_tokens > (1 << 30) || num_kv_tokens > (1 << 30))
-    return MLA_ERR_UNSUPPORTED;
-  if (num_tokens == 0 || num_seqs == 0) return MLA_OK;
-  const Heads hq{q, q_row_stride, q_head_stride, q_pe ? nope_dim : nope_dim + rope_dim};
-  const Heads hqp = q_pe ? Heads{q_pe, q_pe_row_stride, q_pe_head_stride, rope_dim}
-                         : Heads{q ? static_cast<const uint16_t*>(q) + nope_dim : nullptr,
-                                 q_row_stride, q_head_stride, rope_dim};
-  const Heads hk{k_nope, k_row_stride, k_head_stride, nope_dim};
-  const Heads hv{v, v_row_stride, v_head_stride, v_dim};
-  const Heads hkp{k_pe, k_pe_row_stride, 0, rope_dim};
-  const Heads ho{o, o_row_stride, o_head_stride, v_dim};
-  if (!heads_ok(hq, num_tokens, num_heads) || !heads_ok(hqp, num_tokens, num_heads) ||
-      !heads_ok(ho, num_tokens, num_heads) || !heads_disjoint(ho, num_tokens, num_heads))
-    return MLA_ERR_INVALID_ARG;
-  if (num_kv_tokens > 0 &&
-      (!heads_ok(hk, num_kv_tokens, num_heads) || !heads_ok(hv, num_kv_tokens, num_heads) ||
-       !heads_ok(hkp, num_kv_tokens, 1)))
-    return MLA_ERR_INVALID_ARG;
-  if (!cu_seqlens_q || !cu_seqlens_k || !lse || !aligned4(cu_seqlens_q) ||
-      !aligned4(cu_seqlens_k) || !aligned4(lse) || !aligned4(err_count))
-    return MLA_ERR_INVALID_ARG;
-  const size_t need = mla_prefill_workspace_bytes(num_tokens, num_heads, num_kv_splits, v_dim);
-  if (need > 0) {
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 31u) != 0)
-      return MLA_ERR_INVALID_ARG;
-    if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  }
-  // one CTA per 256-row block slot, head and split
-  if ((num_tokens / 256 + static_cast<int64_t>(num_seqs)) * 2 * num_heads * num_kv_splits >
-      INT32_MAX)
-    return MLA_ERR_UNSUPPORTED;
-  const int64_t n_cu = (static_cast<int64_t>(num_seqs) + 1) * 4;
-  Runs in[7] = {runs(hq, num_tokens, num_heads), runs(hqp, num_tokens, num_heads),
-                runs(cu_seqlens_q, n_cu), runs(cu_seqlens_k, n_cu)};
-  int n_in = 4;
-  if (num_kv_tokens > 0) {
-    in[n_in++] = runs(hk, num_kv_tokens, num_heads);
-    in[n_in++] = runs(hv, num_kv_tokens, num_heads);
-    in[n_in++] = runs(hkp, num_kv_tokens, 1);
-  }
-  // what is not written (a workspace that is not needed) overlaps nothing
-  const Runs out[3] = {runs(ho, num_tokens, num_heads),
-                       runs(lse, static_cast<int64_t>(num_tokens) * num_heads * 4),
-                       runs(workspace, need > INT64_MAX ? INT64_MAX : static_cast<int64_t>(need))};
-  for (int i = 0; i < 3; ++i) {
-    for (int j = 0; j < n_in; ++j)
-      if (intersect(out[i], in[j])) return MLA_ERR_INVALID_ARG;
-    for (int j = 0; j < i; ++j)
-      if (intersect(out[i], out[j])) return MLA_ERR_INVALID_ARG;
-  }
-  mla::PrefillParams p = {};
-  p.num_tokens = num_tokens;
-  p.num_kv = num_kv_tokens;
-  p.heads = num_heads;
-  p.num_seqs = num_seqs;
-  p.cu_q = cu_seqlens_q;
-  p.cu_k = cu_seqlens_k;
-  p.pe_col = q_pe ? 0 : nope_dim;
-  p.causal = causal != 0;
-  p.sm_scale = sm_scale;
-  p.num_splits = num_kv_splits;
-  p.v = static_cast<const uint16_t*>(v);
-  p.v_row_stride = v_row_stride;
-  p.v_head_stride = num_heads > 1 ? v_head_stride : 0;
-  p.o = static_cast<uint16_t*>(o);
-  p.o_row_stride = o_row_stride;
-  p.o_head_stride = num_heads > 1 ? o_head_stride : 0;
-  p.o_aligned32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0 && o_row_stride % 16 == 0 &&
-                  p.o_head_stride % 16 == 0;
-  p.lse = lse;
-  p.ws_o = static_cast<float*>(workspace);
-  p.ws_lse = need ? p.ws_o + static_cast<size_t>(num_tokens) * num_heads * num_kv_splits * v_dim
-                  : nullptr;
-  p.err_count = err_count;
-  mla::PrefillMaps m;
-  memset(&m, 0, sizeof m);
-  mla_status st = heads_map(&m.q, hq, num_tokens, num_heads, 128);
-  if (st == MLA_OK && q_pe) st = heads_map(&m.q_pe, hqp, num_tokens, num_heads, 128);
-  if (num_kv_tokens > 0) {
-    if (st == MLA_OK) st = heads_map(&m.k, hk, num_kv_tokens, num_heads, 128);
-    if (st == MLA_OK) st = heads_map(&m.k_pe, hkp, num_kv_tokens, 1, 128);
-    if (st == MLA_OK) st = heads_map(&m.v, hv, num_kv_tokens, num_heads, 64);
-  }
-  if (st != MLA_OK) return st;
-  cudaError_t e = mla::launch_prefill(p, m, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+  return prefill(q, q_row_stride, q_head_stride, q_pe, q_pe_row_stride, q_pe_head_stride, num_tokens,
+                 num_heads, k_nope, k_row_stride, k_head_stride, v, v_row_stride, v_head_stride,
+                 k_pe, k_pe_row_stride, num_kv_tokens, nope_dim, rope_dim, v_dim, cu_seqlens_q,
+                 cu_seqlens_k, num_seqs, Groups{}, causal, sm_scale, num_kv_splits, workspace,
+                 workspace_bytes, o, o_row_stride, o_head_stride, lse, err_count, stream);
+}
+
+// Parts of the prefix: as many as give every SM one where its 256-row blocks leave
+// SMs idle, no part shorter than 1024 keys; of the sequences' own keys as
+// mla_prefill_num_kv_splits cuts them, where those are long.
+int mla_prefill_shared_num_kv_splits(int num_tokens, int num_seqs, int num_groups, int num_heads,
+                                     int64_t max_prefix_len, int64_t max_kv_len, int sm_count,
+                                     int* num_kv_splits) {
+  if (num_kv_splits)
+    *num_kv_splits =
+        mla_prefill_num_kv_splits(num_tokens, num_seqs, num_heads, max_kv_len, sm_count);
+  if (num_tokens < 1 || num_groups < 1 || num_heads < 1 || max_prefix_len < 1 || sm_count < 1)
+    return 1;
+  const int64_t by_rows = (static_cast<int64_t>(num_tokens) + 255) / 256;
+  const int64_t blocks = num_groups > by_rows ? num_groups : by_rows;
+  int64_t s = sm_count / (blocks * num_heads);
+  const int64_t most = max_prefix_len / 1024;
+  if (s > most) s = most;
+  if (s > 64) s = 64;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+mla_status mla_prefill_shared(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* q_pe,
+    int64_t q_pe_row_stride, int64_t q_pe_head_stride, int num_tokens, int num_heads,
+    const void* k_nope, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+    int64_t v_row_stride, int64_t v_head_stride, const void* k_pe, int64_t k_pe_row_stride,
+    int num_kv_tokens, int nope_dim, int rope_dim, int v_dim, const int32_t* cu_seqlens_q,
+    const int32_t* cu_seqlens_k, int num_seqs, const int32_t* group_seqs,
+    const int32_t* cu_prefix, int num_groups, int causal, float sm_scale, int num_prefix_splits,
+    int num_kv_splits, void* workspace, size_t workspace_bytes, void* o, int64_t o_row_stride,
+    int64_t o_head_stride, float* lse, int* err_count, void* stream) {
+  if (num_groups < 1) return MLA_ERR_INVALID_ARG;
+  const Groups groups{group_seqs, cu_prefix, num_groups, num_prefix_splits};
+  return prefill(q, q_row_stride, q_head_stride, q_pe, q_pe_row_stride, q_pe_head_stride, num_tokens,
+                 num_heads, k_nope, k_row_stride, k_head_stride, v, v_row_stride, v_head_stride,
+                 k_pe, k_pe_row_stride, num_kv_tokens, nope_dim, rope_dim, v_dim, cu_seqlens_q,
+                 cu_seqlens_k, num_seqs, groups, causal, sm_scale, num_kv_splits, workspace,
+                 workspace_bytes, o, o_row_stride, o_head_stride, lse, err_count, stream);
 }
 
 }  // extern "C"

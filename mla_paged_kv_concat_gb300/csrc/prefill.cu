@@ -71,7 +71,7 @@ constexpr int OFF_UNIT = OFF_RING + kRing * kBox;
 constexpr int OFF_FLAG = OFF_UNIT + kUnits * 64;
 constexpr int kCuCached = 64;          // cumulative lengths kept in shared memory
 constexpr int OFF_CU = OFF_FLAG + kUnits * 64;
-constexpr int OFF_BAR = OFF_CU + 2 * kCuCached * 4;
+constexpr int OFF_BAR = OFF_CU + 4 * kCuCached * 4;
 constexpr int kBars = 2 * kRing + 2 * kUnits + 15;
 constexpr int OFF_NEXT = (OFF_BAR + kBars * 8 + 15) & ~15;
 constexpr int OFF_TMEM = OFF_NEXT + 16;
@@ -123,32 +123,56 @@ __device__ __forceinline__ int first_masked(const Unit& u, int row0, bool causal
   return bound <= u.ks ? 0 : (bound - u.ks) / kTile;
 }
 
+// First rows and keys of the sequences, and of the groups that share a prefix:
+// the caller's arrays, or copies of them in shared memory.
+struct Starts {
+  const int32_t *q, *k;    // [num_seqs + 1]
+  const int32_t *gs, *gk;  // [num_groups + 1] first sequence (copies: first row), prefix keys
+  bool gs_rows;            // gs holds rows
+};
+
 // Unit `x` of the launch; false when it is empty.  Sequence b owns the block
 // slots from cu_q[b] / 256 + b on, at least as many as it has blocks, so
 // that a slot is found by one binary search with no sums.  Blocks run from
 // the last to the first (with a causal mask the longest come first); the
 // heads of a group share a block's turn, so that the CTAs at work together
 // read few heads' keys, from L2.
-// `cu_q`, `cu_k`: p's, or their copies in shared memory.
-__device__ bool unit_at(const PrefillParams& p, const int32_t* cu_q, const int32_t* cu_k,
-                        uint32_t x, Unit& u) {
-  const uint32_t x1 = x / p.num_splits, x2 = x1 / p.head_group, x3 = x2 / p.slots;
-  u.split = static_cast<int>(x - x1 * p.num_splits);
+// SHARED: the units of the prefixes come first.  There the rows of all sequences
+// of a group are one sequence's, in blocks that pass over the sequences' ends, and
+// attend to all of the group's prefix keys.
+template <bool SHARED>
+__device__ bool unit_at(const PrefillParams& p, const Starts& at, uint32_t x, Unit& u) {
+  const bool pre = SHARED && x < p.prefix_units;
+  if (SHARED && !pre) x -= p.prefix_units;
+  const int splits = !SHARED ? p.num_splits
+                     : pre   ? p.prefix_splits
+                             : p.num_splits - p.prefix_splits;
+  const int slots = pre ? p.prefix_slots : p.slots;
+  const int seqs = pre ? p.num_groups : p.num_seqs;
+  auto first_row = [&](int m) -> int {
+    if (!pre) return at.q[m];
+    const int g = at.gs[m];
+    return at.gs_rows ? g : at.q[clampi(g, 0, p.num_seqs)];
+  };
+  const int32_t* cu_k = pre ? at.gk : at.k;
+  const uint32_t x1 = x / splits, x2 = x1 / p.head_group, x3 = x2 / slots;
+  const int part = static_cast<int>(x - x1 * splits);
+  u.split = SHARED && !pre ? p.prefix_splits + part : part;
   u.h = static_cast<int>(x3 * p.head_group + (x1 - x2 * p.head_group));
-  const int slot = p.slots - 1 - static_cast<int>(x2 - x3 * p.slots);
+  const int slot = slots - 1 - static_cast<int>(x2 - x3 * slots);
   if (u.h >= p.heads) return false;
-  int a = 0, z = p.num_seqs - 1;
+  int a = 0, z = seqs - 1;
   while (a < z) {
     const int m = (a + z + 1) >> 1;
-    const int c = clampi(cu_q[m], 0, p.num_tokens);
+    const int c = clampi(first_row(m), 0, p.num_tokens);
     if (c / kUnitRows + m <= slot) a = m; else z = m - 1;
   }
-  const int q0 = cu_q[a], q1 = cu_q[a + 1];
+  const int q0 = first_row(a), q1 = first_row(a + 1);
   const int k0 = cu_k[a], k1 = cu_k[a + 1];
   const int qa = clampi(q0, 0, p.num_tokens), qz = clampi(q1, qa, p.num_tokens);
   const int ka = clampi(k0, 0, p.num_kv), kz = clampi(k1, ka, p.num_kv);
   const int blk = slot - (qa / kUnitRows + a);
-  if (blk == 0 && u.h == 0 && u.split == 0 && p.err_count &&
+  if (blk == 0 && u.h == 0 && part == 0 && p.err_count &&
       (qa != q0 || qz != q1 || ka != k0 || kz != k1))
     atomicAdd(p.err_count, 1);
   const int lq = qz - qa;
@@ -158,9 +182,9 @@ __device__ bool unit_at(const PrefillParams& p, const int32_t* cu_q, const int32
   u.q_row = qa + r0;
   u.k_row = ka;
   u.rows = min(kUnitRows, lq - r0);
-  u.lim0 = p.causal ? r0 + (u.lk - lq) + 1 : u.lk;
-  const int per = ((u.lk + p.num_splits - 1) / p.num_splits + kTile - 1) / kTile * kTile;
-  const int64_t ks = static_cast<int64_t>(u.split) * per;
+  u.lim0 = p.causal && !pre ? r0 + (u.lk - lq) + 1 : u.lk;
+  const int per = ((u.lk + splits - 1) / splits + kTile - 1) / kTile * kTile;
+  const int64_t ks = static_cast<int64_t>(part) * per;
   u.ks = ks < u.lk ? static_cast<int>(ks) : u.lk;
   u.ke = ks + per < u.lk ? static_cast<int>(ks + per) : u.lk;
   auto tiles = [&](int t) {
@@ -237,6 +261,7 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+template <bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const PrefillParams p, const __grid_constant__ PrefillMaps maps) {
   extern __shared__ uint8_t smem_raw[];
@@ -322,17 +347,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- producer
       // a few sequences' lengths come in at once, not one search step after
       // the other
-      const int32_t *cu_q = p.cu_q, *cu_k = p.cu_k;
+      Starts at{p.cu_q, p.cu_k, p.group_seqs, p.cu_prefix, false};
+      int32_t* cu = reinterpret_cast<int32_t*>(smem + OFF_CU);
       if (p.num_seqs < kCuCached) {
-        int32_t* cu = reinterpret_cast<int32_t*>(smem + OFF_CU);
         for (int b = lane; b <= p.num_seqs; b += 32) {
           cu[b] = __ldg(p.cu_q + b);
           cu[kCuCached + b] = __ldg(p.cu_k + b);
         }
-        __syncwarp();
-        cu_q = cu;
-        cu_k = cu + kCuCached;
+        at.q = cu;
+        at.k = cu + kCuCached;
       }
+      if (SHARED && p.num_groups < kCuCached) {
+        for (int b = lane; b <= p.num_groups; b += 32) {
+          cu[2 * kCuCached + b] = __ldg(p.cu_q + clampi(__ldg(p.group_seqs + b), 0, p.num_seqs));
+          cu[3 * kCuCached + b] = __ldg(p.cu_prefix + b);
+        }
+        at.gs = cu + 2 * kCuCached;
+        at.gk = cu + 3 * kCuCached;
+        at.gs_rows = true;
+      }
+      __syncwarp();
       if (lane == 0) {
         int i = 0, cut = 0, pos = 0, qn[2] = {0, 0};
         // The next box of the ring, once it is free.
@@ -397,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Unit u;
           if (x < 0) u.q_row = -1;
           // after a wait that gave up, the CTAs left are taken over and dropped
-          if (ok && (x < 0 || unit_at(p, cu_q, cu_k, static_cast<uint32_t>(x), u))) {
+          if (ok && (x < 0 || unit_at<SHARED>(p, at, static_cast<uint32_t>(x), u))) {
             ok = mbar_wait(&unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
             if (ok) {
               *unit_slot(i) = u;
@@ -783,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The splits of a row and head joined: M = max lse_s, o = sum e^{lse_s - M}
 // o_s / sum e^{lse_s - M}, in split order.  One warp each, four dims a lane.
 constexpr int kMergeWarps = 8;
+template <bool SHARED>
 __global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const PrefillParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -795,13 +830,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const P
   // rows of no sequence are left as they were
   if (row < __ldg(p.cu_q) || row >= __ldg(p.cu_q + p.num_seqs)) return;
   const int S = p.num_splits;
+  int first = 0;
+  if (SHARED) {
+    // rows of no group have no parts of a prefix
+    const int r0 = __ldg(p.cu_q + clampi(__ldg(p.group_seqs), 0, p.num_seqs));
+    const int r1 = __ldg(p.cu_q + clampi(__ldg(p.group_seqs + p.num_groups), 0, p.num_seqs));
+    if (row < r0 || row >= r1) first = p.prefix_splits;
+  }
   float M = -INFINITY;
-  for (int s = lane; s < S; s += 32) M = fmaxf(M, p.ws_lse[s * records + rec]);
+  for (int s = first + lane; s < S; s += 32) M = fmaxf(M, p.ws_lse[s * records + rec]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f;
-  for (int s0 = 0; s0 < S; s0 += 32) {
+  for (int s0 = first; s0 < S; s0 += 32) {
     const float ls = s0 + lane < S ? p.ws_lse[(s0 + lane) * records + rec] : -INFINITY;
     const float w = ls == -INFINITY ? 0.f : ex2((ls - M) * kLog2e);
     uint32_t mask = __ballot_sync(0xffffffffu, ls != -INFINITY);
@@ -828,11 +870,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const P
 
 }  // namespace
 
-cudaError_t launch_prefill(const PrefillParams& p_in, const PrefillMaps& maps,
-                           cudaStream_t stream) {
+template <bool SHARED>
+static cudaError_t launch(const PrefillParams& p_in, const PrefillMaps& maps, cudaStream_t stream) {
   PrefillParams p = p_in;
   static std::atomic<uint64_t> attr_done{0};
-  cudaError_t e = set_smem_attr_once(prefill_kernel, kSmem, attr_done);
+  cudaError_t e = set_smem_attr_once(prefill_kernel<SHARED>, kSmem, attr_done);
   if (e != cudaSuccess) return e;
   p.slots = p.num_tokens / kUnitRows + p.num_seqs;
   // heads side by side in the order of units: as many as keep their keys and
@@ -840,16 +882,27 @@ cudaError_t launch_prefill(const PrefillParams& p_in, const PrefillMaps& maps,
   const int64_t fit = (int64_t{64} << 20) / (512 * static_cast<int64_t>(p.num_kv > 0 ? p.num_kv : 1));
   p.head_group = static_cast<int>(fit < 8 ? 8 : fit > p.heads ? p.heads : fit);
   if (p.head_group > p.heads) p.head_group = p.heads;
-  const int groups = (p.heads + p.head_group - 1) / p.head_group;
-  const int64_t units = static_cast<int64_t>(groups) * p.slots * p.head_group * p.num_splits;
+  const int64_t heads = (p.heads + p.head_group - 1) / p.head_group * static_cast<int64_t>(p.head_group);
+  int64_t units = heads * p.slots * (p.num_splits - (SHARED ? p.prefix_splits : 0));
+  if (SHARED) {
+    p.prefix_slots = p.num_tokens / kUnitRows + p.num_groups;
+    const int64_t pre = heads * p.prefix_slots * p.prefix_splits;
+    units += pre;
+    if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
+    p.prefix_units = static_cast<uint32_t>(pre);
+  }
   if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
   const int grid = static_cast<int>(units);
-  e = launch_overlapped(prefill_kernel, dim3(grid), dim3(kThreads), kSmem, stream, p, maps);
+  e = launch_overlapped(prefill_kernel<SHARED>, dim3(grid), dim3(kThreads), kSmem, stream, p, maps);
   if (e != cudaSuccess || p.num_splits == 1) return e;
   const int64_t records = static_cast<int64_t>(p.num_tokens) * p.heads;
-  return launch_overlapped(prefill_merge_kernel,
+  return launch_overlapped(prefill_merge_kernel<SHARED>,
                            dim3(static_cast<unsigned>((records + kMergeWarps - 1) / kMergeWarps)),
                            dim3(kMergeWarps * 32), 0, stream, p);
+}
+
+cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream) {
+  return p.num_groups ? launch<true>(p, maps, stream) : launch<false>(p, maps, stream);
 }
 
 }  // namespace mla
