@@ -273,6 +273,50 @@ mla_status mla_decode_ex(const void* q, int64_t q_row_stride,
                          mla_decode_path path);
 
 /*
+ * mla_decode_shared - mla_decode for a batch whose sequences share prefixes (a
+ * system prompt, a document): the same result, with a prefix's cached rows read
+ * once for all query vectors of its group instead of once for each sequence.
+ *
+ * Group g is the sequences [group_seqs[g], group_seqs[g + 1]); the first
+ * prefix_lens[g] tokens of each of them are the same (their block tables name
+ * the same pages, or pages of the same contents), and which of the tables they
+ * are read through is not specified.  Sequences shorter than the prefix, padded
+ * ones of length 0 among them, and those of no group are decoded by themselves.
+ * A prefix is shared in whole tiles of 128 tokens.
+ *
+ *   q, q_pe         as in the plans below: q holds all R+P dims (q_pe NULL), or
+ *                   dims [0, R) and q_pe the others.
+ *   group_seqs      device int32 [num_groups + 1], non-decreasing (clamped to
+ *                   [0, num_seqs]); prefix_lens  device int32 [num_groups]
+ *                   (clamped to the block table, counted).
+ *   num_groups      1 .. 4096; num_seqs at most 16384 (else
+ *                   MLA_ERR_UNSUPPORTED, as are block tables of more than 2^30
+ *                   tokens, or more than 2^31 tiles of 128 tokens x 128 vectors).
+ *   workspace       >= mla_decode_shared_workspace_bytes(...) with the device's
+ *                   SM count, 256-byte aligned.  Calls that may overlap on the
+ *                   GPU need one each.
+ * Other arguments as mla_decode.  The work is shared out on the device from the
+ * lengths, so the call can be captured into a graph and replayed with others.
+ * Run-to-run deterministic; a row's result depends on the batch through the
+ * places where its tokens are cut.
+ */
+mla_status mla_decode_shared(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                             const void* q_pe, int64_t q_pe_row_stride, int64_t q_pe_head_stride,
+                             int num_rows, int num_heads, const void* kv_cache,
+                             mla_kv_dtype kv_dtype, int num_blocks, int block_size,
+                             int64_t block_stride, int kv_lora_rank, int rope_dim,
+                             const int32_t* block_table, int64_t block_table_stride,
+                             int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+                             const int32_t* group_seqs, const int32_t* prefix_lens, int num_groups,
+                             float sm_scale, const float* kv_scale, void* workspace,
+                             size_t workspace_bytes, void* o, float* lse, int* err_count,
+                             void* stream);
+
+/* Bytes of the workspace of mla_decode_shared; 0 for arguments that it refuses. */
+size_t mla_decode_shared_workspace_bytes(int num_rows, int num_heads, int num_seqs, int num_groups,
+                                         int kv_lora_rank, int sm_count);
+
+/*
  * mla_decode_splitkv - stage 1 alone: the split-KV pass of mla_decode
  * ([diff] triton_decode_attention.py, _decode_grouped_att_m_fwd launching
  * _fwd_grouped_kernel_stage1).  With num_kv_splits == 1 it writes o and lse

@@ -7,6 +7,8 @@ Thin Python binding over the C ABI of ``libmla.so`` (``include/mla.h``):
   under the same names, taking raw device pointers (ints) and a stream handle.
 * ``mla_norm_rope_cache_write`` and ``norm_rope_cache_write(...)`` — the cache
   write fused with the RMSNorm of kv_c and the rotary embedding of k_pe / q_pe.
+* ``decode_shared(...)`` — the decode of a batch whose sequences share prefixes,
+  a prefix read once for all of them.
 * ``DecodePlan`` — ``mla_plan_create`` / ``mla_plan_run``: a validated step
   over fixed tensors whose ``run()`` only launches kernels (CUDA-graph safe).
 * ``mla_lse_merge`` and ``lse_merge(...)`` — the cross-shard LSE merge of
@@ -44,6 +46,7 @@ __all__ = [
     "mla_prefill", "mla_prefill_num_kv_splits", "mla_prefill_workspace_bytes", "prefill",
     "batch_build", "blocks_release", "gather_cache", "BatchTables", "mla_linear", "linear",
     "mla_prefill_shared", "mla_prefill_shared_num_kv_splits", "prefill_shared",
+    "mla_decode_shared", "mla_decode_shared_workspace_bytes", "decode_shared",
     "MlaError", "load",
     "MLA_KV_BF16", "MLA_KV_FP8_E4M3", "MLA_KV_FP8_E5M2", "MLA_PATH_AUTO", "MLA_PATH_MMA_SYNC",
     "MLA_PATH_TCGEN05", "MLA_ACT_NONE", "MLA_ACT_RELU", "MLA_ACT_SILU", "MLA_ACT_GELU",
@@ -62,6 +65,16 @@ def mla_decode(*args) -> int:
 
 def mla_decode_ex(*args) -> int:
     return load().mla_decode_ex(*args)
+
+
+def mla_decode_shared(*args) -> int:
+    return load().mla_decode_shared(*args)
+
+
+def mla_decode_shared_workspace_bytes(num_rows: int, num_heads: int, num_seqs: int,
+                                      num_groups: int, kv_lora_rank: int, sm_count: int) -> int:
+    return int(load().mla_decode_shared_workspace_bytes(num_rows, num_heads, num_seqs, num_groups,
+                                                        kv_lora_rank, sm_count))
 
 
 def mla_norm_rope_cache_write(*args) -> int:
@@ -301,6 +314,29 @@ def decode(q, kv_cache, block_table, seq_lens, sm_scale: float, num_kv_splits: i
         int(path))
     _lib.check(st, "mla_decode")
     return out, lse
+
+
+def decode_shared(q, kv_cache, block_table, seq_lens, group_seqs, prefix_lens, sm_scale: float, *,
+                  kv_lora_rank: int | None = None, kv_cache_dtype: str | None = None,
+                  kv_scale=None, workspace=None, out=None, lse=None, err_count=None, stream=None):
+    """:func:`decode` for sequences that share prefixes; returns (o [rows, H, R]
+    bf16, lse [rows, H] fp32).
+
+    Group g is the sequences ``group_seqs[g]`` to ``group_seqs[g + 1]`` (int32
+    [groups + 1]); the first ``prefix_lens[g]`` (int32 [groups]) tokens of each are
+    the same, through whichever of their block tables they are read.  Sequences
+    shorter than that (padded rows of length 0) or of no group are decoded by
+    themselves.  Other arguments as :func:`decode`; ``workspace`` a device buffer of
+    ``mla_decode_shared_workspace_bytes`` bytes, 256-byte aligned (allocated here
+    when omitted).  The work is shared out on the device: the call can be captured
+    and replayed with other lengths.
+    """
+    q, q_pe = q if isinstance(q, (tuple, list)) else (q, None)
+    return _bind().decode_shared(
+        q, q_pe, kv_cache, -1 if kv_cache_dtype is None else _kv_dtype(kv_cache, kv_cache_dtype),
+        block_table, seq_lens, group_seqs, prefix_lens, sm_scale,
+        -1 if kv_lora_rank is None else kv_lora_rank, kv_scale, workspace, out, lse, err_count,
+        stream)
 
 
 class DecodePlan:

@@ -80,6 +80,10 @@ SIGNATURES = {
     "mla_decode_ex": (_I32, [_P, _I64, _I64, _I32, _I32, _P, _I32, _I32, _I32, _I64, _I32,
                              _I32, _P, _I64, _I32, _P, _I32, _F32, _P, _I32, _P, _SZ, _P, _P,
                              _P, _P, _I32]),
+    "mla_decode_shared": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _I32, _I32, _I32,
+                                 _I64, _I32, _I32, _P, _I64, _I32, _P, _I32, _P, _P, _I32, _F32, _P,
+                                 _P, _SZ, _P, _P, _P, _P]),
+    "mla_decode_shared_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "mla_decode_splitkv": (_I32, [_P, _I64, _I64, _I32, _I32, _P, _I32, _I32, _I32, _I64,
                                   _I32, _I32, _P, _I64, _I32, _P, _I32, _F32, _P, _I32, _P,
                                   _SZ, _P, _P, _P, _P, _I32]),

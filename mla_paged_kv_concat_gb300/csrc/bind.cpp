@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/cuda/CUDAContextLight.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -218,6 +219,10 @@ PyObject* tuple(std::initializer_list<Tensor> ts) {
   return r;
 }
 
+int sm_count(int device) {
+  return at::cuda::getDeviceProperties(static_cast<c10::DeviceIndex>(device))->multiProcessorCount;
+}
+
 // Raises MlaError for a status other than MLA_OK.
 void done(mla_status st, const char* where) {
   if (st == MLA_OK) return;
@@ -336,6 +341,22 @@ PyObject* blocks_release(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The format of a cache whose mla_kv_dtype is `fmt` or, below 0, told by its type.
+int cache_format(const Tensor& cache, int fmt) {
+  if (fmt < 0) {
+    switch (cache.scalar_type()) {
+      case at::kBFloat16: fmt = MLA_KV_BF16; break;
+      case at::kByte:
+      case at::kFloat8_e4m3fn: fmt = MLA_KV_FP8_E4M3; break;
+      case at::kFloat8_e5m2: fmt = MLA_KV_FP8_E5M2; break;
+      default: throw BadValue("unsupported cache dtype");
+    }
+  }
+  CHECK(cache.element_size() == (fmt == MLA_KV_BF16 ? 2u : 1u),
+        "kv_cache_dtype does not fit the cache");
+  return fmt;
+}
+
 // (kv_cache, kv_dtype (-1: from the tensor), block_table, cu_seqlens,
 //  num_tokens (-1: from kv_c), kv_lora_rank (-1: the row less 64),
 //  seq_starts, kv_scale, kv_c, k_pe, err_count, stream)
@@ -348,17 +369,7 @@ PyObject* gather_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor starts = c.maybe("seq_starts"), scale = c.maybe("kv_scale");
     Tensor kv_c = c.maybe("kv_c"), k_pe = c.maybe("k_pe"), err = c.maybe("err_count");
     c.take_stream();
-    if (fmt < 0) {
-      switch (cache.scalar_type()) {
-        case at::kBFloat16: fmt = MLA_KV_BF16; break;
-        case at::kByte:
-        case at::kFloat8_e4m3fn: fmt = MLA_KV_FP8_E4M3; break;
-        case at::kFloat8_e5m2: fmt = MLA_KV_FP8_E5M2; break;
-        default: throw BadValue("unsupported cache dtype");
-      }
-    }
-    CHECK(cache.element_size() == (fmt == MLA_KV_BF16 ? 2u : 1u),
-          "kv_cache_dtype does not fit the cache");
+    fmt = cache_format(cache, fmt);
     CHECK(cache.dim() == 3 && cache.stride(2) == 1 && cache.stride(1) == cache.size(2),
           "cache rows must be dense");
     const int64_t nb = cache.size(0), bs = cache.size(1), d = cache.size(2);
@@ -573,6 +584,70 @@ PyObject* prefill_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return prefill_call(a, n, true);
 }
 
+// (q, q_pe, kv_cache, kv_dtype (-1: from the tensor), block_table, seq_lens,
+//  group_seqs, prefix_lens, sm_scale, kv_lora_rank (-1: the row less 64),
+//  kv_scale, workspace, out, lse, err_count, stream)
+PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, [](Call& c) {
+    Tensor q = c.tensor("q"), q_pe = c.maybe("q_pe"), cache = c.tensor("kv_cache");
+    int fmt = c.small("kv_dtype");
+    Tensor table = c.tensor("block_table"), lens = c.tensor("seq_lens");
+    Tensor gs = c.tensor("group_seqs"), pre = c.tensor("prefix_lens");
+    const float sm_scale = static_cast<float>(c.real());
+    int64_t R = c.integer();
+    Tensor scale = c.maybe("kv_scale"), ws = c.maybe("workspace"), out = c.maybe("out");
+    Tensor lse = c.maybe("lse"), err = c.maybe("err_count");
+    c.take_stream();
+    fmt = cache_format(cache, fmt);
+    CHECK(cache.dim() == 3 && cache.stride(2) == 1 && cache.stride(1) == cache.size(2),
+          "cache rows must be dense");
+    const int64_t nb = cache.size(0), bs = cache.size(1), d = cache.size(2);
+    if (R < 0) R = d - kRope;
+    const int64_t P = d - R;
+    CHECK(R > 0 && P > 0, "kv_lora_rank does not fit the cache");
+    CHECK(q.dim() == 3, "q must be [rows, heads, dims]");
+    const int64_t T = q.size(0), H = q.size(1);
+    typed(q, kBf16, {T, H, q_pe.defined() ? R : d}, "q");
+    typed(q_pe, kBf16, {T, H, P}, "q_pe");
+    typed(lens, kI32, {-1}, "seq_lens");
+    const int64_t B = lens.size(0);
+    typed(table, kI32, {B, -1}, "block_table");
+    typed(gs, kI32, {-1}, "group_seqs");
+    const int64_t G = gs.size(0) - 1;
+    CHECK(G >= 1, "group_seqs must hold a group");
+    typed(pre, kI32, {G}, "prefix_lens");
+    CHECK(!scale.defined() || (scale.scalar_type() == at::kFloat && scale.numel() == 1),
+          "kv_scale must be one float32");
+    if (!out.defined()) out = c.empty({T, H, R}, kBf16);
+    if (!lse.defined()) lse = c.empty({T, H}, at::kFloat);
+    typed(out, kBf16, {T, H, R}, "out");
+    typed(lse, at::kFloat, {T, H}, "lse");
+    typed(err, kI32, {1}, "err_count");
+    CHECK(out.is_contiguous() && lse.is_contiguous(), "out and lse must be contiguous");
+    if (T > 0 && !ws.defined()) {
+      const size_t need = mla_decode_shared_workspace_bytes(
+          as_int(T, "the number of rows"), as_int(H, "the number of heads"),
+          as_int(B, "the number of sequences"), as_int(G, "the number of groups"),
+          as_int(R, "kv_lora_rank"), sm_count(c.dev));
+      ws = c.empty({static_cast<int64_t>(need)}, at::kByte, false);
+    }
+    CHECK(!ws.defined() || ws.is_contiguous(), "workspace must be contiguous");
+    const Strides sq(q), sp = q_pe.defined() ? Strides(q_pe) : Strides();
+    done(mla_decode_shared(
+             ptr(q), sq.row, sq.head, ptr(q_pe), sp.row, sp.head, as_int(T, "the number of rows"),
+             as_int(H, "the number of heads"), ptr(cache), static_cast<mla_kv_dtype>(fmt),
+             as_int(nb, "the cache"), as_int(bs, "the block size"), nb > 1 ? cache.stride(0) : bs * d,
+             as_int(R, "kv_lora_rank"), as_int(P, "rope_dim"), ptr<int32_t>(table),
+             B > 1 ? table.stride(0) : table.size(1), as_int(table.size(1), "the block table"),
+             ptr<int32_t>(lens), as_int(B, "the number of sequences"), ptr<int32_t>(gs),
+             ptr<int32_t>(pre), as_int(G, "the number of groups"), sm_scale, ptr<float>(scale),
+             ptr(ws), ws.defined() ? ws.nbytes() : 0, ptr(out), ptr<float>(lse), ptr<int>(err),
+             c.s()),
+         "mla_decode_shared");
+    return tuple({out, lse});
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL,
@@ -584,7 +659,8 @@ PyMethodDef kMethods[] = {
     method<gather_cache>("gather_cache"), method<expand_kv>("expand_kv"),
     method<absorb_q>("absorb_q"),         method<project_v>("project_v"),
     method<linear>("linear"),             method<prefill>("prefill"),
-    method<prefill_shared>("prefill_shared"), {nullptr, nullptr, 0, nullptr}};
+    method<prefill_shared>("prefill_shared"), method<decode_shared>("decode_shared"),
+    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 

@@ -161,6 +161,59 @@ cudaError_t launch_lse_merge(const void* o_parts, int64_t o_part_stride, const f
                              int64_t lse_part_stride, int num_parts, int64_t records, int R,
                              void* o, float* lse, cudaStream_t stream);
 
+// ---------------------------------------------------------------- shared prefixes
+constexpr int kMaxSharedSeqs = 16384, kMaxSharedGroups = 4096;
+
+// A group's shared tokens or a sequence's other ones, [tok0, tok1) through row
+// `table` of the block table, for `vecs` query vectors from row0 on; its place
+// in the list of tiles and units.
+struct SharedPart {
+  int tile0, tiles, blocks, unit0, row0, vecs, tok0, tok1, table;
+  int group;  // of a sequence that takes part in its group's pass, else -1
+  int pad0, pad1;
+};
+// What one pair of CTAs does of a unit.
+struct SharedSegment {
+  int table, row0, vec0, vecs, tok0, tok1, pad0, pad1;
+};
+static_assert(sizeof(SharedSegment) == 32, "read as two int4");
+
+struct SharedParams {
+  const uint16_t* q;     // dims [0, R) of each query vector
+  int64_t q_row_stride, q_head_stride;
+  const uint16_t* q_pe;  // dims [R, R+P)
+  int64_t q_pe_row_stride, q_pe_head_stride;
+  int num_rows, num_heads, rows_per_seq, num_seqs;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int capacity;          // tokens of a block table row
+  const int32_t* seq_lens;
+  const int32_t* group_seqs;   // [num_groups + 1]
+  const int32_t* prefix_lens;  // [num_groups]
+  int num_groups;
+  int block_size, num_blocks;
+  float sm_scale;
+  const float* kv_scale;  // fp8 cache only (else nullptr)
+  bool e5m2;
+  uint16_t* o;
+  float* lse;
+  int* err_count;
+  int pairs;              // of CTAs
+  // workspace
+  int* header;            // [0]: tiles of a pair
+  int2* pair_segments;    // first segment and number of each pair
+  SharedPart* parts;      // groups, then sequences
+  SharedSegment* segments;
+  float2* ml;             // [segment][128] maximum (log2 units) and sum
+  float* partial;         // [segment][128][R]
+};
+// Bytes of the workspace; with `base` its addresses into *p.
+size_t shared_layout(int num_rows, int num_heads, int num_seqs, int num_groups, int R, int pairs,
+                     uint8_t* base, SharedParams* p);
+// `tmap` as for the warp-MMA kernel.  Three kernels, launched overlapped.
+cudaError_t launch_decode_shared(const SharedParams& p, const CUtensorMap& tmap, int R, bool fp8,
+                                 cudaStream_t stream);
+
 // ---------------------------------------------------------------- prompts
 // Largest number of requests mla_batch_build and mla_blocks_release take
 // (their prefix sums live in shared memory).

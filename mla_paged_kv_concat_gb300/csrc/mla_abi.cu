@@ -503,6 +503,96 @@ mla_status run_stage1(const mla::DecodeParams& p_in, const void* kv_cache,
 
 extern "C" {
 
+size_t mla_decode_shared_workspace_bytes(int num_rows, int num_heads, int num_seqs, int num_groups,
+                                         int kv_lora_rank, int sm_count) {
+  if (num_rows <= 0 || num_heads < 1 || num_heads > 128 || num_seqs < 1 ||
+      num_seqs > mla::kMaxSharedSeqs || num_groups < 1 || num_groups > mla::kMaxSharedGroups ||
+      (kv_lora_rank != 512 && kv_lora_rank != 256) || sm_count < 2 || sm_count > 4096)
+    return 0;
+  return mla::shared_layout(num_rows, num_heads, num_seqs, num_groups, kv_lora_rank, sm_count / 2,
+                            nullptr, nullptr);
+}
+
+mla_status mla_decode_shared(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                             const void* q_pe, int64_t q_pe_row_stride, int64_t q_pe_head_stride,
+                             int num_rows, int num_heads, const void* kv_cache,
+                             mla_kv_dtype kv_dtype, int num_blocks, int block_size,
+                             int64_t block_stride, int kv_lora_rank, int rope_dim,
+                             const int32_t* block_table, int64_t block_table_stride,
+                             int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+                             const int32_t* group_seqs, const int32_t* prefix_lens, int num_groups,
+                             float sm_scale, const float* kv_scale, void* workspace,
+                             size_t workspace_bytes, void* o, float* lse, int* err_count,
+                             void* stream) {
+  if (num_groups < 1) return MLA_ERR_INVALID_ARG;
+  mla::DecodeParams d = {};
+  mla_status st = prepare_decode(
+      q, q_row_stride, q_head_stride, q_pe, q_pe_row_stride, q_pe_head_stride, num_rows, num_heads,
+      kv_cache, kv_dtype, num_blocks, block_size, block_stride, kv_lora_rank, rope_dim, block_table,
+      block_table_stride, max_blocks_per_seq, seq_lens, num_seqs, sm_scale, kv_scale, 1, nullptr, 0,
+      o, lse, err_count, MLA_PATH_AUTO, &d);
+  if (st != MLA_OK) return st;
+  if (num_seqs > mla::kMaxSharedSeqs || num_groups > mla::kMaxSharedGroups)
+    return MLA_ERR_UNSUPPORTED;
+  if (num_rows == 0) return MLA_OK;
+  if (!group_seqs || !prefix_lens || !mla::aligned4(group_seqs) || !mla::aligned4(prefix_lens) ||
+      !mla::aligned4(block_table) || !mla::aligned4(seq_lens) || !mla::aligned4(kv_scale) ||
+      !mla::aligned4(err_count))
+    return MLA_ERR_INVALID_ARG;
+  // the tiles of all blocks of 128 vectors are counted in 32 bits
+  const int64_t capacity = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+  const int64_t blocks = static_cast<int64_t>(num_rows) * num_heads / 64 + num_seqs + num_groups;
+  if (capacity > (1 << 30) || (capacity / 128 + 1) > INT32_MAX / blocks) return MLA_ERR_UNSUPPORTED;
+  int sms = 0;
+  cudaError_t e = mla::device_sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const size_t need = mla_decode_shared_workspace_bytes(num_rows, num_heads, num_seqs, num_groups,
+                                                        kv_lora_rank, sms);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const bool fp8 = kv_dtype != MLA_KV_BF16;
+  mla::SharedParams p = {};
+  p.q = d.q;
+  p.q_row_stride = d.q_row_stride;
+  p.q_head_stride = d.q_head_stride;
+  p.q_pe = d.q_pe;
+  p.q_pe_row_stride = d.q_pe_row_stride;
+  p.q_pe_head_stride = d.q_pe_head_stride;
+  p.num_rows = num_rows;
+  p.num_heads = num_heads;
+  p.rows_per_seq = d.rows_per_seq;
+  p.num_seqs = num_seqs;
+  p.block_table = block_table;
+  p.bt_stride = block_table_stride;
+  p.capacity = static_cast<int>(capacity);
+  p.seq_lens = seq_lens;
+  p.group_seqs = group_seqs;
+  p.prefix_lens = prefix_lens;
+  p.num_groups = num_groups;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.sm_scale = sm_scale;
+  p.kv_scale = d.kv_scale;
+  p.e5m2 = kv_dtype == MLA_KV_FP8_E5M2;
+  p.o = d.o;
+  p.lse = lse;
+  p.err_count = err_count;
+  p.pairs = sms / 2;
+  mla::shared_layout(num_rows, num_heads, num_seqs, num_groups, kv_lora_rank, p.pairs,
+                     static_cast<uint8_t*>(workspace), &p);
+  CUtensorMap tmap;
+  st = make_cache_tmap(&tmap, kv_cache, fp8, kv_lora_rank + rope_dim, block_size, num_blocks,
+                       block_stride, 64);
+  if (st != MLA_OK) return st;
+  e = mla::launch_decode_shared(p, tmap, kv_lora_rank, fp8, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+}  // extern "C"
+
+extern "C" {
+
 mla_status mla_decode_splitkv(const void* q, int64_t q_row_stride,
                               int64_t q_head_stride, int num_rows,
                               int num_heads, const void* kv_cache,
