@@ -289,7 +289,7 @@ mla_status mla_decode_ex(const void* q, int64_t q_row_stride,
  *   group_seqs      device int32 [num_groups + 1], non-decreasing (clamped to
  *                   [0, num_seqs]); prefix_lens  device int32 [num_groups]
  *                   (clamped to the block table, counted).
- *   num_groups      1 .. 4096; num_seqs at most 16384 (else
+ *   num_groups      1 .. 1024; num_seqs at most 8192 (else
  *                   MLA_ERR_UNSUPPORTED, as are block tables of more than 2^30
  *                   tokens, or more than 2^31 tiles of 128 tokens x 128 vectors).
  *   workspace       >= mla_decode_shared_workspace_bytes(...) with the device's

@@ -23,8 +23,8 @@
 // Per tile the tensor cores have 36 x 74 cycles (M = 128, N = 128) on rank 0 and
 // 16 x 138 (N = 256) on rank 1.  Rank 1 reads the latent part of the rows again,
 // from L2.
-//   rank 0: Q 256 + S 2 x 128 TMEM columns; a ring of five 32 KiB boxes of K (128
-//     dims x 128 tokens) and one of two rope boxes (16 KiB)
+//   rank 0: Q R / 2 + S 2 x 128 TMEM columns; a ring of 11 boxes of 16 KiB (64 dims
+//     x 128 tokens of K or 128 vectors of Q), 32 KiB of P on its way
 //   rank 1: O R TMEM columns; P 2 x 32 KiB; a ring of five 32 KiB boxes of V (256
 //     dims x 64 tokens)
 // An fp8 cache lands in staging boxes and four more warps of each CTA turn it into
@@ -32,15 +32,17 @@
 // scores and to the joined output.
 //
 // Schedule.  A first kernel (one CTA) turns lengths into a list of all tiles: the
-// groups' prefixes, then the sequences, each cut into blocks of 128 vectors.  Pair
-// c of CTAs takes tiles [c C, (c + 1) C).  Blocks of one prefix are listed in
-// chunks of C tiles side by side, so that pairs at work together read the same
-// rows.  Unit u (chunk of a block) meets pair c in segment u + c, which is also
-// its place in the workspace: list positions only grow, so no two are alike.
+// groups' prefixes, then the sequences, each cut into blocks of 128 vectors.  Blocks
+// of one prefix are listed in chunks side by side, so that pairs at work together
+// read the same rows.  A unit (chunk of a block) has kStart places in the list
+// before its tiles, for what its start and end take, and pair c of CTAs has the
+// places [c C, (c + 1) C).  Unit u meets pair c in segment u + c, which is also its
+// place in the workspace: list positions only grow, so no two are alike.
 //
-// Roles (320 threads, 448 with an fp8 cache): warps 0-7 softmax (rank 0) or
-// rescaling and output of O (rank 1), thread = TMEM lane = vector, two warps a
-// lane quarter (token or dim halves); warp 8 TMA, warp 9 MMA, 10-13 conversion.
+// Roles (384 threads, 512 with an fp8 cache): rank 0 warps 0-3 softmax, thread =
+// TMEM lane = vector, 4-7 loading Q; rank 1 warps 0-7 rescaling and output of O, two
+// a lane quarter (dim halves); warp 9 MMA, warps 8, 10, 11 TMA (8, 14, 15 with an fp8
+// cache, whose conversion takes 10-13).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
@@ -54,13 +56,13 @@ namespace mla {
 namespace {
 
 constexpr int TT = 128;                 // tokens of a tile
-constexpr int kBig = 32768;             // ring box
-constexpr int kRope = 16384;            // rope box: 128 tokens x 64 dims
+constexpr int kKBox = 16384;            // rank 0's ring box: 64 dims x 128 tokens (or vectors)
+constexpr int kVBox = 32768;            // rank 1's: 256 dims x 64 tokens
 constexpr int kPBuf = 32768;            // P: two boxes of 128 vectors x 64 tokens
 // Shared memory of rank 0 and rank 1.
 constexpr int S_QPE = 0;
-constexpr int S_ROPE = S_QPE + 16384;   // two boxes
-constexpr int S_RING = S_ROPE + 2 * kRope;
+constexpr int S_OUT = S_QPE + kKBox;    // P on its way to rank 1, 8 KiB a warp
+constexpr int S_RING = S_OUT + kPBuf;
 constexpr int V_RING = 2 * kPBuf;
 constexpr int kData = 229376;
 constexpr int OFF_MISC = kData;         // rank 1: rescale factors, two buffers of 128
@@ -68,16 +70,17 @@ constexpr int OFF_BAR = OFF_MISC + 1024;
 constexpr int OFF_TMEM = OFF_BAR + 512;
 constexpr int kSmem = OFF_TMEM + 16 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory");
+constexpr int kMostBoxes = 11, kMostStages = 6;
 template <bool FP8>
 struct Ring {
-  static constexpr int S_BOXES = FP8 ? 4 : 5, V_BOXES = FP8 ? 3 : 5;
-  static constexpr int STAGES = FP8 ? 2 : 1, V_STAGES = FP8 ? 4 : 1;  // fp8 staging boxes
-  static constexpr int S_STAGE = S_RING + S_BOXES * kBig;             // 16 KiB each
-  static constexpr int S_RSTAGE = S_STAGE + (FP8 ? 2 * 16384 : 0);    // rope: 8 KiB
-  static constexpr int S_RED = S_RSTAGE + (FP8 ? 8192 : 0);           // [2][2][128] fp32
-  static constexpr int V_STAGE = V_RING + V_BOXES * kBig;
-  static_assert(V_STAGE + (FP8 ? 4 * 16384 : 0) <= kData, "rank 1's shared memory");
-  static_assert(S_RED + 2048 <= kData, "rank 0's shared memory");
+  static constexpr int S_BOXES = FP8 ? 8 : 11, V_BOXES = FP8 ? 3 : 5;
+  // fp8 staging boxes: 8 KiB on rank 0, 16 KiB on rank 1
+  static constexpr int S_STAGES = FP8 ? 6 : 0, V_STAGES = FP8 ? 4 : 0;
+  static constexpr int S_STAGE = S_RING + S_BOXES * kKBox;
+  static constexpr int V_STAGE = V_RING + V_BOXES * kVBox;
+  static_assert(S_STAGE + S_STAGES * 8192 <= kData, "rank 0's shared memory");
+  static_assert(V_STAGE + V_STAGES * 16384 <= kData, "rank 1's shared memory");
+  static_assert(S_BOXES <= kMostBoxes && S_STAGES <= kMostStages, "barriers");
 };
 
 constexpr uint32_t S_COL = 256;  // rank 0: Q below, S 2 x 128 columns
@@ -92,6 +95,30 @@ __device__ __forceinline__ int clampi(int x, int lo, int hi) {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   const bool ok = mbar_wait(bar, parity);
   return __all_sync(0xffffffffu, ok);
+}
+// Packed fp32 pairs.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void mul2(uint32_t& a, uint32_t& b, float c) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(pack2(__uint_as_float(a), __uint_as_float(b))), "l"(pack2(c, c)));
+  float x, y;
+  unpack2(d, x, y);
+  a = __float_as_uint(x);
+  b = __float_as_uint(y);
 }
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
   const bool ok = tc::mbar_wait_cluster(bar, parity);
@@ -115,7 +142,7 @@ __device__ void block_scan(int* a, int n, int* tot, Op op) {
     if (lane == 31) tot[warp] = v;
     __syncthreads();
     if (warp == 0) {
-      int w = tot[lane];
+      int w = lane < static_cast<int>(blockDim.x >> 5) ? tot[lane] : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int t = __shfl_up_sync(0xffffffffu, w, d);
@@ -132,38 +159,46 @@ __device__ void block_scan(int* a, int n, int* tot, Op op) {
   }
 }
 
-// Where unit (chunk j, block g) of a part lies in the list.
-__device__ __forceinline__ int chunk_tiles(const SharedPart& v, int C) {
-  return v.blocks == 1 || v.tiles < C ? v.tiles : C;
-}
+constexpr int kStart = 2;
 
 __global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParams p) {
   extern __shared__ int sm[];
   const int G = p.num_groups, B = p.num_seqs, V = G + B;
   int* ends = sm;             // [G + 1] first sequence of each group
-  int* shared = ends + G + 1; // [G] tokens of its shared part
-  int* lead = shared + G;     // [G] the sequence whose table they are read through
-  int* pre = lead + G;        // [V + 1] tiles before a part
+  int* lead = ends + G + 1;   // [G] the sequence whose table its shared part is read through
+  int* tok0 = lead + G;       // [V] a part's tokens: groups, then sequences
+  int* tok1 = tok0 + V;
+  int* pre = tok1 + V;        // [V + 1] tiles before a part
   int* unit = pre + V + 1;    // [V + 1] units before a part
   __shared__ int tot[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
   const int per = p.rows_per_seq * p.num_heads;  // vectors of a sequence
-  const int own_blocks = cdiv(per, 128);
-  auto length = [&](int b) { return clampi(__ldg(p.seq_lens + b), 0, p.capacity); };
 
   for (int g = threadIdx.x; g <= G; g += blockDim.x)
     ends[g] = clampi(__ldg(p.group_seqs + g), 0, B);
+  for (int g = threadIdx.x; g < G; g += blockDim.x) {
+    const int n = __ldg(p.prefix_lens + g);
+    tok0[g] = 0;
+    tok1[g] = clampi(n, 0, p.capacity) & ~(TT - 1);
+    if ((n < 0 || n > p.capacity) && p.err_count) atomicAdd(p.err_count, 1);
+  }
+  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+    const int n = __ldg(p.seq_lens + b);
+    tok1[G + b] = clampi(n, 0, p.capacity);
+    if ((n < 0 || n > p.capacity) && p.err_count) atomicAdd(p.err_count, 1);
+  }
   __syncthreads();
-  block_scan(ends, G + 1, tot, [](int a, int b) { return max(a, b); });
-  for (int g = warp; g < G; g += 32) {
-    const int raw = __ldg(p.prefix_lens + g);
-    const int n = clampi(raw, 0, p.capacity) & ~(TT - 1);
-    if (lane == 0 && (raw < 0 || raw > p.capacity) && p.err_count) atomicAdd(p.err_count, 1);
+  if (G > 1) block_scan(ends, G + 1, tot, [](int a, int b) { return max(a, b); });
+  if (G == 1 && threadIdx.x == 0) ends[1] = max(ends[0], ends[1]);
+  __syncthreads();
+  // what the sequences of a group can share, when there are two at least
+  for (int g = warp; g < G; g += static_cast<int>(blockDim.x >> 5)) {
+    const int n = tok1[g];
     int count = 0, first = B;
     for (int b = ends[g] + lane; b < ends[g + 1]; b += 32)
-      if (length(b) >= n) {
+      if (tok1[G + b] >= n) {
         ++count;
         first = min(first, b);
       }
@@ -173,71 +208,76 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParam
       first = min(first, __shfl_xor_sync(0xffffffffu, first, d));
     }
     if (lane == 0) {
-      shared[g] = count > 1 ? n : 0;
+      if (count < 2) tok1[g] = 0;
       lead[g] = first;
     }
   }
   __syncthreads();
-  // the parts: groups, then sequences
-  auto part = [&](int v) {
-    SharedPart x = {};
-    x.group = -1;
-    if (v < G) {
-      x.row0 = ends[v] * p.rows_per_seq;
-      x.vecs = (ends[v + 1] - ends[v]) * per;
-      x.tok1 = shared[v];
-      x.table = lead[v];
-    } else {
-      const int b = v - G;
-      int a = 0, z = G;  // the last group that starts at or before b
-      while (a < z) {
-        const int m = (a + z + 1) >> 1;
-        if (ends[m] <= b) a = m; else z = m - 1;
-      }
-      x.row0 = b * p.rows_per_seq;
-      x.vecs = per;
-      x.tok1 = length(b);
-      x.table = b;
-      if (a < G && b >= ends[a] && shared[a] > 0 && x.tok1 >= shared[a]) {
-        x.group = a;
-        x.tok0 = shared[a];
-      }
+  auto blocks_of = [&](int v) {
+    return tok1[v] <= tok0[v] ? 0 : cdiv(v < G ? (ends[v + 1] - ends[v]) * per : per, 128);
+  };
+  auto tiles_of = [&](int v) { return cdiv(tok1[v] - tok0[v], TT); };
+  // the group whose shared part sequence b takes part in, or -1
+  auto group_of = [&](int b) {
+    int a = 0, z = G;  // the last group that starts at or before b
+    while (a < z) {
+      const int m = (a + z + 1) >> 1;
+      if (ends[m] <= b) a = m; else z = m - 1;
     }
-    x.tiles = cdiv(x.tok1 - x.tok0, TT);
-    x.blocks = x.tiles ? cdiv(x.vecs, 128) : 0;
-    return x;
+    return a < G && b >= ends[a] && tok1[a] > 0 && tok1[G + b] >= tok1[a] ? a : -1;
   };
   for (int v = threadIdx.x; v < V; v += blockDim.x) {
-    const SharedPart x = part(v);
-    pre[v + 1] = x.tiles * x.blocks;
     if (v >= G) {
-      const int raw = __ldg(p.seq_lens + v - G);
-      if ((raw < 0 || raw > p.capacity) && p.err_count) atomicAdd(p.err_count, 1);
+      const int g = group_of(v - G);
+      tok0[v] = g < 0 ? 0 : tok1[g];
     }
+    pre[v + 1] = tiles_of(v) * blocks_of(v);
   }
   if (threadIdx.x == 0) pre[0] = unit[0] = 0;
   __syncthreads();
   block_scan(pre + 1, V, tot, [](int a, int b) { return a + b; });
-  const int total = pre[V];
-  const int C = max(1, cdiv(total, p.pairs));
+  // chunks of a pair's share of the tiles, then places and units
+  const int chunk = max(1, cdiv(pre[V], p.pairs));
+  auto chunk_of = [&](int blocks, int tiles) {
+    return blocks == 1 || tiles < chunk ? tiles : chunk;
+  };
+  __syncthreads();
   for (int v = threadIdx.x; v < V; v += blockDim.x) {
-    const SharedPart x = part(v);
-    unit[v + 1] = x.blocks == 0 ? 0 : x.blocks * cdiv(x.tiles, chunk_tiles(x, C));
+    const int n = blocks_of(v), t = tiles_of(v);
+    const int units = n == 0 ? 0 : n * cdiv(t, chunk_of(n, t));
+    unit[v + 1] = units;
+    pre[v + 1] = t * n + kStart * units;
   }
   __syncthreads();
   block_scan(unit + 1, V, tot, [](int a, int b) { return a + b; });
-  for (int v = threadIdx.x; v < V; v += blockDim.x) {
-    SharedPart x = part(v);
-    x.tile0 = pre[v];
+  block_scan(pre + 1, V, tot, [](int a, int b) { return a + b; });
+  const int total = pre[V];
+  const int C = max(1, cdiv(total, p.pairs));
+  auto place = [&](int v) {
+    SharedPlace x;
+    x.first = pre[v];
+    x.tiles = tiles_of(v);
+    x.blocks = blocks_of(v);
+    x.chunk = x.blocks == 0 ? 1 : chunk_of(x.blocks, x.tiles);
     x.unit0 = unit[v];
-    p.parts[v] = x;
+    x.row0 = (v < G ? ends[v] : v - G) * p.rows_per_seq;
+    return x;
+  };
+  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+    const int g = group_of(b);
+    SharedRow x;
+    x.own = place(G + b);
+    x.group = place(g < 0 ? 0 : g);
+    if (g < 0) x.group.blocks = 0;
+    x.per_pair = C;
+    x.pad = 0;
+    p.rows[b] = x;
   }
-  if (threadIdx.x == 0) p.header[0] = C;
   // the segments of each pair
   for (int c = threadIdx.x; c < p.pairs; c += blockDim.x) {
     const int64_t lo64 = static_cast<int64_t>(c) * C;
     const int lo = lo64 < total ? static_cast<int>(lo64) : total;
-    const int hi = lo + C < total ? lo + C : total;
+    const int hi = total - lo > C ? lo + C : total;
     int2 mine = make_int2(0, 0);
     if (lo < hi) {
       int a = 0, z = V - 1;  // the last part that starts at or before lo
@@ -248,26 +288,31 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParam
       int t = lo;
       for (int v = a; t < hi; ++v) {
         if (pre[v + 1] <= t) continue;
-        const SharedPart x = part(v);
-        const int ch = chunk_tiles(x, C);
+        const SharedPlace x = place(v);
+        const int vecs = v < G ? (ends[v + 1] - ends[v]) * per : per;
+        const int full_chunk = (x.chunk + kStart) * x.blocks;  // places of a whole chunk
         while (t < hi && t < pre[v + 1]) {
-          const int in = t - pre[v];
-          const int j = in / (ch * x.blocks);
-          const int len = min(ch, x.tiles - j * ch);
-          const int y = in - j * ch * x.blocks, g = y / len, k = y - g * len;
-          const int n = min(len - k, hi - t);
-          SharedSegment s;
-          s.table = x.table;
-          s.row0 = x.row0;
-          s.vec0 = g * 128;
-          s.vecs = min(128, x.vecs - g * 128);
-          s.tok0 = x.tok0 + (j * ch + k) * TT;
-          s.tok1 = min(x.tok1, s.tok0 + n * TT);
-          s.pad0 = s.pad1 = 0;
-          const int slot = unit[v] + j * x.blocks + g + c;
-          p.segments[slot] = s;
-          if (mine.y == 0) mine.x = slot;
-          ++mine.y;
+          const int in = t - x.first;
+          const int j = in / full_chunk;
+          const int len = min(x.chunk, x.tiles - j * x.chunk);
+          const int y = in - j * full_chunk;
+          const int g = y / (len + kStart), k = y - g * (len + kStart);  // place of the unit
+          const int n = min(len + kStart - k, hi - t);
+          const int k0 = max(k - kStart, 0), k1 = k + n - kStart;  // its tiles here
+          if (k1 > k0) {
+            SharedSegment s;
+            s.table = v < G ? lead[v] : v - G;
+            s.row0 = x.row0;
+            s.vec0 = g * 128;
+            s.vecs = min(128, vecs - g * 128);
+            s.tok0 = tok0[v] + (j * x.chunk + k0) * TT;
+            s.tok1 = min(tok1[v], s.tok0 + (k1 - k0) * TT);
+            s.pad0 = s.pad1 = 0;
+            const int slot = x.unit0 + j * x.blocks + g + c;
+            p.segments[slot] = s;
+            if (mine.y == 0) mine.x = slot;
+            ++mine.y;
+          }
           t += n;
         }
       }
@@ -310,64 +355,57 @@ __device__ __forceinline__ void convert_box(const uint8_t* src, uint8_t* dst, in
 
 // ---------------------------------------------------------------- main kernel
 template <int R, bool FP8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 448 : 320, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
     decode_shared_kernel(const SharedParams p, const __grid_constant__ CUtensorMap tmap) {
   using RG = Ring<FP8>;
-  constexpr int KB = R / 128;   // 32 KiB boxes of K a tile
+  constexpr int NQ = R / 64;    // boxes of the latent dims: of Q, and of K a tile
   constexpr int VB = R / 256;   // 256-dim parts of O
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   // The same places in both CTAs; each uses its own.
-  uint64_t* full = bars;             // [5] ring box landed (converted)
-  uint64_t* empty = full + 5;        // [5]
-  uint64_t* rfull = empty + 5;       // [2] rank 0: rope box landed
-  uint64_t* rempty = rfull + 2;      // [2]
-  uint64_t* st_full = rempty + 2;    // [4] fp8 staging box landed
-  uint64_t* st_empty = st_full + 4;  // [4]
-  uint64_t* rs_full = st_empty + 4;  // rank 0: fp8 staging of a rope box
-  uint64_t* rs_empty = rs_full + 1;
-  uint64_t* s_full = rs_empty + 1;   // [2] rank 0: S of a tile of this parity
-  uint64_t* s_free = s_full + 2;     // [2] rank 0: S read
-  uint64_t* q_full = s_free + 2;     // rank 0: the segment's Q is in place
-  uint64_t* q_free = q_full + 1;     // rank 0: the segment's last Q K^T is done
-  uint64_t* p_free = q_free + 1;     // [2] rank 0: P buffer read by rank 1's products
-  uint64_t* p_full = p_free + 2;     // [2] rank 1: P and rescale factors landed
-  uint64_t* o_ready = p_full + 2;    // [2] rank 1: O rescaled for this tile's P
-  uint64_t* pv_done = o_ready + 2;   // [2] rank 1
-  uint64_t* o_free = pv_done + 2;    // rank 1: the segment's O has been read out
-  static_assert((5 + 5 + 2 + 2 + 4 + 4 + 1 + 1 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 2 + 1) * 8 <= 512,
-                "barriers");
+  uint64_t* full = bars;                      // [kMostBoxes] ring box landed (converted)
+  uint64_t* empty = full + kMostBoxes;        // [kMostBoxes]
+  uint64_t* st_full = empty + kMostBoxes;     // [kMostStages] fp8 staging box landed
+  uint64_t* st_empty = st_full + kMostStages; // [kMostStages]
+  uint64_t* s_full = st_empty + kMostStages;  // [2] rank 0: S of a tile of this parity
+  uint64_t* s_free = s_full + 2;              // [2] rank 0: S read
+  uint64_t* q_full = s_free + 2;              // rank 0: the segment's Q is in place
+  uint64_t* q_free = q_full + 1;              // rank 0: the segment's last Q K^T is done
+  uint64_t* p_free = q_free + 1;              // [2] rank 0: P buffer read by rank 1's products
+  uint64_t* p_full = p_free + 2;              // [2] rank 1: P and rescale factors landed
+  uint64_t* o_ready = p_full + 2;             // [2] rank 1: O rescaled for this tile's P
+  uint64_t* pv_done = o_ready + 2;            // [2] rank 1
+  uint64_t* o_free = pv_done + 2;             // rank 1: the segment's O has been read out
+  uint64_t* seg_filled = o_free + 1;          // rank 0: the segment's last K box has been filled
+  static_assert((2 * kMostBoxes + 2 * kMostStages + 16) * 8 <= 512, "barriers");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
 
   const uint32_t rank = tc::cluster_ctarank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmap);
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < kMostBoxes; ++i) {
       mbar_init(&full[i], FP8 ? 4 : 1);
       mbar_init(&empty[i], 1);
     }
+    for (int i = 0; i < kMostStages; ++i) {
+      mbar_init(&st_full[i], 1);
+      mbar_init(&st_empty[i], 4);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&rfull[i], FP8 ? 4 : 1);
-      mbar_init(&rempty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 8);
+      mbar_init(&s_free[i], 4);
       mbar_init(&p_free[i], 1);
       mbar_init(&p_full[i], 1);
       mbar_init(&o_ready[i], 8);
       mbar_init(&pv_done[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&st_full[i], 1);
-      mbar_init(&st_empty[i], 4);
-    }
-    mbar_init(rs_full, 1);
-    mbar_init(rs_empty, 4);
-    mbar_init(q_full, 8);
+    mbar_init(q_full, 4);
     mbar_init(q_free, 1);
     mbar_init(o_free, 8);
+    mbar_init(seg_filled, FP8 ? 4 : 3);
     fence_mbar_init();
     if (rank == 1)
       for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&p_full[i], kPBuf + 512);
@@ -396,83 +434,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 448 : 320, 1)
     return r;
   };
   bool ok = true;
-
-  if (warp == 8) {
-    // ------------------------------------------------------------ producer
-    // Lane l loads (page l % 8, 64-dim part l / 8) of a K box, page l % 4 and
-    // part l / 4 of a V box.  Page ids are read one tile before they are used.
+  // ---------------------------------------------------- producer
+  auto produce = [&]() {
+    // Three warps share the boxes of the ring: one, at 0.28 us a box, did not keep
+    // up.  Lane l loads page l of a K box, page l % 4 and 64-dim part l / 4 of a V
+    // box.  Page ids are read one tile before they are used.
+    const int which = warp == 8 ? 0 : FP8 ? warp - 13 : warp - 9;
     const int pages = TT / box_rows;  // of a tile: 2, 4 or 8
+    const int my_page = lane & 7;
+    const int v_page = lane & 3, v_part = lane >> 2;
     constexpr int kRowBytes = FP8 ? 64 : 128;  // a row of a 64-dim part
-    int nb = 0, nr = 0;
+    int nb = 0;  // position in the ring (fp8: of the staging boxes, where Q has none)
     for (int k = 0; k < mine.y && ok; ++k) {
       const SharedSegment sg = segment(k);
       const int32_t* bt = p.block_table + static_cast<int64_t>(sg.table) * p.bt_stride;
       const int tiles = cdiv(sg.tok1 - sg.tok0, TT);
       auto id_of = [&](int t) -> int {
-        const int tk = sg.tok0 + t * TT + (lane & 7) * box_rows;
-        return lane < pages && t < tiles && tk < sg.tok1 ? __ldg(bt + tk / bs) : 0;
+        const int tk = sg.tok0 + t * TT + my_page * box_rows;
+        return my_page < pages && t < tiles && tk < sg.tok1 ? __ldg(bt + tk / bs) : 0;
       };
       int id = id_of(0);
+      if (!FP8 && rank == 0) nb += NQ;  // the segment's Q comes first
       for (int t = 0; t < tiles && ok; ++t) {
         const int next = id_of(t + 1);
         const int tok = sg.tok0 + t * TT;
         const int have = min(pages, cdiv(sg.tok1 - tok, box_rows));  // pages to load
-        if (rank == 0 && lane < have && (id < 0 || id >= p.num_blocks) && p.err_count)
-          atomicAdd(p.err_count, 1);
-        // a box: `parts` 64-dim parts from dim `d0` on, pages [p0, p0 + np)
-        auto load = [&](uint8_t* dst, uint64_t* bar, int parts, int part_bytes, int d0, int p0,
-                        int np, int page, int part) {
-          const int blk = __shfl_sync(0xffffffffu, id, (p0 + page) & 31);
-          if (lane == 0)
-            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(parts * np * box_rows * kRowBytes));
-          __syncwarp();
-          if (page < np && part < parts) {
-            const int tk = tok + (p0 + page) * box_rows;
-            tma_load_3d(dst + part * part_bytes + page * box_rows * kRowBytes, &tmap, bar,
-                        d0 + part * 64, tk % bs, blk);
-          }
-        };
         if (rank == 0) {
-          for (int c = 0; c < KB && ok; ++c, ++nb) {
-            const int st = FP8 ? nb % RG::STAGES : nb % RG::S_BOXES;
-            const int use = FP8 ? nb / RG::STAGES : nb / RG::S_BOXES;
-            ok = warp_wait(FP8 ? &st_empty[st] : &empty[st], (use & 1) ^ 1);
+          if (which == 0 && lane < have && (id < 0 || id >= p.num_blocks) && p.err_count)
+            atomicAdd(p.err_count, 1);
+          constexpr int N = FP8 ? RG::S_STAGES : RG::S_BOXES;
+          const int row = (tok + my_page * box_rows) % bs;
+          for (int c = 0; c <= NQ && ok; ++c, ++nb) {  // the last box: the rope part
+            if (nb % 3 != which) continue;
+            const int st = nb % N;
+            ok = warp_wait(FP8 ? &st_empty[st] : &empty[st], ((nb / N) & 1) ^ 1);
             if (!ok) break;
-            uint8_t* dst = smem + (FP8 ? RG::S_STAGE + st * 16384 : S_RING + st * kBig);
-            load(dst, FP8 ? &st_full[st] : &full[st], 2, TT * kRowBytes, c * 128, 0, have,
-                 lane & 7, lane >> 3);
+            uint64_t* bar = FP8 ? &st_full[st] : &full[st];
+            if (lane == 0)
+              mbar_arrive_expect_tx(bar, static_cast<uint32_t>(have * box_rows * kRowBytes));
+            __syncwarp();
+            if (lane < have)
+              tma_load_3d(smem + (FP8 ? RG::S_STAGE + st * 8192 : S_RING + st * kKBox) +
+                              lane * box_rows * kRowBytes,
+                          &tmap, bar, c * 64, row, id);
           }
-          if (!ok) break;
-          const int st = nr & 1;
-          ok = FP8 ? warp_wait(rs_empty, st ^ 1) : warp_wait(&rempty[st], ((nr >> 1) & 1) ^ 1);
-          if (!ok) break;
-          load(smem + (FP8 ? RG::S_RSTAGE : S_ROPE + st * kRope), FP8 ? rs_full : &rfull[st], 1, TT * kRowBytes, R, 0, have, lane & 7, lane >> 3);
-          ++nr;
         } else {
+          constexpr int N = FP8 ? RG::V_STAGES : RG::V_BOXES;
           const int half = pages / 2;
-          for (int e = 0; e < 2 && e * half < have && ok; ++e)
+          for (int e = 0; e < 2 && e * half < have && ok; ++e) {
+            const int np = min(half, have - e * half);
+            const int blk = __shfl_sync(0xffffffffu, id, e * half + v_page);
+            const int row = (tok + (e * half + v_page) * box_rows) % bs;
             for (int d = 0; d < VB; ++d, ++nb) {
-              const int st = FP8 ? nb % RG::V_STAGES : nb % RG::V_BOXES;
-              const int use = FP8 ? nb / RG::V_STAGES : nb / RG::V_BOXES;
-              ok = warp_wait(FP8 ? &st_empty[st] : &empty[st], (use & 1) ^ 1);
+              if (nb % 3 != which) continue;
+              const int st = nb % N;
+              ok = warp_wait(FP8 ? &st_empty[st] : &empty[st], ((nb / N) & 1) ^ 1);
               if (!ok) break;
-              uint8_t* dst = smem + (FP8 ? RG::V_STAGE + st * 16384 : V_RING + st * kBig);
-              load(dst, FP8 ? &st_full[st] : &full[st], 4, 64 * kRowBytes, d * 256, e * half,
-                   min(half, have - e * half), lane & 3, lane >> 2);
+              uint64_t* bar = FP8 ? &st_full[st] : &full[st];
+              if (lane == 0)
+                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(4 * np * box_rows * kRowBytes));
+              __syncwarp();
+              if (v_page < np && v_part < 4)
+                tma_load_3d(smem + (FP8 ? RG::V_STAGE + st * 16384 : V_RING + st * kVBox) +
+                                (v_part * 64 + v_page * box_rows) * kRowBytes,
+                            &tmap, bar, d * 256 + v_part * 64, row, blk);
             }
+          }
         }
         id = next;
       }
+      if (!FP8 && rank == 0 && ok) {
+        // a segment of few boxes can be filled before its Q is there: not told
+        // before those who wait have seen the last one
+        ok = warp_wait(q_full, k & 1);
+        if (lane == 0) mbar_arrive(seg_filled);
+      }
     }
-  } else if (FP8 && warp >= 10) {
-    // ---------------------------------------------------------- conversion
+  };
+  // -------------------------------------------------- conversion
+  auto convert = [&]() {
     const int t = threadIdx.x - 320;
     const bool e5m2 = p.e5m2;
-    int nb = 0, nr = 0;
+    int ns = 0, nb = 0;  // positions among the staging boxes and in the ring
     // staging box -> ring box, `parts` 64-dim parts of `rows` rows each
-    auto turn = [&](uint64_t* sf, uint64_t* se, int su, const uint8_t* src, uint64_t* bf,
-                    uint64_t* be, int bu, uint8_t* dst, int parts, int rows) -> bool {
-      if (!warp_wait(sf, su & 1) || !warp_wait(be, (bu & 1) ^ 1)) return false;
+    auto turn = [&](int stages, int boxes, const uint8_t* src, uint8_t* dst, int parts,
+                    int rows) -> bool {
+      uint64_t *se = &st_empty[ns % stages], *bf = &full[nb % boxes];
+      if (!warp_wait(&st_full[ns % stages], (ns / stages) & 1) ||
+          !warp_wait(&empty[nb % boxes], ((nb / boxes) & 1) ^ 1))
+        return false;
       for (int c = 0; c < parts; ++c)
         convert_box(src + c * rows * 64, dst + c * rows * 128, rows, t, e5m2);
       fence_proxy_async_smem();
@@ -481,89 +531,112 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 448 : 320, 1)
         mbar_arrive(bf);
         mbar_arrive(se);
       }
+      ++ns;
+      ++nb;
       return true;
+    };
+    for (int k = 0; FP8 && k < mine.y && ok; ++k) {
+      const SharedSegment sg = segment(k);
+      if (rank == 0) {
+        // the segment's Q boxes, which these warps do not follow, have been filled
+        // and read: a ring barrier's parity tells no more than one use apart
+        nb += NQ;
+        ok = warp_wait(q_full, k & 1);
+      }
+      for (int tok = sg.tok0; tok < sg.tok1 && ok; tok += TT) {
+        if (rank == 0) {
+          for (int c = 0; c <= NQ && ok; ++c)
+            ok = turn(kMostStages, RG::S_BOXES, smem + RG::S_STAGE + (ns % kMostStages) * 8192,
+                      smem + S_RING + (nb % RG::S_BOXES) * kKBox, 1, TT);
+        } else {
+          for (int e = 0; e < 2 && tok + e * 64 < sg.tok1 && ok; ++e)
+            for (int d = 0; d < VB && ok; ++d)
+              ok = turn(4, RG::V_BOXES, smem + RG::V_STAGE + (ns % 4) * 16384,
+                        smem + V_RING + (nb % RG::V_BOXES) * kVBox, 4, 64);
+        }
+      }
+      if (rank == 0 && lane == 0) mbar_arrive(seg_filled);
+    }
+  };
+  // ------------------------------------------------------- Q K^T
+  auto scores = [&]() {
+    constexpr uint32_t idesc = tc::idesc_bf16(128, TT, 0, 0);
+    const uint64_t dq = tc::smem_desc(smem_u32(smem + S_QPE), 16, 1024, tc::kLayoutSw128);
+    const uint64_t ring =
+        tc::smem_desc(smem_u32(smem + S_RING), 16, 1024, tc::kLayoutSw128);
+    int n = 0, bx = 0;       // tile, ring box
+    uint32_t phase = 0;      // of the box's barrier
+    auto skip = [&](int boxes) {
+      bx += boxes;
+      if (bx >= RG::S_BOXES) {
+        bx -= RG::S_BOXES;
+        phase ^= 1;
+      }
     };
     for (int k = 0; k < mine.y && ok; ++k) {
       const SharedSegment sg = segment(k);
-      for (int tok = sg.tok0; tok < sg.tok1 && ok; tok += TT) {
-        if (rank == 0) {
-          for (int c = 0; c < KB && ok; ++c, ++nb) {
-            const int st = nb % RG::STAGES, bx = nb % RG::S_BOXES;
-            ok = turn(&st_full[st], &st_empty[st], nb / RG::STAGES,
-                      smem + RG::S_STAGE + st * 16384, &full[bx], &empty[bx], nb / RG::S_BOXES,
-                      smem + S_RING + bx * kBig, 2, TT);
-          }
-          if (ok) {
-            const int st = nr & 1;
-            ok = turn(rs_full, rs_empty, nr, smem + RG::S_RSTAGE, &rfull[st], 
-                      &rempty[st], nr >> 1, smem + S_ROPE + st * kRope, 1, TT);
-            ++nr;
-          }
-        } else {
-          for (int e = 0; e < 2 && tok + e * 64 < sg.tok1 && ok; ++e)
-            for (int d = 0; d < VB && ok; ++d, ++nb) {
-              const int st = nb % RG::V_STAGES, bx = nb % RG::V_BOXES;
-              ok = turn(&st_full[st], &st_empty[st], nb / RG::V_STAGES,
-                        smem + RG::V_STAGE + st * 16384, &full[bx], &empty[bx], nb / RG::V_BOXES,
-                        smem + V_RING + bx * kBig, 4, 64);
-            }
-        }
-      }
-    }
-  } else if (warp == 9 && rank == 0) {
-    // ------------------------------------------------------------- Q K^T
-    constexpr uint32_t idesc = tc::idesc_bf16(128, TT, 0, 0);
-    const uint64_t dq = tc::smem_desc(smem_u32(smem + S_QPE), 16, 1024, tc::kLayoutSw128);
-    int n = 0, nb = 0;
-    for (int k = 0; k < mine.y && ok; ++k) {
-      const SharedSegment sg = segment(k);
       const int tiles = cdiv(sg.tok1 - sg.tok0, TT);
+      skip(NQ);  // Q's boxes
       ok = warp_wait(q_full, k & 1);
       for (int t = 0; t < tiles && ok; ++t, ++n) {
         const uint32_t dS = tmem + S_COL + (n & 1) * TT;
         ok = warp_wait(&s_free[n & 1], ((n >> 1) & 1) ^ 1);
         if (!ok) break;
-        tc::fence_after_sync();
+        // Three boxes for each wait, vote and issuing block: those cost about as
+        // much as the four instructions of a box (one box at a time a tile took
+        // 2.1 us to issue, 1.4 us of products).
 #pragma unroll
-        for (int c = 0; c < KB; ++c, ++nb) {
-          const int bx = nb % RG::S_BOXES;
-          ok = ok && warp_wait(&full[bx], (nb / RG::S_BOXES) & 1);
+        for (int c0 = 0; c0 <= NQ; c0 += 3) {
+          constexpr int kAll = NQ + 1;
+          const int cnt = kAll - c0 < 3 ? kAll - c0 : 3;
+          int b[3];
+          uint32_t ph[3];
+          bool r = true;
+#pragma unroll
+          for (int i = 0; i < cnt; ++i) {
+            b[i] = bx;
+            ph[i] = phase;
+            skip(1);
+            r = mbar_try_wait(&full[b[i]], ph[i]) && r;
+          }
+          if (!__all_sync(0xffffffffu, r)) {
+            r = true;
+#pragma unroll
+            for (int i = 0; i < cnt; ++i) r = r && mbar_wait(&full[b[i]], ph[i]);
+            ok = __all_sync(0xffffffffu, r);
+          }
           if (!ok) break;
           tc::fence_after_sync();
           if (tc::elect_one()) {
-            const uint64_t db =
-                tc::smem_desc(smem_u32(smem + S_RING + bx * kBig), 16, 1024, tc::kLayoutSw128);
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-              tc::mma_ts(dS, tmem + c * 64 + s * 8,
-                         db + static_cast<uint64_t>((s >> 2) * (16384 >> 4) + (s & 3) * 2), idesc,
-                         (c > 0 || s > 0) ? 1u : 0u);
-            tc::commit(&empty[bx]);
+            for (int i = 0; i < cnt; ++i) {
+              const int c = c0 + i;
+              const uint64_t db = ring + static_cast<uint64_t>(b[i] * (kKBox >> 4));
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+                if (c < NQ)
+                  tc::mma_ts(dS, tmem + c * 32 + s * 8, db + static_cast<uint64_t>(s * 2), idesc,
+                             (c > 0 || s > 0) ? 1u : 0u);
+                else  // the rope part
+                  tc::mma_ss(dS, dq + static_cast<uint64_t>(s * 2),
+                             db + static_cast<uint64_t>(s * 2), idesc, 1u);
+              }
+              tc::commit(&empty[b[i]]);
+            }
+            if (c0 + cnt == kAll) {
+              tc::commit(&s_full[n & 1]);
+              if (t + 1 == tiles) tc::commit(q_free);
+            }
           }
           __syncwarp();
         }
-        if (!ok) break;
-        ok = warp_wait(&rfull[n & 1], (n >> 1) & 1);
-        if (!ok) break;
-        tc::fence_after_sync();
-        if (tc::elect_one()) {
-          const uint64_t db = tc::smem_desc(smem_u32(smem + S_ROPE + (n & 1) * kRope), 16, 1024,
-                                            tc::kLayoutSw128);
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            tc::mma_ss(dS, dq + static_cast<uint64_t>(s * 2), db + static_cast<uint64_t>(s * 2),
-                       idesc, 1u);
-          tc::commit(&rempty[n & 1]);
-          tc::commit(&s_full[n & 1]);
-          if (t + 1 == tiles) tc::commit(q_free);
-        }
-        __syncwarp();
       }
     }
     // nothing of this CTA's still runs on the tensor core when TMEM is freed
     if (ok && mine.y > 0) ok = warp_wait(q_free, (mine.y - 1) & 1);
-  } else if (warp == 9) {
-    // --------------------------------------------------------------- P V
+  };
+  // --------------------------------------------------------- P V
+  auto values = [&]() {
     constexpr uint32_t idesc = tc::idesc_bf16(128, 256, 0, 1);
     int n = 0, nb = 0;
     for (int k = 0; k < mine.y && ok; ++k) {
@@ -584,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 448 : 320, 1)
             const int bx = nb % RG::V_BOXES;
             ok = ok && warp_wait(&full[bx], (nb / RG::V_BOXES) & 1);
             if (!ok) break;
-            uint8_t* box = smem + V_RING + bx * kBig;
+            uint8_t* box = smem + V_RING + bx * kVBox;
             if (left < e * 64 + 64) {
               // Rows past the sequence's end hold other tokens, or what was
               // there before: zeros, since 0 * NaN is NaN (their P is 0).
@@ -620,101 +693,124 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 448 : 320, 1)
       }
     }
     if (ok && n > 0) ok = warp_wait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
-  } else if (rank == 0) {
-    // ------------------------------------------------------------- softmax
-    const int quad = warp & 3, h = warp >> 2;  // lane quarter, token half
-    const int r = quad * 32 + lane;            // vector of the block
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  };
+  // ----------------------------------------------------------- Q
+  auto load_q = [&]() {
+    // The latent dims come through the K ring, as boxes of 64 dims x 128 vectors
+    // that are asked for together (loaded row by row straight into TMEM they took
+    // 8.7 us), and go on into TMEM; the rope dims stay in shared memory.
+    const int tq = threadIdx.x - 128, r = tq;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int nb = 0;
+    for (int k = 0; k < mine.y && ok; ++k) {
+      const SharedSegment sg = segment(k);
+      const int tiles = cdiv(sg.tok1 - sg.tok0, TT);
+      // the boxes before these have been filled: a ring barrier's parity tells no
+      // more than one use apart
+      if (k > 0) ok = warp_wait(seg_filled, (k - 1) & 1);
+      for (int c = 0; c < NQ && ok; ++c)
+        ok = warp_wait(&empty[(nb + c) % RG::S_BOXES], (((nb + c) / RG::S_BOXES) & 1) ^ 1);
+      // this thread copies 16 bytes (dims 8 (tq % 8) on) of vectors tq / 8 + 16 j;
+      // vectors that there are not become zeros
+      auto copy = [&](auto&& f) {
+#pragma unroll 2
+        for (int j = 0; j < 8; ++j) {
+          const int v = (tq >> 3) + 16 * j;
+          const bool live = v < sg.vecs;
+          const int vec = sg.vec0 + v;
+          const int row = live ? sg.row0 + vec / H : 0, hd = live ? vec % H : 0;
+          f(row, hd, sw128(v, tq & 7), live ? 16u : 0u);
+        }
+      };
+      if (ok)
+        copy([&](int row, int hd, uint32_t at, uint32_t bytes) {
+          const uint16_t* src = p.q + row * p.q_row_stride + hd * p.q_head_stride + (tq & 7) * 8;
+#pragma unroll
+          for (int c = 0; c < NQ; ++c)
+            cp_async16(smem_u32(smem + S_RING) + (nb + c) % RG::S_BOXES * kKBox + at, src + c * 64,
+                       bytes);
+        });
+      // the last segment's products have read their Q
+      if (ok && k > 0) ok = warp_wait(q_free, (k - 1) & 1);
+      if (ok)
+        copy([&](int row, int hd, uint32_t at, uint32_t bytes) {
+          cp_async16(smem_u32(smem + S_QPE) + at,
+                     p.q_pe + row * p.q_pe_row_stride + hd * p.q_pe_head_stride + (tq & 7) * 8, bytes);
+        });
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      ok = named_bar_and(1, 128, ok);  // the four warps leave together
+      if (!ok) break;
+      tc::fence_after_sync();
+#pragma unroll 2
+      for (int c = 0; c < NQ; ++c) {
+        const uint8_t* src = smem + S_RING + ((nb + c) % RG::S_BOXES) * kKBox;
+        uint32_t x[32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 y = *reinterpret_cast<const uint4*>(src + sw128(r, j));
+          x[4 * j] = y.x;
+          x[4 * j + 1] = y.y;
+          x[4 * j + 2] = y.z;
+          x[4 * j + 3] = y.w;
+        }
+        tc::st_32x32b_x32(tmem + lanes + c * 32, x);
+      }
+      tc::wait_st();
+      tc::fence_before_sync();
+      // the ring's barriers count these boxes as filled and read, too
+      if (FP8 ? lane < NQ : tq < NQ) mbar_arrive(&full[(nb + lane) % RG::S_BOXES]);
+      named_bar_sync(1, 128);
+      if (lane == 0) mbar_arrive(q_full);
+      if (tq < NQ) mbar_arrive(&empty[(nb + tq) % RG::S_BOXES]);
+      nb += NQ + tiles * (NQ + 1);
+    }
+  };
+  // ----------------------------------------------------- softmax
+  auto softmax = [&]() {
+    const int r = threadIdx.x;  // vector of the block, TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const float c = p.sm_scale * (FP8 ? __ldg(p.kv_scale) : 1.f) * kLog2e;
-    float* red = reinterpret_cast<float*>(smem + RG::S_RED);
-    const uint32_t p_peer = tc::map_peer(smem_u32(smem), 1);
-    const uint32_t a_peer = tc::map_peer(smem_u32(smem + OFF_MISC), 1);
+    const uint32_t p_peer = tc::map_peer(smem_u32(smem), 1) + warp * 4096;
+    const uint32_t a_peer = tc::map_peer(smem_u32(smem + OFF_MISC), 1) + r * 4;
     const uint32_t bar_peer = tc::map_peer(smem_u32(&p_full[0]), 1);
-    // The meeting of the two warps of a quarter; one that gave up passes false
-    // and both leave.
-    auto meet = [&](bool good) -> bool { return named_bar_and(1 + quad, 64, good); };
+    uint8_t* out = smem + S_OUT + warp * 8192;  // 32 vectors x 64 tokens, twice
     int n = 0;
     for (int k = 0; k < mine.y && ok; ++k) {
       const SharedSegment sg = segment(k);
       const int tiles = cdiv(sg.tok1 - sg.tok0, TT);
-      // ---- Q: this vector's half of the latent dims into TMEM, of the rope dims
-      // into the swizzled box, once the last segment's products have read theirs
-      bool good = k == 0 || warp_wait(q_free, (k - 1) & 1);
-      const bool live = r < sg.vecs;
-      if (good) {
-        tc::fence_after_sync();
-        const int vec = sg.vec0 + r;
-        const int row = live ? sg.row0 + vec / H : 0, hd = live ? vec % H : 0;
-        const uint16_t* qn = p.q + row * p.q_row_stride + hd * p.q_head_stride + h * (R / 2);
-        const uint16_t* qp = p.q_pe + row * p.q_pe_row_stride + hd * p.q_pe_head_stride + h * 32;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        uint4 pe[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) pe[j] = live ? __ldg(reinterpret_cast<const uint4*>(qp) + j) : zero;
-#pragma unroll 2
-        for (int d = 0; d < R / 128; ++d) {
-          uint32_t x[32];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 y = live ? __ldg(reinterpret_cast<const uint4*>(qn + d * 64) + j) : zero;
-            x[4 * j] = y.x;
-            x[4 * j + 1] = y.y;
-            x[4 * j + 2] = y.z;
-            x[4 * j + 3] = y.w;
-          }
-          tc::st_32x32b_x32(tmem + lanes + h * (R / 4) + d * 32, x);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(smem + S_QPE + sw128(r, h * 4 + j)) = pe[j];
-        tc::wait_st();
-        tc::fence_before_sync();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-      }
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < tiles; ++t, ++n) {
         const int b = n & 1;
         const uint32_t par = (n >> 1) & 1;
-        uint32_t s[64];
-        float mt = -INFINITY;
-        if (good && warp_wait(&s_full[b], par)) {
-          tc::fence_after_sync();
-          const uint32_t col = tmem + lanes + S_COL + b * TT + h * 64;
-          tc::ld_32x32b_x32(col, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-          tc::ld_32x32b_x32(col + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-          tc::wait_ld();
-          tc::reg_fence(s);
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[b]);
-          const int left = sg.tok1 - (sg.tok0 + t * TT) - h * 64;  // tokens of this half
-          float mx[4] = {mt, mt, mt, mt};
+        ok = warp_wait(&s_full[b], par);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t col = tmem + lanes + S_COL + b * TT;
+        const int left = sg.tok1 - (sg.tok0 + t * TT);  // tokens of the tile
+        uint32_t s[128];
 #pragma unroll
-          for (int j = 0; j < 64; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * c);
-          if (left < 64) {
+        for (int q = 0; q < 4; ++q)
+          tc::ld_32x32b_x32(col + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[q * 32]));
+        tc::wait_ld();
+        tc::reg_fence(s);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[b]);
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (j >= left) s[j] = 0xFF800000u;  // -inf
-          }
+        for (int j = 0; j < 128; j += 2) mul2(s[j], s[j + 1], c);
+        if (left < TT) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
-          mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // the P buffer's last tile has been read by rank 1
-          if (n >= 2 && !warp_wait_cluster(&p_free[b], par ^ 1)) good = false;
-        } else {
-          good = false;
+          for (int j = 0; j < 128; ++j)
+            if (j >= left) s[j] = 0xFF800000u;  // -inf
         }
-        // ---- the vector's maximum over both halves (by tile parity: the other
-        // warp reads this tile's value before either writes the one after next's)
-        float* rp = red + b * 256;
-        rp[h * 128 + r] = mt;
-        if (!meet(good)) {
-          ok = false;
-          break;
-        }
-        const float m_new = fmaxf(m, fmaxf(rp[r], rp[128 + r]));
+        float mx[4] = {m, m, m, m};
+#pragma unroll
+        for (int j = 0; j < 128; j += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[j + 2 * e]), __uint_as_float(s[j + 2 * e + 1])));
+        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         // O is rescaled only when the maximum has grown by more than 2^8
         float alpha = 1.f;
         if (m_new > m + kRescaleAt) {
@@ -722,41 +818,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 448 : 320, 1)
           l *= alpha;
           m = m_new;
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t dst = p_peer + b * kPBuf + h * 16384, bar = bar_peer + b * 8;
+        // the P buffer's last tile has been read by rank 1's products, the last
+        // copies have read what they send
+        if (n >= 2) ok = warp_wait_cluster(&p_free[b], par ^ 1);
+        if (!ok) break;
+        if (lane == 0) tc::bulk_wait_read();
+        __syncwarp();
+        const uint32_t bar = bar_peer + b * 8;
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t w[4];
+        for (int q = 0; q < 2; ++q) {  // 64 tokens, a box of P
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a0 = ex2(__uint_as_float(s[8 * j + 2 * e]) - m);
-            const float a1 = ex2(__uint_as_float(s[8 * j + 2 * e + 1]) - m);
-            sum[e] += a0 + a1;
-            w[e] = pack_bf16x2(a0, a1);
+          for (int j = 0; j < 8; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = q * 64 + j * 8 + e * 2;
+              float x0, x1;
+              unpack2(add2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack2(-m, -m)), x0,
+                      x1);
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              sum[e & 1] = add2(sum[e & 1], pack2(x0, x1));
+              w[e] = pack_bf16x2(x0, x1);
+            }
+            *reinterpret_cast<uint4*>(out + q * 4096 + sw128(lane, j)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
-          tc::st_async_v4u(dst + sw128(r, j), w[0], w[1], w[2], w[3], bar);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0)
+            tc::bulk_copy_to_peer(p_peer + b * kPBuf + q * 16384, out + q * 4096, 4096, bar);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (h == 0) tc::st_async_b32(a_peer + b * 512 + r * 4, __float_as_uint(alpha), bar);
+        float s0, s1, s2, s3;
+        unpack2(sum[0], s0, s1);
+        unpack2(sum[1], s2, s3);
+        l += (s0 + s1) + (s2 + s3);
+        tc::st_async_b32(a_peer + b * 512, __float_as_uint(alpha), bar);
       }
       if (!ok) break;
-      // ---- the segment's maximum and sum
-      if (!meet(good)) {
-        ok = false;
-        break;
-      }
-      float* rl = red;
-      if (h == 1) rl[r] = l;
-      meet(true);
-      if (h == 0 && live)
-        p.ml[static_cast<int64_t>(mine.x + k) * 128 + r] = make_float2(m, l + rl[r]);
-      meet(true);
+      if (r < sg.vecs) p.ml[static_cast<int64_t>(mine.x + k) * 128 + r] = make_float2(m, l);
     }
+    if (lane == 0) tc::bulk_wait_read();
     // rank 1's last arrivals here have landed before this CTA can leave
     for (int j = 1; j <= 2 && ok; ++j)
       if (n >= j) ok = warp_wait_cluster(&p_free[(n - j) & 1], ((n - j) >> 1) & 1);
-  } else {
-    // ------------------------------------------------------ O of rank 1
+  };
+  // ------------------------------------------------- O of rank 1
+  auto output = [&]() {
     const int quad = warp & 3, h = warp >> 2;  // lane quarter, half of the dims
     const int r = quad * 32 + lane;
     const uint32_t o_col = tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * (R / 2);
@@ -797,8 +906,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 448 : 320, 1)
       ok = warp_wait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
       if (!ok) break;
       tc::fence_after_sync();
-      float* dst = p.partial + (static_cast<int64_t>(mine.x + k) * 128 + r) * R + h * (R / 2);
-#pragma unroll 1
+      // [8-dim group][vector]: a warp's store is 1 KiB in one piece (rows of R
+      // each took 9.5 us a block)
+      float* dst = p.partial + static_cast<int64_t>(mine.x + k) * 128 * R +
+                   (static_cast<int64_t>(h) * (R / 16) * 128 + r) * 8;
+#pragma unroll 2
       for (int q = 0; q < R / 2; q += 32) {
         uint32_t o[32];
         tc::ld_32x32b_x32(o_col + q, o);
@@ -807,7 +919,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 448 : 320, 1)
         if (r < sg.vecs) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + q + e),
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             dst + (q + e) * 128),
                          "r"(o[e]), "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]),
                          "r"(o[e + 5]), "r"(o[e + 6]), "r"(o[e + 7])
                          : "memory");
@@ -816,6 +929,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 448 : 320, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
+    }
+  };
+
+  // With an fp8 cache's 512 threads the softmax warps take registers of the
+  // others (128 x 168 + 384 x 112 < 512 x 128).
+  if (warp < 4) {
+    if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    if (rank == 0)
+      softmax();
+    else
+      output();
+  } else {
+    if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    if (warp < 8) {
+      if (rank == 0)
+        load_q();
+      else
+        output();
+    } else if (warp == 8 || warp >= (FP8 ? 14 : 10)) {
+      produce();
+    } else if (warp == 9) {
+      if (rank == 0)
+        scores();
+      else
+        values();
+    } else if (FP8) {
+      convert();
     }
   }
   if (!ok && lane == 0) gave_up(p.err_count);
@@ -830,111 +970,128 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 448 : 320, 1)
 }
 
 // ---------------------------------------------------------------- join
-// One warp for each vector: the segments of its sequence's part and of its
-// group's, weighted by their maxima.  Lane j finds segment j; the outputs of a
-// few are in flight together.
-constexpr int kJoinWarps = 8;
+// A CTA joins eight vectors of one sequence: the segments of its own part and of
+// its group's, weighted by their maxima.  Thread = vector (lane % 8) and groups of
+// eight dims, so that a warp reads pieces of 256 bytes; the segments' places,
+// maxima and sums come in first, all at once.
+constexpr int kJoin = 8;          // vectors
 constexpr int kInFlight = 4;
 
 template <int R>
-__global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const SharedParams p) {
-  constexpr int NV = R / 128;  // float4 groups a lane
+__global__ void __launch_bounds__(256) shared_join_kernel(const SharedParams p) {
+  constexpr int NV = R / 256;  // groups of 8 dims a thread
+  extern __shared__ int sm[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int H = p.num_heads, per = p.rows_per_seq * H, ctas = cdiv(per, kJoin);
+  const int seq = static_cast<int>(blockIdx.x) / ctas;
+  const int vec0 = (static_cast<int>(blockIdx.x) - seq * ctas) * kJoin;  // of the sequence
+  int* rec = sm;                                        // [items][8] slot * 128 + vector, or -1
+  float* m = reinterpret_cast<float*>(sm + p.most_items * kJoin);  // maxima, then weights
+  float* l = m + p.most_items * kJoin;
+  __shared__ float inverse[kJoin];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t vec = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  const int H = p.num_heads;
-  if (vec >= static_cast<int64_t>(p.num_rows) * H) return;
-  const int row = static_cast<int>(vec / H);
-  const int C = p.header[0];
-  SharedPart part[2];
-  part[0] = p.parts[p.num_groups + row / p.rows_per_seq];
-  const bool two = part[0].group >= 0;
-  part[1] = p.parts[two ? part[0].group : 0];
-  int block[2], at[2], items[2], span[2];  // slots to look at: chunks x pairs a chunk can meet
+  const SharedRow at = p.rows[seq];
+  const SharedPlace part[2] = {at.own, at.group};
+  const int C = at.per_pair;
+  int items[2], span[2];  // slots to look at: chunks x pairs that a chunk can meet
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int v = static_cast<int>(vec - static_cast<int64_t>(part[i].row0) * H);
-    block[i] = v >> 7;
-    at[i] = v & 127;
-    const bool any = part[i].blocks > 0 && (i == 0 || two);
-    span[i] = part[i].blocks == 1 ? cdiv(part[i].tiles, C) + 1 : 2;
-    items[i] = any ? cdiv(part[i].tiles, chunk_tiles(part[i], C)) * span[i] : 0;
+    span[i] = cdiv(part[i].chunk, C) + 1;
+    items[i] = part[i].blocks == 0 ? 0 : cdiv(part[i].tiles, part[i].chunk) * span[i];
   }
   const int n = items[0] + items[1];
-  // record (slot * 128 + vector) of item i, or -1
-  auto record = [&](int i) -> int64_t {
-    if (i >= n) return -1;
-    const int w = i >= items[0];
-    const SharedPart& x = w ? part[1] : part[0];
-    const int k = w ? i - items[0] : i, sp = w ? span[1] : span[0];
-    const int g = w ? block[1] : block[0], ch = chunk_tiles(x, C);
-    const int j = k / sp, len = min(ch, x.tiles - j * ch);
-    const int first = x.tile0 + j * ch * x.blocks + g * len;
-    const int c = first / C + (k - j * sp);
-    if (static_cast<int64_t>(c) * C >= first + len) return -1;
-    return static_cast<int64_t>(x.unit0 + j * x.blocks + g + c) * 128 + (w ? at[1] : at[0]);
-  };
-  int64_t rec = record(lane);
-  float2 ml = rec >= 0 ? p.ml[rec] : make_float2(-INFINITY, 0.f);
-  float M = ml.x;
-  for (int i = lane + 32; i < n; i += 32) {
-    const int64_t x = record(i);
-    if (x >= 0) M = fmaxf(M, p.ml[x].x);
+  for (int i = threadIdx.x; i < n * kJoin; i += 256) {
+    const int v = i & (kJoin - 1), item = i / kJoin;
+    const int w = item >= items[0];
+    const SharedPlace& x = w ? part[1] : part[0];
+    const int k = w ? item - items[0] : item, sp = w ? span[1] : span[0];
+    const int j = k / sp, len = min(x.chunk, x.tiles - j * x.chunk);
+    // the vector among the part's: of its sequence alone, or of the group's
+    const int u = vec0 + v + (w ? (seq * p.rows_per_seq - x.row0) * H : 0);
+    const int g = u >> 7;
+    const int tile0 = x.first + j * (x.chunk + kStart) * x.blocks + g * (len + kStart) + kStart;
+    const int c = tile0 / C + (k - j * sp);
+    int r = -1;
+    if (vec0 + v < per && static_cast<int64_t>(c) * C < tile0 + len)
+      r = (x.unit0 + j * x.blocks + g + c) * 128 + (u & 127);
+    const float2 ml = r >= 0 ? p.ml[r] : make_float2(-INFINITY, 0.f);
+    rec[i] = r;
+    m[i] = ml.x;
+    l[i] = ml.y;
   }
+  __syncthreads();
+  {  // warp v: the weights of vector v
+    const int v = warp;
+    float M = -INFINITY, den = 0.f;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, m[i * kJoin + v]);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  float4 acc[NV];
-#pragma unroll
-  for (int k = 0; k < NV; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    if (i0 > 0) {
-      rec = record(i0 + lane);
-      ml = rec >= 0 ? p.ml[rec] : make_float2(-INFINITY, 0.f);
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    for (int i = lane; i < n; i += 32) {
+      const int a = i * kJoin + v;
+      const float w = rec[a] >= 0 ? ex2(m[a] - M) : 0.f;
+      den += w * l[a];
+      m[a] = w;
     }
-    const float w = rec >= 0 ? ex2(ml.x - M) : 0.f;
-    den += w * ml.y;
-    uint32_t mask = __ballot_sync(0xffffffffu, rec >= 0);
-    while (mask) {
-      int js[kInFlight];
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        js[u] = mask ? __ffs(mask) - 1 : -1;
-        mask &= mask ? mask - 1 : 0u;
-      }
-      float4 v[kInFlight][NV];
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const int64_t x = __shfl_sync(0xffffffffu, rec, js[u] < 0 ? 0 : js[u]);
-        if (js[u] < 0) continue;
-        const float4* src = reinterpret_cast<const float4*>(p.partial + x * R);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) v[u][k] = src[k * 32 + lane];
-      }
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const float wj = __shfl_sync(0xffffffffu, w, js[u] < 0 ? 0 : js[u]);
-        if (js[u] < 0) continue;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-          acc[k].x += wj * v[u][k].x;
-          acc[k].y += wj * v[u][k].y;
-          acc[k].z += wj * v[u][k].z;
-          acc[k].w += wj * v[u][k].w;
-        }
-      }
+    for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
+    if (lane == 0 && vec0 + v < per) {
+      inverse[v] = n == 0 ? 0.f : (p.kv_scale ? __ldg(p.kv_scale) : 1.f) / den;
+      p.lse[static_cast<int64_t>(seq) * per + vec0 + v] =
+          n == 0 ? -INFINITY : (M + log2f(den)) * kLn2;
     }
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
-  const float inv = n == 0 ? 0.f : (p.kv_scale ? __ldg(p.kv_scale) : 1.f) / den;
-  uint2* o = reinterpret_cast<uint2*>(p.o + vec * R);
+  __syncthreads();
+  const int v = lane & 7;
+  if (vec0 + v >= per) return;
+  float acc[NV][8];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
-    o[k * 32 + lane] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
-                                  pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
-  if (lane == 0) p.lse[vec] = n == 0 ? -INFINITY : (M + log2f(den)) * kLn2;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+  const int group = warp * 4 + (lane >> 3);
+  for (int i0 = 0; i0 < n; i0 += kInFlight) {
+    float4 x[kInFlight][NV][2];
+    float w[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      const int r = i0 + u < n ? rec[(i0 + u) * kJoin + v] : -1;
+      w[u] = 0.f;
+      if (r < 0) continue;
+      w[u] = m[(i0 + u) * kJoin + v];
+      const float* src = p.partial + static_cast<int64_t>(r >> 7) * 128 * R + (r & 127) * 8;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const float4* g = reinterpret_cast<const float4*>(src + (group + k * 32) * 1024);
+        x[u][k][0] = g[0];
+        x[u][k][1] = g[1];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      if (i0 + u >= n || rec[(i0 + u) * kJoin + v] < 0) continue;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        acc[k][0] += w[u] * x[u][k][0].x;
+        acc[k][1] += w[u] * x[u][k][0].y;
+        acc[k][2] += w[u] * x[u][k][0].z;
+        acc[k][3] += w[u] * x[u][k][0].w;
+        acc[k][4] += w[u] * x[u][k][1].x;
+        acc[k][5] += w[u] * x[u][k][1].y;
+        acc[k][6] += w[u] * x[u][k][1].z;
+        acc[k][7] += w[u] * x[u][k][1].w;
+      }
+    }
+  }
+  const float inv = inverse[v];
+  uint16_t* o = p.o + (static_cast<int64_t>(seq) * per + vec0 + v) * R;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    *reinterpret_cast<uint4*>(o + (group + k * 32) * 8) =
+        make_uint4(pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv),
+                   pack_bf16x2(acc[k][2] * inv, acc[k][3] * inv),
+                   pack_bf16x2(acc[k][4] * inv, acc[k][5] * inv),
+                   pack_bf16x2(acc[k][6] * inv, acc[k][7] * inv));
 }
 
 size_t align_up(size_t x) { return (x + 255) & ~size_t{255}; }
@@ -944,7 +1101,7 @@ cudaError_t launch_main(const SharedParams& p, const CUtensorMap& tmap, cudaStre
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e = set_smem_attr_once(decode_shared_kernel<R, FP8>, kSmem, attr_done);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(decode_shared_kernel<R, FP8>, dim3(2 * p.pairs), dim3(FP8 ? 448 : 320),
+  return launch_overlapped(decode_shared_kernel<R, FP8>, dim3(2 * p.pairs), dim3(FP8 ? 512 : 384),
                            kSmem, stream, p, tmap);
 }
 
@@ -965,16 +1122,14 @@ size_t shared_layout(int num_rows, int num_heads, int num_seqs, int num_groups, 
     at += align_up(bytes);
     return q;
   };
-  uint8_t* header = take(64 * sizeof(int));
   uint8_t* pair_segments = take(pairs * sizeof(int2));
-  uint8_t* parts = take((static_cast<size_t>(num_groups) + num_seqs) * sizeof(SharedPart));
+  uint8_t* rows = take(static_cast<size_t>(num_seqs) * sizeof(SharedRow));
   uint8_t* segments = take(slots * sizeof(SharedSegment));
   uint8_t* ml = take(slots * 128 * sizeof(float2));
   uint8_t* partial = take(slots * 128 * sizeof(float) * R);
   if (p) {
-    p->header = reinterpret_cast<int*>(header);
     p->pair_segments = reinterpret_cast<int2*>(pair_segments);
-    p->parts = reinterpret_cast<SharedPart*>(parts);
+    p->rows = reinterpret_cast<SharedRow*>(rows);
     p->segments = reinterpret_cast<SharedSegment*>(segments);
     p->ml = reinterpret_cast<float2*>(ml);
     p->partial = reinterpret_cast<float*>(partial);
@@ -982,28 +1137,38 @@ size_t shared_layout(int num_rows, int num_heads, int num_seqs, int num_groups, 
   return at;
 }
 
-cudaError_t launch_decode_shared(const SharedParams& p, const CUtensorMap& tmap, int R, bool fp8,
+cudaError_t launch_decode_shared(const SharedParams& p_in, const CUtensorMap& tmap, int R, bool fp8,
                                  cudaStream_t stream) {
+  SharedParams p = p_in;
   static std::atomic<uint64_t> attr_done{0};
-  constexpr int kMostSmem = (3 * (kMaxSharedGroups + 1) + 2 * (kMaxSharedGroups + kMaxSharedSeqs + 1)) * 4;
+  constexpr int kMostSmem =
+      (2 * (kMaxSharedGroups + 1) + 4 * (kMaxSharedGroups + kMaxSharedSeqs + 1)) * 4;
   static_assert(kMostSmem <= 226 * 1024, "the schedule's shared memory");
   cudaError_t e = set_smem_attr_once(shared_schedule_kernel, kMostSmem, attr_done);
   if (e != cudaSuccess) return e;
   const int G = p.num_groups, V = G + p.num_seqs;
-  const size_t smem = (3 * static_cast<size_t>(G + 1) + 2 * static_cast<size_t>(V + 1)) * 4;
-  e = launch_overlapped(shared_schedule_kernel, dim3(1), dim3(1024), smem, stream, p);
+  const size_t smem = (2 * static_cast<size_t>(G + 1) + 4 * static_cast<size_t>(V + 1)) * 4;
+  // as many threads as parts, or pairs: its barriers are what a short list takes
+  int threads = V > p.pairs ? V : p.pairs;
+  threads = threads > 1024 ? 1024 : (threads + 127) / 128 * 128;
+  e = launch_overlapped(shared_schedule_kernel, dim3(1), dim3(threads), smem, stream, p);
   if (e != cudaSuccess) return e;
+  // A part's chunks and the pairs that each meets: one chunk meets all pairs at
+  // most; a part of several blocks has at most pairs / blocks + 1 chunks, each the
+  // tiles of a pair long at most, and with those places before meets three at most.
+  p.most_items = 2 * (2 * p.pairs + 4);
   if (R == 512)
     e = fp8 ? launch_main<512, true>(p, tmap, stream) : launch_main<512, false>(p, tmap, stream);
   else
     e = fp8 ? launch_main<256, true>(p, tmap, stream) : launch_main<256, false>(p, tmap, stream);
   if (e != cudaSuccess) return e;
-  const int64_t vecs = static_cast<int64_t>(p.num_rows) * p.num_heads;
-  const dim3 grid(static_cast<unsigned>((vecs + kJoinWarps - 1) / kJoinWarps));
-  return R == 512 ? launch_overlapped(shared_join_kernel<512>, grid, dim3(kJoinWarps * 32), 0,
-                                      stream, p)
-                  : launch_overlapped(shared_join_kernel<256>, grid, dim3(kJoinWarps * 32), 0,
-                                      stream, p);
+  const int64_t per = static_cast<int64_t>(p.rows_per_seq) * p.num_heads;
+  const int64_t ctas = (per + kJoin - 1) / kJoin * p.num_seqs;
+  const size_t join = static_cast<size_t>(p.most_items) * kJoin * 12;
+  const dim3 grid(static_cast<unsigned>(ctas));
+  return R == 512
+             ? launch_overlapped(shared_join_kernel<512>, grid, dim3(256), join, stream, p)
+             : launch_overlapped(shared_join_kernel<256>, grid, dim3(256), join, stream, p);
 }
 
 }  // namespace mla

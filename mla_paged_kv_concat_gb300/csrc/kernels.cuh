@@ -162,15 +162,17 @@ cudaError_t launch_lse_merge(const void* o_parts, int64_t o_part_stride, const f
                              void* o, float* lse, cudaStream_t stream);
 
 // ---------------------------------------------------------------- shared prefixes
-constexpr int kMaxSharedSeqs = 16384, kMaxSharedGroups = 4096;
+constexpr int kMaxSharedSeqs = 8192, kMaxSharedGroups = 1024;
 
-// A group's shared tokens or a sequence's other ones, [tok0, tok1) through row
-// `table` of the block table, for `vecs` query vectors from row0 on; its place
-// in the list of tiles and units.
-struct SharedPart {
-  int tile0, tiles, blocks, unit0, row0, vecs, tok0, tok1, table;
-  int group;  // of a sequence that takes part in its group's pass, else -1
-  int pad0, pad1;
+// A part of the work, a group's shared tokens or a sequence's other ones, in the
+// list of tiles and units: blocks of 128 query vectors from row0 on.
+struct SharedPlace {
+  int first, tiles, blocks, chunk, unit0, row0;  // chunk: tiles of one
+};
+// What the join needs for the rows of a sequence (group.blocks 0: no shared part).
+struct SharedRow {
+  SharedPlace own, group;
+  int per_pair, pad;  // places of a pair of CTAs
 };
 // What one pair of CTAs does of a unit.
 struct SharedSegment {
@@ -199,13 +201,13 @@ struct SharedParams {
   float* lse;
   int* err_count;
   int pairs;              // of CTAs
+  int most_items;         // segments that a vector's join can look at; set by the launch
   // workspace
-  int* header;            // [0]: tiles of a pair
   int2* pair_segments;    // first segment and number of each pair
-  SharedPart* parts;      // groups, then sequences
+  SharedRow* rows;        // of each sequence
   SharedSegment* segments;
   float2* ml;             // [segment][128] maximum (log2 units) and sum
-  float* partial;         // [segment][128][R]
+  float* partial;         // [segment][R / 8][128][8]
 };
 // Bytes of the workspace; with `base` its addresses into *p.
 size_t shared_layout(int num_rows, int num_heads, int num_seqs, int num_groups, int R, int pairs,

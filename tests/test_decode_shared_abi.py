@@ -27,7 +27,7 @@ BASE = dict(q=at(1), qs=16 * 576, qh=576, qp=None, qps=0, qph=0, T=8, H=16, cach
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(G=0), 1), (dict(G=-1), 1), (dict(G=4097), 2), (dict(T=16385, B=16385), 2),
+    (dict(G=0), 1), (dict(G=-1), 1), (dict(G=1025), 2), (dict(T=8193, B=8193), 2),
     (dict(q=None), 1), (dict(cache=None), 1), (dict(bt=None), 1), (dict(lens=None), 1),
     (dict(gs=None), 1), (dict(pre=None), 1), (dict(o=None), 1), (dict(lse=None), 1),
     (dict(gs=at(5) + 2), 1), (dict(pre=at(6) + 1), 1), (dict(err=at(10) + 1), 1),
@@ -35,7 +35,7 @@ BASE = dict(q=at(1), qs=16 * 576, qh=576, qp=None, qps=0, qph=0, T=8, H=16, cach
     (dict(R=384), 2), (dict(P=32), 2), (dict(kvd=1), 1), (dict(kvd=7), 1), (dict(qs=8), 1),
     (dict(qh=568), 1), (dict(q=at(1) + 8), 1), (dict(bts=9), 1), (dict(bstride=100), 1),
     (dict(maxb=(1 << 24) + 1, bts=1 << 25), 2),                       # past 2^30 tokens
-    (dict(maxb=1 << 24, bts=1 << 24, T=16384, B=16384), 2),    # past 2^31 tiles
+    (dict(maxb=1 << 24, bts=1 << 24, T=8192, B=8192), 2),    # past 2^31 tiles
 ])
 def test_decode_shared_refusals(lib, over, code):
     a = dict(BASE)
@@ -56,7 +56,7 @@ def test_workspace_size(lib):
     assert f(64, 16, 64, 1, 256, 152) < n < f(64, 16, 64, 40, 512, 152)
     for bad in ((0, 16, 64, 1, 512, 152), (64, 0, 64, 1, 512, 152), (64, 16, 0, 1, 512, 152),
                 (64, 16, 64, 0, 512, 152), (64, 16, 64, 1, 384, 152), (64, 16, 64, 1, 512, 1),
-                (64, 16, 64, 4097, 512, 152), (20000, 1, 20000, 1, 512, 152)):
+                (64, 16, 64, 1025, 512, 152), (8193, 1, 8193, 1, 512, 152)):
         assert f(*bad) == 0
 
 
