@@ -275,3 +275,26 @@ def test_captured_and_replayed_with_other_lengths(cuda_dev):
         graph.replay()
         torch.cuda.synchronize()
         d.check(o, lse)
+
+
+@pytest.mark.parametrize("fmt,R", [("e4m3", 512), ("e5m2", 256)])
+def test_every_finite_code(cuda_dev, fmt, R):
+    """Subnormal codes and the largest ones among them; those that are not finite
+    give NaN or infinities for their sequence alone."""
+    c = Case([0, 3], [256], [300, 260, 400], 8, R=R, fmt=fmt, seed=12, scale=2.0 ** -7)
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda")
+    codes = codes[codes.view(FP8[fmt]).float().isfinite()]
+    g = torch.Generator("cuda").manual_seed(4)
+    raw = codes[torch.randint(len(codes), c.cache.shape, generator=g, device="cuda")]
+    # the largest codes alone would leave one key to every softmax
+    small = codes[codes.view(FP8[fmt]).float().abs() < 16]
+    raw[..., 8:] = small[torch.randint(len(small), raw[..., 8:].shape, generator=g, device="cuda")]
+    c.cache = raw.view(FP8[fmt])
+    c.q[..., :8] = 0
+    sm = SCALE
+    c.check(*c.run(sm=sm), sm=sm)
+    o, lse = c.run(sm=sm)
+    raw[c.table[2, 5].long(), 3, 40] = 0x7F   # a NaN in an own token of the last one
+    o2, lse2 = c.run(sm=sm)
+    assert torch.equal(o[:2], o2[:2]) and torch.equal(lse[:2], lse2[:2])
+    assert not bool(o2[2].isfinite().all())
