@@ -27,8 +27,8 @@
 //     x 128 tokens of K or 128 vectors of Q), 32 KiB of P on its way
 //   rank 1: O R TMEM columns; P 2 x 32 KiB; a ring of five 32 KiB boxes of V (256
 //     dims x 64 tokens)
-// An fp8 cache lands in staging boxes and four more warps of each CTA turn it into
-// the bf16 boxes; its values are exact in bf16, and the scale is applied to the
+// An fp8 cache lands in staging boxes and two groups of four warps of each CTA turn
+// it into the bf16 boxes (on rank 0 one of them also loads Q); its values are exact in bf16, and the scale is applied to the
 // scores and to the joined output.
 //
 // Schedule.  A first kernel (one CTA) turns lengths into a list of all tiles: the
@@ -41,8 +41,8 @@
 //
 // Roles (384 threads, 512 with an fp8 cache): rank 0 warps 0-3 softmax, thread =
 // TMEM lane = vector, 4-7 loading Q; rank 1 warps 0-7 rescaling and output of O, two
-// a lane quarter (dim halves); warp 9 MMA, warps 8, 10, 11 TMA (8, 14, 15 with an fp8
-// cache, whose conversion takes 10-13).
+// a lane quarter (dim halves); warp 9 MMA, warps 8, 10, 11 TMA.  With an fp8 cache 8,
+// 14, 15 TMA, 4-7 (besides Q) and 10-13 conversion, rank 1's output warps 0-3 alone.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
@@ -322,56 +322,34 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParam
 }
 
 // ---------------------------------------------------------------- conversion
-// 16 fp8 codes to bf16, exactly.  Sign, exponent and mantissa are moved to their
-// places, with an exponent that is too small by the difference of the biases, and
-// one product with a power of two sets it right, subnormal codes included.  Codes
-// that are not finite (E4M3's NaN, E5M2's largest exponent) take the conversion
-// instructions, which at a quarter of the rate bound the kernel when all did (3.6 us
-// a tile at R = 512).
+// A thread's part (t of 128) of an 8 KiB staging box, rows of 64 codes, to bf16
+// (exactly) in swizzled 128-byte rows: four pieces of 16 codes, two at a time.  Alone
+// on an SM two groups of four warps take 270 cycles a box, 232 of them what loading
+// 8 and storing 16 KiB takes (moving the bits with integer operations instead of the
+// conversion instructions: 330 to 530).
 template <bool E5M2>
-__device__ __forceinline__ void fp8x16(const uint4& raw, uint4& lo, uint4& hi) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t o[8];
-  constexpr uint32_t kAbove = E5M2 ? 0x04040404u : 0x01010101u;
-  uint32_t over = 0;
+__device__ __forceinline__ void convert_box(const uint8_t* src, uint8_t* dst, int t) {
+#pragma unroll 1
+  for (int at = t; at < 512; at += 256) {
+    uint4 raw[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) over |= (w[i] & 0x7F7F7F7Fu) + kAbove;
-  if (over & 0x80808080u) {
+    for (int i = 0; i < 2; ++i)
+      raw[i] = *reinterpret_cast<const uint4*>(src + (at + i * 128) * 16);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint16_t two = static_cast<uint16_t>(w[i >> 1] >> ((i & 1) * 16));
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, E5M2 ? __NV_E5M2 : __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
-      o[i] = pack_bf16x2(f.x, f.y);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint16_t two = static_cast<uint16_t>(w[e >> 1] >> ((e & 1) * 16));
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, E5M2 ? __NV_E5M2 : __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        o[e] = pack_bf16x2(f.x, f.y);
+      }
+      const int r = (at + i * 128) >> 2, c = (at & 3) * 2;
+      *reinterpret_cast<uint4*>(dst + sw128(r, c)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(dst + sw128(r, c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
     }
-  } else {
-    const __nv_bfloat162 up = __float2bfloat162_rn(E5M2 ? 0x1p112f : 0x1p120f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // the two codes in the upper bytes of the halves
-      const uint32_t h = __byte_perm(w[i >> 1], 0, i & 1 ? 0x3424 : 0x1404);
-      const uint32_t x = (h & 0x80008000u) |
-                         (E5M2 ? (h >> 3) & 0x0FE00FE0u : (h >> 4) & 0x07F007F0u);
-      const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), up);
-      o[i] = *reinterpret_cast<const uint32_t*>(&y);
-    }
-  }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
-}
-
-// A thread's part (t of 128) of `rows` x 64 dims: staging rows of 64 bytes to a
-// swizzled box of 128-byte rows.
-template <bool E5M2>
-__device__ __forceinline__ void convert_box(const uint8_t* src, uint8_t* dst, int rows, int t) {
-#pragma unroll 4
-  for (int i = t; i < rows * 4; i += 128) {
-    const uint4 x = *reinterpret_cast<const uint4*>(src + i * 16);
-    uint4 lo, hi;
-    fp8x16<E5M2>(x, lo, hi);
-    const int r = i >> 2, c = (i & 3) * 2;
-    *reinterpret_cast<uint4*>(dst + sw128(r, c)) = lo;
-    *reinterpret_cast<uint4*>(dst + sw128(r, c + 1)) = hi;
   }
 }
 
@@ -421,12 +399,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
       mbar_init(&s_free[i], 4);
       mbar_init(&p_free[i], 1);
       mbar_init(&p_full[i], 1);
-      mbar_init(&o_ready[i], 8);
+      mbar_init(&o_ready[i], FP8 ? 4 : 8);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(q_full, 4);
     mbar_init(q_free, 1);
-    mbar_init(o_free, 8);
+    mbar_init(o_free, FP8 ? 4 : 8);
     mbar_init(seg_filled, FP8 ? 4 : 3);
     fence_mbar_init();
     if (rank == 1)
@@ -508,7 +486,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
             const int blk = __shfl_sync(0xffffffffu, id, e * half + v_page);
             const int row = (tok + (e * half + v_page) * box_rows) % bs;
             for (int d = 0; d < VB; ++d, ++nb) {
-              if (nb % 3 != which) continue;
+              // (with the two groups of converting warps a staging box's fillers and
+              // readers have to be the same ones every time)
+              if (nb % (FP8 ? 2 : 3) != which) continue;
               const int st = nb % N;
               ok = warp_wait(FP8 ? &st_empty[st] : &empty[st], ((nb / N) & 1) ^ 1);
               if (!ok) break;
@@ -540,54 +520,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
       }
     }
   };
-  // -------------------------------------------------- conversion
-  auto convert = [&]() {
-    const int t = threadIdx.x - 320;
-    const bool e5m2 = p.e5m2;
+  // ---------------------------------------------------- conversion
+  // Staging box number ns to ring box number nb, by four warps (t of 128): 8 KiB,
+  // twice on rank 1, rows of 64 codes one after the other in both (two 64-dim parts
+  // of 64 rows lie as one of 128).
+  auto turn = [&](int ns, int nb, int t) -> bool {
+    const int stages = rank == 0 ? RG::S_STAGES : RG::V_STAGES;
+    const int boxes = rank == 0 ? RG::S_BOXES : RG::V_BOXES;
+    const int st = ns % (FP8 ? stages : 1), bx = nb % boxes;
+    if (!warp_wait(&st_full[st], (ns / (FP8 ? stages : 1)) & 1) ||
+        !warp_wait(&empty[bx], ((nb / boxes) & 1) ^ 1))
+      return false;
+    const uint8_t* src = smem + (rank == 0 ? RG::S_STAGE + st * 8192 : RG::V_STAGE + st * 16384);
+    uint8_t* dst = smem + (rank == 0 ? S_RING + bx * kKBox : V_RING + bx * kVBox);
+#pragma unroll 1
+    for (int c = 0; c < (rank == 0 ? 1 : 2); ++c) {
+      if (p.e5m2)
+        convert_box<true>(src + c * 8192, dst + c * 16384, t);
+      else
+        convert_box<false>(src + c * 8192, dst + c * 16384, t);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&full[bx]);
+      mbar_arrive(&st_empty[st]);
+    }
+    return true;
+  };
+  // `count` boxes from staging box ns and ring box nb on (behind Q's), every other
+  // one for each of two groups of four warps.
+  auto convert_boxes = [&](int count, int ns, int nb, int group, int t) -> bool {
+#pragma unroll 1
+    for (int i = (ns ^ group) & 1; i < count; i += 2)
+      if (!turn(ns + i, nb + i, t)) return false;
+    return true;
+  };
+  auto box_count = [&](const SharedSegment& sg) {
+    const int tokens = sg.tok1 - sg.tok0;
+    return rank == 0 ? cdiv(tokens, TT) * (NQ + 1) : cdiv(tokens, 64) * VB;
+  };
+  auto convert = [&](int group, int t) {
     int ns = 0, nb = 0;  // positions among the staging boxes and in the ring
-    // staging box -> ring box, `parts` 64-dim parts of `rows` rows each
-    auto turn = [&](int stages, int boxes, const uint8_t* src, uint8_t* dst, int parts,
-                    int rows) -> bool {
-      uint64_t *se = &st_empty[ns % stages], *bf = &full[nb % boxes];
-      if (!warp_wait(&st_full[ns % stages], (ns / stages) & 1) ||
-          !warp_wait(&empty[nb % boxes], ((nb / boxes) & 1) ^ 1))
-        return false;
-      for (int c = 0; c < parts; ++c) {
-        if (e5m2)
-          convert_box<true>(src + c * rows * 64, dst + c * rows * 128, rows, t);
-        else
-          convert_box<false>(src + c * rows * 64, dst + c * rows * 128, rows, t);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bf);
-        mbar_arrive(se);
-      }
-      ++ns;
-      ++nb;
-      return true;
-    };
-    for (int k = 0; FP8 && k < mine.y && ok; ++k) {
-      const SharedSegment sg = segment(k);
+    for (int k = 0; k < mine.y && ok; ++k) {
+      const int count = box_count(segment(k));
       if (rank == 0) {
         // the segment's Q boxes, which these warps do not follow, have been filled
         // and read: a ring barrier's parity tells no more than one use apart
         nb += NQ;
         ok = warp_wait(q_full, k & 1);
       }
-      for (int tok = sg.tok0; tok < sg.tok1 && ok; tok += TT) {
-        if (rank == 0) {
-          for (int c = 0; c <= NQ && ok; ++c)
-            ok = turn(kMostStages, RG::S_BOXES, smem + RG::S_STAGE + (ns % kMostStages) * 8192,
-                      smem + S_RING + (nb % RG::S_BOXES) * kKBox, 1, TT);
-        } else {
-          for (int e = 0; e < 2 && tok + e * 64 < sg.tok1 && ok; ++e)
-            for (int d = 0; d < VB && ok; ++d)
-              ok = turn(4, RG::V_BOXES, smem + RG::V_STAGE + (ns % 4) * 16384,
-                        smem + V_RING + (nb % RG::V_BOXES) * kVBox, 4, 64);
-        }
-      }
+      ok = ok && convert_boxes(count, ns, nb, group, t);
+      ns += count;
+      nb += count;
       if (rank == 0 && lane == 0) mbar_arrive(seg_filled);
     }
   };
@@ -615,54 +600,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
         const uint32_t dS = tmem + S_COL + (n & 1) * TT;
         ok = warp_wait(&s_free[n & 1], ((n >> 1) & 1) ^ 1);
         if (!ok) break;
-        // Three boxes for each wait, vote and issuing block: those cost about as
-        // much as the four instructions of a box (one box at a time a tile took
-        // 2.1 us to issue, 1.4 us of products).
-#pragma unroll
-        for (int c0 = 0; c0 <= NQ; c0 += 3) {
-          constexpr int kAll = NQ + 1;
-          const int cnt = kAll - c0 < 3 ? kAll - c0 : 3;
-          int b[3];
-          uint32_t ph[3];
-          bool r = true;
-#pragma unroll
-          for (int i = 0; i < cnt; ++i) {
-            b[i] = bx;
-            ph[i] = phase;
-            skip(1);
-            r = mbar_try_wait(&full[b[i]], ph[i]) && r;
-          }
+        // Two boxes for each wait, vote and issuing block: those cost about as much as
+        // the four instructions of a box.  The latent parts' loop is not unrolled
+        // (the roles' code shares the instruction caches).
+#pragma unroll 1
+        for (int c = 0; c < NQ && ok; c += 2) {
+          const int b0 = bx;
+          const uint32_t ph0 = phase;
+          skip(1);
+          const int b1 = bx;
+          const uint32_t ph1 = phase;
+          skip(1);
+          bool r = mbar_try_wait(&full[b0], ph0);
+          r = mbar_try_wait(&full[b1], ph1) && r;
           if (!__all_sync(0xffffffffu, r)) {
-            r = true;
-#pragma unroll
-            for (int i = 0; i < cnt; ++i) r = r && mbar_wait(&full[b[i]], ph[i]);
+            r = mbar_wait(&full[b0], ph0) && mbar_wait(&full[b1], ph1);
             ok = __all_sync(0xffffffffu, r);
           }
           if (!ok) break;
           tc::fence_after_sync();
           if (tc::elect_one()) {
+            const uint64_t d0 = ring + static_cast<uint64_t>(b0 * (kKBox >> 4));
+            const uint64_t d1 = ring + static_cast<uint64_t>(b1 * (kKBox >> 4));
 #pragma unroll
-            for (int i = 0; i < cnt; ++i) {
-              const int c = c0 + i;
-              const uint64_t db = ring + static_cast<uint64_t>(b[i] * (kKBox >> 4));
+            for (int s = 0; s < 4; ++s)
+              tc::mma_ts(dS, tmem + c * 32 + s * 8, d0 + static_cast<uint64_t>(s * 2), idesc,
+                         (c > 0 || s > 0) ? 1u : 0u);
+            tc::commit(&empty[b0]);
 #pragma unroll
-              for (int s = 0; s < 4; ++s) {
-                if (c < NQ)
-                  tc::mma_ts(dS, tmem + c * 32 + s * 8, db + static_cast<uint64_t>(s * 2), idesc,
-                             (c > 0 || s > 0) ? 1u : 0u);
-                else  // the rope part
-                  tc::mma_ss(dS, dq + static_cast<uint64_t>(s * 2),
-                             db + static_cast<uint64_t>(s * 2), idesc, 1u);
-              }
-              tc::commit(&empty[b[i]]);
-            }
-            if (c0 + cnt == kAll) {
-              tc::commit(&s_full[n & 1]);
-              if (t + 1 == tiles) tc::commit(q_free);
-            }
+            for (int s = 0; s < 4; ++s)
+              tc::mma_ts(dS, tmem + c * 32 + 32 + s * 8, d1 + static_cast<uint64_t>(s * 2), idesc, 1u);
+            tc::commit(&empty[b1]);
           }
           __syncwarp();
         }
+        if (!ok) break;
+        const int b0 = bx;
+        ok = warp_wait(&full[b0], phase);
+        skip(1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {  // the rope part
+          const uint64_t d0 = ring + static_cast<uint64_t>(b0 * (kKBox >> 4));
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            tc::mma_ss(dS, dq + static_cast<uint64_t>(s * 2), d0 + static_cast<uint64_t>(s * 2), idesc,
+                       1u);
+          tc::commit(&empty[b0]);
+          tc::commit(&s_full[n & 1]);
+          if (t + 1 == tiles) tc::commit(q_free);
+        }
+        __syncwarp();
       }
     }
     // nothing of this CTA's still runs on the tensor core when TMEM is freed
@@ -734,7 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
     // 8.7 us), and go on into TMEM; the rope dims stay in shared memory.
     const int tq = threadIdx.x - 128, r = tq;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int nb = 0;
+    int nb = 0, ns = 0;  // positions in the ring and among the staging boxes
     for (int k = 0; k < mine.y && ok; ++k) {
       const SharedSegment sg = segment(k);
       const int tiles = cdiv(sg.tok1 - sg.tok0, TT);
@@ -815,7 +803,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
       if (tq < NQ) mbar_arrive(&empty[(nb + tq) % RG::S_BOXES]);
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      nb += NQ + tiles * (NQ + 1);
+      nb += NQ;
+      if (FP8) {  // these warps have time for half of the conversion
+        ok = convert_boxes(tiles * (NQ + 1), ns, nb, 1, tq);
+        ns += tiles * (NQ + 1);
+      }
+      nb += tiles * (NQ + 1);
     }
   };
   // ----------------------------------------------------- softmax
@@ -918,7 +911,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
   };
   // ------------------------------------------------- O of rank 1
   auto output = [&]() {
-    const int quad = warp & 3, h = warp >> 2;  // lane quarter, half of the dims
+    // two warps a lane quarter, each with half of the dims; one with an fp8 cache
+    constexpr int kDims = FP8 ? R : R / 2;
+    const int quad = warp & 3, h = warp >> 2;
     const int r = quad * 32 + lane;
     const uint32_t o_col = tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * (R / 2);
     const float* factors = reinterpret_cast<const float*>(smem + OFF_MISC);
@@ -937,7 +932,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
           if (!ok) break;
           tc::fence_after_sync();
 #pragma unroll 1
-          for (int q = 0; q < R / 2; q += 32) {
+          for (int q = 0; q < kDims; q += 32) {
             uint32_t o[32];
             tc::ld_32x32b_x32(o_col + q, o);
             tc::wait_ld();
@@ -963,7 +958,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
       float* dst = p.partial + static_cast<int64_t>(mine.x + k) * 128 * R +
                    (static_cast<int64_t>(h) * (R / 16) * 128 + r) * 8;
 #pragma unroll 2
-      for (int q = 0; q < R / 2; q += 32) {
+      for (int q = 0; q < kDims; q += 32) {
         uint32_t o[32];
         tc::ld_32x32b_x32(o_col + q, o);
         tc::wait_ld();
@@ -997,6 +992,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
     if (warp < 8) {
       if (rank == 0)
         load_q();
+      else if (FP8)
+        convert(1, threadIdx.x - 128);
       else
         output();
     } else if (warp == 8 || warp >= (FP8 ? 14 : 10)) {
@@ -1007,7 +1004,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
       else
         values();
     } else if (FP8) {
-      convert();
+      convert(0, threadIdx.x - 320);
     }
   }
   if (!ok && lane == 0) gave_up(p.err_count);
