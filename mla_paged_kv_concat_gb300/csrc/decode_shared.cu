@@ -31,7 +31,7 @@
 // it into the bf16 boxes (on rank 0 one of them also loads Q); its values are exact in bf16, and the scale is applied to the
 // scores and to the joined output.
 //
-// Schedule.  A first kernel (one CTA) turns lengths into a list of all tiles: the
+// Schedule.  A first kernel (one CTA) turns the lengths into a list of all tiles: the
 // groups' prefixes, then the sequences, each cut into blocks of 128 vectors.  Blocks
 // of one prefix are listed in chunks side by side, so that pairs at work together
 // read the same rows.  A unit (chunk of a block) has kStart places in the list
@@ -126,72 +126,72 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity
 }
 
 // ---------------------------------------------------------------- schedule
-// Inclusive scan of a[0, n) by the block; values are not negative.
-template <typename Op>
-__device__ void block_scan(int* a, int n, int* tot, Op op) {
+// Sum over the CTA, and inclusive sums of a[0, n) in place; `tot`: 32 shared values.
+__device__ __forceinline__ int cta_sum(int v, int64_t* tot) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) tot[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) v += static_cast<int>(tot[w]);
+  return v;
+}
+__device__ __forceinline__ void cta_scan(int64_t* a, int n, int64_t* tot) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int carry = 0;
+  int64_t carry = 0;
   for (int base = 0; base < n; base += blockDim.x) {
     const int i = base + threadIdx.x;
-    int v = i < n ? a[i] : 0;
+    int64_t v = i < n ? a[i] : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v = op(v, t);
+      const int64_t t = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += t;
     }
+    __syncthreads();
     if (lane == 31) tot[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-      int w = lane < static_cast<int>(blockDim.x >> 5) ? tot[lane] : 0;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, w, d);
-        if (lane >= d) w = op(w, t);
-      }
-      tot[lane] = w;
+    int64_t all = 0;
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
+      if (w == warp) v += all;
+      all += tot[w];
     }
-    __syncthreads();
-    if (warp > 0) v = op(v, tot[warp - 1]);
-    v = op(v, carry);
-    if (i < n) a[i] = v;
-    carry = op(carry, tot[31]);
-    __syncthreads();
-  }
-}
-
-constexpr int kStart = 2;
-
-__global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParams p) {
-  extern __shared__ int sm[];
-  const int G = p.num_groups, B = p.num_seqs, V = G + B;
-  int* ends = sm;             // [G + 1] first sequence of each group
-  int* lead = ends + G + 1;   // [G] the sequence whose table its shared part is read through
-  int* tok0 = lead + G;       // [V] a part's tokens: groups, then sequences
-  int* tok1 = tok0 + V;
-  int* pre = tok1 + V;        // [V + 1] tiles before a part
-  int* unit = pre + V + 1;    // [V + 1] units before a part
-  __shared__ int tot[32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int per = p.rows_per_seq * p.num_heads;  // vectors of a sequence
-
-  for (int g = threadIdx.x; g <= G; g += blockDim.x)
-    ends[g] = clampi(__ldg(p.group_seqs + g), 0, B);
-  for (int g = threadIdx.x; g < G; g += blockDim.x) {
-    const int n = __ldg(p.prefix_lens + g);
-    tok0[g] = 0;
-    tok1[g] = clampi(n, 0, p.capacity) & ~(TT - 1);
-    if ((n < 0 || n > p.capacity) && p.err_count) atomicAdd(p.err_count, 1);
-  }
-  for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    const int n = __ldg(p.seq_lens + b);
-    tok1[G + b] = clampi(n, 0, p.capacity);
-    if ((n < 0 || n > p.capacity) && p.err_count) atomicAdd(p.err_count, 1);
+    if (i < n) a[i] = v + carry;
+    carry += all;
   }
   __syncthreads();
-  if (G > 1) block_scan(ends, G + 1, tot, [](int a, int b) { return max(a, b); });
-  if (G == 1 && threadIdx.x == 0) ends[1] = max(ends[0], ends[1]);
+}
+
+// Places that a unit has in the list before its tiles.
+constexpr int kStart = 2;
+
+// The lists in shared memory (free again afterwards).
+struct Lists {
+  int64_t* before;    // [V + 1] places (low half) and units before a part: groups, then sequences
+  int *tok0, *tok1;   // [V] a part's tokens
+  int *ends, *lead;   // [G + 1] first sequence of each group; [G] the one whose table is read
+  int* group;         // [B] the group whose shared part a sequence takes part in, or -1
+};
+
+// The list; returns (tiles of a chunk, places of a pair).
+__device__ __forceinline__ int2 make_list(const SharedParams& p, const Lists& lists, int64_t* tot) {
+  const int G = p.num_groups, B = p.num_seqs, V = G + B;
+  int64_t* before = lists.before;
+  int *tok0 = lists.tok0, *tok1 = lists.tok1, *ends = lists.ends, *lead = lists.lead;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = p.rows_per_seq * p.num_heads;  // vectors of a sequence
+  // first sequences that do not decrease, whatever the caller gave
+  if (warp == 0) {
+    int carry = 0;
+    for (int base = 0; base <= G; base += 32) {
+      int v = base + lane <= G ? ends[base + lane] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) v = max(v, __shfl_up_sync(0xffffffffu, v, d));
+      v = max(v, carry);
+      if (base + lane <= G) ends[base + lane] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
   __syncthreads();
   // what the sequences of a group can share, when there are two at least
   for (int g = warp; g < G; g += static_cast<int>(blockDim.x >> 5)) {
@@ -207,16 +207,13 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParam
       count += __shfl_xor_sync(0xffffffffu, count, d);
       first = min(first, __shfl_xor_sync(0xffffffffu, first, d));
     }
+    __syncwarp();
     if (lane == 0) {
       if (count < 2) tok1[g] = 0;
       lead[g] = first;
     }
   }
   __syncthreads();
-  auto blocks_of = [&](int v) {
-    return tok1[v] <= tok0[v] ? 0 : cdiv(v < G ? (ends[v + 1] - ends[v]) * per : per, 128);
-  };
-  auto tiles_of = [&](int v) { return cdiv(tok1[v] - tok0[v], TT); };
   // the group whose shared part sequence b takes part in, or -1
   auto group_of = [&](int b) {
     int a = 0, z = G;  // the last group that starts at or before b
@@ -226,99 +223,162 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParam
     }
     return a < G && b >= ends[a] && tok1[a] > 0 && tok1[G + b] >= tok1[a] ? a : -1;
   };
-  for (int v = threadIdx.x; v < V; v += blockDim.x) {
+  auto blocks_of = [&](int v) {
+    return tok1[v] <= tok0[v] ? 0 : cdiv(v < G ? (ends[v + 1] - ends[v]) * per : per, 128);
+  };
+  auto tiles_of = [&](int v) { return cdiv(tok1[v] - tok0[v], TT); };
+  int all_tiles = 0;
+  for (int v = static_cast<int>(threadIdx.x); v < V; v += static_cast<int>(blockDim.x)) {
     if (v >= G) {
       const int g = group_of(v - G);
+      lists.group[v - G] = g;
       tok0[v] = g < 0 ? 0 : tok1[g];
     }
-    pre[v + 1] = tiles_of(v) * blocks_of(v);
+    all_tiles += tiles_of(v) * blocks_of(v);
   }
-  if (threadIdx.x == 0) pre[0] = unit[0] = 0;
-  __syncthreads();
-  block_scan(pre + 1, V, tot, [](int a, int b) { return a + b; });
-  // chunks of a pair's share of the tiles, then places and units
-  const int chunk = max(1, cdiv(pre[V], p.pairs));
-  auto chunk_of = [&](int blocks, int tiles) {
-    return blocks == 1 || tiles < chunk ? tiles : chunk;
-  };
-  __syncthreads();
-  for (int v = threadIdx.x; v < V; v += blockDim.x) {
+  const int tiles = cta_sum(all_tiles, tot);  // at most 2^30
+  // Chunks of a pair's share, which with its start is the share itself where that
+  // comes out (found in a few steps: larger chunks are fewer starts).
+  auto chunk_of = [&](int blocks, int t, int chunk) { return blocks == 1 || t < chunk ? t : chunk; };
+  const int least = max(1, cdiv(tiles, p.pairs));
+  int chunk = least, C = 1;
+  for (int step = 0; step < 3; ++step) {
+    int all_units = 0;
+    for (int v = static_cast<int>(threadIdx.x); v < V; v += static_cast<int>(blockDim.x)) {
+      const int n = blocks_of(v), t = tiles_of(v);
+      if (n > 0) all_units += n * cdiv(t, chunk_of(n, t, chunk));
+    }
+    C = max(1, cdiv(tiles + kStart * cta_sum(all_units, tot), p.pairs));
+    const int next = max(least, C - kStart);
+    if (next <= chunk || step == 2) break;
+    chunk = next;
+  }
+  C = max(C, chunk + kStart);
+  for (int v = static_cast<int>(threadIdx.x); v < V; v += static_cast<int>(blockDim.x)) {
     const int n = blocks_of(v), t = tiles_of(v);
-    const int units = n == 0 ? 0 : n * cdiv(t, chunk_of(n, t));
-    unit[v + 1] = units;
-    pre[v + 1] = t * n + kStart * units;
+    const int64_t units = n == 0 ? 0 : n * cdiv(t, chunk_of(n, t, chunk));
+    before[v + 1] = units << 32 | static_cast<int64_t>(t * n + kStart * units);
   }
+  if (threadIdx.x == 0) before[0] = 0;
   __syncthreads();
-  block_scan(unit + 1, V, tot, [](int a, int b) { return a + b; });
-  block_scan(pre + 1, V, tot, [](int a, int b) { return a + b; });
-  const int total = pre[V];
-  const int C = max(1, cdiv(total, p.pairs));
+  cta_scan(before + 1, V, tot);
+  return make_int2(chunk, C);
+}
+
+// Segments of pair c: walks its places of the list.
+__device__ __forceinline__ void walk(const SharedParams& p, const Lists& l, int chunk, int C, int c) {
+  const int G = p.num_groups, V = G + p.num_seqs;
+  const int per = p.rows_per_seq * p.num_heads;
+  auto places = [&](int v) { return static_cast<int>(l.before[v] & 0xFFFFFFFF); };
+  const int total = places(V);
+  const int64_t lo64 = static_cast<int64_t>(c) * C;
+  const int lo = lo64 < total ? static_cast<int>(lo64) : total;
+  const int hi = total - lo > C ? lo + C : total;
+  int a = 0, z = V - 1;  // the last part that starts at or before lo
+  while (a < z) {
+    const int m = (a + z + 1) >> 1;
+    if (places(m) <= lo) a = m; else z = m - 1;
+  }
+  int2 mine = make_int2(0, 0);
+  int t = lo;
+  for (int v = a; t < hi; ++v) {
+    const int end = places(v + 1);
+    if (end <= t) continue;
+    const int start = places(v), unit0 = static_cast<int>(l.before[v] >> 32);
+    const int vecs = v < G ? (l.ends[v + 1] - l.ends[v]) * per : per, blocks = cdiv(vecs, 128);
+    const int tiles = cdiv(l.tok1[v] - l.tok0[v], TT);
+    const int ch = blocks == 1 || tiles < chunk ? tiles : chunk;
+    const int whole = (ch + kStart) * blocks;  // places of a whole chunk
+    while (t < hi && t < end) {
+      const int in = t - start;
+      const int j = in / whole;
+      const int len = min(ch, tiles - j * ch);
+      const int y = in - j * whole;
+      const int g = y / (len + kStart), k = y - g * (len + kStart);  // place of the unit
+      const int n = min(len + kStart - k, hi - t);
+      const int k0 = max(k - kStart, 0), k1 = k + n - kStart;  // its tiles here
+      if (k1 > k0) {
+        SharedSegment s;
+        s.table = v < G ? l.lead[v] : v - G;
+        s.row0 = (v < G ? l.ends[v] : v - G) * p.rows_per_seq;
+        s.vec0 = g * 128;
+        s.vecs = min(128, vecs - g * 128);
+        s.tok0 = l.tok0[v] + (j * ch + k0) * TT;
+        s.tok1 = min(l.tok1[v], s.tok0 + (k1 - k0) * TT);
+        s.pad0 = s.pad1 = 0;
+        const int slot = unit0 + j * blocks + g + c;
+        p.segments[slot] = s;
+        if (mine.y == 0) mine.x = slot;
+        ++mine.y;
+      }
+      t += n;
+    }
+  }
+  p.pair_segments[c] = mine;
+}
+
+// What the join needs for sequence b.
+__device__ __forceinline__ void fill_row(const SharedParams& p, const Lists& l, int chunk, int C,
+                                         int b) {
+  const int G = p.num_groups, per = p.rows_per_seq * p.num_heads;
   auto place = [&](int v) {
     SharedPlace x;
-    x.first = pre[v];
-    x.tiles = tiles_of(v);
-    x.blocks = blocks_of(v);
-    x.chunk = x.blocks == 0 ? 1 : chunk_of(x.blocks, x.tiles);
-    x.unit0 = unit[v];
-    x.row0 = (v < G ? ends[v] : v - G) * p.rows_per_seq;
+    x.first = static_cast<int>(l.before[v] & 0xFFFFFFFF);
+    x.tiles = cdiv(l.tok1[v] - l.tok0[v], TT);
+    x.blocks = x.tiles <= 0 ? 0 : cdiv(v < G ? (l.ends[v + 1] - l.ends[v]) * per : per, 128);
+    x.chunk = x.blocks == 0 ? 1 : x.blocks == 1 || x.tiles < chunk ? x.tiles : chunk;
+    x.unit0 = static_cast<int>(l.before[v] >> 32);
+    x.row0 = (v < G ? l.ends[v] : v - G) * p.rows_per_seq;
     return x;
   };
+  const int g = l.group[b];
+  SharedRow x;
+  x.own = place(G + b);
+  x.group = place(g < 0 ? 0 : g);
+  if (g < 0) x.group.blocks = 0;
+  x.per_pair = C;
+  x.pad = 0;
+  p.rows[b] = x;
+}
+
+// One CTA.  (The same in every CTA of the main kernel instead saved its launch but
+// not its time: 53 us for 56, and 25 for 23 in a short step.)
+__global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParams p) {
+  extern __shared__ int64_t list_sm[];
+  const int G = p.num_groups, B = p.num_seqs, V = G + B;
+  Lists l;
+  l.before = list_sm;
+  int64_t* tot = l.before + V + 1;
+  l.tok0 = reinterpret_cast<int*>(tot + 32);
+  l.tok1 = l.tok0 + V;
+  l.ends = l.tok1 + V;
+  l.lead = l.ends + G + 1;
+  l.group = l.lead + G;
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int g = threadIdx.x; g <= G; g += blockDim.x)
+    l.ends[g] = clampi(__ldg(p.group_seqs + g), 0, B);
+  for (int g = threadIdx.x; g < G; g += blockDim.x) {
+    const int n = __ldg(p.prefix_lens + g);
+    l.tok0[g] = 0;
+    l.tok1[g] = clampi(n, 0, p.capacity) & ~(TT - 1);
+    if ((n < 0 || n > p.capacity) && p.err_count) atomicAdd(p.err_count, 1);
+  }
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    const int g = group_of(b);
-    SharedRow x;
-    x.own = place(G + b);
-    x.group = place(g < 0 ? 0 : g);
-    if (g < 0) x.group.blocks = 0;
-    x.per_pair = C;
-    x.pad = 0;
-    p.rows[b] = x;
+    const int n = __ldg(p.seq_lens + b);
+    l.tok1[G + b] = clampi(n, 0, p.capacity);
+    if ((n < 0 || n > p.capacity) && p.err_count) atomicAdd(p.err_count, 1);
   }
-  // the segments of each pair
-  for (int c = threadIdx.x; c < p.pairs; c += blockDim.x) {
-    const int64_t lo64 = static_cast<int64_t>(c) * C;
-    const int lo = lo64 < total ? static_cast<int>(lo64) : total;
-    const int hi = total - lo > C ? lo + C : total;
-    int2 mine = make_int2(0, 0);
-    if (lo < hi) {
-      int a = 0, z = V - 1;  // the last part that starts at or before lo
-      while (a < z) {
-        const int m = (a + z + 1) >> 1;
-        if (pre[m] <= lo) a = m; else z = m - 1;
-      }
-      int t = lo;
-      for (int v = a; t < hi; ++v) {
-        if (pre[v + 1] <= t) continue;
-        const SharedPlace x = place(v);
-        const int vecs = v < G ? (ends[v + 1] - ends[v]) * per : per;
-        const int full_chunk = (x.chunk + kStart) * x.blocks;  // places of a whole chunk
-        while (t < hi && t < pre[v + 1]) {
-          const int in = t - x.first;
-          const int j = in / full_chunk;
-          const int len = min(x.chunk, x.tiles - j * x.chunk);
-          const int y = in - j * full_chunk;
-          const int g = y / (len + kStart), k = y - g * (len + kStart);  // place of the unit
-          const int n = min(len + kStart - k, hi - t);
-          const int k0 = max(k - kStart, 0), k1 = k + n - kStart;  // its tiles here
-          if (k1 > k0) {
-            SharedSegment s;
-            s.table = v < G ? lead[v] : v - G;
-            s.row0 = x.row0;
-            s.vec0 = g * 128;
-            s.vecs = min(128, vecs - g * 128);
-            s.tok0 = tok0[v] + (j * x.chunk + k0) * TT;
-            s.tok1 = min(tok1[v], s.tok0 + (k1 - k0) * TT);
-            s.pad0 = s.pad1 = 0;
-            const int slot = x.unit0 + j * x.blocks + g + c;
-            p.segments[slot] = s;
-            if (mine.y == 0) mine.x = slot;
-            ++mine.y;
-          }
-          t += n;
-        }
-      }
-    }
-    p.pair_segments[c] = mine;
-  }
+  __syncthreads();
+  const int2 found = make_list(p, l, tot);
+  // the pairs' segments by the first threads, the sequences' rows by the last
+  for (int c = threadIdx.x; c < p.pairs; c += blockDim.x) walk(p, l, found.x, found.y, c);
+  for (int b = blockDim.x - 1 - threadIdx.x; b < B; b += blockDim.x)
+    fill_row(p, l, found.x, found.y, b);
+}
+
+size_t schedule_smem(int G, int V) {
+  return (static_cast<size_t>(V) + 1 + 32) * 8 + (3 * static_cast<size_t>(V) + G + 1) * 4;
 }
 
 // ---------------------------------------------------------------- conversion
@@ -1215,17 +1275,16 @@ cudaError_t launch_decode_shared(const SharedParams& p_in, const CUtensorMap& tm
                                  cudaStream_t stream) {
   SharedParams p = p_in;
   static std::atomic<uint64_t> attr_done{0};
-  constexpr int kMostSmem =
-      (2 * (kMaxSharedGroups + 1) + 4 * (kMaxSharedGroups + kMaxSharedSeqs + 1)) * 4;
-  static_assert(kMostSmem <= 226 * 1024, "the schedule's shared memory");
+  constexpr int kMostSmem = 200 * 1024;
   cudaError_t e = set_smem_attr_once(shared_schedule_kernel, kMostSmem, attr_done);
   if (e != cudaSuccess) return e;
+  static_assert((kMaxSharedGroups + kMaxSharedSeqs + 33) * 8 +
+                        (3 * (kMaxSharedGroups + kMaxSharedSeqs) + kMaxSharedGroups + 1) * 4 <=
+                    kMostSmem,
+                "the schedule's shared memory");
   const int G = p.num_groups, V = G + p.num_seqs;
-  const size_t smem = (2 * static_cast<size_t>(G + 1) + 4 * static_cast<size_t>(V + 1)) * 4;
-  // as many threads as parts, or pairs: its barriers are what a short list takes
-  int threads = V > p.pairs ? V : p.pairs;
-  threads = threads > 1024 ? 1024 : (threads + 127) / 128 * 128;
-  e = launch_overlapped(shared_schedule_kernel, dim3(1), dim3(threads), smem, stream, p);
+  e = launch_overlapped(shared_schedule_kernel, dim3(1), dim3(V <= 512 ? 256 : 1024),
+                        schedule_smem(G, V), stream, p);
   if (e != cudaSuccess) return e;
   // A part's chunks and the pairs that each meets: one chunk meets all pairs at
   // most; a part of several blocks has at most pairs / blocks + 1 chunks, each the

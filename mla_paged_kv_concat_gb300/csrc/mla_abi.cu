@@ -542,7 +542,7 @@ mla_status mla_decode_shared(const void* q, int64_t q_row_stride, int64_t q_head
   // the tiles of all blocks of 128 vectors are counted in 32 bits
   const int64_t capacity = static_cast<int64_t>(max_blocks_per_seq) * block_size;
   const int64_t blocks = static_cast<int64_t>(num_rows) * num_heads / 64 + num_seqs + num_groups;
-  if (capacity > (1 << 30) || (capacity / 128 + 1) > INT32_MAX / blocks) return MLA_ERR_UNSUPPORTED;
+  if (capacity > (1 << 30) || (capacity / 128 + 4) > INT32_MAX / 2 / blocks) return MLA_ERR_UNSUPPORTED;
   int sms = 0;
   cudaError_t e = mla::device_sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);

@@ -35,7 +35,7 @@ BASE = dict(q=at(1), qs=16 * 576, qh=576, qp=None, qps=0, qph=0, T=8, H=16, cach
     (dict(R=384), 2), (dict(P=32), 2), (dict(kvd=1), 1), (dict(kvd=7), 1), (dict(qs=8), 1),
     (dict(qh=568), 1), (dict(q=at(1) + 8), 1), (dict(bts=9), 1), (dict(bstride=100), 1),
     (dict(maxb=(1 << 24) + 1, bts=1 << 25), 2),                       # past 2^30 tokens
-    (dict(maxb=1 << 24, bts=1 << 24, T=8192, B=8192), 2),    # past 2^31 tiles
+    (dict(maxb=1 << 24, bts=1 << 24, T=8192, B=8192), 2),    # past 2^30 tiles
 ])
 def test_decode_shared_refusals(lib, over, code):
     a = dict(BASE)

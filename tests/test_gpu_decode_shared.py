@@ -298,3 +298,13 @@ def test_every_finite_code(cuda_dev, fmt, R):
     o2, lse2 = c.run(sm=sm)
     assert torch.equal(o[:2], o2[:2]) and torch.equal(lse[:2], lse2[:2])
     assert not bool(o2[2].isfinite().all())
+
+
+def test_many_sequences(cuda_dev):
+    """More parts than one warp lists by itself."""
+    lens = [(37 * i) % 500 + (300 if i % 3 else 0) for i in range(700)]
+    c = Case([0, 250, 250, 600, 640], [256, 100, 130, 384], lens, 2, seed=13, bs=128)
+    c.check(*c.run())
+    many = [128 + i % 70 for i in range(1200)]
+    c = Case([2 * i for i in range(601)], [128] * 600, many, 1, R=256, seed=14)
+    c.check(*c.run())
