@@ -826,9 +826,13 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
  *   group_seqs, cu_prefix   device int32 [num_groups + 1], non-decreasing;
  *                   values are clamped (cu_prefix counted).  num_groups 1 ..
  *                   65535.
- *   num_prefix_splits, num_kv_splits   1 .. 64 parts of a prefix's keys and of a
- *                   sequence's own, joined by a second kernel (see
- *                   mla_prefill_shared_num_kv_splits).
+ *   num_prefix_splits  1 .. 64 parts of a prefix's keys.
+ *   num_kv_splits   1 .. 64 parts of a sequence's own keys, passed over apart from
+ *                   the prefix's, one sequence at a time; or 0: together with the
+ *                   prefix's first part, by the same 256 rows, each attending to its
+ *                   sequence's (best where those are few, or the rows many).  With
+ *                   more than one part in all a second kernel joins them.  See
+ *                   mla_prefill_shared_num_kv_splits.
  *   workspace       >= mla_prefill_workspace_bytes(num_tokens, num_heads,
  *                   num_prefix_splits + num_kv_splits, v_dim).
  * Otherwise as mla_prefill.
@@ -845,7 +849,7 @@ mla_status mla_prefill_shared(
     int64_t o_head_stride, float* lse, int* err_count, void* stream);
 
 /* Parts that mla_prefill_shared should cut the prefixes' keys into (returned) and
- * the sequences' own (*num_kv_splits, may be NULL).  max_prefix_len, max_kv_len:
+ * the sequences' own (*num_kv_splits, may be NULL; 0: with the prefix).  max_prefix_len, max_kv_len:
  * the longest prefix and the longest sequence's own keys (upper bounds will do). */
 int mla_prefill_shared_num_kv_splits(int num_tokens, int num_seqs, int num_groups, int num_heads,
                                      int64_t max_prefix_len, int64_t max_kv_len, int sm_count,

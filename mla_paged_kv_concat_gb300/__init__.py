@@ -129,7 +129,8 @@ def mla_prefill_shared(*args) -> int:
 def mla_prefill_shared_num_kv_splits(num_tokens: int, num_seqs: int, num_groups: int,
                                      num_heads: int, max_prefix_len: int, max_kv_len: int,
                                      sm_count: int) -> tuple[int, int]:
-    """(parts of a prefix's keys, parts of a sequence's own keys)."""
+    """(parts of a prefix's keys, parts of a sequence's own keys or 0: those
+    together with the prefix's)."""
     import ctypes
     own = ctypes.c_int()
     pre = load().mla_prefill_shared_num_kv_splits(num_tokens, num_seqs, num_groups, num_heads,
@@ -613,11 +614,12 @@ def prefill_shared(q, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, group_seqs, c
     [groups + 1]); their rows all attend to the key rows ``cu_prefix[g]`` to
     ``cu_prefix[g + 1]`` (int32 [groups + 1]) of ``k_nope``, ``v`` and ``k_pe``,
     besides their own keys there (``cu_seqlens_k``, masked as by ``causal``).
-    ``num_kv_splits``: parts of the prefixes' keys and of the sequences' own, a
-    pair from ``mla_prefill_shared_num_kv_splits``, or the first of them.
+    ``num_kv_splits``: parts of the prefixes' keys and of the sequences' own (0:
+    those together with the prefix's), a pair from
+    ``mla_prefill_shared_num_kv_splits``, or the first of them alone.
     """
     q, q_pe = q if isinstance(q, (tuple, list)) else (q, None)
-    pre, own = num_kv_splits if isinstance(num_kv_splits, (tuple, list)) else (num_kv_splits, 1)
+    pre, own = num_kv_splits if isinstance(num_kv_splits, (tuple, list)) else (num_kv_splits, 0)
     return _bind().prefill_shared(q, q_pe, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, group_seqs,
                                   cu_prefix, sm_scale, causal, pre, own, workspace, out, lse,
                                   err_count, stream)

@@ -542,7 +542,7 @@ PyObject* prefill_call(PyObject* const* a, Py_ssize_t n, bool shared) {
       G = gs.size(0) - 1;
       CHECK(G >= 1, "group_seqs must hold a group");
       typed(cu_p, kI32, {G + 1}, "cu_prefix");
-      CHECK(pre >= 1 && pre <= 64 && splits >= 1 && splits <= 64, "1 to 64 parts of the keys");
+      CHECK(pre >= 1 && pre <= 64 && splits >= 0 && splits <= 64, "1 to 64 parts of the keys");
     }
     typed(out, kBf16, {T, H, kV}, "out");
     typed(lse, at::kFloat, {T, H}, "lse");

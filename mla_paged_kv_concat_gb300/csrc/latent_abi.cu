@@ -140,7 +140,7 @@ mla_status prefill(const void* q, int64_t q_row_stride, int64_t q_head_stride, c
                    void* stream) {
   const int parts = num_kv_splits + groups.splits;
   if (num_tokens < 0 || num_kv_tokens < 0 || num_seqs < 0 || num_heads < 1 || num_heads > 1024 ||
-      num_kv_splits < 1 || num_kv_splits > 64 || groups.num < 0 ||
+      num_kv_splits < (groups.num > 0 ? 0 : 1) || num_kv_splits > 64 || groups.num < 0 ||
       (groups.num > 0 && (groups.splits < 1 || groups.splits > 64)) || nope_dim < 1 || rope_dim < 1 || v_dim < 1 ||
       !(sm_scale >= 1e-30f && sm_scale <= 1e30f))
     return MLA_ERR_INVALID_ARG;
@@ -177,7 +177,7 @@ mla_status prefill(const void* q, int64_t q_row_stride, int64_t q_head_stride, c
   }
   // one CTA per 256-row block slot, head and split
   if ((num_tokens / 256 + static_cast<int64_t>(num_seqs)) * 2 * num_heads * num_kv_splits +
-          (num_tokens / 256 + static_cast<int64_t>(groups.num)) * 2 * num_heads * groups.splits >
+          (num_tokens / 256 + static_cast<int64_t>(groups.num) + 2) * 2 * num_heads * groups.splits >
       INT32_MAX)
     return MLA_ERR_UNSUPPORTED;
   const int64_t n_cu = (static_cast<int64_t>(num_seqs) + 1) * 4;
@@ -561,24 +561,45 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
                  workspace_bytes, o, o_row_stride, o_head_stride, lse, err_count, stream);
 }
 
-// Parts of the prefix: as many as give every SM one where its 256-row blocks leave
-// SMs idle, no part shorter than 1024 keys; of the sequences' own keys as
-// mla_prefill_num_kv_splits cuts them, where those are long.
+// Times in microseconds, as measured on GB300: 1.6 for 128 keys of a unit of 256
+// rows, 4 for its start and end, 2.3e-4 for a row and head of a part that is written
+// and joined, 5 for the join.  Own keys apart from the prefix where a block's window of
+// them would be long beside the prefix's part.
 int mla_prefill_shared_num_kv_splits(int num_tokens, int num_seqs, int num_groups, int num_heads,
                                      int64_t max_prefix_len, int64_t max_kv_len, int sm_count,
                                      int* num_kv_splits) {
-  if (num_kv_splits)
-    *num_kv_splits =
-        mla_prefill_num_kv_splits(num_tokens, num_seqs, num_heads, max_kv_len, sm_count);
-  if (num_tokens < 1 || num_groups < 1 || num_heads < 1 || max_prefix_len < 1 || sm_count < 1)
+  if (num_kv_splits) *num_kv_splits = 0;
+  if (num_tokens < 1 || num_seqs < 1 || num_groups < 1 || num_heads < 1 || max_prefix_len < 1 ||
+      sm_count < 1)
     return 1;
   const int64_t by_rows = (static_cast<int64_t>(num_tokens) + 255) / 256;
-  const int64_t blocks = num_groups > by_rows ? num_groups : by_rows;
-  int64_t s = sm_count / (blocks * num_heads);
-  const int64_t most = max_prefix_len / 1024;
-  if (s > most) s = most;
-  if (s > 64) s = 64;
-  return s < 1 ? 1 : static_cast<int>(s);
+  const int64_t units = (num_groups > by_rows ? num_groups : by_rows) * num_heads;
+  // own keys that a block of 256 rows passes over
+  const double rows = static_cast<double>(num_tokens) / num_seqs;
+  const double window = max_kv_len > 0 ? static_cast<double>(max_kv_len) *
+                                             (rows < 256 ? 256 / (rows < 1 ? 1 : rows) : 1)
+                                       : 0;
+  const double longest = max_prefix_len / 2 > 4096 ? static_cast<double>(max_prefix_len / 2) : 4096;
+  const bool apart = window > longest && (rows < 256 || units < 2 * static_cast<int64_t>(sm_count));
+  if (apart && num_kv_splits)
+    *num_kv_splits =
+        mla_prefill_num_kv_splits(num_tokens, num_seqs, num_heads, max_kv_len, sm_count);
+  const double own = apart ? 0 : window / 128 * 1.6;
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= 64 && (s == 1 || max_prefix_len / s >= 512); ++s) {
+    const double rounds = static_cast<double>((units * s + sm_count - 1) / sm_count);
+    const double part = static_cast<double>((max_prefix_len + 128LL * s - 1) / (128LL * s)) * 1.6 + 4;
+    const double cost =
+        rounds * part + (s == 1 ? rounds * own : own) +
+        (s > 1 || apart ? 5 + (s + (apart ? 1 : 0)) * static_cast<double>(num_tokens) * num_heads * 2.3e-4
+                        : 0);
+    if (s == 1 || cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 mla_status mla_prefill_shared(

@@ -87,6 +87,10 @@ constexpr float kRescale = 8.0f;  // log2 units
 // again.
 constexpr float kLarge = 65536.0f;  // log2 units
 
+// What shares a prefix: nothing; groups, whose prefixes and own keys are passed over
+// by units apart from each other (kApart) or by the same ones (kFused).
+enum { kPlain = 0, kApart = 1, kFused = 2 };
+
 struct Unit {
   int q_row;   // first query row (of all tokens); -1: no more units
   int rows;    // query rows, 1 .. 256
@@ -97,6 +101,11 @@ struct Unit {
   int lim0;    // keys the first row may attend to (lk when not causal)
   int ks, ke;  // this unit's keys [ks, ke)
   int n0, n1;  // key tiles of each query tile
+  int p_row;   // kFused: first prefix key row; k_row, lk are those of the own keys' window
+  // kFused: prefix tiles, keys of the last of them, first own tile that a mask cuts
+  __device__ __forceinline__ int np() const { return ks; }
+  __device__ __forceinline__ int rem() const { return ke; }
+  __device__ __forceinline__ int im() const { return lim0; }
   __device__ __forceinline__ int n(int t) const { return t == 0 ? n0 : n1; }
   __device__ __forceinline__ int most() const { return max(n0, n1); }
 };
@@ -131,20 +140,39 @@ struct Starts {
   bool gs_rows;            // gs holds rows
 };
 
+// Whether a mask may cut key tile j of the unit, its first key row, and its keys that
+// some row attends to (more than a tile's 128 at times).
+template <int MODE>
+__device__ __forceinline__ bool is_cut(const Unit& u, int j, bool causal) {
+  if (MODE != kFused) return j >= first_masked(u, 0, causal);
+  return j < u.np() ? j == u.np() - 1 && u.rem() < kTile : j - u.np() >= u.im();
+}
+template <int MODE>
+__device__ __forceinline__ int key_row(const Unit& u, int j) {
+  if (MODE != kFused) return u.k_row + u.ks + j * kTile;
+  return j < u.np() ? u.p_row + j * kTile : u.k_row + (j - u.np()) * kTile;
+}
+template <int MODE>
+__device__ __forceinline__ int keys_left(const Unit& u, int j) {
+  if (MODE != kFused) return u.lk - (u.ks + j * kTile);
+  if (j >= u.np()) return u.lk - (j - u.np()) * kTile;
+  return j == u.np() - 1 ? u.rem() : kTile;
+}
+
 // Unit `x` of the launch; false when it is empty.  Sequence b owns the block
 // slots from cu_q[b] / 256 + b on, at least as many as it has blocks, so
 // that a slot is found by one binary search with no sums.  Blocks run from
 // the last to the first (with a causal mask the longest come first); the
 // heads of a group share a block's turn, so that the CTAs at work together
 // read few heads' keys, from L2.
-// SHARED: the units of the prefixes come first.  There the rows of all sequences
+// kApart: the units of the prefixes come first.  There the rows of all sequences
 // of a group are one sequence's, in blocks that pass over the sequences' ends, and
 // attend to all of the group's prefix keys.
-template <bool SHARED>
+template <int MODE>
 __device__ bool unit_at(const PrefillParams& p, const Starts& at, uint32_t x, Unit& u) {
-  const bool pre = SHARED && x < p.prefix_units;
-  if (SHARED && !pre) x -= p.prefix_units;
-  const int splits = !SHARED ? p.num_splits
+  const bool pre = MODE == kApart && x < p.prefix_units;
+  if (MODE == kApart && !pre) x -= p.prefix_units;
+  const int splits = MODE == kPlain ? p.num_splits
                      : pre   ? p.prefix_splits
                              : p.num_splits - p.prefix_splits;
   const int slots = pre ? p.prefix_slots : p.slots;
@@ -157,7 +185,7 @@ __device__ bool unit_at(const PrefillParams& p, const Starts& at, uint32_t x, Un
   const int32_t* cu_k = pre ? at.gk : at.k;
   const uint32_t x1 = x / splits, x2 = x1 / p.head_group, x3 = x2 / slots;
   const int part = static_cast<int>(x - x1 * splits);
-  u.split = SHARED && !pre ? p.prefix_splits + part : part;
+  u.split = MODE == kApart && !pre ? p.prefix_splits + part : part;
   u.h = static_cast<int>(x3 * p.head_group + (x1 - x2 * p.head_group));
   const int slot = slots - 1 - static_cast<int>(x2 - x3 * slots);
   if (u.h >= p.heads) return false;
@@ -194,6 +222,94 @@ __device__ bool unit_at(const PrefillParams& p, const Starts& at, uint32_t x, Un
   };
   u.n0 = tiles(0);
   u.n1 = tiles(1);
+  return true;
+}
+
+// The sequence of [lo, hi) that query row `row` belongs to.
+__device__ __forceinline__ int seq_of(const int32_t* cu_q, int lo, int hi, int row) {
+  int a = lo, z = hi - 1;
+  while (a < z) {
+    const int m = (a + z + 1) >> 1;
+    if (cu_q[m] <= row) a = m; else z = m - 1;
+  }
+  return a;
+}
+
+// Own keys [lo, hi) of row `row`, of sequence b, counted from key row `first`.
+__device__ __forceinline__ int2 own_keys(const PrefillParams& p, const int32_t* cu_q,
+                                         const int32_t* cu_k, int b, int row, int first) {
+  const int q0 = cu_q[b], k0 = clampi(cu_k[b], 0, p.num_kv), k1 = clampi(cu_k[b + 1], k0, p.num_kv);
+  const int lk = k1 - k0;
+  const int n = p.causal ? min(lk, row - q0 + lk - (cu_q[b + 1] - q0) + 1) : lk;
+  return make_int2(max(k0 - first, 0), max(k0 - first, 0) + max(n, 0));
+}
+
+// kFused: 256 rows of a group in the order they lie in, over the sequences' ends.
+// They attend to the group's prefix, whose parts are the splits', and, in the first
+// split, to the window of own keys from their first sequence's first key to their
+// last row's last one, each row to its own.  Sequences of no group are two more
+// groups without a prefix, before the first and behind the last one.
+template <>
+__device__ bool unit_at<kFused>(const PrefillParams& p, const Starts& at, uint32_t x, Unit& u) {
+  const int G = p.num_groups;
+  auto first_seq = [&](int m) -> int {
+    return m == 0 ? 0 : m > G + 1 ? p.num_seqs : clampi(__ldg(p.group_seqs + m - 1), 0, p.num_seqs);
+  };
+  auto first_row = [&](int m) -> int {
+    return m > 0 && m <= G + 1 && at.gs_rows ? at.gs[m - 1] : at.q[first_seq(m)];
+  };
+  const uint32_t x1 = x / p.num_splits, x2 = x1 / p.head_group, x3 = x2 / p.slots;
+  u.split = static_cast<int>(x - x1 * p.num_splits);
+  u.h = static_cast<int>(x3 * p.head_group + (x1 - x2 * p.head_group));
+  const int slot = p.slots - 1 - static_cast<int>(x2 - x3 * p.slots);
+  if (u.h >= p.heads) return false;
+  int a = 0, z = G + 1;
+  while (a < z) {
+    const int m = (a + z + 1) >> 1;
+    if (clampi(first_row(m), 0, p.num_tokens) / kUnitRows + m <= slot) a = m; else z = m - 1;
+  }
+  const int q0 = first_row(a), q1 = first_row(a + 1);
+  const int qa = clampi(q0, 0, p.num_tokens), qz = clampi(q1, qa, p.num_tokens);
+  const bool prefix = a >= 1 && a <= G;
+  const int k0 = prefix ? at.gk[a - 1] : 0, k1 = prefix ? at.gk[a] : 0;
+  const int ka = clampi(k0, 0, p.num_kv), kz = clampi(k1, ka, p.num_kv);
+  const int blk = slot - (qa / kUnitRows + a);
+  if (blk == 0 && u.h == 0 && u.split == 0 && p.err_count &&
+      (qa != q0 || qz != q1 || ka != k0 || kz != k1))
+    atomicAdd(p.err_count, 1);
+  const int r0 = blk * kUnitRows;
+  if (blk < 0 || r0 >= qz - qa) return false;
+  u.q_row = qa + r0;
+  u.rows = min(kUnitRows, qz - qa - r0);
+  const int lp = kz - ka;
+  const int per = ((lp + p.num_splits - 1) / p.num_splits + kTile - 1) / kTile * kTile;
+  const int64_t ks = static_cast<int64_t>(u.split) * per;
+  const int part = ks < lp ? min(per, lp - static_cast<int>(ks)) : 0;
+  u.p_row = ka + (part ? static_cast<int>(ks) : 0);
+  u.ks = (part + kTile - 1) / kTile;                 // np
+  u.ke = part ? part - (u.ks - 1) * kTile : kTile;   // rem
+  u.k_row = u.lk = u.lim0 = 0;
+  int own[2] = {0, 0};
+  if (u.split == 0) {
+    const int s0 = first_seq(a), s1 = max(first_seq(a + 1), s0 + 1);
+    const int b0 = seq_of(at.q, s0, s1, u.q_row);
+    u.k_row = clampi(at.k[b0], 0, p.num_kv);
+    int last = b0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (u.rows <= t * kTile) break;
+      const int row = u.q_row + min(u.rows, (t + 1) * kTile) - 1;
+      last = seq_of(at.q, last, s1, row);
+      const int2 keys = own_keys(p, at.q, at.k, last, row, u.k_row);
+      own[t] = max(keys.x, keys.y);
+      u.lk = max(u.lk, own[t]);
+    }
+    // of one sequence all rows attend to what the first one does
+    if (last == b0)
+      u.lim0 = own_keys(p, at.q, at.k, b0, u.q_row, u.k_row).y / kTile;
+  }
+  u.n0 = u.np() + (own[0] + kTile - 1) / kTile;
+  u.n1 = u.rows > kTile ? u.np() + (own[1] + kTile - 1) / kTile : 0;
   return true;
 }
 
@@ -261,7 +377,7 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <bool SHARED>
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const PrefillParams p, const __grid_constant__ PrefillMaps maps) {
   extern __shared__ uint8_t smem_raw[];
@@ -357,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         at.q = cu;
         at.k = cu + kCuCached;
       }
-      if (SHARED && p.num_groups < kCuCached) {
+      if (MODE != kPlain && p.num_groups < kCuCached) {
         for (int b = lane; b <= p.num_groups; b += 32) {
           cu[2 * kCuCached + b] = __ldg(p.cu_q + clampi(__ldg(p.group_seqs + b), 0, p.num_seqs));
           cu[3 * kCuCached + b] = __ldg(p.cu_prefix + b);
@@ -392,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(dst + 2 * kBox, &maps.q_pe, &q_full[t], 0, u.h, row);
         };
         auto load_k = [&](const Unit& u, int j) {
-          const int row = u.k_row + u.ks + j * kTile;
+          const int row = key_row<MODE>(u, j);
           for (int c = 0; c < 3; ++c) {
             const int b = slot();
             if (!ok) return;
@@ -402,9 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         auto load_v = [&](const Unit& u, int j) {
-          const int row = u.k_row + u.ks + j * kTile;
+          const int row = key_row<MODE>(u, j);
           uint64_t* cut_bar = nullptr;
-          if (j >= first_masked(u, 0, p.causal)) cut_bar = &cut_full[cut++ & 1];
+          if (is_cut<MODE>(u, j, p.causal)) cut_bar = &cut_full[cut++ & 1];
           for (int c = 0; c < 2; ++c) {
             const int b = slot();
             if (!ok) return;
@@ -431,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Unit u;
           if (x < 0) u.q_row = -1;
           // after a wait that gave up, the CTAs left are taken over and dropped
-          if (ok && (x < 0 || unit_at<SHARED>(p, at, static_cast<uint32_t>(x), u))) {
+          if (ok && (x < 0 || unit_at<MODE>(p, at, static_cast<uint32_t>(x), u))) {
             ok = mbar_wait(&unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
             if (ok) {
               *unit_slot(i) = u;
@@ -509,7 +625,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = for_each_unit(false, [&](const Unit& u, int) -> bool {
         const int n = u.most(), nt = u.n(t);
         if (n == 0) return true;
-        const int im = first_masked(u, 0, p.causal);
         if (nt > 0) {
           if (!warp_wait(&q_full[t], qn & 1)) return false;
           ++qn;
@@ -518,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < nt; ++j, ++pn) {
           // O (+)= P V of key tile j
           int b = pos + 5 * j + 3;
-          const bool cut = j >= im;
+          const bool cut = is_cut<MODE>(u, j, p.causal);
           bool r = ready(b);
           r = ready(b + 1) && r;
           if (cut) r = mbar_try_wait(&v_ok[vn & 1], (vn >> 1) & 1) && r;
@@ -550,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // key tiles that only the other query tile reads
         for (int b = pos + 5 * nt; b < pos + 5 * n; ++b) {
-          if ((b - pos) % 5 == 3 && (b - pos) / 5 >= im) ++vn;
+          if ((b - pos) % 5 == 3 && is_cut<MODE>(u, (b - pos) / 5, p.causal)) ++vn;
           if (!__all_sync(0xffffffffu, await(b))) return false;
           if (lane == 0) mbar_arrive(&empty[b % kRing]);
         }
@@ -561,11 +676,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------ value keeper
       int pos = 0, vn = 0;
       ok = for_each_unit(false, [&](const Unit& u, int i) -> bool {
-        const int n = u.most(), im = first_masked(u, 0, p.causal);
-        for (int j = im; j < n; ++j, ++vn) {
+        const int n = u.most(), im = MODE == kFused ? 0 : first_masked(u, 0, p.causal);
+        uint32_t any = 0;
+        for (int j = im; j < n; ++j) {
+          if (MODE == kFused && !is_cut<MODE>(u, j, p.causal)) continue;
           const int b = pos + 5 * j + 3;
           if (!warp_wait(&cut_full[vn & 1], (vn >> 1) & 1)) return false;
-          const int valid = u.lk - (u.ks + j * kTile);  // keys of the sequence in this tile
+          const int valid = keys_left<MODE>(u, j);  // keys of the sequence in this tile
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             const int r = q * 32 + lane;  // key of the tile
@@ -601,10 +718,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const uint32_t word = __ballot_sync(0xffffffffu, bad);
-            if (lane == 0) flags(i)[(j - im) * 4 + q] = word;
+            // kFused: that there are any; its cut tiles are more than the words
+            any |= word;
+            if (lane == 0) flags(i)[MODE == kFused ? 0 : (j - im) * 4 + q] = MODE == kFused ? any : word;
           }
           fence_proxy_async_smem();
           mbar_arrive(&v_ok[vn & 1]);
+          ++vn;
         }
         pos += 5 * n;
         return true;
@@ -625,8 +745,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = t * kTile + r;         // row of the unit
       const int n = u.n(t);
       const bool live = row < u.rows;
-      const int lim = min(u.ke, row_limit(u, row, p.causal)) - u.ks;  // keys of this unit
-      const int im = first_masked(u, t * kTile, p.causal);
+      // keys of this unit; kFused: of the window from `own.x` to `own.y`
+      const int lim = MODE == kFused ? 0 : min(u.ke, row_limit(u, row, p.causal)) - u.ks;
+      const int im = MODE == kFused ? 0 : first_masked(u, t * kTile, p.causal);
+      int2 own = make_int2(0, 0);
+      if (MODE == kFused && live && n > u.np())
+        own = own_keys(p, p.cu_q, p.cu_k, seq_of(p.cu_q, 0, p.num_seqs, u.q_row + row),
+                       u.q_row + row, u.k_row);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++sn) {
         if (!warp_wait(&s_full[t], sn & 1)) return false;
@@ -639,7 +764,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::ld_32x32b_x32(s_col + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[q * 32]));
         tc::wait_ld();
         tc::reg_fence(s);
-        if (j >= im) {
+        if (MODE == kFused) {
+          if (is_cut<MODE>(u, j, p.causal)) {
+            const bool pre = j < u.np();
+            const int base = (j - u.np()) * kTile;
+            const int from = pre ? 0 : own.x - base, to = pre ? u.rem() : own.y - base;
+#pragma unroll
+            for (int q = 0; q < 128; ++q)
+              if (q < from || q >= to) s[q] = 0xFF800000u;  // -inf
+          }
+        } else if (j >= im) {
           const int left = lim - j * kTile;
 #pragma unroll
           for (int q = 0; q < 128; ++q)
@@ -717,8 +851,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       // keys of the cut tiles with values that are not finite
       uint32_t any = 0;
-      const int um = first_masked(u, 0, p.causal), nm = u.n(t) - um;
-      if (n > 0) {
+      const int um = MODE == kFused ? 0 : first_masked(u, 0, p.causal);
+      const int nm = MODE == kFused ? 0 : u.n(t) - um;
+      if (MODE == kFused) {
+        // (its cut tiles wrote the word, if there are any)
+        const int all = u.most();
+        if (n > 0 && ((u.np() > 0 && u.rem() < kTile) || all > u.np() + u.im())) any = flags(i)[0];
+      } else if (n > 0) {
         for (int k = 0; k < nm; ++k) {
           const uint4 x = *reinterpret_cast<const uint4*>(flags(i) + k * 4);
           any |= x.x | x.y | x.z | x.w;
@@ -731,19 +870,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::ld_32x32b_x32(o_col + q, o);
           tc::wait_ld();
           tc::reg_fence(o);
-          for (int k = 0; k < nm * 4; ++k) {
-            uint32_t bits = flags(i)[k];
-            while (bits) {
-              const int key = um * kTile + k * 32 + __ffs(bits) - 1;
-              bits &= bits - 1;
-              if (key >= lim || !live) continue;
-              const uint16_t* v = p.v + (static_cast<int64_t>(u.k_row) + u.ks + key) * p.v_row_stride +
-                                  u.h * p.v_head_stride + q;
+          auto add = [&](int64_t key) {  // key row
+            const uint16_t* v = p.v + key * p.v_row_stride + u.h * p.v_head_stride + q;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const uint32_t x = __ldg(v + e);
-                if (!finite_bf16(x))
-                  o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(x << 16));
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t x = __ldg(v + e);
+              if (!finite_bf16(x))
+                o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(x << 16));
+            }
+          };
+          if (MODE == kFused) {
+            for (int j = 0; live && j < n; ++j) {
+              if (!is_cut<MODE>(u, j, p.causal)) continue;
+              const bool pre = j < u.np();
+              const int base = (j - u.np()) * kTile;
+              const int from = pre ? 0 : max(own.x - base, 0);
+              const int to = pre ? u.rem() : min(own.y - base, kTile);
+              for (int k = from; k < to; ++k) add(static_cast<int64_t>(key_row<MODE>(u, j)) + k);
+            }
+          } else {
+            for (int k = 0; k < nm * 4; ++k) {
+              uint32_t bits = flags(i)[k];
+              while (bits) {
+                const int key = um * kTile + k * 32 + __ffs(bits) - 1;
+                bits &= bits - 1;
+                if (key >= lim || !live) continue;
+                add(static_cast<int64_t>(u.k_row) + u.ks + key);
               }
             }
           }
@@ -817,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The splits of a row and head joined: M = max lse_s, o = sum e^{lse_s - M}
 // o_s / sum e^{lse_s - M}, in split order.  One warp each, four dims a lane.
 constexpr int kMergeWarps = 8;
-template <bool SHARED>
+template <bool APART>
 __global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const PrefillParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -831,7 +983,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const P
   if (row < __ldg(p.cu_q) || row >= __ldg(p.cu_q + p.num_seqs)) return;
   const int S = p.num_splits;
   int first = 0;
-  if (SHARED) {
+  if (APART) {
     // rows of no group have no parts of a prefix
     const int r0 = __ldg(p.cu_q + clampi(__ldg(p.group_seqs), 0, p.num_seqs));
     const int r1 = __ldg(p.cu_q + clampi(__ldg(p.group_seqs + p.num_groups), 0, p.num_seqs));
@@ -870,21 +1022,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const P
 
 }  // namespace
 
-template <bool SHARED>
+template <int MODE>
 static cudaError_t launch(const PrefillParams& p_in, const PrefillMaps& maps, cudaStream_t stream) {
   PrefillParams p = p_in;
   static std::atomic<uint64_t> attr_done{0};
-  cudaError_t e = set_smem_attr_once(prefill_kernel<SHARED>, kSmem, attr_done);
+  cudaError_t e = set_smem_attr_once(prefill_kernel<MODE>, kSmem, attr_done);
   if (e != cudaSuccess) return e;
-  p.slots = p.num_tokens / kUnitRows + p.num_seqs;
+  p.slots = p.num_tokens / kUnitRows + (MODE == kFused ? p.num_groups + 2 : p.num_seqs);
   // heads side by side in the order of units: as many as keep their keys and
   // values (512 bytes a key and head) in half of L2, at least eight
   const int64_t fit = (int64_t{64} << 20) / (512 * static_cast<int64_t>(p.num_kv > 0 ? p.num_kv : 1));
   p.head_group = static_cast<int>(fit < 8 ? 8 : fit > p.heads ? p.heads : fit);
   if (p.head_group > p.heads) p.head_group = p.heads;
   const int64_t heads = (p.heads + p.head_group - 1) / p.head_group * static_cast<int64_t>(p.head_group);
-  int64_t units = heads * p.slots * (p.num_splits - (SHARED ? p.prefix_splits : 0));
-  if (SHARED) {
+  int64_t units = heads * p.slots * (p.num_splits - (MODE == kApart ? p.prefix_splits : 0));
+  if (MODE == kApart) {
     p.prefix_slots = p.num_tokens / kUnitRows + p.num_groups;
     const int64_t pre = heads * p.prefix_slots * p.prefix_splits;
     units += pre;
@@ -893,16 +1045,18 @@ static cudaError_t launch(const PrefillParams& p_in, const PrefillMaps& maps, cu
   }
   if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
   const int grid = static_cast<int>(units);
-  e = launch_overlapped(prefill_kernel<SHARED>, dim3(grid), dim3(kThreads), kSmem, stream, p, maps);
+  e = launch_overlapped(prefill_kernel<MODE>, dim3(grid), dim3(kThreads), kSmem, stream, p, maps);
   if (e != cudaSuccess || p.num_splits == 1) return e;
   const int64_t records = static_cast<int64_t>(p.num_tokens) * p.heads;
-  return launch_overlapped(prefill_merge_kernel<SHARED>,
+  return launch_overlapped(prefill_merge_kernel<MODE == kApart>,
                            dim3(static_cast<unsigned>((records + kMergeWarps - 1) / kMergeWarps)),
                            dim3(kMergeWarps * 32), 0, stream, p);
 }
 
 cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream) {
-  return p.num_groups ? launch<true>(p, maps, stream) : launch<false>(p, maps, stream);
+  if (p.num_groups == 0) return launch<kPlain>(p, maps, stream);
+  return p.num_splits > p.prefix_splits ? launch<kApart>(p, maps, stream)
+                                        : launch<kFused>(p, maps, stream);
 }
 
 }  // namespace mla

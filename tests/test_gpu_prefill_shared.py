@@ -121,7 +121,8 @@ CASES = [
 
 @pytest.mark.parametrize("case", CASES, ids=range(len(CASES)))
 @pytest.mark.parametrize("causal,splits", [(True, (1, 1)), (True, (3, 2)), (False, (2, 1)),
-                                           (False, (1, 3))])
+                                           (False, (1, 3)), (True, (1, 0)), (True, (3, 0)),
+                                           (False, (1, 0)), (False, (2, 0))])
 def test_matches_64_bits(cuda_dev, case, causal, splits):
     c = Case(*case, seed=len(case[2]))
     c.check(*c.run(causal, splits), causal)
@@ -132,7 +133,7 @@ def test_many_parts_and_the_rule(cuda_dev):
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     n = mla.mla_prefill_shared_num_kv_splits(77, 5, 2, 8, 9000, 4000, sms)
     assert n[0] > 1
-    for s in (n, (64, 64), (40, 1), n[0]):
+    for s in (n, (64, 64), (40, 1), n[0], (1, 0), (7, 0)):
         c.check(*c.run(True, s))
 
 
@@ -143,24 +144,40 @@ def test_rows_of_no_sequence_and_gaps_are_left(cuda_dev):
     c.k[-50:], c.v[-50:] = NAN, NAN
     o = torch.full((c.q.shape[0], 3, 128), 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((c.q.shape[0], 3), 7.0, device="cuda")
-    for s in ((1, 1), (2, 2)):
+    for s in ((1, 1), (2, 2), (1, 0), (3, 0)):
         c.check(*c.run(True, s, out=o, lse=lse))
         assert bool((o[:7] == 7).all()) and bool((o[-50:] == 7).all())
         assert bool((lse[:7] == 7).all()) and bool((lse[-50:] == 7).all())
 
 
 @pytest.mark.parametrize("bad", [NAN, math.inf])
-def test_masked_keys_have_no_influence(cuda_dev, bad):
+@pytest.mark.parametrize("splits", [(1, 1), (1, 0), (2, 0)])
+def test_masked_keys_have_no_influence(cuda_dev, bad, splits):
     c = Case([0, 2], [130], [40, 150], [60, 400], 2)
-    o, lse = c.run()
+    o, lse = c.run(True, splits)
     # the last own key of sequence 0: only its last row attends to it
     at = c.k0 + 59
     c.v[at, :, 3] = bad
     c.k[at, :, 5] = NAN
-    o2, lse2 = c.run()
+    o2, lse2 = c.run(True, splits)
     keep = torch.arange(190, device="cuda") != 39
     assert torch.equal(o2[keep], o[keep]) and torch.equal(lse2[keep], lse[keep])
     assert not bool(o2[39, :, 3].isfinite().any())
+    # one of the prefix's last keys (its last tile is cut): every row
+    c.v[at, :, 3] = 0
+    c.k[at, :, 5] = 0
+    c.v[c.p0 + 129, 1, 7] = bad
+    o3, _ = c.run(True, splits)
+    assert not bool(o3[:, 1, 7].isfinite().any()) and bool(o3[:, 0].isfinite().all())
+
+
+def test_many_short_sequences(cuda_dev):
+    """More sequences in a block than lengths kept in shared memory."""
+    lq = [(i * 7) % 5 for i in range(300)]
+    c = Case([0, 100, 300], [300, 129], lq, [n + (i % 3) * 40 for i, n in enumerate(lq)], 2, seed=3)
+    for s in ((1, 0), (2, 0), (1, 1)):
+        c.check(*c.run(True, s))
+        c.check(*c.run(False, s), False)
 
 
 def test_equals_prefill_of_the_joined_keys(cuda_dev):
@@ -174,13 +191,13 @@ def test_equals_prefill_of_the_joined_keys(cuda_dev):
 
 def test_pair_of_q_strides_and_determinism(cuda_dev):
     c = Case([0, 2], [500], [33, 70], [40, 70], 6)
-    o, lse = c.run(True, (2, 1))
-    again = c.run(True, (2, 1))
+    o, lse = c.run(True, (2, 0))
+    again = c.run(True, (2, 0))
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
     wide = torch.zeros(103, 8, 160, dtype=torch.bfloat16, device="cuda")
     out = wide[:, 1:7, 16:144]
     pair = (c.q[..., :128].contiguous(), c.q[..., 128:])
-    got, _ = c.run(True, (2, 1), q=pair, out=out)
+    got, _ = c.run(True, (2, 0), q=pair, out=out)
     assert torch.equal(got, o)
     wide[:, 1:7, 16:144] = 0
     assert not bool(wide.any())
@@ -190,20 +207,23 @@ def test_bad_lengths_are_clamped_and_counted(cuda_dev):
     c = Case([0, 2], [100], [8, 8], [8, 8], 2)
     c.cu_p[1] = 1 << 20  # past the keys
     c.gs[1] = 99         # past the sequences
-    o, lse = mla.prefill_shared(c.q, c.k, c.v, c.k_pe, c.cu_q, c.cu_k, c.gs, c.cu_p, SCALE,
-                                err_count=c.err)
-    assert c.err.item() > 0 and bool(o.isfinite().all())
+    for s in (1, (1, 1)):
+        c.err.zero_()
+        o, lse = mla.prefill_shared(c.q, c.k, c.v, c.k_pe, c.cu_q, c.cu_k, c.gs, c.cu_p, SCALE,
+                                    num_kv_splits=s, err_count=c.err)
+        assert c.err.item() > 0 and bool(o.isfinite().all())
 
 
-def test_captured(cuda_dev):
+@pytest.mark.parametrize("splits", [(2, 1), (1, 0), (2, 0)])
+def test_captured(cuda_dev, splits):
     c = Case([0, 2], [700], [16, 16], [48, 48], 4)
     o = torch.empty(32, 4, 128, dtype=torch.bfloat16, device="cuda")
     lse = torch.empty(32, 4, device="cuda")
-    c.run(True, (2, 1), out=o, lse=lse)
+    c.run(True, splits, out=o, lse=lse)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         mla.prefill_shared(c.q, c.k, c.v, c.k_pe, c.cu_q, c.cu_k, c.gs, c.cu_p, SCALE,
-                           num_kv_splits=(2, 1), out=o, lse=lse)
+                           num_kv_splits=splits, out=o, lse=lse)
     # other lengths in the same buffers
     d = Case([0, 2], [650], [20, 12], [70, 30], 4, seed=9)
     for dst, src in ((c.q, d.q), (c.k_pe[:d.k_pe.shape[0]], d.k_pe), (c.k[:d.k.shape[0]], d.k),

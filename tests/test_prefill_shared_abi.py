@@ -34,7 +34,7 @@ BASE = dict(q=at(1), qs=H * 192, qh=192, qp=None, qps=0, qph=0, T=T, H=H, k=at(2
 @pytest.mark.parametrize("over,code", [
     (dict(gs=None), 1), (dict(cup=None), 1), (dict(G=0), 1), (dict(G=-1), 1), (dict(G=65536), 2),
     (dict(gs=at(7) + 2), 1), (dict(cup=at(8) + 1), 1), (dict(pre=0), 1), (dict(pre=65), 1),
-    (dict(own=0), 1), (dict(own=65), 1), (dict(ws=None), 1), (dict(ws=at(9) + 16), 1),
+    (dict(own=-1), 1), (dict(own=65), 1), (dict(ws=None), 1), (dict(ws=at(9) + 16), 1),
     (dict(wsb=WS - 1), 3), (dict(pre=3), 3), (dict(own=2), 3), (dict(q=None), 1), (dict(k=None), 1),
     (dict(vd=64), 2), (dict(sm=0.0), 1), (dict(cuq=None), 1), (dict(lse=None), 1),
     # outputs over the groups' arrays
@@ -53,15 +53,17 @@ def test_nothing_to_do(lib):
 
 def test_split_rule(lib):
     rule = mla.mla_prefill_shared_num_kv_splits
-    # 256-row blocks of the prefix leave SMs idle: parts of at least 1024 keys
-    assert rule(60, 3, 1, 16, 8192, 60, 152)[0] == 8
-    assert rule(60, 3, 1, 16, 65536, 60, 152)[0] == 9
-    assert rule(60, 3, 1, 16, 1000, 60, 152)[0] == 1
-    assert rule(4096, 3, 1, 16, 8192, 2000, 152)[0] == 1
+    # 256-row blocks of the prefix leave SMs idle: parts of at least 512 keys
+    pre, own = rule(60, 3, 1, 16, 8192, 60, 152)
+    assert 6 <= pre <= 9 and own == 0
+    assert rule(60, 3, 1, 16, 1000, 60, 152) == (1, 0)
+    # many rows: one part; a few rows each with long keys of their own: apart
+    assert rule(8213, 40, 1, 32, 4000, 300, 152) == (1, 0)
+    assert rule(16, 8, 1, 16, 8192, 30000, 152)[1] > 0
     for a in ((10, 2, 1, 1, 10 ** 6, 10 ** 6, 152), (0, 0, 0, 0, 0, 0, 0), (5, 5, 5, 5, 5, 5, 5)):
         pre, own = rule(*a)
-        assert 1 <= pre <= 64 and 1 <= own <= 64
-    assert lib.mla_prefill_shared_num_kv_splits(60, 3, 1, 16, 8192, 60, 152, None) == 8
+        assert 1 <= pre <= 64 and 0 <= own <= 64
+    assert lib.mla_prefill_shared_num_kv_splits(8213, 40, 1, 32, 4000, 300, 152, None) == 1
 
 
 def test_python_refusals():
