@@ -32,7 +32,10 @@ mla_status cuda_fail_text(const char* text) {
   return MLA_ERR_CUDA;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+CUresult encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base,
+                    const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                    const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle,
+                    CUtensorMapL2promotion l2) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -43,7 +46,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
   });
-  return fn;
+  if (!fn) return CUDA_ERROR_NOT_SUPPORTED;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const auto encode = [&] {
+    return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  const CUresult r = encode();
+  int dev = 0;
+  if (r != CUDA_ERROR_INVALID_CONTEXT || cudaGetDevice(&dev) != cudaSuccess ||
+      cudaSetDevice(dev) != cudaSuccess)
+    return r;
+  return encode();
 }
 
 }  // namespace mla
@@ -52,7 +66,7 @@ namespace {
 
 using mla::aligned16;
 using mla::cuda_fail;
-using mla::encode_fn;
+using mla::encode_map;
 
 bool valid_kv_dtype(mla_kv_dtype t) {
   return t == MLA_KV_BF16 || t == MLA_KV_FP8_E4M3 || t == MLA_KV_FP8_E5M2;
@@ -66,12 +80,6 @@ bool valid_kv_dtype(mla_kv_dtype t) {
 mla_status make_cache_tmap(CUtensorMap* map, const void* cache, bool fp8,
                            int D, int block_size, int num_blocks,
                            int64_t block_stride, int max_box_rows, int box_dims = 64) {
-  auto fn = encode_fn();
-  if (!fn) {
-    snprintf(g_last_cuda_error, sizeof g_last_cuda_error,
-             "cuTensorMapEncodeTiled unavailable");
-    return MLA_ERR_CUDA;
-  }
   const size_t elt = fp8 ? 1 : 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(D),
                         static_cast<cuuint64_t>(block_size),
@@ -85,14 +93,9 @@ mla_status make_cache_tmap(CUtensorMap* map, const void* cache, bool fp8,
   const CUtensorMapSwizzle swz = fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE
                                  : box_dims == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                   : CU_TENSOR_MAP_SWIZZLE_128B;
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(map,
-                  fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                  3, const_cast<void*>(cache), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = encode_map(map,
+                          fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          cache, dims, strides, box, swz);
   if (r != CUDA_SUCCESS) {
     snprintf(g_last_cuda_error, sizeof g_last_cuda_error,
              "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
@@ -107,18 +110,15 @@ mla_status make_cache_tmap(CUtensorMap* map, const void* cache, bool fp8,
 // multiple of 16; returns false when q does not qualify.
 bool make_q_tmap(CUtensorMap* map, const void* q, int D, int H, int rows,
                  int64_t q_head_stride, int64_t q_row_stride) {
-  auto fn = encode_fn();
-  if (!fn || H % 16 != 0) return false;
+  if (H % 16 != 0) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
                         static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(q_head_stride) * 2,
                            static_cast<cuuint64_t>(q_row_stride) * 2};
   cuuint32_t box[3] = {64, 16, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
-            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_128B) == CUDA_SUCCESS;
 }
 
 bool supported_latent(int R, int P) {

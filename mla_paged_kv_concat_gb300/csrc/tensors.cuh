@@ -3,7 +3,6 @@
 #pragma once
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <stdint.h>
 
 #include "abi.cuh"
@@ -14,16 +13,12 @@ namespace mla {
 // swizzled, box {64, b1, b2}.
 inline mla_status make_map(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2,
                     int64_t s1, int64_t s2, int b1, int b2) {
-  auto fn = mla::encode_fn();
-  if (!fn) return mla::cuda_fail_text("cuTensorMapEncodeTiled unavailable");
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1),
                               static_cast<cuuint64_t>(d2)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  if (fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  if (encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, dims, strides, box,
+                 CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return mla::cuda_fail_text("cuTensorMapEncodeTiled failed");
   return MLA_OK;
 }
