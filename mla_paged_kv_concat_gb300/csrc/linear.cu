@@ -111,6 +111,13 @@ __device__ __forceinline__ void load_residual(const LinearParams& p, int row, in
 }
 
 template <int N>
+__device__ __forceinline__ void load_bias(const LinearParams& p, int c, uint4 (&b)[N / 8]) {
+#pragma unroll
+  for (int q = 0; q < N / 8; ++q)
+    b[q] = p.bias ? load8(p.bias, c + 8 * q, p.n) : make_uint4(0, 0, 0, 0);
+}
+
+template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
   if constexpr (N == 32)
     tc::ld_32x32b_x32(addr, r);
@@ -130,8 +137,9 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
                                          int row0, int lane, uint8_t* boxes, int& nb,
                                          const CUtensorMap* map, Before&& before, After&& after) {
   constexpr int N = ACT ? 16 : 32;  // columns of a step
-  uint4 res[N / 8];
+  uint4 res[N / 8], bias[N / 8];
   load_residual<N>(p, row0 + lane, c0, res);
+  load_bias<N>(p, c0, bias);
   if (!before()) return false;
   tc::fence_after_sync();
 #pragma unroll 1
@@ -139,11 +147,11 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
     const int c = c0 + j;
     uint32_t r[N];
     tmem_load<N>(acc + j, r);
-    uint4 nxt[N / 8], bias[N / 8];
-    if (j + N < cols) load_residual<N>(p, row0 + lane, c + N, nxt);
-#pragma unroll
-    for (int q = 0; q < N / 8; ++q)
-      bias[q] = p.bias ? load8(p.bias, c + 8 * q, p.n) : make_uint4(0, 0, 0, 0);
+    uint4 nxt[N / 8], bias_nxt[N / 8];
+    if (j + N < cols) {
+      load_residual<N>(p, row0 + lane, c + N, nxt);
+      load_bias<N>(p, c + N, bias_nxt);
+    }
     tc::wait_ld();
     tc::reg_fence(r);
     if (j + N >= cols) {
@@ -186,6 +194,7 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
       *reinterpret_cast<uint4*>(dst + sw128(lane, (j & 63) / 8 + q)) =
           make_uint4(o[0], o[1], o[2], o[3]);
       res[q] = nxt[q];
+      bias[q] = bias_nxt[q];
     }
     if ((j & 63) == 64 - N) {
       fence_proxy_async_smem();
@@ -513,6 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
 // partial sums in TMEM and sends them, four tokens at a time, to the CTA of the
 // cluster that finishes those tokens, which adds the parts in rank order.  A
 // thread has one column of y: a warp stores 64 bytes of a token's row at once.
+constexpr int kMostSplits = 8;  // a cluster
 constexpr int kAhead = 8;  // chunks of W asked for before the kernel before has ended
 
 __device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int c0, int c1, int c2) {
@@ -521,19 +531,55 @@ __device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int c0, 
                : "memory");
 }
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Four consecutive bf16 of a row from column c, a multiple of 4, on; those past
+// `n` are zeros and are not stored.
+__device__ __forceinline__ uint2 load4(const uint16_t* row, int c, int n) {
+  if (c + 4 <= n) return *reinterpret_cast<const uint2*>(row + c);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c + e < n) w[e >> 1] |= static_cast<uint32_t>(row[c + e]) << ((e & 1) * 16);
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store4(uint16_t* row, int c, int n, uint2 v) {
+  if (c + 4 <= n) {
+    *reinterpret_cast<uint2*>(row + c) = v;
+    return;
+  }
+  const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c + e < n) row[c + e] = static_cast<uint16_t>(w[e >> 1] >> ((e & 1) * 16));
+}
+
 template <int TN>
 struct FewCfg {
   static constexpr int STAGE = A_BYTES + TN * KC * 2;
-  static constexpr int CTAS = TN >= 64 ? 1 : 2;  // an SM
-  // parts received: at most TN / 4 groups of four tokens from all ranks
-  static constexpr int RECV = 128 * 16 * (TN / 4 + 8);
-  static constexpr int STAGES = TN == 16 ? 4 : TN == 32 ? 3 : TN == 64 ? 7 : 4;
+  static constexpr int CTAS = TN == 128 ? 1 : 2;  // an SM
+  // groups of four tokens received from the other ranks, at most
+  static constexpr int groups() {
+    int most = 0;
+    for (int s = 2; s <= kMostSplits; ++s) {
+      const int g = (s - 1) * ((TN / 4 + s - 1) / s);
+      if (g > most) most = g;
+    }
+    return most;
+  }
+  static constexpr int RECV = 2048 * groups();
+  static constexpr int STAGES = TN == 16 ? 5 : TN == 64 ? 3 : 4;
   static constexpr int OFF_RECV = STAGES * STAGE;
   static constexpr int OFF_BAR = OFF_RECV + RECV;
   static constexpr int OFF_TMEM = OFF_BAR + (2 * STAGES + 2) * 8;
   static constexpr int SMEM = OFF_TMEM + 16 + 1024;
   static constexpr uint32_t COLS = TN < 32 ? 32 : TN;
-  static_assert(SMEM * CTAS <= 227 * 1024, "shared memory");
+  static_assert((SMEM + 1024) * CTAS <= 228 * 1024, "shared memory");
 };
 
 template <int TN, bool ACT>
@@ -558,11 +604,20 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
   const int quads = (nt + 3) / 4, per = (quads + S - 1) / S;
   const int q_lo = min(quads, rank * per), q_hi = min(quads, q_lo + per);
 
+  const int nk = (p.k + KC - 1) / KC;
+  const int k_lo = static_cast<int>(static_cast<int64_t>(nk) * rank / S);
+  const int k_hi = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) / S);
+  auto request = [&](int kc) {
+    const int st = (kc - k_lo) % C::STAGES;
+    uint8_t* dst = smem + st * C::STAGE;
+    mbar_arrive_expect_tx(&full[st], C::STAGE);
+    tma_load_3d(dst, &mw, &full[st], kc * KC, 0, n0);
+    tma_load_3d(dst + A_BYTES, &mx, &full[st], kc * KC, 0, t0);
+  };
+
   if (threadIdx.x == 128) {
-    tma_prefetch_desc(&mx);
     tma_prefetch_desc(&mw);
-  }
-  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&mx);
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -570,7 +625,13 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
     mbar_init(acc_full, 1);
     mbar_init(recv_full, 1);
     fence_mbar_init();
-    mbar_arrive_expect_tx(recv_full, static_cast<uint32_t>(S * (q_hi - q_lo) * 128 * 16));
+    mbar_arrive_expect_tx(recv_full, static_cast<uint32_t>((S - 1) * (q_hi - q_lo) * 2048));
+    // The first of this CTA's W comes on its way into L2 while the kernel before
+    // still runs: L2 holds what that one may write of it, so nothing stale is read.
+    for (int kc = k_lo; kc < min(k_hi, k_lo + kAhead); ++kc) tma_prefetch_l2(&mw, kc * KC, 0, n0);
+    griddep_wait();
+    // the ring is filled under the cluster's start
+    for (int kc = k_lo; kc < min(k_hi, k_lo + C::STAGES); ++kc) request(kc);
   }
   if (warp == 5) {
     tc::tmem_alloc(tmem_slot, C::COLS);
@@ -581,31 +642,23 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
   tc::cluster_sync();  // every CTA's barrier is there before parts are sent
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int nk = (p.k + KC - 1) / KC;
-  const int k_lo = static_cast<int>(static_cast<int64_t>(nk) * rank / S);
-  const int k_hi = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) / S);
   bool ok = true;
-  // The first of this CTA's W comes on its way into L2 while the kernel before
-  // still runs: L2 holds what that one may write of it, so nothing stale is read.
-  if (threadIdx.x == 128)
-    for (int kc = k_lo; kc < min(k_hi, k_lo + kAhead); ++kc) tma_prefetch_l2(&mw, kc * KC, 0, n0);
   griddep_wait();
   griddep_launch_dependents();
 
   if (warp == 4) {
     if (lane == 0) {
-      for (int kc = k_lo; kc < k_hi; ++kc) {
-        const int it = kc - k_lo, st = it % C::STAGES;
-        if (!mbar_wait(&empty[st], ((it / C::STAGES) & 1) ^ 1)) {
+      for (int kc = k_lo + C::STAGES; kc < k_hi; ++kc) {
+        const int it = kc - k_lo;
+        if (!mbar_wait(&empty[it % C::STAGES], ((it / C::STAGES) & 1) ^ 1)) {
           ok = false;
           break;
         }
-        uint8_t* dst = smem + st * C::STAGE;
-        mbar_arrive_expect_tx(&full[st], C::STAGE);
-        tma_load_3d(dst, &mw, &full[st], kc * KC, 0, n0);
-        tma_load_3d(dst + A_BYTES, &mx, &full[st], kc * KC, 0, t0);
+        request(kc);
       }
     }
+    __syncwarp();
+    cluster_arrive();
   } else if (warp == 5) {
     constexpr uint32_t idesc = tc::idesc_bf16(128, TN, 0, 0);
     for (int kc = k_lo; kc < k_hi; ++kc) {
@@ -629,13 +682,32 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
       __syncwarp();
     }
     if (ok) ok = warp_wait(acc_full, 0);  // nothing is in flight when TMEM is freed
+    cluster_arrive();
   } else {
-    const int row = warp * 32 + lane;  // TMEM lane, row of W
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    // What this warp finishes: groups of four tokens warp, warp + 4, .. of this
+    // CTA's, a lane four columns from n on.  The first residual under the wait.
+    const int n = n0 + 4 * lane;
+    uint2 res[4];
+    auto load = [&](int quad) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = quad * 4 + e;
+        res[e] = p.residual && quad < q_hi && t < nt
+                     ? load4(p.residual + (t0 + t) * p.res_stride, n, p.n)
+                     : make_uint2(0, 0);
+      }
+    };
+    load(q_lo + warp);
+    const uint2 bias = p.bias ? load4(p.bias, n, p.n) : make_uint2(0, 0);
     ok = warp_wait(acc_full, 0);
     if (ok) {
+      // Parts [warp][group][32 rows][4 tokens] in the ring's place, which nothing
+      // reads any more.  Row 4 l + j lies in slot 8 j + (l + 2 j) % 8, so that eight
+      // lanes write and read all banks.
       tc::fence_after_sync();
-      const uint32_t recv = smem_u32(smem + C::OFF_RECV);
+      uint8_t* part = smem + warp * quads * 512;
+      const int slot = 8 * (lane & 3) + (((lane >> 2) + 2 * (lane & 3)) & 7);
+      const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
 #pragma unroll 1
       for (int c = 0; c < nt; c += 16) {
         uint32_t r[16];
@@ -643,68 +715,76 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
         tc::wait_ld();
         tc::reg_fence(r);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int quad = c / 4 + q;
-          if (quad >= quads) break;
-          const int to = quad / per;
-          const uint32_t slot = static_cast<uint32_t>((rank * per + quad - to * per) * 128 + row) * 16;
-          tc::st_async_v4u(tc::map_peer(recv + slot, to), r[4 * q], r[4 * q + 1], r[4 * q + 2],
-                           r[4 * q + 3], tc::map_peer(smem_u32(recv_full), to));
-        }
+        for (int q = 0; q < 4; ++q)
+          if (c / 4 + q < quads)
+            *reinterpret_cast<uint4*>(part + (c / 4 + q) * 512 + slot * 16) =
+                make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      const int lo = min(quads, lane * per), hi = min(quads, lo + per);  // rank `lane`'s
+      if (lane < S && lane != rank && hi > lo)
+        tc::bulk_copy_to_peer(tc::map_peer(smem_u32(smem + C::OFF_RECV), lane) +
+                                  ((rank - (rank > lane)) * 4 + warp) * per * 512,
+                              part + lo * 512, (hi - lo) * 512,
+                              tc::map_peer(smem_u32(recv_full), lane));
     }
+    named_bar_sync(1, 128);  // this CTA's own parts
     if (q_hi > q_lo) {
-      const int n = n0 + row;
-      const bool mine = n < p.n;
-      const float bias = p.bias && mine ? lo_f(p.bias[n]) : 0.f;
-      // the residual of the next 16 tokens, under the wait or the last ones' work
-      float res[16];
-      auto load = [&](int quad) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int t = quad * 4 + e;
-          res[e] = p.residual && mine && t < nt && quad + e / 4 < q_hi
-                       ? lo_f(p.residual[(t0 + t) * p.res_stride + n])
-                       : 0.f;
-        }
-      };
-      load(q_lo);
       const bool got = tc::mbar_wait_cluster(recv_full, 0);
       ok = __all_sync(0xffffffffu, got) && ok;
-      if (ok && mine) {
+    }
+    cluster_arrive();
+    if (ok) {
+      const float b[4] = {lo_f(bias.x), hi_f(bias.x), lo_f(bias.y), hi_f(bias.y)};
 #pragma unroll 1
-        for (int quad = q_lo; quad < q_hi; quad += 4) {
-          float r[16];
+      for (int quad = q_lo + warp; quad < q_hi; quad += 4) {
+        uint2 r[4];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r[e] = res[e];
-          if (quad + 4 < q_hi) load(quad + 4);
+        for (int e = 0; e < 4; ++e) r[e] = res[e];
+        load(quad + 4);
+        float x[16];  // [column][token]
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (quad + q >= q_hi) break;
-            float x[4] = {bias, bias, bias, bias};
-            for (int s = 0; s < S; ++s) {
-              const float4 v = *reinterpret_cast<const float4*>(
-                  smem + C::OFF_RECV + ((s * per + quad + q - q_lo) * 128 + row) * 16);
-              x[0] += v.x;
-              x[1] += v.y;
-              x[2] += v.z;
-              x[3] += v.w;
-            }
-            if (ACT) activate(p.act, x);
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int t = (quad + q) * 4 + e;
-              if (t >= nt) break;
-              p.y[(t0 + t) * p.y_stride + n] =
-                  __bfloat16_as_ushort(__float2bfloat16_rn(p.residual ? x[e] + r[4 * q + e] : x[e]));
-            }
+          for (int e = 0; e < 4; ++e) x[4 * j + e] = b[j];
+#pragma unroll 1
+        for (int s = 0; s < S; ++s) {
+          const uint8_t* src =
+              s == rank ? smem + ((lane >> 3) * quads + quad) * 512
+                        : smem + C::OFF_RECV +
+                              (((s - (s > rank)) * 4 + (lane >> 3)) * per + quad - q_lo) * 512;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 v =
+                *reinterpret_cast<const float4*>(src + (8 * j + ((lane + 2 * j) & 7)) * 16);
+            x[4 * j] += v.x;
+            x[4 * j + 1] += v.y;
+            x[4 * j + 2] += v.z;
+            x[4 * j + 3] += v.w;
           }
+        }
+        if (ACT) activate(p.act, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = quad * 4 + e;
+          if (t >= nt) break;
+          if (p.residual) {
+            x[e] += lo_f(r[e].x);
+            x[4 + e] += hi_f(r[e].x);
+            x[8 + e] += lo_f(r[e].y);
+            x[12 + e] += hi_f(r[e].y);
+          }
+          store4(p.y + (t0 + t) * p.y_stride, n, p.n,
+                 make_uint2(pack_bf16x2(x[e], x[4 + e]), pack_bf16x2(x[8 + e], x[12 + e])));
         }
       }
     }
+    __syncwarp();
   }
   if (!ok && lane == 0) gave_up(p.err_count);
 
+  cluster_wait();  // every CTA has received its parts: this one's are sent
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 5) {
@@ -790,10 +870,15 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 }  // namespace
 
 // The kernel and tile with the least estimated time, in cycles.  A chunk of K
-// takes what its operands' way through L2 does, about 55 bytes a cycle and SM
-// (7/3 cycles for a row of 128 bytes), or its products (2.16 cycles a column of
-// 128 rows); a tile's start and end come to about 4000, once for a persistent
-// CTA and for every CTA of the kernel for few tokens.
+// takes what its operands' way into shared memory does, about 55 bytes a cycle
+// and SM (7/3 cycles for a row of 128 bytes), or its products (2.16 cycles a
+// column of 128 rows); a tile's start and end come to about 4000, once for a
+// persistent CTA and for every wave of the kernel for few tokens.  Two CTAs of an
+// SM share its rate, and clusters leave SMs out: of 152, those of 3, 4 and 8 CTAs
+// fill 138, 144 and 120 (6 as many as 3, 7 fewer than 8).  Measured (us, clusters
+// of 1, 2, 3, 4, 8): 16 x 2048 -> 5120 10.4, 7.1, 6.1, 6.8, 10.6; 64 tokens 12.5,
+// 8.6, 7.8, 8.3, 14.1; 200 x 7168 -> 1536 35.7, 21.3, 16.8, 14.8, 21.1; 1 x 8192 ->
+// 7168 33, 22, 22, 20.3, 24; 8 x 7168 -> 576 28, 15.8, 11.9, 9.7, 7.0.
 LinearPlan linear_plan(int tokens, int n, int k, int sm_count) {
   const int64_t nk = cdiv64(k, KC);
   LinearPlan best = {};
@@ -811,10 +896,16 @@ LinearPlan linear_plan(int tokens, int n, int k, int sm_count) {
   if (tokens <= 1024) {
     const int tn = tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
     const int64_t ctas = cdiv64(n, 128) * cdiv64(tokens, tn);
-    for (int s = 1; s <= 8 && s <= nk; ++s)
-      take(cdiv64(ctas * s, (tn >= 64 ? 1 : 2) * sm_count) *
-               (cdiv64(nk, s) * chunk(128 + tn, 128) + 4000),
+    const int slots = tn == 128 ? 1 : 2;
+    for (int s : {8, 4, 3, 2, 1}) {
+      if (s > nk) continue;
+      const int fit = s == 8 ? sm_count * 15 / 19 : s == 4 ? sm_count * 18 / 19
+                                                : s == 3   ? sm_count * 10 / 11
+                                                           : sm_count;
+      take(cdiv64(ctas * s, fit) * cdiv64(nk, s) * chunk(128 + tn, 128) +
+               cdiv64(ctas * s, slots * fit) * 4000,
            {kLinearFew, tn, s, tn, 128});
+    }
   }
   if (tokens > 128) {
     for (int bn = 256; bn >= 128; bn -= 64)
