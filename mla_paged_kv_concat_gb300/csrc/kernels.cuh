@@ -310,13 +310,12 @@ struct LinearParams {
   uint16_t* y;
   int64_t y_stride;
   int form, bn, splits;      // from the plan
-  int a_rows;
   int* err_count;
 };
 // How a product is cut: its kernel, the columns of a tile (few tokens: the padded
 // tokens), the CTAs that share a sum, and the rows of the boxes that the tensor
 // maps of x (`a`) and W (`b`) take.
-enum { kLinearTile = 0, kLinearPair = 1, kLinearFew = 2 };
+enum { kLinearPair = 0, kLinearFew = 1 };
 struct LinearPlan {
   int form, bn, splits, a_rows, b_rows;
 };

@@ -487,7 +487,6 @@ mla_status mla_linear(const void* x, int64_t x_row_stride, int num_tokens, int i
   p.form = plan.form;
   p.bn = plan.bn;
   p.splits = plan.splits;
-  p.a_rows = plan.a_rows;
   p.err_count = err_count;
   mla::LinearMaps m;
   mla_status st = make_map(&m.a, x, in_features, 1, num_tokens, x_row_stride, x_row_stride, 1,

@@ -2,15 +2,18 @@
 // [N][K] bf16 as a linear layer stores it, fp32 accumulation in TMEM and fp32
 // epilogue, one rounding to bf16.
 //
-// One kernel: 128 tokens x BN columns per tile, K in chunks of 64 through a TMA
-// ring (128-byte swizzle; what lies past K, N or T is filled with zeros),
-// tcgen05 M=128 N=BN K=16, two accumulators in TMEM so that one tile's epilogue
-// runs under the next one's products, one persistent CTA per SM.  Epilogue warps
-// own 32 rows each: TMEM -> registers, bias, activation and residual there, bf16
-// in a swizzled 4 KiB staging box -> TMA store, which clips the tensor's edges.
-// The residual's next 64 columns are loaded while the current ones are worked on
-// (the first before the accumulator is waited for).  Roles: warps 0-3 epilogue,
-// warp 4 TMA producer, warp 5 MMA issuer and TMEM owner.
+// Two kernels, by an estimate of their times (linear_plan): one for many tokens,
+// which the tensor core bounds, and one for few, which W's way into shared memory
+// does.  Both bring K in chunks of 64 through a TMA ring (128-byte swizzle; what
+// lies past K, N or T is filled with zeros).
+//
+// Measured on GB300, back to back (W mostly in L2) and behind a flush of L2, and
+// bounded by: 1 x 8192 -> 7168 with bias and residual 20.2 / 28.8 us (memory: 17.3
+// at 6.8 TB/s); 64 x 2048 -> 5120 with a residual 7.8 / 12.7 us (start and join 4 us, 264
+// KB a CTA at 100 B/ns; memory 3.3); 1001 x 1536 -> 6136 with bias and silu 21.7 / 25.2
+// us (two waves of tiles at 100 B/ns a SM, 3 us of the last tile's epilogue; products
+// 9.8); 8192 x 16384 -> 5120 with bias and residual 744 us, 1.85 PFLOP/s (products: 714;
+// the library's product alone takes 727 to 750).
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -30,19 +33,6 @@ constexpr int STORE_BYTES = STORE_ROWS * 128;
 // Token blocks side by side in the order of tiles: the tiles of a wave then
 // share about as many rows of x as of W, and L2 serves the others.
 constexpr int kGroup = 8;
-
-template <int BN>
-struct Cfg {
-  static constexpr int B_BYTES = BN * KC * 2;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  static constexpr int OFF_STORE = STAGES * STAGE;  // two boxes per epilogue warp
-  static constexpr int OFF_BAR = OFF_STORE + 4 * 2 * STORE_BYTES;
-  static constexpr int NBARS = 2 * STAGES + 4;
-  static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
-  static constexpr int SMEM = OFF_TMEM + 16 + 1024;
-  static_assert(SMEM <= 227 * 1024, "shared memory");
-};
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   const bool ok = mbar_wait(bar, parity);
@@ -221,146 +211,18 @@ __device__ __forceinline__ void tile_at(int64_t t, int mt, int nt, int& m, int& 
   m = g * kGroup + in % rows;
 }
 
-template <int BN, bool ACT>
-__global__ void __launch_bounds__(192, 1)
-    linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap ma,
-                  const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mc) {
-  using C = Cfg<BN>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [STAGES]
-  uint64_t* empty = full + C::STAGES;                               // [STAGES]
-  uint64_t* acc_full = empty + C::STAGES;                           // [2]
-  uint64_t* acc_empty = acc_full + 2;                               // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 128) {
-    tma_prefetch_desc(&ma);
-    tma_prefetch_desc(&mb);
-  }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
-    }
-    fence_mbar_init();
-  }
-  if (warp == 5) {
-    tc::tmem_alloc(tmem_slot, 2 * BN);
-    tc::tmem_relinquish();
-  }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
-  griddep_wait();
-  griddep_launch_dependents();
-
-  const int nk = (p.k + KC - 1) / KC;
-  const int mt = (p.tokens + TM - 1) / TM, nt = (p.n + BN - 1) / BN;
-  const int64_t total = static_cast<int64_t>(mt) * nt;
-
-  if (warp == 4) {
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        int m, n;
-        tile_at(t, mt, nt, m, n);
-        for (int kc = 0; kc < nk; ++kc, ++it) {
-          const int st = it % C::STAGES;
-          if (!mbar_wait(&empty[st], ((it / C::STAGES) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = smem + st * C::STAGE;
-          // fewer than 128 tokens: the tile's other rows hold what was there; an
-          // accumulator's row depends on its own row of A only
-          mbar_arrive_expect_tx(&full[st], p.a_rows * 128 + C::B_BYTES);
-          tma_load_3d(dst, &ma, &full[st], kc * KC, 0, m * TM);
-          tma_load_3d(dst + A_BYTES, &mb, &full[st], kc * KC, 0, n * BN);
-        }
-      }
-      if (!ok) gave_up(p.err_count);
-    }
-  } else if (warp == 5) {
-    constexpr uint32_t idesc = tc::idesc_bf16(TM, BN, 0, 0);
-    int it = 0, ta = 0;
-    bool ok = true;
-    for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x, ++ta) {
-      const int a = ta & 1;
-      if (!warp_wait(&acc_empty[a], ((ta >> 1) & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
-      tc::fence_after_sync();
-      for (int kc = 0; kc < nk; ++kc, ++it) {
-        const int st = it % C::STAGES;
-        if (!warp_wait(&full[st], (it / C::STAGES) & 1)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
-        if (tc::elect_one()) {
-          const uint32_t base = smem_u32(smem + st * C::STAGE);
-          const uint64_t da = tc::smem_desc(base, 16, 1024, tc::kLayoutSw128);
-          const uint64_t db = tc::smem_desc(base + A_BYTES, 16, 1024, tc::kLayoutSw128);
-#pragma unroll
-          for (int k = 0; k < KC / 16; ++k)
-            tc::mma_ss(tmem + a * BN, da + static_cast<uint64_t>(k * 2),
-                       db + static_cast<uint64_t>(k * 2), idesc, (kc > 0 || k > 0) ? 1u : 0u);
-          tc::commit(&empty[st]);
-          if (kc == nk - 1) tc::commit(&acc_full[a]);
-        }
-        __syncwarp();
-      }
-    }
-    if (!ok && lane == 0) gave_up(p.err_count);
-    // nothing of this CTA's still runs on the tensor core when TMEM is freed
-    for (int j = 0; ok && j < 2 && j < ta; ++j) {
-      const int u = ta - 1 - j;
-      warp_wait(&acc_full[u & 1], (u >> 1) & 1);
-    }
-  } else {
-    uint8_t* box = smem + C::OFF_STORE + warp * 2 * STORE_BYTES;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    int ta = 0, nb = 0;
-    bool ok = true;
-    for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x, ++ta) {
-      int m, n;
-      tile_at(t, mt, nt, m, n);
-      const int a = ta & 1;
-      ok = epilogue<ACT>(
-          p, tmem + lanes + a * BN, BN, n * BN, m * TM + warp * STORE_ROWS, lane, box, nb, &mc,
-          [&] { return warp_wait(&acc_full[a], (ta >> 1) & 1); },
-          [&] {
-            if (lane == 0) mbar_arrive(&acc_empty[a]);
-          });
-    }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    if (!ok && lane == 0) gave_up(p.err_count);
-  }
-
-  tc::fence_before_sync();
-  __syncthreads();
-  if (warp == 5) {
-    tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 2 * BN);
-  }
-}
-
 // ---------------------------------------------------------------- CTA pairs
-// For many tokens, which the tensor core bounds: two CTAs of a cluster share a
-// tile of 256 tokens x BN columns, each holds its 128 tokens of A and half of
-// the columns of B, and cta_group::2 products read both halves.  Rank 0 issues
-// for both; the ring's "landed" barrier is rank 0's and counts both CTAs' bytes;
-// "read" and "accumulator ready" arrive in both.  Eight epilogue warps.
+// Two CTAs of a cluster share a tile of 256 tokens x BN columns, each holds its
+// 128 tokens of A and half of the columns of B, and cta_group::2 products read both
+// halves: at BN = 256 a chunk takes 597 cycles to come in and 553 to multiply.
+// One persistent pair per two SMs, two accumulators in TMEM so that one tile's
+// epilogue runs under the next one's products.  Rank 0 issues for both; the ring's
+// "landed" barrier is rank 0's and counts both CTAs' bytes; "read" and "accumulator
+// ready" arrive in both.  Eight epilogue warps own 32 rows and half of the columns
+// each: TMEM -> registers, bias, activation and residual there, bf16 in a swizzled
+// 4 KiB staging box -> TMA store, which clips the tensor's edges.  The next columns'
+// residual and bias are loaded while the current ones are worked on (the first
+// before the accumulator is waited for).
 constexpr int kPairStages = 5;
 constexpr int kPairHalf = A_BYTES;  // A, and room for the half of B, of one stage
 constexpr int PP_STORE = kPairStages * 2 * kPairHalf;
@@ -515,13 +377,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
 }
 
 // ---------------------------------------------------------------- few tokens
-// Up to 128 tokens the weight is the work, and it has to come in at the rate of
-// memory: the operands change places (128 rows of W are A, the tokens B, padded
-// to TN), and the sum over K is split over a cluster of up to eight CTAs, so that
-// nearly every SM has its part of W under way whatever N is.  Each CTA keeps its
-// partial sums in TMEM and sends them, four tokens at a time, to the CTA of the
-// cluster that finishes those tokens, which adds the parts in rank order.  A
-// thread has one column of y: a warp stores 64 bytes of a token's row at once.
+// The weight is the work, and it has to come in at the rate of memory: the
+// operands change places (128 rows of W are A, the tokens B, padded to TN), and the
+// sum over K is split over a cluster of up to eight CTAs, so that nearly every SM
+// has its part of W under way whatever N is.  The partial sums go from TMEM, in
+// groups of four tokens, to the CTA of the cluster that finishes those tokens, which
+// adds the parts in rank order.  They are laid out in the ring's place and go as one
+// bulk copy a warp and CTA: stores to the peer one vector at a time took 2 us per 32
+// KB (64 x 2048 -> 5120: 10.3 us then, 9.3 with the copies, 7.8 with room for two
+// CTAs an SM, so that the next kernel starts under this one's end).  A lane finishes
+// four columns of four tokens and stores 8 bytes of each.
 constexpr int kMostSplits = 8;  // a cluster
 constexpr int kAhead = 8;  // chunks of W asked for before the kernel before has ended
 
@@ -794,18 +659,6 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
 }
 
 template <int BN, bool ACT>
-cudaError_t launch(const LinearParams& p, const LinearMaps& m, int sm_count, cudaStream_t stream) {
-  using C = Cfg<BN>;
-  static std::atomic<uint64_t> attr_done{0};
-  cudaError_t e = set_smem_attr_once(linear_kernel<BN, ACT>, C::SMEM, attr_done);
-  if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((p.tokens + TM - 1) / TM) * ((p.n + BN - 1) / BN);
-  const int grid = tiles < sm_count ? static_cast<int>(tiles) : sm_count;
-  return launch_overlapped(linear_kernel<BN, ACT>, dim3(grid), dim3(192), C::SMEM, stream, p, m.a,
-                           m.b, m.c);
-}
-
-template <int BN, bool ACT>
 cudaError_t launch_pair(const LinearParams& p, const LinearMaps& m, int sm_count,
                         cudaStream_t stream) {
   static std::atomic<uint64_t> attr_done{0};
@@ -851,17 +704,10 @@ cudaError_t launch_any(const LinearParams& p, const LinearMaps& m, int sm_count,
       default: return launch_few<128, ACT>(p, m, stream);
     }
   }
-  if (p.form == kLinearPair) {
-    switch (p.bn) {
-      case 256: return launch_pair<256, ACT>(p, m, sm_count, stream);
-      case 192: return launch_pair<192, ACT>(p, m, sm_count, stream);
-      default: return launch_pair<128, ACT>(p, m, sm_count, stream);
-    }
-  }
   switch (p.bn) {
-    case 256: return launch<256, ACT>(p, m, sm_count, stream);
-    case 128: return launch<128, ACT>(p, m, sm_count, stream);
-    default: return launch<64, ACT>(p, m, sm_count, stream);
+    case 256: return launch_pair<256, ACT>(p, m, sm_count, stream);
+    case 192: return launch_pair<192, ACT>(p, m, sm_count, stream);
+    default: return launch_pair<128, ACT>(p, m, sm_count, stream);
   }
 }
 
@@ -912,9 +758,6 @@ LinearPlan linear_plan(int tokens, int n, int k, int sm_count) {
       take(cdiv64(cdiv64(tokens, 256) * cdiv64(n, bn), sm_count / 2) * nk *
                    chunk(128 + bn / 2, bn) + 4000,
            {kLinearPair, bn, 1, TM, bn / 2});
-    for (int bn = 256; bn >= 64; bn /= 2)
-      take(cdiv64(cdiv64(tokens, TM) * cdiv64(n, bn), sm_count) * nk * chunk(128 + bn, bn) + 4000,
-           {kLinearTile, bn, 1, TM, bn});
   }
   return best;
 }
