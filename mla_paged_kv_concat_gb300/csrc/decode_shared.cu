@@ -937,6 +937,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
           l *= alpha;
           m = m_new;
         }
+        const float base = m == -INFINITY ? 0.f : m;  // scores of -inf alone: weights of 0
         // the P buffer's last tile has been read by rank 1's products, the last
         // copies have read what they send
         if (n >= 2) ok = warp_wait_cluster(&p_free[b], par ^ 1);
@@ -962,7 +963,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
               for (int e = 0; e < 4; ++e) {
                 const int i = i0 + j * 8 + e * 2;
                 float x0, x1;
-                unpack2(add2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack2(-m, -m)),
+                unpack2(add2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack2(-base, -base)),
                         x0, x1);
                 x0 = ex2(x0);
                 x1 = ex2(x1);

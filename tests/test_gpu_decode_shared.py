@@ -308,3 +308,30 @@ def test_many_sequences(cuda_dev):
     many = [128 + i % 70 for i in range(1200)]
     c = Case([2 * i for i in range(601)], [128] * 600, many, 1, R=256, seed=14)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e5m2"])
+def test_scores_of_minus_infinity(cuda_dev, fmt):
+    """Whole tiles of them, the first ones among them, have no weight."""
+    c = Case([0, 3], [512], [700, 900, 520], 16, fmt=fmt, seed=14)
+    c.q[..., 520] = c.q[..., 520].abs() + 0.1
+    kept = c.keys
+
+    def put(b, first, last):
+        for t in range(first, last):
+            c.cache[c.table[b, t // 64].long(), t % 64, 520] = -math.inf
+
+    put(0, 0, 128), put(0, 256, 300), put(1, 512, 700)
+    o, lse = c.run()
+    for b, n in enumerate(c.lens):
+        k = kept(b)
+        out = torch.isinf(k[:, 520])
+        k[:, 520] = torch.where(out, 0.0, k[:, 520])
+        x = c.q[b].double() @ k.t() * SCALE
+        x[:, out] = -math.inf
+        z = torch.logsumexp(x, 1)
+        ref = torch.exp(x - z[:, None]) @ k[:, :512]
+        # P and o are rounded to bf16, 2^-8 each; the sums' share is far smaller
+        bound = 2 ** -7 * 1.1 * torch.exp(x - z[:, None]) @ k[:, :512].abs() + 1e-4
+        assert bool(((o[b].double() - ref).abs() <= bound).all()), b
+        assert float((lse[b].double() - z).abs().max()) < 1e-3
