@@ -581,39 +581,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
     }
   };
   // ---------------------------------------------------- conversion
-  // Staging box number ns to ring box number nb, by four warps (t of 128): 8 KiB,
-  // twice on rank 1, rows of 64 codes one after the other in both (two 64-dim parts
-  // of 64 rows lie as one of 128).
-  auto turn = [&](int ns, int nb, int t) -> bool {
-    const int stages = rank == 0 ? RG::S_STAGES : RG::V_STAGES;
-    const int boxes = rank == 0 ? RG::S_BOXES : RG::V_BOXES;
-    const int st = ns % (FP8 ? stages : 1), bx = nb % boxes;
-    if (!warp_wait(&st_full[st], (ns / (FP8 ? stages : 1)) & 1) ||
-        !warp_wait(&empty[bx], ((nb / boxes) & 1) ^ 1))
-      return false;
-    const uint8_t* src = smem + (rank == 0 ? RG::S_STAGE + st * 8192 : RG::V_STAGE + st * 16384);
-    uint8_t* dst = smem + (rank == 0 ? S_RING + bx * kKBox : V_RING + bx * kVBox);
-#pragma unroll 1
-    for (int c = 0; c < (rank == 0 ? 1 : 2); ++c) {
-      if (p.e5m2)
-        convert_box<true>(src + c * 8192, dst + c * 16384, t);
-      else
-        convert_box<false>(src + c * 8192, dst + c * 16384, t);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&full[bx]);
-      mbar_arrive(&st_empty[st]);
-    }
-    return true;
-  };
   // `count` boxes from staging box ns and ring box nb on (behind Q's), every other
-  // one for each of two groups of four warps.
+  // one for each of two groups of four warps (t of 128): 8 KiB, twice on rank 1, rows
+  // of 64 codes one after the other in both (two 64-dim parts of 64 rows lie as one of
+  // 128).  Positions and phases are counted on: divisions by the rank's own ring sizes
+  // took 0.14 us a box.
   auto convert_boxes = [&](int count, int ns, int nb, int group, int t) -> bool {
+    const int stages = FP8 ? (rank == 0 ? RG::S_STAGES : RG::V_STAGES) : 1;
+    const int boxes = rank == 0 ? RG::S_BOXES : RG::V_BOXES;
+    const int first = (ns ^ group) & 1;
+    int st = (ns + first) % stages, bx = (nb + first) % boxes;
+    uint32_t sp = ((ns + first) / stages) & 1, bp = (((nb + first) / boxes) & 1) ^ 1;
 #pragma unroll 1
-    for (int i = (ns ^ group) & 1; i < count; i += 2)
-      if (!turn(ns + i, nb + i, t)) return false;
+    for (int i = first; i < count; i += 2) {
+      bool r = mbar_try_wait(&st_full[st], sp);
+      r = mbar_try_wait(&empty[bx], bp) && r;
+      if (!__all_sync(0xffffffffu, r)) {
+        r = mbar_wait(&st_full[st], sp) && mbar_wait(&empty[bx], bp);
+        if (!__all_sync(0xffffffffu, r)) return false;
+      }
+      const uint8_t* src = smem + (rank == 0 ? RG::S_STAGE + st * 8192 : RG::V_STAGE + st * 16384);
+      uint8_t* dst = smem + (rank == 0 ? S_RING + bx * kKBox : V_RING + bx * kVBox);
+#pragma unroll 1
+      for (int c = 0; c < (rank == 0 ? 1 : 2); ++c) {
+        if (p.e5m2)
+          convert_box<true>(src + c * 8192, dst + c * 16384, t);
+        else
+          convert_box<false>(src + c * 8192, dst + c * 16384, t);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane < 2) mbar_arrive(lane == 0 ? &full[bx] : &st_empty[st]);
+      st += 2;
+      if (st >= stages) {
+        st -= stages;
+        sp ^= 1;
+      }
+      bx += 2;
+      if (bx >= boxes) {
+        bx -= boxes;
+        bp ^= 1;
+      }
+    }
     return true;
   };
   auto box_count = [&](const SharedSegment& sg) {
