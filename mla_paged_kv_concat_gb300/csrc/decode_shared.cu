@@ -390,26 +390,20 @@ size_t schedule_smem(int G, int V) {
 template <bool E5M2>
 __device__ __forceinline__ void convert_box(const uint8_t* src, uint8_t* dst, int t) {
 #pragma unroll 1
-  for (int at = t; at < 512; at += 256) {
-    uint4 raw[2];
+  for (int at = t; at < 512; at += 128) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(src + at * 16);
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      raw[i] = *reinterpret_cast<const uint4*>(src + (at + i * 128) * 16);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      uint32_t o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint16_t two = static_cast<uint16_t>(w[e >> 1] >> ((e & 1) * 16));
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, E5M2 ? __NV_E5M2 : __NV_E4M3);
-        const float2 f = __half22float2(__half2(h));
-        o[e] = pack_bf16x2(f.x, f.y);
-      }
-      const int r = (at + i * 128) >> 2, c = (at & 3) * 2;
-      *reinterpret_cast<uint4*>(dst + sw128(r, c)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(dst + sw128(r, c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int e = 0; e < 8; ++e) {
+      const uint16_t two = static_cast<uint16_t>(w[e >> 1] >> ((e & 1) * 16));
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, E5M2 ? __NV_E5M2 : __NV_E4M3);
+      const float2 f = __half22float2(__half2(h));
+      o[e] = pack_bf16x2(f.x, f.y);
     }
+    const int r = at >> 2, c = (at & 3) * 2;
+    *reinterpret_cast<uint4*>(dst + sw128(r, c)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(dst + sw128(r, c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -629,22 +623,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
     const int tokens = sg.tok1 - sg.tok0;
     return rank == 0 ? cdiv(tokens, TT) * (NQ + 1) : cdiv(tokens, 64) * VB;
   };
-  auto convert = [&](int group, int t) {
-    int ns = 0, nb = 0;  // positions among the staging boxes and in the ring
-    for (int k = 0; k < mine.y && ok; ++k) {
-      const int count = box_count(segment(k));
-      if (rank == 0) {
-        // the segment's Q boxes, which these warps do not follow, have been filled
-        // and read: a ring barrier's parity tells no more than one use apart
-        nb += NQ;
-        ok = warp_wait(q_full, k & 1);
-      }
-      ok = ok && convert_boxes(count, ns, nb, group, t);
-      ns += count;
-      nb += count;
-      if (rank == 0 && lane == 0) mbar_arrive(seg_filled);
-    }
-  };
   // ------------------------------------------------------- Q K^T
   auto scores = [&]() {
     constexpr uint32_t idesc = tc::idesc_bf16(128, TT, 0, 0);
@@ -785,99 +763,113 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
     if (ok && n > 0) ok = warp_wait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
   };
   // ----------------------------------------------------------- Q
-  auto load_q = [&]() {
+  auto load_q = [&](int k, const SharedSegment& sg, int nb, bool ok) -> bool {
     // The latent dims come through the K ring, as boxes of 64 dims x 128 vectors
     // that are asked for together (loaded row by row straight into TMEM they took
     // 8.7 us), and go on into TMEM; the rope dims stay in shared memory.
     const int tq = threadIdx.x - 128, r = tq;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int nb = 0, ns = 0;  // positions in the ring and among the staging boxes
-    for (int k = 0; k < mine.y && ok; ++k) {
-      const SharedSegment sg = segment(k);
-      const int tiles = cdiv(sg.tok1 - sg.tok0, TT);
-      // This thread copies 16 bytes (dims 8 (tq % 8) on) of vectors tq / 8 + 16 j:
-      // their rows and heads, -1 for vectors that there are not, which become zeros.
-      int place[8];
+    // This thread copies 16 bytes (dims 8 (tq % 8) on) of vectors tq / 8 + 16 j:
+    // their rows and heads, -1 for vectors that there are not, which become zeros.
+    int place[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int v = (tq >> 3) + 16 * j;
+      const int vec = sg.vec0 + v;
+      const int row = vec / H;
+      place[j] = v < sg.vecs ? (sg.row0 + row) * 128 + (vec - row * H) : -1;
+    }
+    auto nope = [&](int j) {
+      const int64_t row = place[j] >> 7, hd = place[j] & 127;
+      return p.q + (place[j] < 0 ? 0 : row * p.q_row_stride + hd * p.q_head_stride) + (tq & 7) * 8;
+    };
+    auto rope = [&](int j) {
+      const int64_t row = place[j] >> 7, hd = place[j] & 127;
+      return p.q_pe + (place[j] < 0 ? 0 : row * p.q_pe_row_stride + hd * p.q_pe_head_stride) +
+             (tq & 7) * 8;
+    };
+    if (k > 0) {  // on their way into L2 while the last segment goes on
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int v = (tq >> 3) + 16 * j;
-        const int vec = sg.vec0 + v;
-        const int row = vec / H;
-        place[j] = v < sg.vecs ? (sg.row0 + row) * 128 + (vec - row * H) : -1;
+        if (place[j] < 0) continue;
+        if ((tq & 7) < NQ)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(nope(j) + (tq & 7) * 56));
+        if ((tq & 7) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(rope(j)));
       }
-      auto nope = [&](int j) {
-        const int64_t row = place[j] >> 7, hd = place[j] & 127;
-        return p.q + (place[j] < 0 ? 0 : row * p.q_row_stride + hd * p.q_head_stride) + (tq & 7) * 8;
-      };
-      auto rope = [&](int j) {
-        const int64_t row = place[j] >> 7, hd = place[j] & 127;
-        return p.q_pe + (place[j] < 0 ? 0 : row * p.q_pe_row_stride + hd * p.q_pe_head_stride) +
-               (tq & 7) * 8;
-      };
-      if (k > 0) {  // on their way into L2 while the last segment goes on
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (place[j] < 0) continue;
-          if ((tq & 7) < NQ)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(nope(j) + (tq & 7) * 56));
-          if ((tq & 7) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(rope(j)));
-        }
-      }
-      // the boxes before these have been filled, and those that wait for these to be
-      // free have seen them so
-      if (k > 0) ok = warp_wait(seg_filled, (k - 1) & 1);
-      for (int c = 0; c < NQ && ok; ++c) {
-        const int bx = (nb + c) % RG::S_BOXES;
-        ok = warp_wait(&empty[bx], (((nb + c) / RG::S_BOXES) & 1) ^ 1);
-        if (!ok) break;
-        const uint32_t dst = smem_u32(smem + S_RING) + bx * kKBox;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          cp_async16(dst + sw128((tq >> 3) + 16 * j, tq & 7), nope(j) + c * 64,
-                     place[j] < 0 ? 0u : 16u);
-      }
-      // the last segment's products have read their Q
-      if (ok && k > 0) ok = warp_wait(q_free, (k - 1) & 1);
-      if (ok) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          cp_async16(smem_u32(smem + S_QPE) + sw128((tq >> 3) + 16 * j, tq & 7), rope(j),
-                     place[j] < 0 ? 0u : 16u);
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      ok = named_bar_and(1, 128, ok);  // the four warps leave together
+    }
+    // the boxes before these have been filled, and those that wait for these to be
+    // free have seen them so
+    if (ok && k > 0) ok = warp_wait(seg_filled, (k - 1) & 1);
+    for (int c = 0; c < NQ && ok; ++c) {
+      const int bx = (nb + c) % RG::S_BOXES;
+      ok = warp_wait(&empty[bx], (((nb + c) / RG::S_BOXES) & 1) ^ 1);
       if (!ok) break;
-      tc::fence_after_sync();
-#pragma unroll 2
-      for (int c = 0; c < NQ; ++c) {
-        const uint8_t* src = smem + S_RING + ((nb + c) % RG::S_BOXES) * kKBox;
-        uint32_t x[32];
+      const uint32_t dst = smem_u32(smem + S_RING) + bx * kKBox;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 y = *reinterpret_cast<const uint4*>(src + sw128(r, j));
-          x[4 * j] = y.x;
-          x[4 * j + 1] = y.y;
-          x[4 * j + 2] = y.z;
-          x[4 * j + 3] = y.w;
-        }
-        tc::st_32x32b_x32(tmem + lanes + c * 32, x);
+      for (int j = 0; j < 8; ++j)
+        cp_async16(dst + sw128((tq >> 3) + 16 * j, tq & 7), nope(j) + c * 64,
+                   place[j] < 0 ? 0u : 16u);
+    }
+    // the last segment's products have read their Q
+    if (ok && k > 0) ok = warp_wait(q_free, (k - 1) & 1);
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        cp_async16(smem_u32(smem + S_QPE) + sw128((tq >> 3) + 16 * j, tq & 7), rope(j),
+                   place[j] < 0 ? 0u : 16u);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    ok = named_bar_and(1, 128, ok);  // the four warps leave together
+    if (!ok) return false;
+    tc::fence_after_sync();
+#pragma unroll 2
+    for (int c = 0; c < NQ; ++c) {
+      const uint8_t* src = smem + S_RING + ((nb + c) % RG::S_BOXES) * kKBox;
+      uint32_t x[32];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 y = *reinterpret_cast<const uint4*>(src + sw128(r, j));
+        x[4 * j] = y.x;
+        x[4 * j + 1] = y.y;
+        x[4 * j + 2] = y.z;
+        x[4 * j + 3] = y.w;
       }
-      tc::wait_st();
-      tc::fence_before_sync();
-      // the ring's barriers count these boxes as filled and read, too
-      if (FP8 ? lane < NQ : tq < NQ) mbar_arrive(&full[(nb + lane) % RG::S_BOXES]);
-      named_bar_sync(1, 128);
-      // read, before anyone is told that Q is there
-      if (tq < NQ) mbar_arrive(&empty[(nb + tq) % RG::S_BOXES]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-      nb += NQ;
-      if (FP8) {  // these warps have time for half of the conversion
-        ok = convert_boxes(tiles * (NQ + 1), ns, nb, 1, tq);
-        ns += tiles * (NQ + 1);
+      tc::st_32x32b_x32(tmem + lanes + c * 32, x);
+    }
+    tc::wait_st();
+    tc::fence_before_sync();
+    // the ring's barriers count these boxes as filled and read, too
+    if (FP8 ? lane < NQ : tq < NQ) mbar_arrive(&full[(nb + lane) % RG::S_BOXES]);
+    named_bar_sync(1, 128);
+    // read, before anyone is told that Q is there
+    if (tq < NQ) mbar_arrive(&empty[(nb + tq) % RG::S_BOXES]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
+    return true;
+  };
+  // Q (the four warps of group 1, on rank 0), and with an fp8 cache the conversion by
+  // both groups: one call of each, since copies of the code would share the
+  // instruction caches.
+  auto fill = [&](int group) {
+    const int t = threadIdx.x - (group == 1 ? 128 : 320);
+    int ns = 0, nb = 0;  // positions among the staging boxes and in the ring
+    const bool q = rank == 0 && group == 1;
+    // (a warp of these whose wait gave up still meets the others at Q's barrier)
+    for (int k = 0; k < mine.y && (ok || q); ++k) {
+      const SharedSegment sg = segment(k);
+      if (rank == 0) {
+        // group 0 does not follow the segment's Q boxes, and waits until they have been
+        // filled and read: a ring barrier's parity tells no more than one use apart
+        ok = q ? load_q(k, sg, nb, ok) : warp_wait(q_full, k & 1);
+        if (!ok) break;
+        nb += NQ;
       }
-      nb += tiles * (NQ + 1);
+      const int count = box_count(sg);
+      if (FP8) ok = convert_boxes(count, ns, nb, group, t);
+      ns += count;
+      nb += count;
+      if (FP8 && rank == 0 && group == 0 && lane == 0) mbar_arrive(seg_filled);
     }
   };
   // ----------------------------------------------------- softmax
@@ -1076,7 +1068,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
 
   // With an fp8 cache's 512 threads the softmax warps take registers of the
   // others (128 x 168 + 384 x 112 < 512 x 128).
-  if (warp < 4) {
+  if (FP8 ? warp < 4 : warp < (rank == 0 ? 4 : 8)) {
     if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     if (rank == 0)
       softmax();
@@ -1084,23 +1076,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
       output();
   } else {
     if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-    if (warp < 8) {
-      if (rank == 0)
-        load_q();
-      else if (FP8)
-        convert(1, threadIdx.x - 128);
-      else
-        output();
-    } else if (warp == 8 || warp >= (FP8 ? 14 : 10)) {
+    if (warp < 8 || (FP8 && warp >= 10 && warp < 14))
+      fill(warp < 8 ? 1 : 0);
+    else if (warp != 9)
       produce();
-    } else if (warp == 9) {
-      if (rank == 0)
-        scores();
-      else
-        values();
-    } else if (FP8) {
-      convert(0, threadIdx.x - 320);
-    }
+    else if (rank == 0)
+      scores();
+    else
+      values();
   }
   if (!ok && lane == 0) gave_up(p.err_count);
 
