@@ -389,6 +389,8 @@ size_t schedule_smem(int G, int V) {
 // conversion instructions: 330 to 530).
 template <bool E5M2>
 __device__ __forceinline__ void convert_box(const uint8_t* src, uint8_t* dst, int t) {
+  uint8_t* const d0 = dst + sw128(t >> 2, (t & 3) * 2);
+  uint8_t* const d1 = dst + sw128(t >> 2, (t & 3) * 2 + 1);
 #pragma unroll 1
   for (int at = t; at < 512; at += 128) {
     const uint4 raw = *reinterpret_cast<const uint4*>(src + at * 16);
@@ -401,9 +403,8 @@ __device__ __forceinline__ void convert_box(const uint8_t* src, uint8_t* dst, in
       const float2 f = __half22float2(__half2(h));
       o[e] = pack_bf16x2(f.x, f.y);
     }
-    const int r = at >> 2, c = (at & 3) * 2;
-    *reinterpret_cast<uint4*>(dst + sw128(r, c)) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(dst + sw128(r, c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(d0 + (at - t) * 32) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(d1 + (at - t) * 32) = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
