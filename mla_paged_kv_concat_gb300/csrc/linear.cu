@@ -396,8 +396,10 @@ __device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int c0, 
                : "memory");
 }
 
+// Relaxed: what the others see of this CTA, its barriers' initial state, has a fence
+// of its own, and what they send it is acquired through its barrier.
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -495,16 +497,16 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
     // still runs: L2 holds what that one may write of it, so nothing stale is read.
     for (int kc = k_lo; kc < min(k_hi, k_lo + kAhead); ++kc) tma_prefetch_l2(&mw, kc * KC, 0, n0);
     griddep_wait();
-    // the ring is filled under the cluster's start
     for (int kc = k_lo; kc < min(k_hi, k_lo + C::STAGES); ++kc) request(kc);
   }
+  __syncwarp();
+  cluster_arrive();  // waited for before parts are sent
   if (warp == 5) {
     tc::tmem_alloc(tmem_slot, C::COLS);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
   __syncthreads();
-  tc::cluster_sync();  // every CTA's barrier is there before parts are sent
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
@@ -523,6 +525,7 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
       }
     }
     __syncwarp();
+    cluster_wait();
     cluster_arrive();
   } else if (warp == 5) {
     constexpr uint32_t idesc = tc::idesc_bf16(128, TN, 0, 0);
@@ -547,6 +550,7 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
       __syncwarp();
     }
     if (ok) ok = warp_wait(acc_full, 0);  // nothing is in flight when TMEM is freed
+    cluster_wait();
     cluster_arrive();
   } else {
     // What this warp finishes: groups of four tokens warp, warp + 4, .. of this
@@ -565,6 +569,7 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
     load(q_lo + warp);
     const uint2 bias = p.bias ? load4(p.bias, n, p.n) : make_uint2(0, 0);
     ok = warp_wait(acc_full, 0);
+    cluster_wait();  // every CTA's barrier is there
     if (ok) {
       // Parts [warp][group][32 rows][4 tokens] in the ring's place, which nothing
       // reads any more.  Row 4 l + j lies in slot 8 j + (l + 2 j) % 8, so that eight
