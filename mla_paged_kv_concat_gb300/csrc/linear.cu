@@ -39,6 +39,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, ok);
 }
 
+// Relaxed: what the others see of this CTA, its barriers' initial state, has a fence
+// of its own, and what they send it is acquired through its barrier.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0,
                                              int c1, int c2) {
   asm volatile(
@@ -247,11 +256,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_ctarank();
 
+  const int nk = (p.k + KC - 1) / KC;
+  const int mt = (p.tokens + 2 * TM - 1) / (2 * TM), nt = (p.n + BN - 1) / BN;
+  const int64_t total = static_cast<int64_t>(mt) * nt;
+  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  auto request = [&](int st, int m, int n, int kc) {
+    uint8_t* dst = smem + st * 2 * kPairHalf;
+    if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * (A_BYTES + BN / 2 * 128));
+    const uint32_t bar = tc::map_peer(smem_u32(&full[st]), 0);
+    tc::pair_tma_load_3d(dst, &ma, bar, kc * KC, 0, m * 2 * TM + rank * TM);
+    tc::pair_tma_load_3d(dst + kPairHalf, &mb, bar, kc * KC, 0, n * BN + rank * (BN / 2));
+  };
+
   if (threadIdx.x == 128) {
     tma_prefetch_desc(&ma);
     tma_prefetch_desc(&mb);
-  }
-  if (threadIdx.x == 0) {
     for (int i = 0; i < kPairStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -262,22 +281,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
     }
     fence_mbar_init();
   }
+  if (warp == 4) __syncwarp();
+  cluster_arrive();
   if (warp == 5) {
     tc::pair_tmem_alloc(tmem_slot, 512);
     tc::pair_tmem_relinquish();
   }
+  cluster_wait();  // both CTAs' barriers are there: the ring is filled at once
+  if (threadIdx.x == 128) {
+    griddep_wait();
+    int m, n;
+    tile_at(first, mt, nt, m, n);
+    for (int kc = 0; kc < min(nk, kPairStages); ++kc) request(kc, m, n, kc);
+  }
+  if (warp == 4) __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
-  tc::cluster_sync();
+  cluster_arrive();
+  if (warp != 4) cluster_wait();  // both have their TMEM
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
   griddep_launch_dependents();
-
-  const int nk = (p.k + KC - 1) / KC;
-  const int mt = (p.tokens + 2 * TM - 1) / (2 * TM), nt = (p.n + BN - 1) / BN;
-  const int64_t total = static_cast<int64_t>(mt) * nt;
-  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (warp == 4) {
     if (lane == 0) {
@@ -287,20 +312,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
         int m, n;
         tile_at(t, mt, nt, m, n);
         for (int kc = 0; kc < nk; ++kc, ++it) {
+          if (it < kPairStages && t == first) continue;  // asked for above
           const int st = it % kPairStages;
           if (!mbar_wait(&empty[st], ((it / kPairStages) & 1) ^ 1)) {
             ok = false;
             break;
           }
-          uint8_t* dst = smem + st * 2 * kPairHalf;
-          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * (A_BYTES + BN / 2 * 128));
-          const uint32_t bar = tc::map_peer(smem_u32(&full[st]), 0);
-          tc::pair_tma_load_3d(dst, &ma, bar, kc * KC, 0, m * 2 * TM + rank * TM);
-          tc::pair_tma_load_3d(dst + kPairHalf, &mb, bar, kc * KC, 0, n * BN + rank * (BN / 2));
+          request(st, m, n, kc);
         }
       }
       if (!ok) gave_up(p.err_count);
     }
+    __syncwarp();
+    cluster_wait();
   } else if (warp == 5) {
     bool ok = true;
     int it = 0, ta = 0;
@@ -394,15 +418,6 @@ __device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int c0, 
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map),
                "r"(c0), "r"(c1), "r"(c2)
                : "memory");
-}
-
-// Relaxed: what the others see of this CTA, its barriers' initial state, has a fence
-// of its own, and what they send it is acquired through its barrier.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Four consecutive bf16 of a row from column c, a multiple of 4, on; those past
