@@ -28,8 +28,8 @@
 //   rank 1: O R TMEM columns; P 2 x 32 KiB; a ring of five 32 KiB boxes of V (256
 //     dims x 64 tokens)
 // An fp8 cache lands in staging boxes and two groups of four warps of each CTA turn
-// it into the bf16 boxes (on rank 0 one of them also loads Q); its values are exact in bf16, and the scale is applied to the
-// scores and to the joined output.
+// it into the bf16 boxes (on rank 0 one of them also loads Q); its values are exact in
+// bf16, and the scale is applied to the scores and to the joined output.
 //
 // Schedule.  A first kernel (one CTA) turns the lengths into a list of all tiles: the
 // groups' prefixes, then the sequences, each cut into blocks of 128 vectors.  Blocks
@@ -38,6 +38,23 @@
 // before its tiles, for what its start and end take, and pair c of CTAs has the
 // places [c C, (c + 1) C).  Unit u meets pair c in segment u + c, which is also its
 // place in the workspace: list positions only grow, so no two are alike.
+//
+// Measured on GB300, one call out of a graph, and what bounds it:
+//   128 sequences, 128 heads, three prefixes, bf16, R = 512   317 us  1.10 PFLOP/s: a tile
+//       of 128 x 128 takes 1.76 us on rank 0, whose 36 products read 147 KB of shared
+//       memory (95 cycles each for 74)
+//   64 sequences behind 8192 tokens, 16 heads, bf16, R = 512   53.6  12 tiles a pair; lists
+//       5, start and Q 5, O 4, join 8
+//   45 sequences, 32 heads, two prefixes, E4M3, R = 256        57.0  conversion on rank 0,
+//       2.1 us a tile
+//   33 sequences of two rows behind 4097, 16 heads, E5M2, 512  47.4  the same, 3.3 us a tile
+//   4 sequences behind 512, 16 heads, bf16, R = 512            24.5  latency: lists 4.3,
+//       start and Q 4.7, three tiles 8.4, O 2, join 4.8
+// The plain decode takes 408, 89, 84, 69 and 12.4 us on these.  It is the faster one
+// where the tokens of all sequences together are few: about 140 thousand with 16 heads
+// and a bf16 cache, 30 thousand with an fp8 one; with 128 heads, which fill the 128 vectors
+// alone, sharing saves cache reads and no products (an fp8 cache with the 256-wide
+// latent, 128 sequences behind 1024: 85 us against 54).
 //
 // Roles (384 threads, 512 with an fp8 cache): rank 0 warps 0-3 softmax, thread =
 // TMEM lane = vector, 4-7 loading Q; rank 1 warps 0-7 rescaling and output of O, two
@@ -383,10 +400,13 @@ size_t schedule_smem(int G, int V) {
 
 // ---------------------------------------------------------------- conversion
 // A thread's part (t of 128) of an 8 KiB staging box, rows of 64 codes, to bf16
-// (exactly) in swizzled 128-byte rows: four pieces of 16 codes, two at a time.  Alone
-// on an SM two groups of four warps take 270 cycles a box, 232 of them what loading
-// 8 and storing 16 KiB takes (moving the bits with integer operations instead of the
-// conversion instructions: 330 to 530).
+// (exactly) in swizzled 128-byte rows: four pieces of 16 codes.  Alone on an SM two
+// groups of four warps take 270 cycles a box, 232 of them what loading 8 and storing
+// 16 KiB takes; beside the other roles 400 to 450, of which a third are waits, fence and
+// arrivals.  One piece at a time, the least code: with two the E4M3 batch of the header
+// took 62.6 us for 61.0, with four 68.8.  (Moving the bits with integer operations
+// instead of the conversion instructions: 330 to 530 cycles; the next box's codes asked
+// for under this one's stores: 59.9 us for 57.5.)
 template <bool E5M2>
 __device__ __forceinline__ void convert_box(const uint8_t* src, uint8_t* dst, int t) {
   uint8_t* const d0 = dst + sw128(t >> 2, (t & 3) * 2);

@@ -560,10 +560,19 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
                  workspace_bytes, o, o_row_stride, o_head_stride, lse, err_count, stream);
 }
 
-// Times in microseconds, as measured on GB300: 1.6 for 128 keys of a unit of 256
-// rows, 4 for its start and end, 2.3e-4 for a row and head of a part that is written
-// and joined, 5 for the join.  Own keys apart from the prefix where a block's window of
-// them would be long beside the prefix's part.
+// The least estimated time, in microseconds as measured on GB300: a unit takes 4 for its
+// start and end and 1.5 for 128 keys (2 where it has a second tile of query rows), half
+// as much again where the own keys of several sequences are masked; the units share the
+// SMs, the last ones overhang by half of the longest; a join takes 3.5 and 2.3e-4 for
+// a row and head of each part.  Own keys together with the prefix's (first loop) or
+// apart (second).  Measured (us: one part together / this rule's / the best of eleven
+// tried), 16 heads: three sequences of 20 rows, 1000 keys before them, 20 of their own
+// 21.0 / 15.2 (3 and 1) / 14.5, 300 of their own 36.2 / 15.4 (3, 1) / 15.4; one of 200
+// rows, 4000 and 200 keys 69.3 / 25.5 (8, 1) / 25.5; eight of 60 rows, 4000 and 60 keys
+// 73.0 / 38.5 (4, 0) / 37.0, 700 and 60 keys 28.6 / 28.6 / 23.8 (the worst found); 64 single
+// rows, 8192 and 1000 keys 1178 / 128 (8, 1) / 126; 48 of 48 rows, 8192 and 48 keys 144 /
+// 144 / 144, apart 180; 32 heads, eight of 1000 rows, 4096 and 1000 keys 533 / 533 / 533,
+// apart 633.
 int mla_prefill_shared_num_kv_splits(int num_tokens, int num_seqs, int num_groups, int num_heads,
                                      int64_t max_prefix_len, int64_t max_kv_len, int sm_count,
                                      int* num_kv_splits) {
@@ -572,29 +581,52 @@ int mla_prefill_shared_num_kv_splits(int num_tokens, int num_seqs, int num_group
       sm_count < 1)
     return 1;
   const int64_t by_rows = (static_cast<int64_t>(num_tokens) + 255) / 256;
-  const int64_t units = (num_groups > by_rows ? num_groups : by_rows) * num_heads;
-  // own keys that a block of 256 rows passes over
-  const double rows = static_cast<double>(num_tokens) / num_seqs;
-  const double window = max_kv_len > 0 ? static_cast<double>(max_kv_len) *
-                                             (rows < 256 ? 256 / (rows < 1 ? 1 : rows) : 1)
-                                       : 0;
-  const double longest = max_prefix_len / 2 > 4096 ? static_cast<double>(max_prefix_len / 2) : 4096;
-  const bool apart = window > longest && (rows < 256 || units < 2 * static_cast<int64_t>(sm_count));
-  if (apart && num_kv_splits)
-    *num_kv_splits =
-        mla_prefill_num_kv_splits(num_tokens, num_seqs, num_heads, max_kv_len, sm_count);
-  const double own = apart ? 0 : window / 128 * 1.6;
+  const int64_t blocks = num_groups > by_rows ? num_groups : by_rows;
+  const double units = static_cast<double>(blocks) * num_heads;
+  const double rows = static_cast<double>(num_tokens) / num_seqs;  // of a sequence
+  const double tile = num_tokens > 128 * blocks ? 2.0 : 1.5;
+  const double record = static_cast<double>(num_tokens) * num_heads * 2.3e-4;
+  auto tiles = [](int64_t keys, int parts) {
+    return static_cast<double>((keys - 1) / (int64_t{128} * parts) + 1);
+  };
+  auto span = [&](double work, double count, double longest) {
+    return count <= sm_count ? longest : work / sm_count + longest / 2;
+  };
+  // own keys that a unit of 256 rows passes over: its sequences' all, of which the
+  // masks cut all tiles but those before a long sequence's rows
+  double own = 0;
+  if (max_kv_len > 0) {
+    const double seqs = static_cast<double>((num_seqs - 1) / num_groups + 1);
+    const double window = static_cast<double>(max_kv_len) / 128 *
+                          (rows >= 256 ? 1 : 256 / rows < seqs ? 256 / rows : seqs);
+    own = tile * (window + (rows >= 256 && window > 2 ? 2 : window) / 2);
+  }
   int best = 1;
   double least = 0;
-  for (int s = 1; s <= 64 && (s == 1 || max_prefix_len / s >= 512); ++s) {
-    const double rounds = static_cast<double>((units * s + sm_count - 1) / sm_count);
-    const double part = static_cast<double>((max_prefix_len + 128LL * s - 1) / (128LL * s)) * 1.6 + 4;
-    const double cost =
-        rounds * part + (s == 1 ? rounds * own : own) +
-        (s > 1 || apart ? 5 + (s + (apart ? 1 : 0)) * static_cast<double>(num_tokens) * num_heads * 2.3e-4
-                        : 0);
+  for (int s = 1; s <= 64 && (s == 1 || max_prefix_len / s >= 256); ++s) {
+    const double part = 4 + tiles(max_prefix_len, s) * tile;
+    double cost = span(units * (s * part + own), units * s, part + own);
+    if (s > 1) cost += 3.5 + s * record;
+    // units without rows, at most two a head and part, take their turns, too
+    if (s > 1 && (num_tokens / 256 + num_groups + 2.0) * num_heads * s > sm_count) cost += 3;
     if (s == 1 || cost < least) {
       best = s;
+      least = cost;
+    }
+  }
+  if (!num_kv_splits || max_kv_len < 1) return best;
+  const int parts = mla_prefill_num_kv_splits(num_tokens, num_seqs, num_heads, max_kv_len, sm_count);
+  const double own_units =
+      static_cast<double>(num_seqs > by_rows ? num_seqs : by_rows) * num_heads * parts;
+  const double own_part = 4 + tiles(max_kv_len, parts) * (rows > 128 ? 2.0 : 1.5);
+  for (int s = 1; s <= 64 && (s == 1 || max_prefix_len / s >= 256); ++s) {
+    const double part = 4 + tiles(max_prefix_len, s) * tile;
+    const double cost = span(units * s * part + own_units * own_part, units * s + own_units,
+                             part > own_part ? part : own_part) +
+                        3.5 + (s + parts) * record;
+    if (cost < least) {
+      best = s;
+      *num_kv_splits = parts;
       least = cost;
     }
   }

@@ -7,13 +7,17 @@
 // does.  Both bring K in chunks of 64 through a TMA ring (128-byte swizzle; what
 // lies past K, N or T is filled with zeros).
 //
-// Measured on GB300, back to back (W mostly in L2) and behind a flush of L2, and
-// bounded by: 1 x 8192 -> 7168 with bias and residual 20.2 / 28.8 us (memory: 17.3
-// at 6.8 TB/s); 64 x 2048 -> 5120 with a residual 7.8 / 12.7 us (start and join 4 us, 264
-// KB a CTA at 100 B/ns; memory 3.3); 1001 x 1536 -> 6136 with bias and silu 21.7 / 25.2
-// us (two waves of tiles at 100 B/ns a SM, 3 us of the last tile's epilogue; products
-// 9.8); 8192 x 16384 -> 5120 with bias and residual 744 us, 1.85 PFLOP/s (products: 714;
-// the library's product alone takes 727 to 750).
+// Measured on GB300, out of a graph back to back (W mostly in L2) and behind a flush
+// of L2, and what bounds it:
+//   1 x 8192 -> 7168, bias, residual         19.1 / 27.5 us  memory: 17.3 at 6.8 TB/s
+//   64 x 2048 -> 5120, residual               7.1 / 11.7     start, join and end 4.4, then
+//                                                            264 KB a CTA at 97 B/ns
+//   1001 x 1536 -> 6136, bias, silu          21.0 / 24.0     1.38 MB a CTA at 97 B/ns in two
+//                                                            rounds of tiles, 3 of silu
+//   8192 x 16384 -> 5120, bias, residual     744             1.85 PFLOP/s
+// What an SM takes in over TMA is 97 B/ns here, however many boxes are under way.  The
+// library's product alone: 20.3, 4.2, 12.4 and 715 to 766 us; it shares the sum over K
+// out among all SMs where tiles do not fill them, for which it keeps a workspace.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -409,8 +413,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
 // adds the parts in rank order.  They are laid out in the ring's place and go as one
 // bulk copy a warp and CTA: stores to the peer one vector at a time took 2 us per 32
 // KB (64 x 2048 -> 5120: 10.3 us then, 9.3 with the copies, 7.8 with room for two
-// CTAs an SM, so that the next kernel starts under this one's end).  A lane finishes
-// four columns of four tokens and stores 8 bytes of each.
+// CTAs an SM, so that the next kernel starts under this one's end, 7.1 without a wait
+// for the cluster at the start).  A lane finishes four columns of four tokens and
+// stores 8 bytes of each.
 constexpr int kMostSplits = 8;  // a cluster
 constexpr int kAhead = 8;  // chunks of W asked for before the kernel before has ended
 
@@ -742,9 +747,11 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // persistent CTA and for every wave of the kernel for few tokens.  Two CTAs of an
 // SM share its rate, and clusters leave SMs out: of 152, those of 3, 4 and 8 CTAs
 // fill 138, 144 and 120 (6 as many as 3, 7 fewer than 8).  Measured (us, clusters
-// of 1, 2, 3, 4, 8): 16 x 2048 -> 5120 10.4, 7.1, 6.1, 6.8, 10.6; 64 tokens 12.5,
-// 8.6, 7.8, 8.3, 14.1; 200 x 7168 -> 1536 35.7, 21.3, 16.8, 14.8, 21.1; 1 x 8192 ->
-// 7168 33, 22, 22, 20.3, 24; 8 x 7168 -> 576 28, 15.8, 11.9, 9.7, 7.0.
+// of 1, 2, 3, 4, 8, before the last steps): 16 x 2048 -> 5120 10.4, 7.1, 6.1, 6.8, 10.6;
+// 64 tokens 12.5, 8.6, 7.8, 8.3, 14.1; 200 x 7168 -> 1536 35.7, 21.3, 16.8, 14.8, 21.1; 1
+// x 8192 -> 7168 33, 22, 22, 20.3, 24; 8 x 7168 -> 576 28, 15.8, 11.9, 9.7, 7.0.  Pairs,
+// tiles of 128, 192 and 256 columns: 512 x 2048 -> 5120 19.2, 14.3, 16.5; 1024 tokens
+// 26.4, 21.9, 25.1; 4096 tokens 76, 60, 58.
 LinearPlan linear_plan(int tokens, int n, int k, int sm_count) {
   const int64_t nk = cdiv64(k, KC);
   LinearPlan best = {};

@@ -53,10 +53,12 @@ def test_nothing_to_do(lib):
 
 def test_split_rule(lib):
     rule = mla.mla_prefill_shared_num_kv_splits
-    # 256-row blocks of the prefix leave SMs idle: parts of at least 512 keys
+    # 256-row blocks of the prefix leave SMs idle: parts of at least 256 keys
     pre, own = rule(60, 3, 1, 16, 8192, 60, 152)
-    assert 6 <= pre <= 9 and own == 0
-    assert rule(60, 3, 1, 16, 1000, 60, 152) == (1, 0)
+    assert 5 <= pre <= 9 and own == 1
+    pre, own = rule(60, 3, 1, 16, 1000, 60, 152)
+    assert 2 <= pre <= 3 and own == 1
+    assert rule(60, 3, 1, 16, 500, 0, 152) == (1, 0)
     # many rows: one part; a few rows each with long keys of their own: apart
     assert rule(8213, 40, 1, 32, 4000, 300, 152) == (1, 0)
     assert rule(16, 8, 1, 16, 8192, 30000, 152)[1] > 0
