@@ -9,8 +9,9 @@
  * and the log-sum-exp merge -- plus the cross-shard merge of decode context
  * parallelism, prepared, CUDA-graph-safe plans of a whole step, and the calls
  * that make a layer of it: a step's block tables and slot map from request
- * lengths, the gather of cached rows, the products with the kv_b weight and
- * the expanded form's attention over prompts:
+ * lengths, the gather of cached rows, the products with the kv_b weight, the
+ * expanded form's attention over prompts, both forms' attention for batches
+ * that share prefixes, and the layer's projections:
  *
  *   [diff] "frozenleaves/vllm compare v0.11.0...mla_cuda_graphs" ("fix TP"),
  *          a unified diff of vLLM, cited by file section;
@@ -282,7 +283,9 @@ mla_status mla_decode_ex(const void* q, int64_t q_row_stride,
  * the same pages, or pages of the same contents), and which of the tables they
  * are read through is not specified.  Sequences shorter than the prefix, padded
  * ones of length 0 among them, and those of no group are decoded by themselves.
- * A prefix is shared in whole tiles of 128 tokens.
+ * A prefix is shared in whole tiles of 128 tokens.  Where the sequences' tokens
+ * together are few mla_decode is faster: with 16 heads up to about 150 thousand
+ * of a bf16 cache, 35 to 100 thousand of an fp8 one.
  *
  *   q, q_pe         as in the plans below: q holds all R+P dims (q_pe NULL), or
  *                   dims [0, R) and q_pe the others.
