@@ -2,9 +2,10 @@
 // [N][K] bf16 as a linear layer stores it, fp32 accumulation in TMEM and fp32
 // epilogue, one rounding to bf16.
 //
-// Two kernels, by an estimate of their times (linear_plan): one for many tokens,
-// which the tensor core bounds, and one for few, which W's way into shared memory
-// does.  Both bring K in chunks of 64 through a TMA ring (128-byte swizzle; what
+// Three kernels, by an estimate of their times (linear_plan): pairs of CTAs for many
+// tokens, which the tensor core bounds, the same with K split where their tiles leave
+// SMs without work, and one for few tokens, which W's way into shared memory bounds.
+// All bring K in chunks of 64 through a TMA ring (128-byte swizzle; what
 // lies past K, N or T is filled with zeros).
 //
 // Measured on GB300, out of a graph back to back (W mostly in L2) and behind a flush
@@ -15,9 +16,10 @@
 //   1001 x 1536 -> 6136, bias, silu          21.0 / 24.0     1.38 MB a CTA at 97 B/ns in two
 //                                                            rounds of tiles, 3 of silu
 //   8192 x 16384 -> 5120, bias, residual     744             1.85 PFLOP/s
+//   442 x 9808 -> 3120, bias, relu           31.1 / 39.6     half of K a pair, 2.5 MB a CTA
 // What an SM takes in over TMA is 97 B/ns here, however many boxes are under way.  The
-// library's product alone: 20.3, 4.2, 12.4 and 715 to 766 us; it shares the sum over K
-// out among all SMs where tiles do not fill them, for which it keeps a workspace.
+// library's product alone: 20.3, 4.2, 12.4, 715 to 766 and 32.6 us; it shares the sum over
+// K out among all SMs whatever the tiles, for which it keeps a workspace.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -404,6 +406,252 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
   }
 }
 
+// ------------------------------------------------------------- split pairs
+// Tiles that do not fill the SMs: 256 tokens x 256 columns, the sum over K split among
+// up to four pairs of CTAs of a cluster.  When all products are done a CTA's partial
+// sums, 128 rows x 256 columns, go in slabs of 32 columns to the CTA of its rows that
+// finishes them, through the ring's place: a warp's 32 rows of a slab are one bulk copy of
+// 4 KiB.  That one adds the parts in order and stores 32 bytes of a row a lane.
+constexpr int SP_RECV = 6 * 16384;  // what is sent lies before: at most six slabs
+constexpr int SP_BAR = SP_RECV + 6 * 16384;  // received: six slabs, too
+static_assert(SP_BAR >= kPairStages * 2 * kPairHalf, "the ring");
+constexpr int SP_TMEM = SP_BAR + (2 * kPairStages + 2) * 8;
+constexpr int SP_SMEM = SP_TMEM + 16 + 1024;
+static_assert(SP_SMEM <= 227 * 1024, "shared memory");
+
+template <bool ACT>
+__global__ void __launch_bounds__(320, 1)
+    linear_split_kernel(const LinearParams p, const __grid_constant__ CUtensorMap ma,
+                        const __grid_constant__ CUtensorMap mb) {
+  constexpr int BN = 256, N = 16;  // columns of a tile, of a step of the end
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SP_BAR);  // [stages] rank 0's: both landed
+  uint64_t* empty = full + kPairStages;                         // [stages]
+  uint64_t* acc_full = empty + kPairStages;
+  uint64_t* recv_full = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SP_TMEM);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.splits;
+  const int cta = static_cast<int>(tc::cluster_ctarank());
+  const int rank = cta & 1, part = cta >> 1;  // of the pair, of the split
+  const int mt = (p.tokens + 2 * TM - 1) / (2 * TM), nt = (p.n + BN - 1) / BN;
+  int m, n;
+  tile_at(blockIdx.x / (2 * S), mt, nt, m, n);
+  const int nk = (p.k + KC - 1) / KC;
+  const int k_lo = static_cast<int>(static_cast<int64_t>(nk) * part / S);
+  const int k_hi = static_cast<int>(static_cast<int64_t>(nk) * (part + 1) / S);
+  const int lo = 8 * part / S, hi = 8 * (part + 1) / S;  // slabs that this CTA finishes
+  auto request = [&](int kc) {
+    const int st = (kc - k_lo) % kPairStages;
+    uint8_t* dst = smem + st * 2 * kPairHalf;
+    if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * (A_BYTES + BN / 2 * 128));
+    const uint32_t bar = tc::map_peer(smem_u32(&full[st]), cta & ~1);
+    tc::pair_tma_load_3d(dst, &ma, bar, kc * KC, 0, m * 2 * TM + rank * TM);
+    tc::pair_tma_load_3d(dst + kPairHalf, &mb, bar, kc * KC, 0, n * BN + rank * (BN / 2));
+  };
+
+  if (threadIdx.x == 128) {
+    tma_prefetch_desc(&ma);
+    tma_prefetch_desc(&mb);
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(recv_full, 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(recv_full, static_cast<uint32_t>((S - 1) * (hi - lo) * 16384));
+  }
+  if (warp == 4) __syncwarp();
+  cluster_arrive();
+  if (warp == 5) {
+    tc::pair_tmem_alloc(tmem_slot, BN);
+    tc::pair_tmem_relinquish();
+  }
+  cluster_wait();  // all barriers are there: the ring is filled at once
+  if (threadIdx.x == 128) {
+    griddep_wait();
+    for (int kc = k_lo; kc < min(k_hi, k_lo + kPairStages); ++kc) request(kc);
+  }
+  if (warp == 4) __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_arrive();
+  if (warp != 4) cluster_wait();  // all have their TMEM
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 4) {
+    if (lane == 0) {
+      for (int kc = k_lo + kPairStages; kc < k_hi; ++kc) {
+        const int it = kc - k_lo;
+        if (!mbar_wait(&empty[it % kPairStages], ((it / kPairStages) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        request(kc);
+      }
+    }
+    __syncwarp();
+    cluster_wait();
+    cluster_arrive();  // (the products' end, for the warps that send)
+    cluster_wait();
+  } else if (warp == 5) {
+    if (rank == 0) {
+      constexpr uint32_t idesc = tc::idesc_bf16(2 * TM, BN, 0, 0);
+      const uint16_t both = static_cast<uint16_t>(3 << cta);
+      for (int kc = k_lo; kc < k_hi; ++kc) {
+        const int it = kc - k_lo, st = it % kPairStages;
+        if (!warp_wait(&full[st], (it / kPairStages) & 1)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+          const uint32_t base = smem_u32(smem + st * 2 * kPairHalf);
+          const uint64_t da = tc::smem_desc(base, 16, 1024, tc::kLayoutSw128);
+          const uint64_t db = tc::smem_desc(base + kPairHalf, 16, 1024, tc::kLayoutSw128);
+#pragma unroll
+          for (int k = 0; k < KC / 16; ++k)
+            tc::pair_mma_ss(tmem, da + static_cast<uint64_t>(k * 2),
+                            db + static_cast<uint64_t>(k * 2), idesc, (it > 0 || k > 0) ? 1u : 0u);
+          tc::pair_commit(&empty[st], both);
+          if (kc == k_hi - 1) tc::pair_commit(acc_full, both);
+        }
+        __syncwarp();
+      }
+      if (ok) ok = warp_wait(acc_full, 0);
+    }
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    const int half = warp >= 6, qd = warp & 3;
+    const uint32_t acc = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+    const int row = m * 2 * TM + rank * TM + qd * 32 + lane;
+    const int first = lo + ((lo ^ half) & 1);  // this warp's slabs: every other one
+    auto column = [&](int step) { return n * BN + (first + (step & ~1)) * 32 + (step & 1) * N; };
+    const int steps = first < hi ? 2 * ((hi - first + 1) / 2) : 0;
+    uint4 res[N / 8];
+    if (steps > 0) load_residual<N>(p, row, column(0), res);
+    ok = warp_wait(acc_full, 0);
+    tc::fence_after_sync();
+    // this pair has read its rings to the end
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    if (ok) {
+#pragma unroll 1
+      for (int sl = half; sl < 8; sl += 2) {
+        if (sl >= lo && sl < hi) continue;
+        uint32_t r[32];
+        tc::ld_32x32b_x32(acc + sl * 32, r);
+        tc::wait_ld();
+        tc::reg_fence(r);
+        uint8_t* dst = smem + ((sl < lo ? sl : sl - (hi - lo)) * 4 + qd) * 4096 + lane * 16;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<uint4*>(dst + q * 512) =
+              make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+      }
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    cluster_wait();  // so have the others
+    if (ok && lane < 4) {
+      const int sl = half + 2 * lane;
+      if (sl < lo || sl >= hi) {
+        const int to = ((sl + 1) * S - 1) / 8;  // the part that finishes it
+        const int to_lo = 8 * to / S, to_hi = 8 * (to + 1) / S;
+        const int slot = (part - (part > to)) * (to_hi - to_lo) + sl - to_lo;
+        tc::bulk_copy_to_peer(
+            tc::map_peer(smem_u32(smem + SP_RECV), 2 * to + rank) + (slot * 4 + qd) * 4096,
+            smem + ((sl < lo ? sl : sl - (hi - lo)) * 4 + qd) * 4096, 4096,
+            tc::map_peer(smem_u32(recv_full), 2 * to + rank));
+      }
+    }
+    __syncwarp();
+    const bool got = tc::mbar_wait_cluster(recv_full, 0);
+    ok = __all_sync(0xffffffffu, got) && ok;
+#pragma unroll 1
+    for (int i = 0; ok && i < steps; ++i) {
+      const int sl = first + (i & ~1), c = column(i);
+      uint32_t r[N];
+      tc::ld_32x32b_x16(acc + sl * 32 + (i & 1) * N, r);
+      uint4 nxt[N / 8], bias[N / 8];
+      load_bias<N>(p, c, bias);
+      if (i + 1 < steps) load_residual<N>(p, row, column(i + 1), nxt);
+      tc::wait_ld();
+      tc::reg_fence(r);
+      float x[N];
+#pragma unroll
+      for (int q = 0; q < N / 8; ++q) {
+        const uint32_t w[4] = {bias[q].x, bias[q].y, bias[q].z, bias[q].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[8 * q + 2 * e] = lo_f(w[e]);
+          x[8 * q + 2 * e + 1] = hi_f(w[e]);
+        }
+      }
+#pragma unroll 1
+      for (int q = 0; q < S; ++q) {
+        if (q == part) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) x[e] += __uint_as_float(r[e]);
+        } else {
+          const uint8_t* src = smem + SP_RECV +
+                               (((q - (q > part)) * (hi - lo) + sl - lo) * 4 + qd) * 4096 +
+                               (i & 1) * (N / 4) * 512 + lane * 16;
+#pragma unroll
+          for (int e = 0; e < N / 4; ++e) {
+            const float4 v = *reinterpret_cast<const float4*>(src + e * 512);
+            x[4 * e] += v.x;
+            x[4 * e + 1] += v.y;
+            x[4 * e + 2] += v.z;
+            x[4 * e + 3] += v.w;
+          }
+        }
+      }
+      if (ACT) activate(p.act, x);
+#pragma unroll
+      for (int q = 0; q < N / 8; ++q) {
+        const uint32_t w[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = 8 * q + 2 * e;
+          o[e] = p.residual ? pack_bf16x2(x[k] + lo_f(w[e]), x[k + 1] + hi_f(w[e]))
+                            : pack_bf16x2(x[k], x[k + 1]);
+        }
+        if (row < p.tokens) {
+          uint16_t* y = p.y + row * p.y_stride;
+          const int col = c + 8 * q;
+          if (col + 8 <= p.n) {
+            *reinterpret_cast<uint4*>(y + col) = make_uint4(o[0], o[1], o[2], o[3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (col + e < p.n) y[col + e] = static_cast<uint16_t>(o[e >> 1] >> ((e & 1) * 16));
+          }
+        }
+        res[q] = nxt[q];
+      }
+    }
+    __syncwarp();
+  }
+  if (!ok && lane == 0) gave_up(p.err_count);
+
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();  // what is sent has been received, the peer's TMEM has been read
+  if (warp == 5) {
+    tc::fence_after_sync();
+    tc::pair_tmem_dealloc(tmem, BN);
+  }
+}
+
 // ---------------------------------------------------------------- few tokens
 // The weight is the work, and it has to come in at the rate of memory: the
 // operands change places (128 rows of W are A, the tokens B, padded to TN), and the
@@ -683,6 +931,26 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
   }
 }
 
+// A launch in clusters of `size` CTAs that may start under the kernel before.
+template <typename K, typename... Args>
+cudaError_t launch_clusters(K kernel, dim3 grid, int threads, int smem, int size,
+                            cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(size);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int BN, bool ACT>
 cudaError_t launch_pair(const LinearParams& p, const LinearMaps& m, int sm_count,
                         cudaStream_t stream) {
@@ -695,27 +963,26 @@ cudaError_t launch_pair(const LinearParams& p, const LinearMaps& m, int sm_count
                            m.a, m.b, m.c);
 }
 
+template <bool ACT>
+cudaError_t launch_split(const LinearParams& p, const LinearMaps& m, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = set_smem_attr_once(linear_split_kernel<ACT>, SP_SMEM, attr_done);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((p.tokens + 255) / 256) * ((p.n + 255) / 256);
+  return launch_clusters(linear_split_kernel<ACT>, dim3(static_cast<unsigned>(tiles * 2 * p.splits)),
+                         320, SP_SMEM, 2 * p.splits, stream, p, m.a, m.b);
+}
+
 template <int TN, bool ACT>
 cudaError_t launch_few(const LinearParams& p, const LinearMaps& m, cudaStream_t stream) {
   using C = FewCfg<TN>;
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e = set_smem_attr_once(linear_few_kernel<TN, ACT>, C::SMEM, attr_done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.n + 127) / 128 * p.splits),
-                     static_cast<unsigned>((p.tokens + TN - 1) / TN));
-  cfg.blockDim = dim3(192);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(p.splits);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_few_kernel<TN, ACT>, p, m.a, m.b);
+  return launch_clusters(linear_few_kernel<TN, ACT>,
+                         dim3(static_cast<unsigned>((p.n + 127) / 128 * p.splits),
+                              static_cast<unsigned>((p.tokens + TN - 1) / TN)),
+                         192, C::SMEM, p.splits, stream, p, m.a, m.b);
 }
 
 template <bool ACT>
@@ -729,6 +996,7 @@ cudaError_t launch_any(const LinearParams& p, const LinearMaps& m, int sm_count,
       default: return launch_few<128, ACT>(p, m, stream);
     }
   }
+  if (p.splits > 1) return launch_split<ACT>(p, m, stream);
   switch (p.bn) {
     case 256: return launch_pair<256, ACT>(p, m, sm_count, stream);
     case 192: return launch_pair<192, ACT>(p, m, sm_count, stream);
@@ -751,7 +1019,10 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // 64 tokens 12.5, 8.6, 7.8, 8.3, 14.1; 200 x 7168 -> 1536 35.7, 21.3, 16.8, 14.8, 21.1; 1
 // x 8192 -> 7168 33, 22, 22, 20.3, 24; 8 x 7168 -> 576 28, 15.8, 11.9, 9.7, 7.0.  Pairs,
 // tiles of 128, 192 and 256 columns: 512 x 2048 -> 5120 19.2, 14.3, 16.5; 1024 tokens
-// 26.4, 21.9, 25.1; 4096 tokens 76, 60, 58.
+// 26.4, 21.9, 25.1; 4096 tokens 76, 60, 58.  Pairs that split K end 3 to 5 us later; 256
+// columns and one, two, three, four parts: 442 x 9808 -> 3120 51.7, 30.9, 47.9, 42.4 (128
+// columns, one part 43); 1008 x 11512 -> 1224 71, 40.9, 31.7, 50.7 (53); 256 x 18432 ->
+// 7168 92, 58, 84, 70 (80); 256 x 2048 -> 5120 15.7, 13.8, 13.6, 24.0 (12.9).
 LinearPlan linear_plan(int tokens, int n, int k, int sm_count) {
   const int64_t nk = cdiv64(k, KC);
   LinearPlan best = {};
@@ -785,6 +1056,13 @@ LinearPlan linear_plan(int tokens, int n, int k, int sm_count) {
       take(cdiv64(cdiv64(tokens, 256) * cdiv64(n, bn), sm_count / 2) * nk *
                    chunk(128 + bn / 2, bn) + 4000,
            {kLinearPair, bn, 1, TM, bn / 2});
+    const int64_t tiles = cdiv64(tokens, 256) * cdiv64(n, 256);
+    for (int s = 2; s <= 4 && s <= nk; ++s) {
+      const int fit = (s == 4 ? sm_count * 15 / 19 : s == 3 ? sm_count * 10 / 11
+                                                            : sm_count * 18 / 19) / (2 * s);
+      take(cdiv64(tiles, fit) * (cdiv64(nk, s) * chunk(256, 256) + (s == 2 ? 9500 : 12000)),
+           {kLinearPair, 256, s, TM, 128});
+    }
   }
   return best;
 }

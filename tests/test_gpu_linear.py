@@ -187,3 +187,34 @@ def test_captured(cuda_dev):
         r.copy_(normal(g, T, N))
         graph.replay()
         check(out, x, w, res=r)
+
+
+@pytest.mark.parametrize("T,N,K", [(442, 3120, 3001), (300, 2500, 4000), (1000, 1223, 4001), (700, 1000, 6000),
+                                   (257, 4090, 9000)])
+@pytest.mark.parametrize("bias,act,residual", [(False, None, False), (True, "gelu_tanh", True)])
+def test_split_sums(cuda_dev, T, N, K, bias, act, residual):
+    """Few large tiles and long sums: two to four pairs a tile."""
+    g = torch.Generator("cuda").manual_seed(T + N)
+    x, w = rows(g, T, K, 1), rows(g, N, K)
+    w *= 1 / math.sqrt(K)  # (in place: its rows start on 16 bytes)
+    b = normal(g, N) if bias else None
+    r = rows(g, T, N, 2) if residual else None
+    y = mla.linear(x, w, bias=b, activation=act, residual=r)
+    check(y, x, w, b, act, r)
+    assert torch.equal(mla.linear(x, w, bias=b, activation=act, residual=r), y)
+    full = normal(g, T, (N + 7) // 8 * 8 + 24)
+    keep = full.clone()
+    out = full[:, 8:8 + N]
+    mla.linear(x, w, bias=b, activation=act, residual=r, out=out)
+    assert torch.equal(out, y)
+    assert torch.equal(full[:, :8], keep[:, :8]) and torch.equal(full[:, 8 + N:], keep[:, 8 + N:])
+    if residual:
+        mla.linear(x, w, bias=b, activation=act, residual=r, out=r)
+        assert torch.equal(r, y)
+    # a row and a column that are not finite stay alone
+    x[T // 2, 3], w[N // 3, K - 1] = float("nan"), float("inf")
+    z = mla.linear(x, w, bias=b)
+    ref = mla.linear(x, w, bias=b).isfinite()
+    assert torch.equal(z.isfinite(), ref) and not bool(ref[T // 2].any()) and not bool(ref[:, N // 3].any())
+    ref[T // 2], ref[:, N // 3] = True, True
+    assert bool(ref.all())
