@@ -179,7 +179,9 @@ __device__ __forceinline__ void cta_scan(int64_t* a, int n, int64_t* tot) {
   __syncthreads();
 }
 
-// Places that a unit has in the list before its tiles.
+// Places that a unit has in the list before its tiles.  Measured (us, 1 / 2 / 3, the
+// first four batches of the header): 338 / 317 / 317, 55.7 / 53.6 / 54.9, 58.4 / 57.0 /
+// 57.2, 53.9 / 47.4 / 47.8.
 constexpr int kStart = 2;
 
 // The lists in shared memory (free again afterwards).
