@@ -48,8 +48,8 @@
 //   45 sequences, 32 heads, two prefixes, E4M3, R = 256        57.0  conversion on rank 0,
 //       2.1 us a tile
 //   33 sequences of two rows behind 4097, 16 heads, E5M2, 512  47.4  the same, 3.3 us a tile
-//   4 sequences behind 512, 16 heads, bf16, R = 512            24.5  latency: lists 4.3,
-//       start and Q 4.7, three tiles 8.4, O 2, join 4.8
+//   4 sequences behind 512, 16 heads, bf16, R = 512            22.5  latency: lists 4.3,
+//       start and Q 4.7, a tile 5, O 2, join 5
 // The plain decode takes 408, 89, 84, 69 and 12.4 us on these.  It is the faster one
 // where the tokens of all sequences together are few: with 16 heads about 150 thousand of
 // a bf16 cache, 35 to 100 thousand of an fp8 one.  128 heads fill the 128 vectors alone, and
@@ -184,6 +184,16 @@ __device__ __forceinline__ void cta_scan(int64_t* a, int n, int64_t* tot) {
 // 57.2, 53.9 / 47.4 / 47.8.
 constexpr int kStart = 2;
 
+// Tiles of a unit of a part: chunks, or all where a single block has nobody beside it
+// to read the same rows.  Up to 16 tiles of such a block go to a pair each where there are
+// pairs to spare (chunks of one tile): joining a piece costs 0.3 us, a tile 1.9 (us, all
+// together / one by one: four sequences behind 512 tokens 24.5 / 22.3, eight behind 1024
+// 28.4 / 26.8, behind 4096 32.5 / 38.3).
+__device__ __forceinline__ int unit_tiles(int blocks, int tiles, int chunk) {
+  const bool whole = blocks == 1 && (chunk > 1 || tiles > 16);
+  return whole || tiles < chunk ? tiles : chunk;
+}
+
 // The lists in shared memory (free again afterwards).
 struct Lists {
   int64_t* before;    // [V + 1] places (low half) and units before a part: groups, then sequences
@@ -258,14 +268,13 @@ __device__ __forceinline__ int2 make_list(const SharedParams& p, const Lists& li
   const int tiles = cta_sum(all_tiles, tot);  // at most 2^30
   // Chunks of a pair's share, which with its start is the share itself where that
   // comes out (found in a few steps: larger chunks are fewer starts).
-  auto chunk_of = [&](int blocks, int t, int chunk) { return blocks == 1 || t < chunk ? t : chunk; };
   const int least = max(1, cdiv(tiles, p.pairs));
   int chunk = least, C = 1;
   for (int step = 0; step < 3; ++step) {
     int all_units = 0;
     for (int v = static_cast<int>(threadIdx.x); v < V; v += static_cast<int>(blockDim.x)) {
       const int n = blocks_of(v), t = tiles_of(v);
-      if (n > 0) all_units += n * cdiv(t, chunk_of(n, t, chunk));
+      if (n > 0) all_units += n * cdiv(t, unit_tiles(n, t, chunk));
     }
     C = max(1, cdiv(tiles + kStart * cta_sum(all_units, tot), p.pairs));
     const int next = max(least, C - kStart);
@@ -275,7 +284,7 @@ __device__ __forceinline__ int2 make_list(const SharedParams& p, const Lists& li
   C = max(C, chunk + kStart);
   for (int v = static_cast<int>(threadIdx.x); v < V; v += static_cast<int>(blockDim.x)) {
     const int n = blocks_of(v), t = tiles_of(v);
-    const int64_t units = n == 0 ? 0 : n * cdiv(t, chunk_of(n, t, chunk));
+    const int64_t units = n == 0 ? 0 : n * cdiv(t, unit_tiles(n, t, chunk));
     before[v + 1] = units << 32 | static_cast<int64_t>(t * n + kStart * units);
   }
   if (threadIdx.x == 0) before[0] = 0;
@@ -306,7 +315,7 @@ __device__ __forceinline__ void walk(const SharedParams& p, const Lists& l, int 
     const int start = places(v), unit0 = static_cast<int>(l.before[v] >> 32);
     const int vecs = v < G ? (l.ends[v + 1] - l.ends[v]) * per : per, blocks = cdiv(vecs, 128);
     const int tiles = cdiv(l.tok1[v] - l.tok0[v], TT);
-    const int ch = blocks == 1 || tiles < chunk ? tiles : chunk;
+    const int ch = unit_tiles(blocks, tiles, chunk);
     const int whole = (ch + kStart) * blocks;  // places of a whole chunk
     while (t < hi && t < end) {
       const int in = t - start;
@@ -345,7 +354,7 @@ __device__ __forceinline__ void fill_row(const SharedParams& p, const Lists& l, 
     x.first = static_cast<int>(l.before[v] & 0xFFFFFFFF);
     x.tiles = cdiv(l.tok1[v] - l.tok0[v], TT);
     x.blocks = x.tiles <= 0 ? 0 : cdiv(v < G ? (l.ends[v + 1] - l.ends[v]) * per : per, 128);
-    x.chunk = x.blocks == 0 ? 1 : x.blocks == 1 || x.tiles < chunk ? x.tiles : chunk;
+    x.chunk = x.blocks == 0 ? 1 : unit_tiles(x.blocks, x.tiles, chunk);
     x.unit0 = static_cast<int>(l.before[v] >> 32);
     x.row0 = (v < G ? l.ends[v] : v - G) * p.rows_per_seq;
     return x;
