@@ -65,6 +65,14 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 __device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
+// 1 / x, results below the normal range 0 (a call of its own: a division's care for
+// them was half of silu's instructions).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The activation over a run of values; the choice is made once for all of them.
 // gelu is written with erfc, whose small values keep their relative precision
 // where 1 + erf cancels; both sigmoid forms go to 0 or x at the ends.
@@ -77,7 +85,7 @@ __device__ __forceinline__ void activate(int act, float (&x)[N]) {
       break;
     case kActSilu:
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = __fdividef(x[i], 1.f + __expf(-x[i]));
+      for (int i = 0; i < N; ++i) x[i] *= rcp(1.f + ex2(-1.4426950f * x[i]));
       break;
     case kActGelu:
 #pragma unroll
@@ -86,10 +94,23 @@ __device__ __forceinline__ void activate(int act, float (&x)[N]) {
     case kActGeluTanh:
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        x[i] = __fdividef(
-            x[i], 1.f + __expf(-1.5957691f * x[i] * fmaf(0.044715f * x[i], x[i], 1.f)));
+        x[i] *= rcp(1.f + ex2(-2.3022082f * x[i] * fmaf(0.044715f * x[i], x[i], 1.f)));
       break;
     default: break;
+  }
+}
+
+// x += the bf16 values in v.
+template <int N>
+__device__ __forceinline__ void add_bf16(float (&x)[N], const uint4 (&v)[N / 8]) {
+#pragma unroll
+  for (int q = 0; q < N / 8; ++q) {
+    const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[8 * q + 2 * e] += lo_f(w[e]);
+      x[8 * q + 2 * e + 1] += hi_f(w[e]);
+    }
   }
 }
 
@@ -166,20 +187,10 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
     }
     float x[N];
 #pragma unroll
-    for (int q = 0; q < N / 8; ++q) {
-      const uint32_t w[4] = {bias[q].x, bias[q].y, bias[q].z, bias[q].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 8 * q + 2 * e;
-        x[i] = __uint_as_float(r[i]);
-        x[i + 1] = __uint_as_float(r[i + 1]);
-        if (p.bias) {
-          x[i] += lo_f(w[e]);
-          x[i + 1] += hi_f(w[e]);
-        }
-      }
-    }
+    for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
+    if (p.bias) add_bf16(x, bias);
     if (ACT) activate(p.act, x);
+    if (p.residual) add_bf16(x, res);
     uint8_t* dst = boxes + (nb & 1) * STORE_BYTES;
     if ((j & 63) == 0) {
       // the store that last used this box, the one before the last, has read it
@@ -188,14 +199,9 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
     }
 #pragma unroll
     for (int q = 0; q < N / 8; ++q) {
-      const uint32_t w[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
       uint32_t o[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 8 * q + 2 * e;
-        o[e] = p.residual ? pack_bf16x2(x[i] + lo_f(w[e]), x[i + 1] + hi_f(w[e]))
-                          : pack_bf16x2(x[i], x[i + 1]);
-      }
+      for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1]);
       *reinterpret_cast<uint4*>(dst + sw128(lane, (j & 63) / 8 + q)) =
           make_uint4(o[0], o[1], o[2], o[3]);
       res[q] = nxt[q];
@@ -585,16 +591,8 @@ __global__ void __launch_bounds__(320, 1)
       if (i + 1 < steps) load_residual<N>(p, row, column(i + 1), nxt);
       tc::wait_ld();
       tc::reg_fence(r);
-      float x[N];
-#pragma unroll
-      for (int q = 0; q < N / 8; ++q) {
-        const uint32_t w[4] = {bias[q].x, bias[q].y, bias[q].z, bias[q].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[8 * q + 2 * e] = lo_f(w[e]);
-          x[8 * q + 2 * e + 1] = hi_f(w[e]);
-        }
-      }
+      float x[N] = {};
+      if (p.bias) add_bf16(x, bias);
 #pragma unroll 1
       for (int q = 0; q < S; ++q) {
         if (q == part) {
@@ -615,16 +613,12 @@ __global__ void __launch_bounds__(320, 1)
         }
       }
       if (ACT) activate(p.act, x);
+      if (p.residual) add_bf16(x, res);
 #pragma unroll
       for (int q = 0; q < N / 8; ++q) {
-        const uint32_t w[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
         uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int k = 8 * q + 2 * e;
-          o[e] = p.residual ? pack_bf16x2(x[k] + lo_f(w[e]), x[k + 1] + hi_f(w[e]))
-                            : pack_bf16x2(x[k], x[k + 1]);
-        }
+        for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1]);
         if (row < p.tokens) {
           uint16_t* y = p.y + row * p.y_stride;
           const int col = c + 8 * q;
