@@ -13,8 +13,10 @@
 //   1 x 8192 -> 7168, bias, residual         19.1 / 27.5 us  memory: 17.3 at 6.8 TB/s
 //   64 x 2048 -> 5120, residual               7.1 / 11.7     start, join and end 4.4, then
 //                                                            264 KB a CTA at 97 B/ns
-//   1001 x 1536 -> 6136, bias, silu          21.0 / 24.0     1.38 MB a CTA at 97 B/ns in two
-//                                                            rounds of tiles, 3 of silu
+//   1001 x 1536 -> 6136, bias, silu          20.3 / 23.8     1.38 MB a CTA at 97 B/ns in two
+//                                                            rounds of tiles, 2 of silu
+//   1262 x 184 -> 16176, bias, silu, res.    43.1 / 48.9     the tiles' ends: 33 without the
+//                                                            residual, 18 without silu, too
 //   8192 x 16384 -> 5120, bias, residual     744             1.85 PFLOP/s
 //   442 x 9808 -> 3120, bias, relu           31.1 / 39.6     half of K a pair, 2.5 MB a CTA
 // What an SM takes in over TMA is 97 B/ns here, however many boxes are under way.  The
@@ -155,7 +157,9 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
 // TMEM column `acc` and y column c0 on: fp32 (a row a lane) through bias,
 // activation and residual to bf16 in swizzled boxes of 64 columns (two in turn,
 // `nb` counts them) and from there to y.  `before` waits for the accumulator,
-// `after` gives it back.  The loop is not unrolled, and products without an
+// `after` gives it back.  The residual comes 128 bytes of a row at a time, a box ahead,
+// and to the lanes of its rows through the box that their results go to (32 bytes of a
+// row a lane: 42.1 us for 37.7, 4096 x 512 -> 7168).  The loop is not unrolled, and products without an
 // activation have kernels of their own: with all activations in 32 copies of the
 // body 1001 x 1536 -> 6136 took 35 us, waiting for instructions, against 22.
 template <bool ACT, typename Before, typename After>
@@ -163,8 +167,16 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
                                          int row0, int lane, uint8_t* boxes, int& nb,
                                          const CUtensorMap* map, Before&& before, After&& after) {
   constexpr int N = ACT ? 16 : 32;  // columns of a step
-  uint4 res[N / 8], bias[N / 8];
-  load_residual<N>(p, row0 + lane, c0, res);
+  uint4 res[8], bias[N / 8];  // of the next box: rows 4 k + lane / 8, eight columns
+  auto load = [&](int c) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int row = row0 + 4 * k + (lane >> 3), col = c + (lane & 7) * 8;
+      res[k] = row < p.tokens && col < p.n ? load8(p.residual + row * p.res_stride, col, p.n)
+                                           : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (p.residual) load(c0);
   load_bias<N>(p, c0, bias);
   if (!before()) return false;
   tc::fence_after_sync();
@@ -173,10 +185,20 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
     const int c = c0 + j;
     uint32_t r[N];
     tmem_load<N>(acc + j, r);
-    uint4 nxt[N / 8], bias_nxt[N / 8];
-    if (j + N < cols) {
-      load_residual<N>(p, row0 + lane, c + N, nxt);
-      load_bias<N>(p, c + N, bias_nxt);
+    uint4 bias_nxt[N / 8];
+    if (j + N < cols) load_bias<N>(p, c + N, bias_nxt);
+    uint8_t* dst = boxes + (nb & 1) * STORE_BYTES;
+    if ((j & 63) == 0) {
+      // the store that last used this box, the one before the last, has read it
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();
+      if (p.residual) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(dst + sw128(4 * k + (lane >> 3), lane & 7)) = res[k];
+        __syncwarp();
+        if (j + 64 < cols) load(c + 64);
+      }
     }
     tc::wait_ld();
     tc::reg_fence(r);
@@ -190,12 +212,12 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
     for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
     if (p.bias) add_bf16(x, bias);
     if (ACT) activate(p.act, x);
-    if (p.residual) add_bf16(x, res);
-    uint8_t* dst = boxes + (nb & 1) * STORE_BYTES;
-    if ((j & 63) == 0) {
-      // the store that last used this box, the one before the last, has read it
-      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-      __syncwarp();
+    if (p.residual) {
+      uint4 v[N / 8];
+#pragma unroll
+      for (int q = 0; q < N / 8; ++q)
+        v[q] = *reinterpret_cast<const uint4*>(dst + sw128(lane, (j & 63) / 8 + q));
+      add_bf16(x, v);
     }
 #pragma unroll
     for (int q = 0; q < N / 8; ++q) {
@@ -204,7 +226,6 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
       for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1]);
       *reinterpret_cast<uint4*>(dst + sw128(lane, (j & 63) / 8 + q)) =
           make_uint4(o[0], o[1], o[2], o[3]);
-      res[q] = nxt[q];
       bias[q] = bias_nxt[q];
     }
     if ((j & 63) == 64 - N) {
