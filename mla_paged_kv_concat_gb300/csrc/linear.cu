@@ -13,10 +13,10 @@
 //   1 x 8192 -> 7168, bias, residual         19.1 / 27.5 us  memory: 17.3 at 6.8 TB/s
 //   64 x 2048 -> 5120, residual               7.1 / 11.7     start, join and end 4.4, then
 //                                                            264 KB a CTA at 97 B/ns
-//   1001 x 1536 -> 6136, bias, silu          20.3 / 23.8     1.38 MB a CTA at 97 B/ns in two
+//   1001 x 1536 -> 6136, bias, silu          19.5 / 22.6     1.38 MB a CTA at 97 B/ns in two
 //                                                            rounds of tiles, 2 of silu
-//   1262 x 184 -> 16176, bias, silu, res.    43.1 / 48.9     the tiles' ends: 33 without the
-//                                                            residual, 18 without silu, too
+//   1262 x 184 -> 16176, bias, silu, res.    41.3 / 46.9     the tiles' ends: 31 without the
+//                                                            residual, 17.5 without silu, too
 //   8192 x 16384 -> 5120, bias, residual     744             1.85 PFLOP/s
 //   442 x 9808 -> 3120, bias, relu           31.1 / 39.6     half of K a pair, 2.5 MB a CTA
 // What an SM takes in over TMA is 97 B/ns here, however many boxes are under way.  The
@@ -141,8 +141,7 @@ __device__ __forceinline__ void load_residual(const LinearParams& p, int row, in
 template <int N>
 __device__ __forceinline__ void load_bias(const LinearParams& p, int c, uint4 (&b)[N / 8]) {
 #pragma unroll
-  for (int q = 0; q < N / 8; ++q)
-    b[q] = p.bias ? load8(p.bias, c + 8 * q, p.n) : make_uint4(0, 0, 0, 0);
+  for (int q = 0; q < N / 8; ++q) b[q] = load8(p.bias, c + 8 * q, p.n);
 }
 
 template <int N>
@@ -177,7 +176,7 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
     }
   };
   if (p.residual) load(c0);
-  load_bias<N>(p, c0, bias);
+  if (p.bias) load_bias<N>(p, c0, bias);
   if (!before()) return false;
   tc::fence_after_sync();
 #pragma unroll 1
@@ -185,8 +184,6 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
     const int c = c0 + j;
     uint32_t r[N];
     tmem_load<N>(acc + j, r);
-    uint4 bias_nxt[N / 8];
-    if (j + N < cols) load_bias<N>(p, c + N, bias_nxt);
     uint8_t* dst = boxes + (nb & 1) * STORE_BYTES;
     if ((j & 63) == 0) {
       // the store that last used this box, the one before the last, has read it
@@ -210,7 +207,10 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
     float x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
-    if (p.bias) add_bf16(x, bias);
+    if (p.bias) {
+      add_bf16(x, bias);
+      if (j + N < cols) load_bias<N>(p, c + N, bias);
+    }
     if (ACT) activate(p.act, x);
     if (p.residual) {
       uint4 v[N / 8];
@@ -226,7 +226,6 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
       for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1]);
       *reinterpret_cast<uint4*>(dst + sw128(lane, (j & 63) / 8 + q)) =
           make_uint4(o[0], o[1], o[2], o[3]);
-      bias[q] = bias_nxt[q];
     }
     if ((j & 63) == 64 - N) {
       fence_proxy_async_smem();
@@ -608,7 +607,7 @@ __global__ void __launch_bounds__(320, 1)
       uint32_t r[N];
       tc::ld_32x32b_x16(acc + sl * 32 + (i & 1) * N, r);
       uint4 nxt[N / 8], bias[N / 8];
-      load_bias<N>(p, c, bias);
+      if (p.bias) load_bias<N>(p, c, bias);
       if (i + 1 < steps) load_residual<N>(p, row, column(i + 1), nxt);
       tc::wait_ld();
       tc::reg_fence(r);
