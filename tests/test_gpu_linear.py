@@ -6,8 +6,9 @@ fp32, added in fp32 in any order, also with truncating steps: off by at most K
 2^-23 s, s = sum |x w|; the bias adds one more step.  The activations' slopes
 are below 1.2.  Their own errors, relative to act(z): expf's fast form is off by
 (2 + 1.2 |u|) 2^-23 of its value at u, plus |u| 2^-22 for u's own rounding, the
-fast division by 2^-22; erfcf by 4 units, plus z^2 2^-23 for its argument's
-rounding (its logarithmic slope is below |z| + 1); so (16 + z^2 + 4 |u|) 2^-23 |act|
+reciprocal by 2^-23; the normal tail's polynomial (eight steps on values up to 2.7),
+reciprocal and exponential by 12 units, plus z^2 2^-23 for its argument's rounding
+(its logarithmic slope is below |z| + 1); so (16 + z^2 + 4 |u|) 2^-23 |act|
 covers each, with u the exponent's argument.  The residual adds one rounding,
 bf16 one of at most 2^-8 of the value.
 """
