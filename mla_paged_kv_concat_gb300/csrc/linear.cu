@@ -17,10 +17,10 @@
 //                                                            rounds of tiles, 2 of silu
 //   1262 x 184 -> 16176, bias, silu, res.    41.3 / 46.9     the tiles' ends: 31 without the
 //                                                            residual, 17.5 without silu, too
-//   8192 x 16384 -> 5120, bias, residual     744             1.85 PFLOP/s
+//   8192 x 16384 -> 5120, bias, residual     732 to 785      1.75 to 1.88 PFLOP/s, by clock
 //   442 x 9808 -> 3120, bias, relu           31.1 / 39.6     half of K a pair, 2.5 MB a CTA
 // What an SM takes in over TMA is 97 B/ns here, however many boxes are under way.  The
-// library's product alone: 20.3, 4.2, 12.4, 715 to 766 and 32.6 us; it shares the sum over
+// library's product alone: 20.3, 4.2, 12.4, 12.1, 715 to 780, 32.6 us; it shares the sum over
 // K out among all SMs whatever the tiles, for which it keeps a workspace.
 #include <cuda_bf16.h>
 #include <stdint.h>
