@@ -577,7 +577,8 @@ def linear(x, weight, *, bias=None, activation: str | None = None, residual=None
     ``x`` bf16 [T, K], ``weight`` bf16 [N, K] as a linear layer stores it,
     ``bias`` bf16 [N], ``residual`` bf16 [T, N] (any row strides that are
     multiples of 8); ``activation``: None, "relu", "silu", "gelu" (x Phi(x)) or
-    "gelu_tanh".  ``out`` may be ``residual`` (updated in place).
+    "gelu_tanh".  ``out`` may be ``residual`` (updated in place).  What is allocated
+    here has rows of N rounded up to a multiple of 8.
     """
     if activation not in _ACTIVATIONS:
         raise ValueError(f"unsupported activation {activation!r}")
@@ -616,7 +617,9 @@ def prefill_shared(q, k_nope, v, k_pe, cu_seqlens_q, cu_seqlens_k, group_seqs, c
     besides their own keys there (``cu_seqlens_k``, masked as by ``causal``).
     ``num_kv_splits``: parts of the prefixes' keys and of the sequences' own (0:
     those together with the prefix's), a pair from
-    ``mla_prefill_shared_num_kv_splits``, or the first of them alone.
+    ``mla_prefill_shared_num_kv_splits``, or the first of them alone (the default
+    takes up to ten times as long where many short sequences have long keys of
+    their own).
     """
     q, q_pe = q if isinstance(q, (tuple, list)) else (q, None)
     pre, own = num_kv_splits if isinstance(num_kv_splits, (tuple, list)) else (num_kv_splits, 0)
