@@ -199,6 +199,7 @@ struct Lists {
   int64_t* before;    // [V + 1] places (low half) and units before a part: groups, then sequences
   int *tok0, *tok1;   // [V] a part's tokens
   int *ends, *lead;   // [G + 1] first sequence of each group; [G] the one whose table is read
+  int* prefix;        // [G] all of a prefix: who takes part has it to the end
   int* group;         // [B] the group whose shared part a sequence takes part in, or -1
 };
 
@@ -224,7 +225,7 @@ __device__ __forceinline__ int2 make_list(const SharedParams& p, const Lists& li
   __syncthreads();
   // what the sequences of a group can share, when there are two at least
   for (int g = warp; g < G; g += static_cast<int>(blockDim.x >> 5)) {
-    const int n = tok1[g];
+    const int n = lists.prefix[g];
     int count = 0, first = B;
     for (int b = ends[g] + lane; b < ends[g + 1]; b += 32)
       if (tok1[G + b] >= n) {
@@ -250,7 +251,7 @@ __device__ __forceinline__ int2 make_list(const SharedParams& p, const Lists& li
       const int m = (a + z + 1) >> 1;
       if (ends[m] <= b) a = m; else z = m - 1;
     }
-    return a < G && b >= ends[a] && tok1[a] > 0 && tok1[G + b] >= tok1[a] ? a : -1;
+    return a < G && b >= ends[a] && tok1[a] > 0 && tok1[G + b] >= lists.prefix[a] ? a : -1;
   };
   auto blocks_of = [&](int v) {
     return tok1[v] <= tok0[v] ? 0 : cdiv(v < G ? (ends[v + 1] - ends[v]) * per : per, 128);
@@ -381,7 +382,8 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParam
   l.tok1 = l.tok0 + V;
   l.ends = l.tok1 + V;
   l.lead = l.ends + G + 1;
-  l.group = l.lead + G;
+  l.prefix = l.lead + G;
+  l.group = l.prefix + G;
   griddep_wait();
   griddep_launch_dependents();
   for (int g = threadIdx.x; g <= G; g += blockDim.x)
@@ -389,7 +391,8 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParam
   for (int g = threadIdx.x; g < G; g += blockDim.x) {
     const int n = __ldg(p.prefix_lens + g);
     l.tok0[g] = 0;
-    l.tok1[g] = clampi(n, 0, p.capacity) & ~(TT - 1);
+    l.prefix[g] = clampi(n, 0, p.capacity);
+    l.tok1[g] = l.prefix[g] & ~(TT - 1);
     if ((n < 0 || n > p.capacity) && p.err_count) atomicAdd(p.err_count, 1);
   }
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(const SharedParam
 }
 
 size_t schedule_smem(int G, int V) {
-  return (static_cast<size_t>(V) + 1 + 32) * 8 + (3 * static_cast<size_t>(V) + G + 1) * 4;
+  return (static_cast<size_t>(V) + 1 + 32) * 8 + (3 * static_cast<size_t>(V) + 2 * G + 1) * 4;
 }
 
 // ---------------------------------------------------------------- conversion
@@ -1304,7 +1307,7 @@ cudaError_t launch_decode_shared(const SharedParams& p_in, const CUtensorMap& tm
   cudaError_t e = set_smem_attr_once(shared_schedule_kernel, kMostSmem, attr_done);
   if (e != cudaSuccess) return e;
   static_assert((kMaxSharedGroups + kMaxSharedSeqs + 33) * 8 +
-                        (3 * (kMaxSharedGroups + kMaxSharedSeqs) + kMaxSharedGroups + 1) * 4 <=
+                        (3 * (kMaxSharedGroups + kMaxSharedSeqs) + 2 * kMaxSharedGroups + 1) * 4 <=
                     kMostSmem,
                 "the schedule's shared memory");
   const int G = p.num_groups, V = G + p.num_seqs;

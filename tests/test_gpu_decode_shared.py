@@ -335,3 +335,14 @@ def test_scores_of_minus_infinity(cuda_dev, fmt):
         bound = 2 ** -7 * 1.1 * torch.exp(x - z[:, None]) @ k[:, :512].abs() + 1e-4
         assert bool(((o[b].double() - ref).abs() <= bound).all()), b
         assert float((lse[b].double() - z).abs().max()) < 1e-3
+
+
+@pytest.mark.parametrize("fmt,R", [("bf16", 512), ("e4m3", 256)])
+@pytest.mark.parametrize("groups,prefix,lens", [
+    ([0, 5], [222], [300, 171, 222, 130, 128]),
+    ([0, 4, 9], [383, 129], [382, 383, 256, 500, 128, 129, 128, 700, 129]),
+    ([0, 6], [1000], [999, 1000, 896, 897, 1100, 1023])])
+def test_longer_than_the_shared_tiles_shorter_than_the_prefix(cuda_dev, groups, prefix, lens, fmt, R):
+    """Those are decoded by themselves: their first tokens are their own."""
+    c = Case(groups, prefix, lens, 16, R=R, fmt=fmt, seed=sum(lens))
+    c.check(*c.run())
