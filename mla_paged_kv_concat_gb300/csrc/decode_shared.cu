@@ -805,21 +805,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? 512 : 384, 1)
     const int tq = threadIdx.x - 128, r = tq;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // This thread copies 16 bytes (dims 8 (tq % 8) on) of vectors tq / 8 + 16 j:
-    // their rows and heads, -1 for vectors that there are not, which become zeros.
+    // their rows, counted from the block's first (at most 128 of them: rows of the
+    // batch times 128 do not fit 32 bits), and heads, -1 for vectors that there are
+    // not, which become zeros.
+    const int row_in = sg.vec0 / H, row0 = sg.row0 + row_in;
     int place[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int v = (tq >> 3) + 16 * j;
-      const int vec = sg.vec0 + v;
+      const int vec = sg.vec0 - row_in * H + v;
       const int row = vec / H;
-      place[j] = v < sg.vecs ? (sg.row0 + row) * 128 + (vec - row * H) : -1;
+      place[j] = v < sg.vecs ? row * 128 + (vec - row * H) : -1;
     }
     auto nope = [&](int j) {
-      const int64_t row = place[j] >> 7, hd = place[j] & 127;
+      const int64_t row = row0 + (place[j] >> 7), hd = place[j] & 127;
       return p.q + (place[j] < 0 ? 0 : row * p.q_row_stride + hd * p.q_head_stride) + (tq & 7) * 8;
     };
     auto rope = [&](int j) {
-      const int64_t row = place[j] >> 7, hd = place[j] & 127;
+      const int64_t row = row0 + (place[j] >> 7), hd = place[j] & 127;
       return p.q_pe + (place[j] < 0 ? 0 : row * p.q_pe_row_stride + hd * p.q_pe_head_stride) +
              (tq & 7) * 8;
     };
