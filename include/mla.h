@@ -294,7 +294,8 @@ mla_status mla_decode_ex(const void* q, int64_t q_row_stride,
  *                   (clamped to the block table, counted).
  *   num_groups      1 .. 1024; num_seqs at most 8192 (else
  *                   MLA_ERR_UNSUPPORTED, as are block tables of more than 2^30
- *                   tokens, or more than 2^30 tiles of 128 tokens x 128 vectors).
+ *                   tokens, more than 2^29 query vectors (rows x heads), or more
+ *                   than 2^30 tiles of 128 tokens x 128 vectors).
  *   workspace       >= mla_decode_shared_workspace_bytes(...) with the device's
  *                   SM count, 256-byte aligned.  Calls that may overlap on the
  *                   GPU need one each.

@@ -163,6 +163,12 @@ cudaError_t launch_lse_merge(const void* o_parts, int64_t o_part_stride, const f
 
 // ---------------------------------------------------------------- shared prefixes
 constexpr int kMaxSharedSeqs = 8192, kMaxSharedGroups = 1024;
+// Rows x heads: each has two places of the workspace, its own part's and its group's,
+// beside those that fill up blocks of 128.
+constexpr int kMaxSharedVectors = 1 << 29;
+static_assert(2 * int64_t{kMaxSharedVectors} +
+                      128 * (int64_t{kMaxSharedSeqs} + kMaxSharedGroups + 4096 + 1) <= INT32_MAX,
+              "places in 32 bits");
 
 // A part of the work, a group's shared tokens or a sequence's other ones, in the
 // list of tiles and units: blocks of 128 query vectors from row0 on.

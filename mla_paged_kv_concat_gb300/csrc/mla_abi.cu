@@ -507,6 +507,7 @@ size_t mla_decode_shared_workspace_bytes(int num_rows, int num_heads, int num_se
                                          int kv_lora_rank, int sm_count) {
   if (num_rows <= 0 || num_heads < 1 || num_heads > 128 || num_seqs < 1 ||
       num_seqs > mla::kMaxSharedSeqs || num_groups < 1 || num_groups > mla::kMaxSharedGroups ||
+      static_cast<int64_t>(num_rows) * num_heads > mla::kMaxSharedVectors ||
       (kv_lora_rank != 512 && kv_lora_rank != 256) || sm_count < 2 || sm_count > 4096)
     return 0;
   return mla::shared_layout(num_rows, num_heads, num_seqs, num_groups, kv_lora_rank, sm_count / 2,
@@ -539,8 +540,10 @@ mla_status mla_decode_shared(const void* q, int64_t q_row_stride, int64_t q_head
       !mla::aligned4(block_table) || !mla::aligned4(seq_lens) || !mla::aligned4(kv_scale) ||
       !mla::aligned4(err_count))
     return MLA_ERR_INVALID_ARG;
-  // the tiles of all blocks of 128 vectors are counted in 32 bits
+  // the places of vectors in the workspace, and the tiles of all blocks of 128 vectors,
+  // are counted in 32 bits
   const int64_t capacity = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+  if (static_cast<int64_t>(num_rows) * num_heads > mla::kMaxSharedVectors) return MLA_ERR_UNSUPPORTED;
   const int64_t blocks = static_cast<int64_t>(num_rows) * num_heads / 64 + num_seqs + num_groups;
   if (capacity > (1 << 30) || (capacity / 128 + 4) > INT32_MAX / 2 / blocks) return MLA_ERR_UNSUPPORTED;
   int sms = 0;
