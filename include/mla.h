@@ -299,6 +299,7 @@ mla_status mla_decode_ex(const void* q, int64_t q_row_stride,
  *   workspace       >= mla_decode_shared_workspace_bytes(...) with the device's
  *                   SM count, 256-byte aligned.  Calls that may overlap on the
  *                   GPU need one each.
+ * o, lse and workspace must not overlap each other or an input (refused).
  * Other arguments as mla_decode.  The work is shared out on the device from the
  * lengths, so the call can be captured into a graph and replayed with others.
  * Run-to-run deterministic; a row's result depends on the batch through the

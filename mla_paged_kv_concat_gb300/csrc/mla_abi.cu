@@ -14,6 +14,7 @@
 #include "../../include/mla.h"
 #include "abi.cuh"
 #include "kernels.cuh"
+#include "tensors.cuh"
 
 namespace {
 thread_local char g_last_cuda_error[256] = "";
@@ -67,6 +68,10 @@ namespace {
 using mla::aligned16;
 using mla::cuda_fail;
 using mla::encode_map;
+using mla::Heads;
+using mla::intersect;
+using mla::Runs;
+using mla::runs;
 
 bool valid_kv_dtype(mla_kv_dtype t) {
   return t == MLA_KV_BF16 || t == MLA_KV_FP8_E4M3 || t == MLA_KV_FP8_E5M2;
@@ -543,9 +548,28 @@ mla_status mla_decode_shared(const void* q, int64_t q_row_stride, int64_t q_head
   // the places of vectors in the workspace, and the tiles of all blocks of 128 vectors,
   // are counted in 32 bits
   const int64_t capacity = static_cast<int64_t>(max_blocks_per_seq) * block_size;
-  if (static_cast<int64_t>(num_rows) * num_heads > mla::kMaxSharedVectors) return MLA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_rows) * num_heads > mla::kMaxSharedVectors)
+    return MLA_ERR_UNSUPPORTED;
   const int64_t blocks = static_cast<int64_t>(num_rows) * num_heads / 64 + num_seqs + num_groups;
   if (capacity > (1 << 30) || (capacity / 128 + 4) > INT32_MAX / 2 / blocks) return MLA_ERR_UNSUPPORTED;
+  const bool fp8 = kv_dtype != MLA_KV_BF16;
+  const int64_t elt = fp8 ? 1 : 2, vecs = static_cast<int64_t>(num_rows) * num_heads;
+  const int D = kv_lora_rank + rope_dim;
+  const Runs in[8] = {
+      runs(Heads{q, q_row_stride, q_head_stride, q_pe ? kv_lora_rank : D}, num_rows, num_heads),
+      q_pe ? runs(Heads{q_pe, q_pe_row_stride, q_pe_head_stride, rope_dim}, num_rows, num_heads)
+           : runs(nullptr, 0),
+      runs(kv_cache, num_blocks, block_stride * elt, 1, 0, int64_t{block_size} * D * elt),
+      runs(block_table, num_seqs, block_table_stride * 4, 1, 0, int64_t{max_blocks_per_seq} * 4),
+      runs(seq_lens, int64_t{num_seqs} * 4), runs(group_seqs, (int64_t{num_groups} + 1) * 4),
+      runs(prefix_lens, int64_t{num_groups} * 4), runs(d.kv_scale, 4)};
+  const Runs ro = runs(o, vecs * kv_lora_rank * 2), rl = runs(lse, vecs * 4);
+  auto over_input = [&](const Runs& out) {
+    for (const Runs& x : in)
+      if (intersect(out, x)) return true;
+    return false;
+  };
+  if (intersect(ro, rl) || over_input(ro) || over_input(rl)) return MLA_ERR_INVALID_ARG;
   int sms = 0;
   cudaError_t e = mla::device_sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -554,7 +578,8 @@ mla_status mla_decode_shared(const void* q, int64_t q_row_stride, int64_t q_head
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return MLA_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  const bool fp8 = kv_dtype != MLA_KV_BF16;
+  const Runs rw = runs(workspace, static_cast<int64_t>(need));
+  if (intersect(rw, ro) || intersect(rw, rl) || over_input(rw)) return MLA_ERR_INVALID_ARG;
   mla::SharedParams p = {};
   p.q = d.q;
   p.q_row_stride = d.q_row_stride;

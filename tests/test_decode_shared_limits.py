@@ -13,7 +13,8 @@ SHAPES = [  # sequences, rows of each, heads: 2^29 query vectors
 @pytest.mark.parametrize("B,rows,H", SHAPES)
 def test_query_vectors(lib, B, rows, H):  # noqa: F811
     def call(n):
-        a = dict(BASE, T=B * n, B=B, H=H, qs=H * 576, maxb=1, wsb=0)
+        a = dict(BASE, q=1 << 44, o=1 << 45, lse=1 << 46, T=B * n, B=B, H=H, qs=H * 576, maxb=1,
+                 wsb=0)
         return lib.mla_decode_shared(*a.values())
 
     assert B * rows * H == 1 << 29
