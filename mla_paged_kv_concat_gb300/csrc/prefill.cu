@@ -214,8 +214,9 @@ __device__ bool unit_at(const PrefillParams& p, const Starts& at, uint32_t x, Un
   const int qa = clampi(q0, 0, p.num_tokens), qz = clampi(q1, qa, p.num_tokens);
   const int ka = clampi(k0, 0, p.num_kv), kz = clampi(k1, ka, p.num_kv);
   const int blk = slot - (qa / kUnitRows + a);
+  // (a group's rows are its sequences', which count theirs)
   if (blk == 0 && u.h == 0 && part == 0 && p.err_count &&
-      (qa != q0 || qz != q1 || ka != k0 || kz != k1))
+      ((!pre && (qa != q0 || qz != q1)) || ka != k0 || kz != k1))
     atomicAdd(p.err_count, 1);
   const int lq = qz - qa;
   u.lk = kz - ka;
@@ -252,10 +253,23 @@ __device__ __forceinline__ int seq_of(const int32_t* cu_q, int lo, int hi, int r
 // Own keys [lo, hi) of row `row`, of sequence b, counted from key row `first`.
 __device__ __forceinline__ int2 own_keys(const PrefillParams& p, const int32_t* cu_q,
                                          const int32_t* cu_k, int b, int row, int first) {
-  const int q0 = cu_q[b], k0 = clampi(cu_k[b], 0, p.num_kv), k1 = clampi(cu_k[b + 1], k0, p.num_kv);
+  const int qz = clampi(cu_q[b + 1], 0, p.num_tokens);
+  const int k0 = clampi(cu_k[b], 0, p.num_kv), k1 = clampi(cu_k[b + 1], k0, p.num_kv);
   const int lk = k1 - k0;
-  const int n = p.causal ? min(lk, row - q0 + lk - (cu_q[b + 1] - q0) + 1) : lk;
+  const int n = p.causal ? min(lk, row + lk - qz + 1) : lk;
   return make_int2(max(k0 - first, 0), max(k0 - first, 0) + max(n, 0));
+}
+
+// kFused: counts the sequences whose rows or keys are clamped.  Its units are groups'
+// rows, in which a sequence without rows has no place: unit x looks at sequences x,
+// x + units and so on.
+__device__ __forceinline__ void count_clamped(const PrefillParams& p, const Starts& at, int64_t x) {
+  for (int64_t b = x; b < p.num_seqs; b += gridDim.x) {
+    const int q0 = at.q[b], q1 = at.q[b + 1], k0 = at.k[b], k1 = at.k[b + 1];
+    const int qa = clampi(q0, 0, p.num_tokens), ka = clampi(k0, 0, p.num_kv);
+    if (qa != q0 || clampi(q1, qa, p.num_tokens) != q1 || ka != k0 || clampi(k1, ka, p.num_kv) != k1)
+      atomicAdd(p.err_count, 1);
+  }
 }
 
 // kFused: 256 rows of a group in the order they lie in, over the sequences' ends.
@@ -288,8 +302,7 @@ __device__ bool unit_at<kFused>(const PrefillParams& p, const Starts& at, uint32
   const int k0 = prefix ? at.gk[a - 1] : 0, k1 = prefix ? at.gk[a] : 0;
   const int ka = clampi(k0, 0, p.num_kv), kz = clampi(k1, ka, p.num_kv);
   const int blk = slot - (qa / kUnitRows + a);
-  if (blk == 0 && u.h == 0 && u.split == 0 && p.err_count &&
-      (qa != q0 || qz != q1 || ka != k0 || kz != k1))
+  if (blk == 0 && u.h == 0 && u.split == 0 && p.err_count && (ka != k0 || kz != k1))
     atomicAdd(p.err_count, 1);
   const int r0 = blk * kUnitRows;
   if (blk < 0 || r0 >= qz - qa) return false;
@@ -585,6 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (ask) next_cta_ask(smem + OFF_NEXT, next_full);
+          if (MODE == kFused && x >= 0 && p.err_count) count_clamped(p, at, x);
           if (x < 0 || !mbar_wait(next_full, asked & 1)) break;
           x = next_cta_answer(smem + OFF_NEXT);
           fence_proxy_async_smem();  // read before the next answer is written
