@@ -257,7 +257,10 @@ __device__ __forceinline__ int2 own_keys(const PrefillParams& p, const int32_t* 
   const int k0 = clampi(cu_k[b], 0, p.num_kv), k1 = clampi(cu_k[b + 1], k0, p.num_kv);
   const int lk = k1 - k0;
   const int n = p.causal ? min(lk, row + lk - qz + 1) : lk;
-  return make_int2(max(k0 - first, 0), max(k0 - first, 0) + max(n, 0));
+  // (with starts that decrease, which nobody may give, they still end in the tensors: values
+  // that are not finite are read again from there)
+  const int lo = max(k0 - first, 0);
+  return make_int2(lo, min(lo + max(n, 0), p.num_kv - first));
 }
 
 // kFused: counts the sequences whose rows or keys are clamped.  Its units are groups'

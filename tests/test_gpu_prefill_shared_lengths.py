@@ -100,3 +100,17 @@ def test_prefixes_are_counted_once(cuda_dev, splits):
     # many sequences, most of them past the rows; none of a group
     n = 300
     assert b.run(list(range(n + 1)), [400] * (n + 1), splits, True, groups=(0, 0))[2] == n - T
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_starts_that_decrease_stay_in_the_tensors(cuda_dev, causal):
+    """Not allowed, so only the first sequence's rows are told; its keys end where the
+    tensors do, and a later sequence's start far before them."""
+    b = Batch()
+    b.v[TK - 1, 0, 5] = math.inf  # of the first sequence's last key: read again for its rows
+    cu_q, cu_k = [0, 20, 20, 60], [TK - 100, TK, 10, TK]
+    o, lse, err = b.run(cu_q, cu_k, (1, 0), causal, groups=(0, 3))
+    ref, ref_lse, _ = b.run([0, 20], cu_k[:2], (1, 0), causal, groups=(0, 1))
+    assert err == 1  # the empty sequence whose end lies before its start
+    assert torch.equal(lse[:20], ref_lse[:20])
+    assert torch.equal(o[:20].isfinite(), ref[:20].isfinite())
