@@ -821,7 +821,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O is rescaled only when the maximum has grown by more than 2^8
         // (-inf - -inf is NaN: no)
         const bool grow = (m_new - mo) * c > kRescale;
-        if (__any_sync(0xffffffffu, (j > 0 && grow) || fabsf(m_new) > large)) {
+        // (a row without keys so far is not large: in a window of several sequences' keys
+        // most tiles have one)
+        if (__any_sync(0xffffffffu,
+                       (j > 0 && grow) || (fabsf(m_new) > large && m_new != -INFINITY))) {
           // This tile's S was issued after the last P.V: O is complete.  The loop
           // does O and S alike, so that the rare case adds little code (64
           // instructions more cost short prompts 4 %).
