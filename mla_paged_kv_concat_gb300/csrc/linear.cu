@@ -977,6 +977,9 @@ __global__ void __launch_bounds__(192, FewCfg<TN>::CTAS)
   }
 }
 
+// Pairs of CTAs at work together (one on a single SM: the launch says that it has no room).
+int pairs_of(int sm_count) { return sm_count < 2 ? 1 : sm_count / 2; }
+
 // A launch in clusters of `size` CTAs that may start under the kernel before.
 template <typename K, typename... Args>
 cudaError_t launch_clusters(K kernel, dim3 grid, int threads, int smem, int size,
@@ -1004,7 +1007,7 @@ cudaError_t launch_pair(const LinearParams& p, const LinearMaps& m, int sm_count
   cudaError_t e = set_smem_attr_once(linear_pair_kernel<BN, ACT>, PP_SMEM, attr_done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>((p.tokens + 255) / 256) * ((p.n + BN - 1) / BN);
-  const int pairs = tiles < sm_count / 2 ? static_cast<int>(tiles) : sm_count / 2;
+  const int most = pairs_of(sm_count), pairs = tiles < most ? static_cast<int>(tiles) : most;
   return launch_overlapped(linear_pair_kernel<BN, ACT>, dim3(2 * pairs), dim3(320), PP_SMEM, stream, p,
                            m.a, m.b, m.c);
 }
@@ -1092,20 +1095,23 @@ LinearPlan linear_plan(int tokens, int n, int k, int sm_count) {
       const int fit = s == 8 ? sm_count * 15 / 19 : s == 4 ? sm_count * 18 / 19
                                                 : s == 3   ? sm_count * 10 / 11
                                                            : sm_count;
+      if (fit < s) continue;  // (a part of a device with few SMs)
       take(cdiv64(ctas * s, fit) * cdiv64(nk, s) * chunk(128 + tn, 128) +
                cdiv64(ctas * s, slots * fit) * 4000,
            {kLinearFew, tn, s, tn, 128});
     }
   }
   if (tokens > 128) {
+    const int most_pairs = pairs_of(sm_count);
     for (int bn = 256; bn >= 128; bn -= 64)
-      take(cdiv64(cdiv64(tokens, 256) * cdiv64(n, bn), sm_count / 2) * nk *
+      take(cdiv64(cdiv64(tokens, 256) * cdiv64(n, bn), most_pairs) * nk *
                    chunk(128 + bn / 2, bn) + 4000,
            {kLinearPair, bn, 1, TM, bn / 2});
     const int64_t tiles = cdiv64(tokens, 256) * cdiv64(n, 256);
     for (int s = 2; s <= 4 && s <= nk; ++s) {
       const int fit = (s == 4 ? sm_count * 15 / 19 : s == 3 ? sm_count * 10 / 11
                                                             : sm_count * 18 / 19) / (2 * s);
+      if (fit < 1) continue;
       take(cdiv64(tiles, fit) * (cdiv64(nk, s) * chunk(256, 256) + (s == 2 ? 9500 : 12000)),
            {kLinearPair, 256, s, TM, 128});
     }
