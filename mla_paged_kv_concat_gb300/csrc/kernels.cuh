@@ -327,7 +327,8 @@ struct LinearPlan {
 };
 LinearPlan linear_plan(int tokens, int n, int k, int sm_count);
 // a: x as {K, 1, tokens}, box {64, 1, a_rows}; b: W as {K, 1, N}, box {64, 1,
-// b_rows}; c: y as {N, 1, tokens}, box {64, 1, 32}.  All 128-byte swizzled bf16.
+// b_rows}; c: y as {N less N % 8 (or 8), 1, tokens}, box {64, 1, 32}: the columns of whole
+// 16 bytes.  All 128-byte swizzled bf16.
 struct LinearMaps {
   CUtensorMap a, b, c;
 };

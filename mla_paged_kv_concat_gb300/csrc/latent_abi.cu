@@ -495,7 +495,8 @@ mla_status mla_linear(const void* x, int64_t x_row_stride, int num_tokens, int i
     st = make_map(&m.b, w, in_features, 1, out_features, w_row_stride, w_row_stride, 1,
                   plan.b_rows);
   if (st == MLA_OK)
-    st = make_map(&m.c, y, out_features, 1, num_tokens, y_row_stride, y_row_stride, 1, 32);
+    st = make_map(&m.c, y, out_features < 8 ? 8 : out_features & ~7, 1, num_tokens, y_row_stride,
+                  y_row_stride, 1, 32);
   if (st != MLA_OK) return st;
   e = mla::launch_linear(p, m, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);

@@ -193,11 +193,17 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
 // row a lane: 42.1 us for 37.7, 4096 x 512 -> 7168).  The loop is not unrolled, and products without an
 // activation have kernels of their own: with all activations in 32 copies of the
 // body 1001 x 1536 -> 6136 took 35 us, waiting for instructions, against 22.
-template <bool ACT, typename Before, typename After>
+// TAIL: N % 8 columns behind those that the map of y has are stored one by one.  A TMA
+// store writes the 16 bytes that a row ends in to their end, so the map ends with the
+// last whole ones.  (Kernels of their own: the others got 1 to 3 % slower with it.)
+template <bool ACT, bool TAIL, typename Before, typename After>
 __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, int cols, int c0,
                                          int row0, int lane, uint8_t* boxes, int& nb,
                                          const CUtensorMap* map, Before&& before, After&& after) {
   constexpr int N = ACT ? 16 : 32;  // columns of a step
+  const int whole = TAIL ? p.n & ~7 : p.n;  // columns that the map has
+  // no box follows the one that has y's last column
+  if (TAIL && p.n - c0 < cols) cols = max(64, (p.n - c0 + 63) & ~63);
   uint4 res[8], bias[N / 8];  // of the next box: rows 4 k + lane / 8, eight columns
   auto load = [&](int c) {
 #pragma unroll
@@ -264,11 +270,21 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, uint32_t acc, in
       __syncwarp();
       if (lane == 0) {
         const int cb = c0 + (j & ~63);
-        if (row0 < p.tokens && cb < p.n) tma_store_3d(map, dst, cb, 0, row0);
+        if (row0 < p.tokens && cb < whole) tma_store_3d(map, dst, cb, 0, row0);
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
       ++nb;
     }
+  }
+  if (TAIL && whole >= c0 + cols - 64 && whole < c0 + cols && row0 + lane < p.tokens) {
+    // a lane's row of the last box, which a store may still read
+    const uint8_t* src = boxes + ((nb - 1) & 1) * STORE_BYTES;
+    const uint4 v = *reinterpret_cast<const uint4*>(src + sw128(lane, (whole & 63) / 8));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint16_t* y = p.y + (row0 + lane) * p.y_stride + whole;
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (whole + e < p.n) y[e] = static_cast<uint16_t>(w[e >> 1] >> ((e & 1) * 16));
   }
   return true;
 }
@@ -293,9 +309,9 @@ __device__ __forceinline__ void tile_at(int64_t t, int mt, int nt, int& m, int& 
 // "landed" barrier is rank 0's and counts both CTAs' bytes; "read" and "accumulator
 // ready" arrive in both.  Eight epilogue warps own 32 rows and half of the columns
 // each: TMEM -> registers, bias, activation and residual there, bf16 in a swizzled
-// 4 KiB staging box -> TMA store, which clips the tensor's edges.  The next columns'
-// residual and bias are loaded while the current ones are worked on (the first
-// before the accumulator is waited for).
+// 4 KiB staging box -> TMA store, which clips the tensor's edges (columns to 16 bytes).
+// The next columns' residual and bias are loaded while the current ones are worked on
+// (the first before the accumulator is waited for).
 constexpr int kPairStages = 5;
 constexpr int kPairHalf = A_BYTES;  // A, and room for the half of B, of one stage
 constexpr int PP_STORE = kPairStages * 2 * kPairHalf;
@@ -304,7 +320,7 @@ constexpr int PP_TMEM = PP_BAR + (2 * kPairStages + 4) * 8;
 constexpr int PP_SMEM = PP_TMEM + 16 + 1024;
 static_assert(PP_SMEM <= 227 * 1024, "shared memory");
 
-template <int BN, bool ACT>
+template <int BN, bool ACT, bool TAIL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
     linear_pair_kernel(const LinearParams p, const __grid_constant__ CUtensorMap ma,
                        const __grid_constant__ CUtensorMap mb,
@@ -443,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
       int m, n;
       tile_at(t, mt, nt, m, n);
       const int a = ta & 1;
-      ok = epilogue<ACT>(
+      ok = epilogue<ACT, TAIL>(
           p, tmem + lanes + a * 256 + half * kFirst, half ? BN - kFirst : kFirst, n * BN + half * kFirst,
           m * 2 * TM + rank * TM + qd * STORE_ROWS, lane, box, nb, &mc,
           [&] { return warp_wait(&acc_full[a], (ta >> 1) & 1); },
@@ -1000,16 +1016,22 @@ cudaError_t launch_clusters(K kernel, dim3 grid, int threads, int smem, int size
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int BN, bool ACT>
-cudaError_t launch_pair(const LinearParams& p, const LinearMaps& m, int sm_count,
+template <int BN, bool ACT, bool TAIL>
+cudaError_t launch_pair_of(const LinearParams& p, const LinearMaps& m, int sm_count,
                         cudaStream_t stream) {
   static std::atomic<uint64_t> attr_done{0};
-  cudaError_t e = set_smem_attr_once(linear_pair_kernel<BN, ACT>, PP_SMEM, attr_done);
+  cudaError_t e = set_smem_attr_once(linear_pair_kernel<BN, ACT, TAIL>, PP_SMEM, attr_done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>((p.tokens + 255) / 256) * ((p.n + BN - 1) / BN);
   const int most = pairs_of(sm_count), pairs = tiles < most ? static_cast<int>(tiles) : most;
-  return launch_overlapped(linear_pair_kernel<BN, ACT>, dim3(2 * pairs), dim3(320), PP_SMEM, stream, p,
-                           m.a, m.b, m.c);
+  return launch_overlapped(linear_pair_kernel<BN, ACT, TAIL>, dim3(2 * pairs), dim3(320), PP_SMEM,
+                           stream, p, m.a, m.b, m.c);
+}
+template <int BN, bool ACT>
+cudaError_t launch_pair(const LinearParams& p, const LinearMaps& m, int sm_count,
+                        cudaStream_t stream) {
+  return p.n % 8 ? launch_pair_of<BN, ACT, true>(p, m, sm_count, stream)
+                 : launch_pair_of<BN, ACT, false>(p, m, sm_count, stream);
 }
 
 template <bool ACT>
