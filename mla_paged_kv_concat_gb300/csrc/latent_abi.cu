@@ -467,7 +467,8 @@ mla_status mla_linear(const void* x, int64_t x_row_stride, int num_tokens, int i
   if (intersect(ry, runs(hx, num_tokens, 1)) || intersect(ry, runs(hw, out_features, 1)) ||
       intersect(ry, runs(bias, 2 * int64_t{out_features})))
     return MLA_ERR_INVALID_ARG;
-  // an element of the residual is read by the thread that writes y's there
+  // the warp that stores y's element has the residual's before it does, and no other
+  // warp reads that one
   const bool in_place = residual == y && (residual_row_stride == y_row_stride || num_tokens == 1);
   if (residual && !in_place && intersect(ry, runs(hr, num_tokens, 1))) return MLA_ERR_INVALID_ARG;
   int sms = 0;
