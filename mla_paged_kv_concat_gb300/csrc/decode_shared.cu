@@ -40,16 +40,17 @@
 // place in the workspace: list positions only grow, so no two are alike.
 //
 // Measured on GB300, one call out of a graph, and what bounds it:
-//   128 sequences, 128 heads, three prefixes, bf16, R = 512   317 us  1.10 PFLOP/s: a tile
-//       of 128 x 128 takes 1.76 us on rank 0, whose 36 products read 147 KB of shared
-//       memory (95 cycles each for 74)
+//   128 sequences, 128 heads, three prefixes, bf16, R = 512   319 us  1.10 PFLOP/s: a tile
+//       of 128 x 128 takes 1.76 us on rank 0, its 36 products 95 cycles each for 74 alone.
+//       What holds them is not shown: the busiest SM's tensor pipe is 58 % and its tensor
+//       memory 61 % busy, shared memory's operand reads 34 % on average
 //   64 sequences behind 8192 tokens, 16 heads, bf16, R = 512   53.6  12 tiles a pair; lists
 //       5, start and Q 5, O 4, join 8
 //   45 sequences, 32 heads, two prefixes, E4M3, R = 256        57.0  conversion on rank 0,
 //       2.1 us a tile
 //   33 sequences of two rows behind 4097, 16 heads, E5M2, 512  47.4  the same, 3.3 us a tile
-//   4 sequences behind 512, 16 heads, bf16, R = 512            22.5  latency: lists 4.3,
-//       start and Q 4.7, a tile 5, O 2, join 5
+//   4 sequences behind 512, 16 heads, bf16, R = 512            22.5  three dependent kernels:
+//       lists 4.3, start and Q 4.7, a tile 5, O 2, join 5
 // The plain decode takes 408, 89, 84, 69 and 12.4 us on these.  It is the faster one
 // where the tokens of all sequences together are few: with 16 heads about 150 thousand of
 // a bf16 cache, 35 to 100 thousand of an fp8 one.  128 heads fill the 128 vectors alone, and

@@ -568,13 +568,15 @@ mla_status mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_strid
 // SMs, the last ones overhang by half of the longest; a join takes 3.5 and 2.3e-4 for
 // a row and head of each part.  Own keys together with the prefix's (first loop) or
 // apart (second).  Measured (us: one part together / this rule's / the best of eleven
-// tried), 16 heads: three sequences of 20 rows, 1000 keys before them, 20 of their own
-// 21.0 / 15.2 (3 and 1) / 14.5, 300 of their own 36.2 / 15.4 (3, 1) / 15.4; one of 200
-// rows, 4000 and 200 keys 69.3 / 25.5 (8, 1) / 25.5; eight of 60 rows, 4000 and 60 keys
-// 73.0 / 38.5 (4, 0) / 37.0, 700 and 60 keys 28.6 / 28.6 / 23.8 (the worst found); 64 single
-// rows, 8192 and 1000 keys 1178 / 128 (8, 1) / 126; 48 of 48 rows, 8192 and 48 keys 144 /
-// 144 / 144, apart 180; 32 heads, eight of 1000 rows, 4096 and 1000 keys 533 / 533 / 533,
-// apart 633.
+// tried, before rows without keys in a tile took less in windows of several sequences; today's
+// first two behind it), 16 heads: three sequences of 20 rows, 1000 keys before them, 20 of
+// their own 21.0 / 15.2 (3 and 1) / 14.5 (20.5 / 14.8), 300 of their own 36.2 / 15.4 (3, 1) /
+// 15.4 (36.0 / 15.0); one of 200 rows, 4000 and 200 keys 69.3 / 25.5 (8, 1) / 25.5 (68.0 /
+// 24.5); eight of 60 rows, 4000 and 60 keys 73.0 / 38.5 (4, 0) / 37.0 (70.0 / 36.5), 700 and 60
+// keys 28.6 / 28.6 / 23.8 (the worst found; 25.3 / 25.3); 64 single rows, 8192 and 1000 keys
+// 1178 / 128 (8, 1) / 126 (1215 / 128); 48 of 48 rows, 8192 and 48 keys 144 / 144 / 144, apart
+// 180 (132 / 132, 183); 32 heads, eight of 1000 rows, 4096 and 1000 keys 533 / 533 / 533, apart
+// 633 (543 / 543, 618).
 int mla_prefill_shared_num_kv_splits(int num_tokens, int num_seqs, int num_groups, int num_heads,
                                      int64_t max_prefix_len, int64_t max_kv_len, int sm_count,
                                      int* num_kv_splits) {

@@ -8,17 +8,20 @@
 // All bring K in chunks of 64 through a TMA ring (128-byte swizzle; what
 // lies past K, N or T is filled with zeros).
 //
-// Measured on GB300, out of a graph back to back (W mostly in L2) and behind a flush
-// of L2, and what bounds it:
-//   1 x 8192 -> 7168, bias, residual         19.1 / 27.5 us  memory: 17.3 at 6.8 TB/s
-//   64 x 2048 -> 5120, residual               7.1 / 11.7     start, join and end 4.4, then
+// Measured on GB300, out of a graph back to back (W mostly in L2) and out of one with a
+// flush of L2 before each call, whose time is taken off, and what bounds it (a single call
+// between others that wait for it takes 20.6, 7.7, 20.9 and 838 us on the first three and the
+// fifth):
+//   1 x 8192 -> 7168, bias, residual         19.7 / 27.5 us  memory: 17.3 at 6.8 TB/s
+//   64 x 2048 -> 5120, residual               7.2 / 11.1     start, join and end 4.4, then
 //                                                            264 KB a CTA at 97 B/ns
-//   1001 x 1536 -> 6136, bias, silu          19.5 / 22.6     1.38 MB a CTA at 97 B/ns in two
+//   1001 x 1536 -> 6136, bias, silu          19.8 / 21.7     1.38 MB a CTA at 97 B/ns in two
 //                                                            rounds of tiles, 2 of silu
-//   1262 x 184 -> 16176, bias, silu, res.    41.3 / 46.9     the tiles' ends: 31 without the
+//   1262 x 184 -> 16176, bias, silu, res.    41.4 / 46.1     the tiles' ends: 31 without the
 //                                                            residual, 17.5 without silu, too
-//   8192 x 16384 -> 5120, bias, residual     732 to 785      1.75 to 1.88 PFLOP/s, by clock
-//   442 x 9808 -> 3120, bias, relu           31.1 / 39.6     half of K a pair, 2.5 MB a CTA
+//   8192 x 16384 -> 5120, bias, residual     768 to 808      1.70 to 1.79 PFLOP/s, by the power
+//                                                            limit's clock (732 at best)
+//   442 x 9808 -> 3120, bias, relu           30.9 / 38.0     half of K a pair, 2.5 MB a CTA
 // What an SM takes in over TMA is 97 B/ns here, however many boxes are under way.  The
 // library's product alone: 20.3, 4.2, 12.4, 12.1, 715 to 780, 32.6 us; it shares the sum over
 // K out among all SMs whatever the tiles, for which it keeps a workspace.

@@ -50,11 +50,12 @@
 // row masked to its own; nothing to join with one part) or by units of each sequence
 // that are joined with the prefix's (kApart: no products outside a sequence, but two
 // parts at least, and a tile of 128 rows that a short sequence does not fill).  Measured,
-// fused / apart: 48 sequences of 48 rows behind 8192 keys, 16 heads 144 / 180 us; eight of
-// 1000 rows and 1000 keys behind 4096, 32 heads 533 / 633; 64 single rows, 1000 keys each,
-// behind 8192, 16 heads 1180 / 126.  The fused units of 8 prompts of 500 to 1500 rows
-// behind two prefixes, 32 heads, take 683 us, 1.41 PFLOP/s, tensor core 64 % busy: the
-// chain of a query tile as above, and the tiles that masks cut, about half as long again.
+// fused / apart, out of a graph back to back: 48 sequences of 48 rows behind 8192 keys, 16
+// heads 132 / 183 us; eight of 1000 rows and 1000 keys behind 4096, 32 heads 543 / 618; 64
+// single rows, 1000 keys each, behind 8192, 16 heads 1215 / 128.  The fused units of 8 prompts
+// of 500 to 1500 rows behind two prefixes, 32 heads, take 699 us back to back (1.38 PFLOP/s,
+// tensor core 63 % busy) and 730 to 740 as one call among others (1.31): the chain of a query
+// tile as above, and the tiles that masks cut, about half as long again.
 //
 // Masked keys.  Scores of masked keys are replaced by -inf, whatever K held.
 // V of a masked key would still meet a zero of P, and 0 * NaN is NaN: in the
